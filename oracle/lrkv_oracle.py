@@ -584,3 +584,108 @@ def prefill_reference_paged(q, k_s, v_s, z_k, z_v, b_k, b_v, block_table, page_s
     max_len = np.asarray(block_table).shape[1] * page_size
     g = [gather_paged(t, block_table, page_size, max_len) for t in (k_s, v_s, z_k, z_v)]
     return prefill_reference(q, g[0], g[1], g[2], g[3], b_k, b_v, seq_lens, scale=scale, pairs=pairs, rows=rows)
+
+
+# --------------------------------------------------------------------------
+# A cache inside a token budget: attention weights per cache row, eviction by
+# them, and rows that carry their positions on several axes.  The pages have
+# no counterpart; the readings are those of include/lrkv.h.
+
+def row_scores(q, k_s, z_k, b_k, h: int, scale: float, key_scale=None, positions=None, sections=None,
+               base: float = 10000.0) -> np.ndarray:
+    """Scaled scores [T, L] of queries q [T, d_h] of head h against the rebuilt
+    keys of rows k_s [L, d_h], z_k [L, H, r]; with positions [L, axes] the keys
+    are turned first (q then arrives rotated); key_scale [L] multiplies."""
+    K = reconstruct_head(_f64(k_s), _f64(z_k)[:, h, :], _f64(b_k)[h])
+    if positions is not None:
+        K = rope_rotate_axes(K, positions, sections, base)
+    s = scale * (_f64(q) @ K.T)
+    return s if key_scale is None else s * _f64(key_scale)
+
+
+def rope_rotate_axes(X, positions, sections, base: float = 10000.0) -> np.ndarray:
+    """Row j of X [L, d_h] with pair (2k, 2k+1) turned by positions[j, a(k)]
+    theta_k, a(k) the axis whose consecutive section of pairs holds k."""
+    X = _f64(X)
+    pos = np.asarray(_f64(positions))
+    axis = np.repeat(np.arange(len(sections)), sections)
+    assert len(axis) == X.shape[1] // 2
+    ang = pos[:, axis] * rope_frequencies(X.shape[1], base)[None, :]
+    z = (X[:, 0::2] + 1j * X[:, 1::2]) * np.exp(1j * ang)
+    out = np.empty_like(X)
+    out[:, 0::2], out[:, 1::2] = z.real, z.imag
+    return out
+
+
+def accumulate_weights(fresh, weights, decay: float, length: int, new: int) -> np.ndarray:
+    """decay * weights on the rows before the last `new` of `length`, plus the
+    fresh ones (rows [0, length))."""
+    out = np.array(fresh, dtype=np.float64)
+    if decay != 0 and length > new:
+        out[:length - new] += decay * _f64(weights)[:length - new]
+    return out
+
+
+def decode_weights_reference(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, scale: Optional[float] = None,
+                             key_scale=None, positions=None, sections=None, base: float = 10000.0):
+    """(out, lse, fresh) of a decode step by the definition, with fresh[b] [L_b]
+    the attention weights of each row summed over the heads."""
+    q = _f64(q)
+    lens = np.asarray(_f64(seq_lens), dtype=np.int64)
+    B, H, dh = q.shape
+    scale = default_scale(dh) if scale is None else scale
+    out, lse, fresh = np.zeros((B, H, dh)), np.full((B, H), -np.inf), []
+    for b in range(B):
+        L = int(lens[b])
+        total = np.zeros(L)
+        for h in range(H if L else 0):
+            s = row_scores(q[b, h:h + 1], k_s[b, :L], z_k[b, :L], b_k, h, scale,
+                           None if key_scale is None else key_scale[b, h, :L],
+                           None if positions is None else positions[b, :L], sections, base)[0]
+            V = reconstruct_head(_f64(v_s[b, :L]), _f64(z_v[b, :L])[:, h, :], _f64(b_v)[h])
+            out[b, h], lse[b, h] = _softmax_attend(s, V)
+            total += np.exp(s - lse[b, h])
+        fresh.append(total)
+    return out, lse, fresh
+
+
+def prefill_weights_reference(q, k_s, z_k, b_k, lse, seq_lens, window: int, scale: Optional[float] = None,
+                              key_scale=None):
+    """fresh[b] [L_b]: exp(score - lse) summed over the heads and the last
+    `window` of the queries q [B, T, H, d_h], each seeing the rows up to its own
+    (row L_b - T + i)."""
+    q, lse = _f64(q), _f64(lse)
+    lens = np.asarray(_f64(seq_lens), dtype=np.int64)
+    B, T, H, dh = q.shape
+    scale = default_scale(dh) if scale is None else scale
+    fresh = []
+    for b in range(B):
+        L = int(lens[b])
+        total = np.zeros(L)
+        for h in range(H):
+            s = row_scores(q[b, :, h], k_s[b, :L], z_k[b, :L], b_k, h, scale,
+                           None if key_scale is None else key_scale[b, h, :L])
+            for i in range(T - window, T):
+                p = L - T + i
+                if lse[b, h, i] != -np.inf:
+                    total[:p + 1] += np.exp(s[i, :p + 1] - lse[b, h, i])
+        fresh.append(total)
+    return fresh
+
+
+def evict_reference(weights, length: int, budget: int, sink: int = 0, recent: int = 0, order=None) -> np.ndarray:
+    """source[i] (i < n = min(length, budget)): the row whose contents row i
+    holds after the eviction."""
+    n = min(length, budget)
+    w = [float(x) for x in np.asarray(weights, dtype=np.float64)[:length]]
+    age = list(range(length)) if order is None else [int(a) for a in np.asarray(order)[:length]]
+    newest = max(age) + 1 if age else 0
+
+    def rank(j):
+        held = age[j] < sink or age[j] >= newest - recent
+        return (not held, -w[j] if w[j] == w[j] else math.inf, j)
+
+    keep = set(sorted(range(length), key=rank)[:n])
+    source = [j if j in keep else None for j in range(n)]
+    movers = iter(sorted(j for j in keep if j >= n))
+    return np.array([next(movers) if j is None else j for j in source], dtype=np.int64)
