@@ -112,6 +112,7 @@ struct DecodePlan {
   int map_len, map_seqs;
   float* out;
   float* lse;
+  float* scores;  // [B][H][max_len] scaled scores (log2 domain) of a weighted decode, or NULL
   // full-RoPE decode: the cos/sin table [max_pos][dh] (pairs (cos, sin) per
   // frequency) and its staged tile ([16][cs_row] fp32 per ring stage)
   const float* rope_cs;

@@ -1,0 +1,537 @@
+// evict.cu — eviction from the factored cache by accumulated attention
+// weight (lrkv_evict): the rows of a sequence that gathered least go, so that
+// at most `budget` stay.
+//
+// A sequence of L rows keeps n = min(L, budget) of them: the held rows (the
+// oldest `sink` and the newest `recent` tokens) and the heaviest others,
+// equal weights by the lower row.  The shared row belongs to every head, so a
+// token goes for all heads at once and its weight is the sum over them.
+//
+// Attention over a set of rows does not depend on their order, so nothing is
+// shifted: a kept row below n stays where it is, and the kept rows at or past
+// n (as many as there are dropped rows below n) move into those holes, the
+// k-th into the k-th.  That moves the fewest rows there can be, no row is both
+// read and written, and all moves run at once.
+//
+// 1. lrkv_evict_select_kernel, one cluster of CTAs per sequence: a radix
+//    selection (11 + 11 + 10 bits) of the order-preserving integer image of
+//    the weights finds the smallest kept value, each CTA counting its rows in
+//    shared memory and the cluster adding the counts up through distributed
+//    shared memory; then ballots and one prefix over the warps of the cluster
+//    rank equal values, holes and moved rows.
+// 2. lrkv_evict_move_kernel copies each moved row: 4 cache tensors, key
+//    scales, positions, weight, age.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "decode_plan.h"
+#include "host_cache.h"
+#include "lrkv.h"
+#include "ptx.cuh"
+#include "trace.h"
+
+namespace cg = cooperative_groups;
+
+namespace lrkv {
+
+namespace {
+
+constexpr int kEvThreads = 1024;
+constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvBins = 2048;          // 11 bits a level (the last level uses 1024)
+constexpr int kEvMaxCluster = 8;       // portable cluster size
+constexpr int kEvCacheRows = 40 * 1024;  // rows whose keys a CTA keeps in shared memory
+constexpr int kMoveThreads = 256;
+constexpr uint32_t kKeyHeld = 0xffffffffu;  // above every weight's key
+constexpr uint32_t kKeyOut = 0u;            // below every weight's key
+
+struct EvictParams {
+  int B, max_len, budget, sink, recent;
+  int cap;                 // entries of a move list: min(budget, max_len - budget)
+  int rows_per_cta;        // rows of one CTA of the cluster (a multiple of 32 * kEvWarps)
+  int cached;              // 1: the keys of a CTA's rows are kept in shared memory
+  int page_shift, num_pages, max_blocks;
+  const int32_t* block_table;  // [B][max_blocks] or NULL
+  const int32_t* seq_lens;
+  const float* weights;
+  const int32_t* order;    // or NULL: a row's age is its index
+  float* weights_out;
+  int32_t* order_out;      // or NULL
+  int32_t* new_lens;
+  int32_t* kept;           // [B][budget] or NULL
+  // workspace
+  uint32_t* status;
+  uint32_t* flags;         // [B] status bits of each sequence, written every call
+  int32_t* moves;          // [B] moved rows
+  int2* src;               // [B][cap] (logical, physical) row of the k-th moved row
+  int2* dst;               // [B][cap] (logical, physical) row of the k-th hole
+  // moved data
+  int n16[4];              // 16-byte pieces of a row of each cache tensor
+  unsigned char* base[4];
+  int H, axes;
+  float* key_scale;        // [B][H][max_len] or NULL
+  int32_t* positions;      // [B][max_len][axes] or NULL
+};
+
+// Order-preserving image of a weight: larger weight, larger integer, -0 as
+// +0 and NaN as -infinity.  Neither kKeyHeld nor kKeyOut is an image.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (!(w == w)) w = -INFINITY;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Exclusive prefix over the CTA's warps of a per-warp count (the same value
+// on every lane of a warp); total receives the CTA's sum.
+__device__ __forceinline__ int warp_prefix(int count, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) s_warp[warp] = count;
+  __syncthreads();
+  int v = lane < kEvWarps ? s_warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  total = __shfl_sync(0xffffffffu, v, kEvWarps - 1);
+  const int mine = __shfl_sync(0xffffffffu, v, warp);
+  return mine - count;
+}
+
+// Physical cache row of logical row t (page * page_size + offset), or -1 when
+// the block table names no page of the pool.
+__device__ __forceinline__ int physical_row(const EvictParams& P, int b, int t) {
+  if (!P.block_table) return b * P.max_len + t;
+  const int page = P.block_table[static_cast<size_t>(b) * P.max_blocks + (t >> P.page_shift)];
+  if (page < 0 || page >= P.num_pages) return -1;
+  return (page << P.page_shift) + (t & ((1 << P.page_shift) - 1));
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const EvictParams P) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), ncta = static_cast<int>(cluster.num_blocks());
+  const int b = blockIdx.x / ncta;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ uint32_t s_keys[];          // [rows_per_cta] when cached
+  __shared__ int s_hist[3][kEvBins];            // one table per level: no level waits to clear another's
+  __shared__ int s_warp[kEvWarps];
+  __shared__ int s_cta[4];                      // this CTA's max age + 1, held rows, equal rows, holes
+  __shared__ int s_cta2;                        // ... moved rows
+  __shared__ int s_bin, s_above, s_bad;
+
+  pdl_trigger();
+  for (int i = tid; i < 3 * kEvBins; i += kEvThreads) (&s_hist[0][0])[i] = 0;
+  if (tid < 4) s_cta[tid] = 0;
+  if (tid == 0) s_bad = 0;
+  pdl_wait();
+  int L = P.seq_lens[b];
+  const bool bad_len = L < 0 || L > P.max_len;
+  L = min(max(L, 0), P.max_len);
+  const int n = min(L, P.budget);
+  const float* w = P.weights + static_cast<size_t>(b) * P.max_len;
+  const int32_t* age = P.order ? P.order + static_cast<size_t>(b) * P.max_len : nullptr;
+  // rows of this CTA, and of this warp: contiguous, a multiple of 32 apart
+  const int lo = min(rank * P.rows_per_cta, L), hi = min(lo + P.rows_per_cta, L);
+  const int per_warp = P.rows_per_cta / kEvWarps;
+  const int wlo = min(lo + warp * per_warp, hi), whi = min(wlo + per_warp, hi);
+  __syncthreads();
+
+  int threshold_need = 0;          // rows equal to the threshold that are kept
+  uint32_t threshold = kKeyOut;    // smallest kept key
+  bool among_held = false;         // more held rows than n: they compete among themselves
+  const bool all = L <= n;         // nothing goes
+  int newest = L;                  // tokens seen: one past the largest age
+  auto held = [&](int t) {
+    const int a = age ? age[t] : t;
+    return a < P.sink || a >= newest - P.recent;
+  };
+  auto key_of = [&](int t) -> uint32_t {
+    const bool hd = held(t);
+    if (among_held) return hd ? weight_key(w[t]) : kKeyOut;
+    return hd ? kKeyHeld : weight_key(w[t]);
+  };
+  auto key_at = [&](int t) -> uint32_t { return P.cached ? s_keys[t - lo] : key_of(t); };
+
+  if (!all) {
+    if (age) {
+      int m = 0;
+      for (int t = wlo + lane; t < whi; t += 32) m = max(m, age[t] + 1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) atomicMax(&s_cta[0], m);
+      cluster.sync();
+      int all_max = 0;
+      for (int c = 0; c < ncta; ++c) all_max = max(all_max, *cluster.map_shared_rank(&s_cta[0], c));
+      newest = all_max;
+    }
+    int count = 0;
+    for (int t = wlo + lane; t < whi; t += 32) {
+      const uint32_t k = key_of(t);
+      if (P.cached) s_keys[t - lo] = k;
+      count += k == kKeyHeld;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    if (lane == 0) atomicAdd(&s_cta[1], count);
+    cluster.sync();
+    int nheld = 0;
+    for (int c = 0; c < ncta; ++c) nheld += *cluster.map_shared_rank(&s_cta[1], c);
+    int need = n - nheld;
+    if (need < 0) {
+      among_held = true;
+      need = n;
+      if (P.cached) {
+        for (int t = wlo + lane; t < whi; t += 32) s_keys[t - lo] = key_of(t);
+        __syncwarp();
+      }
+    }
+    if (need == 0) {
+      threshold = kKeyHeld;  // exactly the held rows
+    } else {
+      // the need-th largest key, 11 + 11 + 10 bits
+      uint32_t prefix = 0;
+      int width = 0;
+#pragma unroll 1
+      for (int level = 0; level < 3; ++level) {
+        const int bits = level < 2 ? 11 : 10, shift = 32 - width - bits;
+        int* hist = s_hist[level];
+        for (int t = wlo + lane; t - lane < whi; t += 32) {
+          bool on = t < whi;
+          uint32_t k = 0;
+          if (on) {
+            k = key_at(t);
+            on = k != kKeyHeld && k != kKeyOut && (width == 0 || (k >> (32 - width)) == prefix);
+          }
+          // one count per distinct bin of the warp (weights cluster in few bins)
+          const int bin = on ? static_cast<int>((k >> shift) & ((1u << bits) - 1u)) : -1;
+          const unsigned peers = __match_any_sync(0xffffffffu, bin);
+          if (on && lane == __ffs(peers) - 1) atomicAdd(&hist[bin], __popc(peers));
+        }
+        cluster.sync();
+        // bins from the top: thread i owns bins 2047 - 2 i and 2046 - 2 i
+        const int b0 = kEvBins - 1 - 2 * tid, b1 = b0 - 1;
+        int c0 = 0, c1 = 0;
+        for (int c = 0; c < ncta; ++c) {
+          const int* other = cluster.map_shared_rank(hist, c);
+          c0 += other[b0];
+          c1 += other[b1];
+        }
+        int v = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        int total;
+        const int before = warp_prefix(__shfl_sync(0xffffffffu, v, 31), s_warp, total) + v - (c0 + c1);
+        if (before < need && before + c0 >= need) {
+          s_bin = b0;
+          s_above = before;
+        } else if (before + c0 < need && before + c0 + c1 >= need) {
+          s_bin = b1;
+          s_above = before + c0;
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | static_cast<uint32_t>(s_bin);
+        need -= s_above;
+        width += bits;
+        __syncthreads();
+      }
+      threshold = prefix;
+      threshold_need = need;
+    }
+  }
+
+  // ---- ranks: equal keys first (the lower rows stay), then holes and moves
+  int eq_before = 0;
+  if (!all && threshold_need > 0) {
+    int eq = 0;
+    for (int t = wlo + lane; t < whi; t += 32) eq += key_at(t) == threshold;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    int total;
+    eq_before = warp_prefix(eq, s_warp, total);
+    if (tid == 0) s_cta[2] = total;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) eq_before += *cluster.map_shared_rank(&s_cta[2], c);
+  }
+  // walks this warp's rows in order: f(row, valid, kept mask of the 32 rows)
+  auto walk = [&](auto f) {
+    int eqs = eq_before;
+    for (int t0 = wlo; t0 < whi; t0 += 32) {
+      const int t = t0 + lane;
+      const bool there = t < whi;
+      bool keep = there;
+      if (!all) {
+        const uint32_t k = there ? key_at(t) : kKeyOut;
+        const bool same = there && threshold_need > 0 && k == threshold;
+        const unsigned m = __ballot_sync(0xffffffffu, same);
+        const int r = eqs + __popc(m & ((1u << lane) - 1u));
+        keep = there && (same ? r < threshold_need : k > threshold || (threshold_need == 0 && k == threshold));
+        eqs += __popc(m);
+      }
+      f(t, there, keep);
+    }
+  };
+  int hole = 0, move = 0;  // this lane's, then its warp's
+  if (!all) {
+    walk([&](int t, bool there, bool keep) {
+      hole += there && t < n && !keep;
+      move += there && t >= n && keep;
+    });
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    hole += __shfl_xor_sync(0xffffffffu, hole, o);
+    move += __shfl_xor_sync(0xffffffffu, move, o);
+  }
+  int hole_total, move_total;
+  int hole_at = warp_prefix(hole, s_warp, hole_total);
+  int move_at = warp_prefix(move, s_warp, move_total);
+  if (tid == 0) {
+    s_cta[3] = hole_total;
+    s_cta2 = move_total;
+  }
+  cluster.sync();
+  int moves = 0;
+  for (int c = 0; c < ncta; ++c) {
+    const int hc = *cluster.map_shared_rank(&s_cta[3], c), mc = *cluster.map_shared_rank(&s_cta2, c);
+    if (c < rank) {
+      hole_at += hc;
+      move_at += mc;
+    }
+    moves += mc;
+  }
+  // ---- lists, and the rows that stay where they are
+  const size_t row0 = static_cast<size_t>(b) * P.max_len;
+  bool no_page = false;
+  walk([&](int t, bool there, bool keep) {
+    const bool is_hole = there && t < n && !keep, is_move = there && t >= n && keep;
+    const unsigned hm = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_move);
+    const unsigned below = (1u << lane) - 1u;
+    if (is_hole || is_move) {
+      const int phys = physical_row(P, b, t);
+      no_page |= phys < 0;
+      if (is_hole)
+        P.dst[static_cast<size_t>(b) * P.cap + hole_at + __popc(hm & below)] = make_int2(t, phys);
+      else
+        P.src[static_cast<size_t>(b) * P.cap + move_at + __popc(mm & below)] = make_int2(t, phys);
+    }
+    hole_at += __popc(hm);
+    move_at += __popc(mm);
+    if (there && t < n && keep) {
+      if (P.weights_out != P.weights) P.weights_out[row0 + t] = w[t];
+      if (P.order_out && P.order_out != P.order) P.order_out[row0 + t] = age ? age[t] : t;
+      if (P.kept) P.kept[static_cast<size_t>(b) * P.budget + t] = t;
+    }
+  });
+  if (P.kept)
+    for (int t = n + rank * kEvThreads + tid; t < P.budget; t += ncta * kEvThreads)
+      P.kept[static_cast<size_t>(b) * P.budget + t] = -1;
+  if (no_page) s_bad = 1;
+  // every CTA has read seq_lens (new_lens may be the same array) and s_bad,
+  // s_cta of its neighbours before any of them goes
+  cluster.sync();
+  if (rank == 0 && tid == 0) {
+    uint32_t bits = bad_len ? kDevBounds : 0u;
+    for (int c = 0; c < ncta; ++c) bits |= *cluster.map_shared_rank(&s_bad, c) ? kDevBounds : 0u;
+    P.flags[b] = bits;
+    P.moves[b] = moves;
+    P.new_lens[b] = n;
+  }
+  cluster.sync();
+}
+
+// One moved row per CTA turn: its 16-byte pieces across the four cache
+// tensors, up to four in flight per thread, then the per-row data.
+// It lets no dependent start early: a decode launched next reads the cache at
+// once, before it waits for the launch before it.
+__global__ void __launch_bounds__(kMoveThreads) lrkv_evict_move_kernel(const EvictParams P) {
+  pdl_wait();
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int m = P.moves[b];
+  const int n0 = P.n16[0], n1 = n0 + P.n16[1], n2 = n1 + P.n16[2], n3 = n2 + P.n16[3];
+  const size_t row0 = static_cast<size_t>(b) * P.max_len;
+  for (int k = blockIdx.x; k < m; k += gridDim.x) {
+    const int2 from = P.src[static_cast<size_t>(b) * P.cap + k], to = P.dst[static_cast<size_t>(b) * P.cap + k];
+    if (from.y >= 0 && to.y >= 0) {
+      for (int i0 = tid; i0 < n3; i0 += 4 * kMoveThreads) {
+        uint4 v[4];
+        unsigned char* out[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * kMoveThreads;
+          if (i < n3) {
+            const int s = i < n0 ? 0 : i < n1 ? 1 : i < n2 ? 2 : 3;
+            const int p = i - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2);
+            const size_t width = static_cast<size_t>(P.n16[s]) * 16;
+            v[u] = *reinterpret_cast<const uint4*>(P.base[s] + from.y * width + 16 * static_cast<size_t>(p));
+            out[u] = P.base[s] + to.y * width + 16 * static_cast<size_t>(p);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (i0 + u * kMoveThreads < n3) *reinterpret_cast<uint4*>(out[u]) = v[u];
+      }
+    }
+    if (P.key_scale)
+      for (int h = tid; h < P.H; h += kMoveThreads) {
+        float* row = P.key_scale + (static_cast<size_t>(b) * P.H + h) * P.max_len;
+        row[to.x] = row[from.x];
+      }
+    if (P.positions && tid < P.axes)
+      P.positions[(row0 + to.x) * P.axes + tid] = P.positions[(row0 + from.x) * P.axes + tid];
+    if (tid == 32) P.weights_out[row0 + to.x] = P.weights[row0 + from.x];
+    if (tid == 64 && P.order_out) P.order_out[row0 + to.x] = P.order ? P.order[row0 + from.x] : from.x;
+    if (tid == 96 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + to.x] = from.x;
+  }
+  if (blockIdx.x == 0 && b == 0 && tid < 32) {
+    uint32_t bits = 0u;
+    for (int i = tid; i < P.B; i += 32) bits |= P.flags[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+    if (tid == 0) *P.status = bits;
+  }
+}
+
+// ======================================================================= host
+namespace {
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+lrkv_status evict_check(int batch, int max_len, int budget) {
+  if (batch < 1 || max_len < 1 || budget < 1 || budget > max_len) return LRKV_ERR_INVALID_ARG;
+  if (batch > kMaxBatch || static_cast<long long>(batch) * max_len > (1LL << 31) - 1) return LRKV_ERR_UNSUPPORTED;
+  return LRKV_OK;
+}
+
+size_t evict_layout(EvictParams& P, void* ws) {
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  P.cap = std::min(P.budget, P.max_len - P.budget);
+  const size_t list = up256(static_cast<size_t>(P.B) * P.cap * sizeof(int2));
+  size_t off = 256;
+  const size_t off_flags = off; off += up256(static_cast<size_t>(P.B) * 4);
+  const size_t off_moves = off; off += up256(static_cast<size_t>(P.B) * 4);
+  const size_t off_src = off; off += list;
+  const size_t off_dst = off; off += list;
+  if (ws) {
+    P.status = reinterpret_cast<uint32_t*>(base);
+    P.flags = reinterpret_cast<uint32_t*>(base + off_flags);
+    P.moves = reinterpret_cast<int32_t*>(base + off_moves);
+    P.src = reinterpret_cast<int2*>(base + off_src);
+    P.dst = reinterpret_cast<int2*>(base + off_dst);
+  }
+  return off;
+}
+
+bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+}  // namespace lrkv
+
+extern "C" {
+
+lrkv_status lrkv_evict_workspace_size(int batch, int max_len, int budget, size_t* bytes) {
+  if (!bytes) return LRKV_ERR_INVALID_ARG;
+  const lrkv_status st = lrkv::evict_check(batch, max_len, budget);
+  if (st != LRKV_OK) return st;
+  lrkv::EvictParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.B = batch; P.max_len = max_len; P.budget = budget;
+  *bytes = lrkv::evict_layout(P, nullptr);
+  return LRKV_OK;
+}
+
+lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, const float* weights,
+                       const int32_t* order, const int32_t* seq_lens, int page_size, int num_pages,
+                       const int32_t* block_table, void* k_s, void* v_s, void* z_k, void* z_v, float* key_scale,
+                       int32_t* positions, int axes, float* weights_out, int32_t* order_out, int32_t* new_lens,
+                       int32_t* kept, void* ws, size_t ws_bytes, lrkv_stream_t stream) {
+  LRKV_TRACE_CALL("lrkv_evict");
+  using namespace lrkv;
+  if (!dims) return LRKV_ERR_INVALID_ARG;
+  if (dims->heads < 1 || dims->head_dim < 1 || dims->rank < 0) return LRKV_ERR_INVALID_ARG;
+  if (dims->dtype != LRKV_F32 && dims->dtype != LRKV_BF16) return LRKV_ERR_INVALID_ARG;
+  lrkv_status st = evict_check(dims->batch, dims->max_len, budget);
+  if (st != LRKV_OK) return st;
+  if (sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget) return LRKV_ERR_INVALID_ARG;
+  if (!weights || !seq_lens || !k_s || !v_s || !weights_out || !new_lens) return LRKV_ERR_INVALID_ARG;
+  if (dims->rank > 0 && (!z_k || !z_v)) return LRKV_ERR_INVALID_ARG;
+  if (positions ? (axes < 1 || axes > 4) : axes != 0) return LRKV_ERR_INVALID_ARG;
+  const int esz = dims->dtype == LRKV_BF16 ? 2 : 4;
+  const long long shared = static_cast<long long>(dims->head_dim) * esz;
+  const long long latent = static_cast<long long>(dims->heads) * dims->rank * esz;
+  if (shared % 16 != 0 || latent % 16 != 0 || shared > (1 << 24) || latent > (1 << 24)) return LRKV_ERR_UNSUPPORTED;
+  if (!a16(k_s) || !a16(v_s) || (dims->rank > 0 && (!a16(z_k) || !a16(z_v)))) return LRKV_ERR_INVALID_ARG;
+  int shift = 0;
+  if (block_table) {
+    if (page_size < 1 || (page_size & (page_size - 1)) != 0 || num_pages < 1 || dims->max_len % page_size != 0)
+      return LRKV_ERR_INVALID_ARG;
+    if (static_cast<long long>(num_pages) * page_size > (1LL << 31) - 1) return LRKV_ERR_UNSUPPORTED;
+    while ((1 << shift) < page_size) ++shift;
+  }
+  if (!ws) return LRKV_ERR_WORKSPACE;
+  if (!a16(ws)) return LRKV_ERR_INVALID_ARG;
+  EvictParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.B = dims->batch; P.max_len = dims->max_len; P.budget = budget; P.sink = sink; P.recent = recent;
+  if (ws_bytes < evict_layout(P, ws)) return LRKV_ERR_WORKSPACE;
+  P.block_table = block_table;
+  P.page_shift = shift;
+  P.num_pages = num_pages;
+  P.max_blocks = block_table ? dims->max_len / page_size : 0;
+  P.seq_lens = seq_lens; P.weights = weights; P.order = order;
+  P.weights_out = weights_out; P.order_out = order_out; P.new_lens = new_lens; P.kept = kept;
+  P.n16[0] = P.n16[1] = static_cast<int>(shared / 16);
+  P.n16[2] = P.n16[3] = static_cast<int>(latent / 16);
+  P.base[0] = static_cast<unsigned char*>(k_s); P.base[1] = static_cast<unsigned char*>(v_s);
+  P.base[2] = static_cast<unsigned char*>(z_k); P.base[3] = static_cast<unsigned char*>(z_v);
+  P.H = dims->heads; P.axes = axes;
+  P.key_scale = key_scale; P.positions = positions;
+  const int sms = device_sm_count();
+  if (sms < 1) return LRKV_ERR_CUDA;
+
+  // CTAs per sequence: more while the sequences leave SMs idle and a CTA has
+  // more than 8192 rows
+  int ncta = 1;
+  while (ncta < kEvMaxCluster && 2LL * ncta * P.B <= sms && P.max_len > 8192 * ncta) ncta *= 2;
+  const int step = 32 * kEvWarps;
+  P.rows_per_cta = ((P.max_len + ncta - 1) / ncta + step - 1) / step * step;
+  P.cached = P.rows_per_cta <= kEvCacheRows;
+  const int smem = P.cached ? P.rows_per_cta * 4 : 0;
+  const void* select = reinterpret_cast<const void*>(&lrkv_evict_select_kernel);
+  // (the kernel's static tables count towards the 48 KB that need no attribute)
+  if (ensure_kernel_smem(select, kEvCacheRows * 4) != cudaSuccess) return LRKV_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ncta;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.B * ncta);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, lrkv_evict_select_kernel, P) != cudaSuccess) return LRKV_ERR_CUDA;
+  // enough CTAs to fill the SMs eight times over, at least one per sequence
+  const long long per_seq = std::max(1LL, (8LL * sms + P.B - 1) / P.B);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1LL, std::min<long long>(P.cap, per_seq))), P.B);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lrkv_evict_move_kernel, P) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "cache_weights.h"
 #include "host_cache.h"
 #include "lrkv.h"
 #include "trace.h"
@@ -193,6 +194,67 @@ lrkv_status lrkv_decode_normed(const lrkv_dims* dims, const void* q, const void*
   if (dims->dtype != LRKV_BF16 || dims->rank < 1) return LRKV_ERR_UNSUPPORTED;
   return decode_common(dims, q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, out, lse, ws, ws_bytes, stream, nullptr,
                        nullptr, key_scale);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The plan and workspace of a weighted decode: the decode's, then the scores.
+lrkv_status weighted_plan(const lrkv_dims* dims, lrkv::DecodePlan& P, size_t* score_off, size_t* bytes) {
+  lrkv_status st = check_decode_dims(dims);
+  if (st != LRKV_OK) return st;
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != LRKV_OK) return st;
+  size_t need = 0;
+  if ((st = lrkv::decode_make_plan(*dims, sms, P, &need)) != LRKV_OK) return st;
+  if (!P.stream) return LRKV_ERR_UNSUPPORTED;  // the bf16 streaming scan leaves the scores
+  *score_off = (need + 255) / 256 * 256;
+  *bytes = *score_off + static_cast<size_t>(dims->batch) * dims->heads * dims->max_len * sizeof(float);
+  return LRKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lrkv_status lrkv_decode_weighted_workspace_size(const lrkv_dims* dims, size_t* bytes) {
+  if (!bytes) return LRKV_ERR_INVALID_ARG;
+  lrkv::DecodePlan P;
+  size_t off = 0;
+  return weighted_plan(dims, P, &off, bytes);
+}
+
+lrkv_status lrkv_decode_weighted(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
+                                 const int32_t* block_table, const void* k_s, const void* v_s, const void* z_k,
+                                 const void* z_v, const void* b_k, const void* b_v, const float* key_scale,
+                                 const int32_t* seq_lens, float decay, const float* weights, float* weights_out,
+                                 float* out, float* lse, void* ws, size_t ws_bytes, lrkv_stream_t stream) {
+  LRKV_TRACE_CALL("lrkv_decode_weighted");
+  lrkv::DecodePlan P;
+  size_t score_off = 0, need = 0;
+  lrkv_status st = weighted_plan(dims, P, &score_off, &need);
+  if (st != LRKV_OK) return st;
+  if (!q || !k_s || !v_s || !seq_lens || !out || !lse) return LRKV_ERR_INVALID_ARG;
+  if (dims->rank > 0 && (!z_k || !z_v || !b_k || !b_v)) return LRKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_s) || !aligned16(v_s)) return LRKV_ERR_INVALID_ARG;
+  if (dims->rank > 0 && (!aligned16(z_k) || !aligned16(z_v))) return LRKV_ERR_INVALID_ARG;
+  if ((st = lrkv::weights_check(decay, weights, weights_out)) != LRKV_OK) return st;
+  const PagedCache pc{block_table, page_size, num_pages};
+  if (block_table && (st = check_paging(dims, pc)) != LRKV_OK) return st;
+  if (!ws) return LRKV_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LRKV_ERR_INVALID_ARG;
+  if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
+  if (block_table) set_paging(P, *dims, pc);
+  lrkv::decode_bind_workspace(P, ws);
+  P.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + score_off);
+  P.q = q; P.k_s = k_s; P.v_s = v_s; P.z_k = z_k; P.z_v = z_v; P.b_k = b_k; P.b_v = b_v;
+  P.seq_lens = seq_lens; P.out = out; P.lse = lse;
+  P.key_scale = key_scale;
+  P.ks_tma = key_scale && P.ks_bytes > 0 && dims->max_len % 4 == 0 && aligned16(key_scale);
+  if ((st = lrkv::decode_launch(P, stream)) != LRKV_OK) return st;
+  return lrkv::weights_sum_launch(P.B, P.H, P.max_len, seq_lens, P.scores, lse, decay, weights, weights_out,
+                                  stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,15 @@ EXPORTED = (
     "lrkv_rope_table",
     "lrkv_decode_rope_workspace_size",
     "lrkv_decode_rope",
+    "lrkv_decode_weighted_workspace_size",
+    "lrkv_decode_weighted",
+    "lrkv_prefill_weights_workspace_size",
+    "lrkv_prefill_weights",
+    "lrkv_evict_workspace_size",
+    "lrkv_evict",
+    "lrkv_rope_rotate",
+    "lrkv_decode_rope_axes_workspace_size",
+    "lrkv_decode_rope_axes",
     "lrkv_dense_decode_workspace_size",
     "lrkv_dense_decode",
     "lrkv_mla_decode_workspace_size",
@@ -155,6 +164,29 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lrkv_decode_rope.restype = ctypes.c_int
     lib.lrkv_decode_rope.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int, i32p, vp, vp, vp, sz,
                                      vp]
+    ci, cf, szp, ip = ctypes.c_int, ctypes.c_float, ctypes.POINTER(sz), ctypes.POINTER(ctypes.c_int)
+    lib.lrkv_decode_weighted_workspace_size.restype = ctypes.c_int
+    lib.lrkv_decode_weighted_workspace_size.argtypes = [dims_p, szp]
+    lib.lrkv_decode_weighted.restype = ctypes.c_int
+    lib.lrkv_decode_weighted.argtypes = [dims_p, vp, ci, ci, i32p, vp, vp, vp, vp, vp, vp, vp, i32p, cf, vp, vp,
+                                         vp, vp, vp, sz, vp]
+    lib.lrkv_prefill_weights_workspace_size.restype = ctypes.c_int
+    lib.lrkv_prefill_weights_workspace_size.argtypes = [dims_p, ci, szp]
+    lib.lrkv_prefill_weights.restype = ctypes.c_int
+    lib.lrkv_prefill_weights.argtypes = [dims_p, ci, ci, vp, ci, ci, i32p, vp, vp, vp, vp, vp, i32p, cf, vp, vp,
+                                         vp, sz, vp]
+    lib.lrkv_evict_workspace_size.restype = ctypes.c_int
+    lib.lrkv_evict_workspace_size.argtypes = [ci, ci, ci, szp]
+    lib.lrkv_evict.restype = ctypes.c_int
+    lib.lrkv_evict.argtypes = [dims_p, ci, ci, ci, vp, i32p, i32p, ci, ci, i32p, vp, vp, vp, vp, vp, i32p, ci, vp,
+                               i32p, i32p, i32p, vp, sz, vp]
+    lib.lrkv_rope_rotate.restype = ctypes.c_int
+    lib.lrkv_rope_rotate.argtypes = [dims_p, ci, vp, i32p, ci, ip, vp, ci, vp, vp, sz, vp]
+    lib.lrkv_decode_rope_axes_workspace_size.restype = ctypes.c_int
+    lib.lrkv_decode_rope_axes_workspace_size.argtypes = [dims_p, szp]
+    lib.lrkv_decode_rope_axes.restype = ctypes.c_int
+    lib.lrkv_decode_rope_axes.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, ci, i32p, ci, ip, i32p, cf, vp,
+                                          vp, vp, vp, vp, sz, vp]
     ddp, mdp = ctypes.POINTER(lrkv_dense_dims), ctypes.POINTER(lrkv_mla_dims)
     lib.lrkv_dense_decode_workspace_size.restype = ctypes.c_int
     lib.lrkv_dense_decode_workspace_size.argtypes = [ddp, ctypes.POINTER(sz)]
@@ -615,6 +647,238 @@ def decode_rope(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, seq_lens, scale: f
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_decode_rope")
     return out, lse
+
+
+# ------------------------------------------------- a cache inside a budget --
+
+def _size_of(call: str, *args) -> int:
+    n = ctypes.c_size_t(0)
+    st = int(getattr(load(), call)(*args, ctypes.byref(n)))
+    if st != LRKV_OK:
+        raise LRKVError(st, call)
+    return int(n.value)
+
+
+def _check(named: dict, shapes: dict, device) -> None:
+    """Every given tensor contiguous and on `device`; the named ones of the
+    given (dtype, shape), None standing for any type."""
+    for name, t in named.items():
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"LRKV tensors must be contiguous: {name}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if name in shapes:
+            dtype, shape = shapes[name]
+            if dtype is not None and t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+            if tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _cache_rows(k_s, block_table, batch: int):
+    """(max_len, page_size, num_pages, leading shape of the cache tensors)."""
+    if block_table is None:
+        return k_s.shape[1], 0, 0, (batch, k_s.shape[1])
+    pages, size = k_s.shape[0], k_s.shape[1]
+    return block_table.shape[1] * size, size, pages, (pages, size)
+
+
+def decode_weighted_workspace(dims: lrkv_dims, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_decode_weighted_workspace_size", ctypes.byref(dims)), dtype=torch.uint8,
+                       device=device)
+
+
+def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: float = 1.0, weights_out=None,
+                    key_scale=None, block_table=None, scale: float = 0.0, out=None, lse=None, ws=None, stream=None):
+    """decode (paged with block_table, normalised keys with key_scale) that
+    also adds each row's attention weights, summed over the heads, to weights
+    [B, max_len] fp32: in place, or into weights_out.  `decay` multiplies the
+    earlier weights (0: weights may be None).  Returns (out, lse, weights_out,
+    ws)."""
+    B, H, dh = q.shape
+    r = z_k.shape[-1] if z_k is not None else 0
+    max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
+    dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
+    if weights_out is None:
+        weights_out = weights if weights is not None else torch.zeros((B, max_len), dtype=torch.float32,
+                                                                      device=q.device)
+    if out is None:
+        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    f32, dt = torch.float32, q.dtype
+    _check(dict(q=q, k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, b_k=b_k, b_v=b_v, seq_lens=seq_lens, weights=weights,
+                weights_out=weights_out, key_scale=key_scale, block_table=block_table, out=out, lse=lse, ws=ws),
+           dict(k_s=(dt, rows + (dh,)), v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)),
+                b_k=(dt, (H, dh, r)), b_v=(dt, (H, dh, r)), seq_lens=(torch.int32, (B,)),
+                weights=(f32, (B, max_len)), weights_out=(f32, (B, max_len)), key_scale=(f32, (B, H, max_len)),
+                block_table=(torch.int32, (B, max_len // page_size if page_size else 0)), out=(f32, (B, H, dh)),
+                lse=(f32, (B, H))), q.device)
+    with torch.cuda.device(q.device):
+        if ws is None:
+            ws = decode_weighted_workspace(dims, q.device)
+        st = int(load().lrkv_decode_weighted(
+            ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s), _ptr(v_s),
+            _ptr(z_k) if r else None, _ptr(z_v) if r else None, _ptr(b_k) if r else None, _ptr(b_v) if r else None,
+            _ptr(key_scale), _ptr(seq_lens), float(decay), _ptr(weights), _ptr(weights_out), _ptr(out), _ptr(lse),
+            _ptr(ws), ws.numel(), _stream_handle(stream)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_decode_weighted")
+    return out, lse, weights_out, ws
+
+
+def prefill_weights_workspace(dims: lrkv_dims, window: int, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_prefill_weights_workspace_size", ctypes.byref(dims), int(window)),
+                       dtype=torch.uint8, device=device)
+
+
+def prefill_weights(q, k_s, z_k, b_k, lse, seq_lens, weights, window: int = 0, decay: float = 1.0,
+                    weights_out=None, key_scale=None, block_table=None, scale: float = 0.0, ws=None, stream=None):
+    """Adds the attention weights of the last `window` (0: all) of the prompt
+    queries q [B, q_len, H, d_h], summed over queries and heads, to weights
+    [B, max_len] fp32, in place or into weights_out; lse [B, H, q_len] as the
+    prefill returned it.  Returns (weights_out, ws)."""
+    B, Tq, H, dh = q.shape
+    r = z_k.shape[-1] if z_k is not None else 0
+    max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
+    dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
+    window = int(window) or Tq
+    if weights_out is None:
+        weights_out = weights if weights is not None else torch.zeros((B, max_len), dtype=torch.float32,
+                                                                      device=q.device)
+    f32, dt = torch.float32, q.dtype
+    _check(dict(q=q, k_s=k_s, z_k=z_k, b_k=b_k, lse=lse, seq_lens=seq_lens, weights=weights,
+                weights_out=weights_out, key_scale=key_scale, block_table=block_table, ws=ws),
+           dict(k_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), b_k=(dt, (H, dh, r)), lse=(f32, (B, H, Tq)),
+                seq_lens=(torch.int32, (B,)), weights=(f32, (B, max_len)), weights_out=(f32, (B, max_len)),
+                key_scale=(f32, (B, H, max_len)),
+                block_table=(torch.int32, (B, max_len // page_size if page_size else 0))), q.device)
+    with torch.cuda.device(q.device):
+        if ws is None:
+            ws = prefill_weights_workspace(dims, window, q.device)
+        st = int(load().lrkv_prefill_weights(
+            ctypes.byref(dims), Tq, window, _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s),
+            _ptr(z_k) if r else None, _ptr(b_k) if r else None, _ptr(key_scale), _ptr(lse), _ptr(seq_lens),
+            float(decay), _ptr(weights), _ptr(weights_out), _ptr(ws), ws.numel(), _stream_handle(stream)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_prefill_weights")
+    return weights_out, ws
+
+
+def evict_workspace(batch: int, max_len: int, budget: int, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_evict_workspace_size", int(batch), int(max_len), int(budget)),
+                       dtype=torch.uint8, device=device)
+
+
+def evict(k_s, v_s, z_k, z_v, weights, seq_lens, budget: int, sink: int = 0, recent: int = 0, order=None,
+          key_scale=None, positions=None, block_table=None, weights_out=None, order_out=None, new_lens=None,
+          kept=None, ws=None, stream=None):
+    """Keeps at most `budget` rows of each sequence: the first `sink` and last
+    `recent` tokens and the rows of the largest weights [B, max_len]; kept rows
+    past the new length move into the holes (cache, key_scale and positions in
+    place; weights, order and seq_lens in place unless given their own
+    outputs).  kept [B, budget] int32 receives the former rows.  Returns
+    (new_lens, weights_out, order_out, ws)."""
+    B = seq_lens.shape[0]
+    dh = k_s.shape[-1]
+    H, r = (z_k.shape[-2], z_k.shape[-1]) if z_k is not None else (1, 0)
+    if key_scale is not None and r == 0:
+        H = key_scale.shape[1]
+    max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
+    dims = make_dims(B, H, dh, r, max_len, k_s.dtype)
+    weights_out = weights if weights_out is None else weights_out
+    order_out = order if order_out is None else order_out
+    new_lens = seq_lens if new_lens is None else new_lens
+    axes = positions.shape[-1] if positions is not None else 0
+    f32, i32, dt = torch.float32, torch.int32, k_s.dtype
+    flat = (B, max_len)
+    _check(dict(k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, weights=weights, seq_lens=seq_lens, order=order,
+                key_scale=key_scale, positions=positions, block_table=block_table, weights_out=weights_out,
+                order_out=order_out, new_lens=new_lens, kept=kept, ws=ws),
+           dict(v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)), weights=(f32, flat),
+                seq_lens=(i32, (B,)), order=(i32, flat), key_scale=(f32, (B, H, max_len)),
+                positions=(i32, flat + (axes,)), weights_out=(f32, flat), order_out=(i32, flat),
+                new_lens=(i32, (B,)), kept=(i32, (B, int(budget))),
+                block_table=(i32, (B, max_len // page_size if page_size else 0))), k_s.device)
+    with torch.cuda.device(k_s.device):
+        if ws is None:
+            ws = evict_workspace(B, max_len, budget, k_s.device)
+        st = int(load().lrkv_evict(
+            ctypes.byref(dims), int(budget), int(sink), int(recent), _ptr(weights), _ptr(order), _ptr(seq_lens),
+            page_size, num_pages, _ptr(block_table), _ptr(k_s), _ptr(v_s), _ptr(z_k) if r else None,
+            _ptr(z_v) if r else None, _ptr(key_scale), _ptr(positions), axes, _ptr(weights_out), _ptr(order_out),
+            _ptr(new_lens), _ptr(kept), _ptr(ws), ws.numel(), _stream_handle(stream)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_evict")
+    return new_lens, weights_out, order_out, ws
+
+
+def _sections(sections):
+    return (ctypes.c_int * len(sections))(*[int(s) for s in sections])
+
+
+def rope_rotate(x, positions, cos_sin, sections, out=None, ws=None, stream=None) -> torch.Tensor:
+    """x [B, n, H, d_h] with every pair turned by its token's position on the
+    pair's axis: positions [B, n, axes] int32, sections the pairs of each axis,
+    cos_sin a table from rope_table().  out may be x.  A status word is kept
+    only in a `ws` of 16 zeroed bytes."""
+    B, n, H, dh = x.shape
+    axes = len(sections)
+    dims = make_dims(B, H, dh, 0, 1, x.dtype)
+    if out is None:
+        out = torch.empty_like(x)
+    _check(dict(x=x, positions=positions, cos_sin=cos_sin, out=out, ws=ws),
+           dict(positions=(torch.int32, (B, n, axes)), cos_sin=(torch.float32, (cos_sin.shape[0], dh)),
+                out=(x.dtype, x.shape)), x.device)
+    with torch.cuda.device(x.device):
+        st = int(load().lrkv_rope_rotate(
+            ctypes.byref(dims), n, _ptr(x), _ptr(positions), axes, _sections(sections), _ptr(cos_sin),
+            cos_sin.shape[0], _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(), _stream_handle(stream)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_rope_rotate")
+    return out
+
+
+def decode_rope_axes_workspace(dims: lrkv_dims, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_decode_rope_axes_workspace_size", ctypes.byref(dims)), dtype=torch.uint8,
+                       device=device)
+
+
+def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, sections, seq_lens, weights=None,
+                     decay: float = 1.0, weights_out=None, scale: float = 0.0, out=None, lse=None, ws=None,
+                     stream=None):
+    """decode_rope whose rows carry their positions [B, max_len, axes] int32
+    (sections: the pairs of each axis); with weights (or weights_out) it also
+    accumulates them as decode_weighted.  Returns (out, lse, weights_out, ws)."""
+    B, H, dh = q_rot.shape
+    r, max_len, axes = z_k.shape[-1], k_s.shape[1], len(sections)
+    dims = make_dims(B, H, dh, r, max_len, q_rot.dtype, scale)
+    weights_out = weights if weights_out is None else weights_out
+    if out is None:
+        out = torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q_rot.device)
+    f32, dt, rows = torch.float32, q_rot.dtype, (B, max_len)
+    _check(dict(q_rot=q_rot, k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, b_k=b_k, b_v=b_v, cos_sin=cos_sin,
+                positions=positions, seq_lens=seq_lens, weights=weights, weights_out=weights_out, out=out, lse=lse,
+                ws=ws),
+           dict(k_s=(dt, rows + (dh,)), v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)),
+                b_k=(dt, (H, dh, r)), b_v=(dt, (H, dh, r)), cos_sin=(f32, (cos_sin.shape[0], dh)),
+                positions=(torch.int32, rows + (axes,)), seq_lens=(torch.int32, (B,)), weights=(f32, rows),
+                weights_out=(f32, rows), out=(f32, (B, H, dh)), lse=(f32, (B, H))), q_rot.device)
+    with torch.cuda.device(q_rot.device):
+        if ws is None:
+            ws = decode_rope_axes_workspace(dims, q_rot.device)
+        st = int(load().lrkv_decode_rope_axes(
+            ctypes.byref(dims), _ptr(q_rot), _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(b_k), _ptr(b_v),
+            _ptr(cos_sin), cos_sin.shape[0], _ptr(positions), axes, _sections(sections), _ptr(seq_lens),
+            float(decay), _ptr(weights), _ptr(weights_out), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+            _stream_handle(stream)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_decode_rope_axes")
+    return out, lse, weights_out, ws
 
 
 # ------------------------------------------------- comparison decodes --

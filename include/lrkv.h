@@ -434,6 +434,143 @@ lrkv_status lrkv_decode_rope(const lrkv_dims* dims, const void* q_rot, const voi
                              void* ws, size_t ws_bytes, lrkv_stream_t stream);
 
 /*
+ * A cache inside a token budget.  Four calls: the attention weights that each
+ * cache row gathers, from decode steps (lrkv_decode_weighted) and from a
+ * prompt's queries (lrkv_prefill_weights); the eviction of the rows that
+ * gathered least (lrkv_evict); and, since a row then no longer sits at its
+ * position, a full-RoPE decode whose rows carry their positions
+ * (lrkv_decode_rope_axes, below).  The pages have no counterpart: eviction
+ * shortens the same cache that the factorisation narrows.  A row's shared part
+ * serves every head, so a token is kept or dropped for all heads at once and
+ * its weight is the sum over them.
+ *
+ * Weights are fp32, [batch][max_len].  A call reads `weights` and writes
+ * `weights_out` (the same array for an update in place) on the rows [0, L_b)
+ * of each sequence and leaves the others as they were:
+ *   weights_out[j] = decay * weights[j] + what the call's queries gave row j
+ * where the rows of the call's own new tokens have no earlier weight: their
+ * slots in `weights` are not read and may hold anything, so nothing has to be
+ * cleared when a row is appended.  decay >= 0 and finite, else
+ * LRKV_ERR_INVALID_ARG; 1 accumulates, less forgets, 0 reads no earlier weight
+ * at all (`weights` may then be NULL).  Sums are fp32, in a fixed order.
+ *
+ * lrkv_decode_weighted is one decode step as lrkv_decode (page_size,
+ * num_pages and block_table as in lrkv_decode_paged, block_table NULL: a
+ * contiguous cache; key_scale as in lrkv_decode_normed, or NULL) that also
+ * accumulates
+ *   sum over the heads of a_{h,j}
+ * into row j; its new token is row L_b - 1.  The cache is read once.  out is
+ * held to fp32 accuracy (the probabilities enter the value products as two
+ * bf16 parts, not one).  lse must not be NULL.  Supported: the shapes on which
+ * lrkv_decode streams bf16 (others return LRKV_ERR_UNSUPPORTED).  Workspace:
+ * lrkv_decode_weighted_workspace_size() bytes (the decode's and the scores,
+ * 4 batch heads max_len).
+ *
+ * lrkv_prefill_weights accumulates what the last `window` of a prompt's q_len
+ * queries looked at,
+ *   sum over those queries i and the heads of exp(score_{h,i,j} - lse_{h,i}),
+ * from q [batch][q_len][heads][head_dim], the keys' half of the cache and the
+ * lse [batch][heads][q_len] that lrkv_prefill (lrkv_prefill_normed with
+ * key_scale, lrkv_prefill_paged with block_table) wrote; a query with lse -inf
+ * gives nothing.  Query i sits at row seq_lens[b] - q_len + i and sees the rows
+ * up to its own; the prompt's q_len rows are the call's new tokens, so call it
+ * once per chunk.  seq_lens[b] outside [q_len, max_len] is clamped and sets
+ * LRKV_ERR_DEVICE_BOUNDS.  1 <= window <= q_len (else LRKV_ERR_INVALID_ARG),
+ * q_len <= max_len.  Supported: dtype BF16, head_dim 64 or 128, rank a
+ * multiple of 8 up to 64, heads <= 256; page_size a power of two >= 16.
+ * z_k and b_k may be NULL when rank == 0.  Workspace:
+ * lrkv_prefill_weights_workspace_size() bytes; its status word is set afresh.
+ */
+lrkv_status lrkv_decode_weighted_workspace_size(const lrkv_dims* dims, size_t* bytes);
+lrkv_status lrkv_decode_weighted(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
+                                 const int32_t* block_table, const void* k_s, const void* v_s, const void* z_k,
+                                 const void* z_v, const void* b_k, const void* b_v, const float* key_scale,
+                                 const int32_t* seq_lens, float decay, const float* weights, float* weights_out,
+                                 float* out, float* lse, void* ws, size_t ws_bytes, lrkv_stream_t stream);
+lrkv_status lrkv_prefill_weights_workspace_size(const lrkv_dims* dims, int window, size_t* bytes);
+lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, const void* q, int page_size,
+                                 int num_pages, const int32_t* block_table, const void* k_s, const void* z_k,
+                                 const void* b_k, const float* key_scale, const float* lse,
+                                 const int32_t* seq_lens, float decay, const float* weights, float* weights_out,
+                                 void* ws, size_t ws_bytes, lrkv_stream_t stream);
+
+/*
+ * Eviction.  Sequence b keeps n = min(L_b, budget) of its L_b = seq_lens[b]
+ * rows:
+ *   - the held rows: age < sink (the first tokens) or age >= newest - recent,
+ *     where the age of a row is order[b][j] (its token's number; NULL: the row
+ *     index) and newest is one past the largest age;
+ *   - then the rows of the largest weights, equal weights by the lower row,
+ *     NaN as -infinity.  (If the ages given hold more than n rows, these
+ *     compete by weight among themselves.)
+ * Attention does not depend on the order of the rows, so none is shifted: a
+ * kept row below n stays, and the k-th kept row at or past n moves into the
+ * k-th dropped row below n (both counted upwards).  Moved with it: k_s, v_s,
+ * z_k, z_v (in place), key_scale [batch][heads][max_len] and positions
+ * [batch][max_len][axes] when given (in place), its weight and its age.
+ *   weights [batch][max_len] -> weights_out (may be the same array)
+ *   order   [batch][max_len] or NULL -> order_out or NULL (may be the same)
+ *   seq_lens -> new_lens [batch] = n (may be the same)
+ *   kept    [batch][budget] int32 or NULL: the former row of row i < n, -1
+ *           past n
+ * Rows at or past n are left as they were, in every array.  With order, number
+ * the tokens appended afterwards on (order[b][new row] = tokens seen so far):
+ * after an eviction the row index no longer tells the age.
+ * block_table as in lrkv_decode_paged (NULL: contiguous), here with any
+ * power-of-two page_size; pages past a sequence's last kept row are free after
+ * the call.  Pages that are written must belong to one sequence only.  A row
+ * whose block names no page of the pool is not moved (its weight, age and
+ * kept entry are) and sets LRKV_ERR_DEVICE_BOUNDS, as a length outside
+ * [0, max_len], which is clamped, does.
+ * dtype BF16 or F32; rows of a multiple of 16 bytes; 1 <= budget <= max_len;
+ * sink, recent >= 0 and sink + recent <= budget; axes 1 .. 4 with positions, 0
+ * without.  z_k, z_v may be NULL when rank == 0.  Workspace:
+ * lrkv_evict_workspace_size() bytes, its status word set afresh.
+ */
+lrkv_status lrkv_evict_workspace_size(int batch, int max_len, int budget, size_t* bytes);
+lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, const float* weights,
+                       const int32_t* order, const int32_t* seq_lens, int page_size, int num_pages,
+                       const int32_t* block_table, void* k_s, void* v_s, void* z_k, void* z_v, float* key_scale,
+                       int32_t* positions, int axes, float* weights_out, int32_t* order_out, int32_t* new_lens,
+                       int32_t* kept, void* ws, size_t ws_bytes, lrkv_stream_t stream);
+
+/*
+ * Rotary positions with several axes.  A head's pairs (2k, 2k+1) are cut into
+ * consecutive sections, sections[a] pairs for axis a (time, height, width;
+ * host array, `axes` of them, 1 .. 4, none negative, adding up to head_dim/2):
+ * pair k turns by p_a theta_k with the position p_a on its axis, theta_k and
+ * the table cos_sin [max_pos][head_dim] as in lrkv_rope_table.  One axis whose
+ * positions are the row indices is the rotation of lrkv_decode_rope.
+ * Positions are int32; one outside [0, max_pos) is clamped and sets
+ * LRKV_ERR_DEVICE_BOUNDS.
+ *
+ * lrkv_rope_rotate turns x [batch][n][heads][head_dim] (dims->dtype, BF16 or
+ * F32; dims->batch, heads and head_dim used) by positions [batch][n][axes]
+ * into out (may be x): the rotated queries of the calls below.  fp32
+ * arithmetic, rounded once.  head_dim * sizeof(elem) a multiple of 16, at most
+ * 1024 elements; x, out 16-byte aligned.  ws: NULL, or 16 bytes whose status
+ * word the call ORs its bits into (the caller clears it).
+ *
+ * lrkv_decode_rope_axes is lrkv_decode_rope with the keys of row j turned by
+ * positions[b][j][axis] (positions [batch][max_len][axes]; rows at or past
+ * seq_lens[b] are not read), so that rows may have been moved or evicted, and
+ * with the accumulation of lrkv_decode_weighted when weights_out is not NULL
+ * (then lse must not be NULL either).  out is held to fp32 accuracy.
+ * Supported: the shapes of lrkv_decode_rope.  Workspace:
+ * lrkv_decode_rope_axes_workspace_size() bytes.
+ */
+lrkv_status lrkv_rope_rotate(const lrkv_dims* dims, int n, const void* x, const int32_t* positions, int axes,
+                             const int* sections, const float* cos_sin, int max_pos, void* out, void* ws,
+                             size_t ws_bytes, lrkv_stream_t stream);
+lrkv_status lrkv_decode_rope_axes_workspace_size(const lrkv_dims* dims, size_t* bytes);
+lrkv_status lrkv_decode_rope_axes(const lrkv_dims* dims, const void* q_rot, const void* k_s, const void* v_s,
+                                  const void* z_k, const void* z_v, const void* b_k, const void* b_v,
+                                  const float* cos_sin, int max_pos, const int32_t* positions, int axes,
+                                  const int* sections, const int32_t* seq_lens, float decay, const float* weights,
+                                  float* weights_out, float* out, float* lse, void* ws, size_t ws_bytes,
+                                  lrkv_stream_t stream);
+
+/*
  * Comparison decodes on the same box ("Low-Rank Key Value Attention | What a
  * shared cache can preserve", §4 "Weight count and the two decode regimes"
  * and §5: a fair serving comparison runs optimized GQA, dense MHA and
