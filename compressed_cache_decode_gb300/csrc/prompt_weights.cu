@@ -11,19 +11,26 @@
 // The sum runs over queries and heads, so the scores are formed transposed,
 // S^T = K q^T, keys as the M rows of tcgen05.mma: a thread of the epilogue then
 // owns one key (one TMEM lane), adds up its row in a register, and neither
-// atomics nor exchanges between threads are needed.  CTA item = (sequence, 128
-// keys, group of heads); k_s of the keys stays in shared memory for the item,
-// z_k,h for the queries of a head; tiles of up to 128 query columns (`wt`
-// queries of `hpt` heads: short windows put several heads side by side, whose
-// shared part is one MMA) stream through a ring.  p = q B_h^K enters as bf16
+// atomics nor exchanges between threads are needed.  p = q B_h^K enters as bf16
 // high + low parts (lrkv_prefill_absorb_kernel), two MMAs over the same
 // latents, as the prefill's own scores do.
 //
-// Persistent: one CTA per SM walks the items, those with the most queries
-// (the first keys) first; the rings run on across items.  Warp 0 copies (TMA),
-// one thread of warp 1 issues the MMAs into four TMEM accumulators, warps 2-9
-// read them back.  Each item leaves one partial sum per key; the last kernel
-// adds the head groups' partials in order.
+// Bound by the tensor pipe and, close behind, by what feeds it.  The keys are
+// the A operand from TMEM: they are the same for every query of the item
+// (k_s) or of the head (z_k,h), and with both operands in shared memory an
+// N = 128 instruction reads 8 KB for 64 cycles of work and took ~95.  CTA item
+// = (sequence, 256 keys as two halves of 128 lanes, group of heads), so that a
+// tile of queries (64 KB with its absorbed parts) is copied once for two M
+// halves: with one half the copies alone took longer than the MMAs.  A tile is
+// `wt` queries of `hpt` heads, 128 columns at most: short windows put several
+// heads side by side, whose shared part is one MMA.
+//
+// Persistent: one CTA per SM walks the items, those with the most queries (the
+// first keys) first and dealt in a snake; the rings run on across items.
+// Warp 0 copies the keys' boxes (TMA), warps 4-7 move them to TMEM, warp 2
+// copies the query tiles, one thread of warp 1 issues the MMAs into two
+// accumulators, warps 8-15 read them back.  Each item leaves one partial sum
+// per key; the last kernel adds the head groups' partials in order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,14 +55,19 @@ using namespace dec;
 
 namespace {
 
-constexpr int kPwThreads = 320;   // copy warp, MMA warp, eight epilogue warps
-constexpr int kPwKeys = 128;      // keys of an item (TMEM lanes)
+constexpr int kPwThreads = 512;   // 16 warps (roles above)
+constexpr int kPwHalf = 128;      // keys of an M half (TMEM lanes)
+constexpr int kPwKeys = 256;      // keys of an item
 constexpr int kPwCols = 128;      // query columns of a tile
-constexpr int kPwSlot = 16384;    // one 128-row x 64-column operand box
-constexpr int kPwZ = 3;           // ring of latent boxes
-constexpr int kPwQ = 6;           // ring of query boxes
-constexpr int kPwAcc = 4;         // TMEM accumulators
-constexpr int kAbThreads = 128;   // absorb: four warps of 16 queries
+constexpr int kPwBox = 16384;     // one 128-row x 64-column operand box
+constexpr int kPwA = 4;           // ring of key boxes in shared memory
+constexpr int kPwQ = 2;           // ring of query tiles (64 KB: queries, absorbed high and low parts)
+constexpr int kPwZ = 4;           // ring of latent boxes in TMEM (32 columns each)
+constexpr int kPwAcc = 2;         // accumulators (128 columns each)
+constexpr int kColK = kPwAcc * kPwCols;         // TMEM: accumulators | k_s of two halves | latents
+constexpr int kColZ = kColK + 128;
+constexpr int kPwTmem = 512;
+constexpr int kAbThreads = 128;   // absorb: four warps of 16 queries each
 
 struct PromptParams {
   int B, H, dh, r, max_len, q_len, window;
@@ -81,21 +93,29 @@ struct PromptParams {
 struct PromptMaps {
   CUtensorMap k;  // k_s rows: (d_h, rows, sequences or pages), box (64, box_rows, 1)
   CUtensorMap z;  // z_k: (r, H, rows, sequences or pages), box (64, 1, box_rows, 1)
-  CUtensorMap q;  // q: (d_h, q_len, H, B), box (64, wt, hpt, 1)
-  CUtensorMap p;  // p: (128, nqt wt, H, B), box (64, wt, hpt, 1)
+  CUtensorMap q;  // q: (64, q_len, H, d_h / 64, B), box (64, wt, hpt, d_h / 64, 1)
+  CUtensorMap p;  // p: (64, nqt wt, H, 2, B), box (64, wt, hpt, 2, 1)
 };
 
 // The units (query tiles) a CTA works through, in the same order for every
-// role: items blockIdx.x, + gridDim.x, ..., in each its heads and their tiles.
+// role: round k takes item k G + c, or k G + G - 1 - c in odd rounds (items
+// fall in work, so the CTAs' totals stay level), and in it its heads and their
+// tiles.
 struct Walk {
-  long long item;
+  int round;
   int b, h0, kt, L;     // item: sequence, first head of the group, key tile, length
+  int halves;           // M halves that hold visible keys
   int hs, qt, qt0;      // unit: first head, query tile; first tile that sees the keys
   int n;                // items begun, minus one
   bool new_item, new_head, last_of_item, last_of_head;
 
   __device__ __forceinline__ bool open(const PromptParams& P) {
-    for (; item < P.items; item += gridDim.x) {
+    const int G = gridDim.x, c = blockIdx.x;
+    for (;; ++round) {
+      const long long base = static_cast<long long>(round) * G;
+      if (base >= P.items) return false;
+      const long long item = base + ((round & 1) ? G - 1 - c : c);
+      if (item >= P.items) continue;
       const int per = P.B * P.nhg;
       kt = static_cast<int>(item / per);
       const int rest = static_cast<int>(item % per);
@@ -104,7 +124,7 @@ struct Walk {
       L = min(max(P.seq_lens[b], P.q_len), P.max_len);
       if (kt * kPwKeys < L) break;
     }
-    if (item >= P.items) return false;
+    halves = kt * kPwKeys + kPwHalf < L ? 2 : 1;
     qt0 = max(0, kt * kPwKeys - (L - P.window)) / P.wt;
     hs = h0;
     qt = qt0;
@@ -118,13 +138,13 @@ struct Walk {
     last_of_item = last_of_head && hs + P.hpt == h0 + P.hg;
   }
   __device__ __forceinline__ bool first(const PromptParams& P) {
-    item = blockIdx.x;
+    round = 0;
     n = -1;
     return open(P);
   }
   __device__ __forceinline__ bool next(const PromptParams& P) {
     if (last_of_item) {
-      item += gridDim.x;
+      ++round;
       return open(P);
     }
     new_item = false;
@@ -150,33 +170,51 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // p = q_h B_h^K of the window's queries in fp32 (mma.sync: exact bf16
 // products), split into bf16 high and low parts; rows past the window and
-// columns past the rank are zeros.
+// columns past the rank are zeros.  64 queries of one head per CTA; the query
+// rows and B_h come in 16-byte pieces, and the two parts leave through shared
+// memory as 256-byte rows.
 __global__ void __launch_bounds__(kAbThreads) lrkv_prefill_absorb_kernel(const PromptParams P) {
   extern __shared__ __align__(16) unsigned char ab_raw[];
+  const int rp = P.kr * 16, zs = rp + 8, qs = P.dh + 8;
   __nv_bfloat16* sB = reinterpret_cast<__nv_bfloat16*>(ab_raw);  // [dh][rp + 8]
+  __nv_bfloat16* sQ = sB + P.dh * zs;                            // [64][dh + 8], then [64][128 + 8]
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
-  const int b = blockIdx.z, h = blockIdx.y, rp = P.kr * 16, zs = rp + 8;
+  const int b = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * 64;
   const int wp = P.nqt * P.wt;
-  for (int i = tid; i < P.dh * rp; i += kAbThreads) {
-    const int d = i / rp, c = i - d * rp;
-    sB[d * zs + c] = c < P.r ? P.b_k[(static_cast<size_t>(h) * P.dh + d) * P.r + c] : __float2bfloat16_rn(0.f);
-  }
-  __syncthreads();
-  const int t0 = blockIdx.x * 64 + warp * 16;
-  float acc[8][4];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  const int ta = t0 + g, tb = ta + 8;
   const size_t tok = static_cast<size_t>(P.H) * P.dh;
   const __nv_bfloat16* qw = P.q + (static_cast<size_t>(b) * P.q_len + P.q_len - P.window) * tok +
                             static_cast<size_t>(h) * P.dh;
+  const int pieces = P.dh / 8;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 8
+  for (int i = tid; i < 64 * pieces; i += kAbThreads) {
+    const int t = i / pieces, c = i % pieces;
+    *reinterpret_cast<uint4*>(sQ + t * qs + 8 * c) =
+        t0 + t < P.window ? *reinterpret_cast<const uint4*>(qw + (t0 + t) * tok + 8 * c) : zero;
+  }
+  const __nv_bfloat16* bh = P.b_k + static_cast<size_t>(h) * P.dh * P.r;
+  if ((reinterpret_cast<uintptr_t>(P.b_k) & 15u) == 0) {
+    const int pr = rp / 8;
+#pragma unroll 8
+    for (int i = tid; i < P.dh * pr; i += kAbThreads) {
+      const int d = i / pr, c = i % pr;
+      *reinterpret_cast<uint4*>(sB + d * zs + 8 * c) =
+          8 * c < P.r ? *reinterpret_cast<const uint4*>(bh + static_cast<size_t>(d) * P.r + 8 * c) : zero;
+    }
+  } else {
+    for (int i = tid; i < P.dh * rp; i += kAbThreads) {
+      const int d = i / rp, c = i % rp;
+      sB[d * zs + c] = c < P.r ? bh[static_cast<size_t>(d) * P.r + c] : __float2bfloat16_rn(0.f);
+    }
+  }
+  __syncthreads();
+  float acc[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
   for (int kk = 0; kk < P.dh / 16; ++kk) {
-    const int k = 16 * kk + 2 * q4;
-    const uint32_t a0 = ta < P.window ? *reinterpret_cast<const uint32_t*>(qw + ta * tok + k) : 0u;
-    const uint32_t a1 = tb < P.window ? *reinterpret_cast<const uint32_t*>(qw + tb * tok + k) : 0u;
-    const uint32_t a2 = ta < P.window ? *reinterpret_cast<const uint32_t*>(qw + ta * tok + k + 8) : 0u;
-    const uint32_t a3 = tb < P.window ? *reinterpret_cast<const uint32_t*>(qw + tb * tok + k + 8) : 0u;
+    uint32_t a0, a1, a2, a3;
+    ldsm_x4(a0, a1, a2, a3, sQ + (16 * warp + (lane & 15)) * qs + 16 * kk + 8 * (lane >> 4));
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       if (8 * j < rp) {
@@ -187,20 +225,28 @@ __global__ void __launch_bounds__(kAbThreads) lrkv_prefill_absorb_kernel(const P
       }
     }
   }
-  __nv_bfloat16* out = P.p + ((static_cast<size_t>(b) * P.H + h) * wp) * 128;
+  __syncthreads();  // every warp has read its queries: their rows now take the results
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int t = u ? tb : ta;
-    if (t >= wp) continue;
+    const int t = 16 * warp + g + 8 * u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = acc[j][2 * u], y = acc[j][2 * u + 1];
       const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
       const __nv_bfloat162 lo = __floats2bfloat162_rn(x - __low2float(hi), y - __high2float(hi));
-      __nv_bfloat162* row = reinterpret_cast<__nv_bfloat162*>(out + static_cast<size_t>(t) * 128 + 8 * j + 2 * q4);
+      __nv_bfloat162* row = reinterpret_cast<__nv_bfloat162*>(sQ + t * 136 + 8 * j + 2 * q4);
       row[0] = hi;
       row[32] = lo;
     }
+  }
+  __syncthreads();
+  __nv_bfloat16* out = P.p + ((static_cast<size_t>(b) * P.H + h) * wp + t0) * 128;
+#pragma unroll 8
+  for (int i = tid; i < 64 * 16; i += kAbThreads) {
+    const int t = i >> 4, c = i & 15;
+    if (t0 + t < wp)
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(t) * 128 + 8 * c) =
+          *reinterpret_cast<const uint4*>(sQ + t * 136 + 8 * c);
   }
 }
 
@@ -208,30 +254,32 @@ template <int DH>
 __global__ void __launch_bounds__(kPwThreads, 1)
     lrkv_prefill_weights_kernel(const __grid_constant__ PromptParams P, const __grid_constant__ PromptMaps maps) {
   constexpr int NB = DH / 64;  // 64-column boxes of a shared row
+  constexpr int kStage = (NB + 2) * kPwBox;
   extern __shared__ __align__(16) unsigned char pw_raw[];
-  __shared__ uint64_t kfull[2], kempty[2], zfull[kPwZ], zempty[kPwZ], qfull[kPwQ], qempty[kPwQ], accf[kPwAcc],
-      acce[kPwAcc];
+  __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready, kfree, zready[kPwZ], zfree[kPwZ],
+      accf[kPwAcc], acce[kPwAcc];
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad;
-  __shared__ int s_k, s_z, s_q, s_acc;  // boxes issued into each ring, units committed
+  __shared__ int s_a, s_q, s_acc;  // boxes and tiles issued, half units committed
   __shared__ __align__(16) float s_lse[2][kPwCols];  // read four columns at a time
-  __shared__ float s_part[2][kPwKeys];
+  __shared__ float s_part[2][2][kPwHalf];
   unsigned char* smem = pw_raw + ((1024u - (smem_u32(pw_raw) & 1023u)) & 1023u);
-  unsigned char* s_keys = smem;                              // [2][NB] boxes
-  unsigned char* s_zring = s_keys + 2 * NB * kPwSlot;        // [kPwZ] boxes
-  unsigned char* s_qring = s_zring + kPwZ * kPwSlot;         // [kPwQ] boxes
+  unsigned char* s_aring = smem;                          // [kPwA] boxes
+  unsigned char* s_qring = s_aring + kPwA * kPwBox;       // [kPwQ] tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* fail = &s_fail;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) { mbar_init(&kfull[i], 1); mbar_init(&kempty[i], 1); }
-    for (int i = 0; i < kPwZ; ++i) { mbar_init(&zfull[i], 1); mbar_init(&zempty[i], 1); }
+    for (int i = 0; i < kPwA; ++i) { mbar_init(&afull[i], 1); mbar_init(&aempty[i], 4); }
     for (int i = 0; i < kPwQ; ++i) { mbar_init(&qfull[i], 1); mbar_init(&qempty[i], 1); }
+    for (int i = 0; i < kPwZ; ++i) { mbar_init(&zready[i], 4); mbar_init(&zfree[i], 1); }
     for (int i = 0; i < kPwAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], 8); }
-    s_fail = s_bad = s_k = s_z = s_q = s_acc = 0;
+    mbar_init(&kready, 4);
+    mbar_init(&kfree, 1);
+    s_fail = s_bad = s_a = s_q = s_acc = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base, kPwAcc * kPwCols);
+  if (warp == 1) tmem_alloc(&tmem_base, kPwTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -242,71 +290,41 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      // ---- copies ------------------------------------------------------------
-      int zi = 0, qi = 0;
+      // ---- key boxes: k_s of both halves per item, z_k,h of both per head -------
+      int ai = 0;
       Walk w;
       for (bool more = w.first(P); more && !*fail; more = w.next(P)) {
-        const int row = w.kt * kPwKeys;
-        const int boxes = (min(kPwKeys, w.L - row) + P.box_rows - 1) / P.box_rows;  // copies of the visible rows
-        auto at = [&](int i, int& seq, int& r0) {  // tensor-map coordinates of copy i
-          const int t = row + i * P.box_rows;
-          if (!P.block_table) {
-            seq = w.b;
-            r0 = t;
-          } else {
-            seq = P.block_table[static_cast<size_t>(w.b) * P.max_blocks + (t >> P.page_shift)];
-            r0 = t & ((1 << P.page_shift) - 1);
-            if (seq < 0 || seq >= P.num_pages) {  // no page of the pool: the copy fills zeros
-              s_bad = 1;
-              seq = P.num_pages;
-            }
-          }
-        };
-        const uint32_t box_bytes = static_cast<uint32_t>(P.box_rows) * 128u;
-        if (w.new_item) {
-          const int kb = w.n & 1;
-          if (w.n >= 2 && !mbar_wait_bounded(&kempty[kb], static_cast<uint32_t>(w.n / 2 - 1) & 1u)) {
-            *fail = 1;
-            break;
-          }
-          mbar_arrive_expect_tx(&kfull[kb], box_bytes * boxes * NB);
-          for (int i = 0; i < boxes; ++i) {
-            int seq, r0;
-            at(i, seq, r0);
-            for (int c = 0; c < NB; ++c)
-              tma_load_3d(s_keys + (kb * NB + c) * kPwSlot + i * box_bytes, &maps.k, 64 * c, r0, seq, &kfull[kb]);
-          }
-          s_k = w.n + 1;
-        }
-        // the tile's queries, then their absorbed parts, then the latents
+        const int nk = w.new_item ? w.halves * NB : 0, nz = w.new_head && P.r > 0 ? w.halves * P.hpt : 0;
         bool live = true;
-        for (int c = 0; c < NB + (P.r > 0 ? 2 : 0) && live; ++c) {
-          const int s = qi % kPwQ;
-          if (qi >= kPwQ && !mbar_wait_bounded(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u)) {
+        for (int i = 0; i < nk + nz && live; ++i) {
+          const int s = ai % kPwA;
+          if (ai >= kPwA && !mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(ai / kPwA - 1) & 1u)) {
             live = false;
             break;
           }
-          mbar_arrive_expect_tx(&qfull[s], static_cast<uint32_t>(ncols) * 128u);
-          if (c < NB)
-            tma_load_4d(s_qring + s * kPwSlot, &maps.q, 64 * c, P.q_len - P.window + w.qt * P.wt, w.hs, w.b,
-                        &qfull[s]);
-          else
-            tma_load_4d(s_qring + s * kPwSlot, &maps.p, 64 * (c - NB), w.qt * P.wt, w.hs, w.b, &qfull[s]);
-          s_q = ++qi;
-        }
-        for (int i = 0; P.r > 0 && w.new_head && i < P.hpt && live; ++i) {
-          const int s = zi % kPwZ;
-          if (zi >= kPwZ && !mbar_wait_bounded(&zempty[s], static_cast<uint32_t>(zi / kPwZ - 1) & 1u)) {
-            live = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&zfull[s], box_bytes * boxes);
+          const bool is_k = i < nk;
+          const int m = is_k ? i / NB : (i - nk) / P.hpt;
+          const int row = w.kt * kPwKeys + m * kPwHalf;
+          const int boxes = (min(kPwHalf, w.L - row) + P.box_rows - 1) / P.box_rows;  // copies of the visible rows
+          const uint32_t box_bytes = static_cast<uint32_t>(P.box_rows) * 128u;
+          mbar_arrive_expect_tx(&afull[s], box_bytes * boxes);
           for (int j = 0; j < boxes; ++j) {
-            int seq, r0;
-            at(j, seq, r0);
-            tma_load_4d(s_zring + s * kPwSlot + j * box_bytes, &maps.z, 0, w.hs + i, r0, seq, &zfull[s]);
+            int seq = w.b, r0 = row + j * P.box_rows;  // tensor-map coordinates of the copy
+            if (P.block_table) {
+              seq = P.block_table[static_cast<size_t>(w.b) * P.max_blocks + (r0 >> P.page_shift)];
+              r0 &= (1 << P.page_shift) - 1;
+              if (seq < 0 || seq >= P.num_pages) {  // no page of the pool: the copy fills zeros
+                s_bad = 1;
+                seq = P.num_pages;
+              }
+            }
+            unsigned char* dst = s_aring + s * kPwBox + j * box_bytes;
+            if (is_k)
+              tma_load_3d(dst, &maps.k, 64 * (i % NB), r0, seq, &afull[s]);
+            else
+              tma_load_4d(dst, &maps.z, 0, w.hs + (i - nk) % P.hpt, r0, seq, &afull[s]);
           }
-          s_z = ++zi;
+          s_a = ++ai;
         }
         if (!live) {
           *fail = 1;
@@ -314,67 +332,129 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
       }
     }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // ---- query tiles -----------------------------------------------------------
+      int qi = 0;
+      Walk w;
+      for (bool more = w.first(P); more && !*fail; more = w.next(P), ++qi) {
+        const int s = qi % kPwQ;
+        if (qi >= kPwQ && !mbar_wait_bounded(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u)) {
+          *fail = 1;
+          break;
+        }
+        unsigned char* st = s_qring + s * kStage;
+        mbar_arrive_expect_tx(&qfull[s], static_cast<uint32_t>(ncols) * 128u * (NB + (P.r > 0 ? 2 : 0)));
+        tma_load_5d(st, &maps.q, 0, P.q_len - P.window + w.qt * P.wt, w.hs, 0, w.b, &qfull[s]);
+        if (P.r > 0) tma_load_5d(st + NB * kPwBox, &maps.p, 0, w.qt * P.wt, w.hs, 0, w.b, &qfull[s]);
+        s_q = qi + 1;
+      }
+    }
   } else if (warp == 1) {
     if (lane == 0) {
-      // ---- MMAs: unit u into accumulator u % kPwAcc ------------------------------
+      // ---- MMAs: half unit x into accumulator x % 2 --------------------------------
       const uint32_t id_all = idesc_bf16(128, ncols, 0, 0), id_head = idesc_bf16(128, P.wt, 0, 0);
-      int u = 0, zi = 0, qi = 0;
+      int x = 0, qi = 0, zi = 0;
       Walk w;
-      for (bool more = w.first(P); more && !*fail; more = w.next(P), ++u) {
-        const int kb = w.n & 1;
-        const uint32_t acc = tmem + (u % kPwAcc) * kPwCols;
-        bool ok = u < kPwAcc || mbar_wait_bounded(&acce[u % kPwAcc], static_cast<uint32_t>(u / kPwAcc - 1) & 1u);
-        if (ok && w.new_item) ok = mbar_wait_bounded(&kfull[kb], static_cast<uint32_t>(w.n / 2) & 1u);
-        for (int c = 0; c < NB && ok; ++c, ++qi) {
-          const int s = qi % kPwQ;
-          ok = mbar_wait_bounded(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u);
+      for (bool more = w.first(P); more && !*fail; more = w.next(P), ++qi) {
+        const int s = qi % kPwQ;
+        bool ok = !w.new_item || mbar_wait_bounded(&kready, static_cast<uint32_t>(w.n) & 1u);
+        ok = ok && mbar_wait_bounded(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u);
+        const uint32_t qa = smem_u32(s_qring + s * kStage), pa = qa + NB * kPwBox;
+        for (int m = 0; m < w.halves && ok; ++m, ++x) {
+          const uint32_t acc = tmem + (x & 1) * kPwCols;
+          ok = x < kPwAcc || mbar_wait_bounded(&acce[x & 1], static_cast<uint32_t>(x / kPwAcc - 1) & 1u);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ka = smem_u32(s_keys + (kb * NB + c) * kPwSlot), qa = smem_u32(s_qring + s * kPwSlot);
+          for (int c = 0; c < NB; ++c) {
+            const uint32_t ka = tmem + kColK + (m * NB + c) * 32, qc = qa + c * ncols * 128;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ss(acc, smem_desc(ka + kk * 32, 16, 1024, 2), smem_desc(qa + kk * 32, 16, 1024, 2), id_all,
-                      c + kk > 0 ? 1u : 0u);
-          tc_commit(&qempty[s]);
-        }
-        if (ok && P.r > 0) {
-          const int s0 = qi % kPwQ, s1 = (qi + 1) % kPwQ;
-          ok = mbar_wait_bounded(&qfull[s0], static_cast<uint32_t>(qi / kPwQ) & 1u) &&
-               mbar_wait_bounded(&qfull[s1], static_cast<uint32_t>((qi + 1) / kPwQ) & 1u);
-          const uint32_t hi = smem_u32(s_qring + s0 * kPwSlot), lo = smem_u32(s_qring + s1 * kPwSlot);
-          for (int i = 0; i < P.hpt && ok; ++i) {
-            const int s = (zi + i) % kPwZ;
-            if (w.new_head) ok = mbar_wait_bounded(&zfull[s], static_cast<uint32_t>((zi + i) / kPwZ) & 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_ts(acc, ka + kk * 8, smem_desc(qc + kk * 32, 16, 1024, 2), id_all, c + kk > 0 ? 1u : 0u);
+          }
+          for (int i = 0; P.r > 0 && i < P.hpt && ok; ++i) {
+            const int z = zi + m * P.hpt + i, sl = z % kPwZ;
+            if (w.new_head) ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / kPwZ) & 1u);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t za = smem_u32(s_zring + s * kPwSlot), off = i * P.wt * 128;
+            const uint32_t za = tmem + kColZ + sl * 32, hi = pa + i * P.wt * 128, lo = hi + ncols * 128;
             for (int kk = 0; kk < P.kr; ++kk) {
-              const uint64_t zd = smem_desc(za + kk * 32, 16, 1024, 2);
-              tc_mma_ss(acc + i * P.wt, zd, smem_desc(hi + off + kk * 32, 16, 1024, 2), id_head, 1u);
-              tc_mma_ss(acc + i * P.wt, zd, smem_desc(lo + off + kk * 32, 16, 1024, 2), id_head, 1u);
+              tc_mma_ts(acc + i * P.wt, za + kk * 8, smem_desc(hi + kk * 32, 16, 1024, 2), id_head, 1u);
+              tc_mma_ts(acc + i * P.wt, za + kk * 8, smem_desc(lo + kk * 32, 16, 1024, 2), id_head, 1u);
             }
-            if (w.last_of_head) tc_commit(&zempty[s]);
+            if (w.last_of_head) tc_commit(&zfree[sl]);
           }
-          if (ok) {
-            tc_commit(&qempty[s0]);
-            tc_commit(&qempty[s1]);
-            qi += 2;
-            if (w.last_of_head) zi += P.hpt;
-          }
+          if (!ok) break;
+          tc_commit(&accf[x & 1]);
+          s_acc = x + 1;
         }
         if (!ok) {
           *fail = 1;
           break;
         }
-        if (w.last_of_item) tc_commit(&kempty[kb]);
-        tc_commit(&accf[u % kPwAcc]);
-        s_acc = u + 1;
+        if (P.r > 0 && w.last_of_head) zi += w.halves * P.hpt;
+        tc_commit(&qempty[s]);
+        if (w.last_of_item) tc_commit(&kfree);
       }
     }
-  } else {
-    // ---- epilogue: key (TMEM lane) 32 quad + lane; 32-column chunks of parity
-    // `half` of the tile --------------------------------------------------------
-    const int quad = warp & 3, half = (warp - 2) >> 2, key = 32 * quad + lane, et = tid - 64;
+  } else if (warp >= 4 && warp < 8) {
+    // ---- key boxes to TMEM: lane = row of the half, two columns per 32-bit word ----
+    const int quad = warp & 3, row = 32 * quad + lane;
+    int ai = 0, zi = 0;
+    bool ok = true;
+    auto move = [&](uint32_t col) {
+      const int s = ai % kPwA;
+      ok = ok && !*fail && mbar_wait_bounded(&afull[s], static_cast<uint32_t>(ai / kPwA) & 1u);
+      ok = __all_sync(0xffffffffu, ok);  // the warp moves together
+      if (!ok) {
+        *fail = 1;
+      } else {
+        const unsigned char* src = s_aring + s * kPwBox + row * 128;
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+          v[4 * c] = u.x; v[4 * c + 1] = u.y; v[4 * c + 2] = u.z; v[4 * c + 3] = u.w;
+        }
+        tmem_st32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + col, v);
+        tmem_wait_st();
+      }
+      fence_proxy_async_smem();  // the reads above before the slot's next copy
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&aempty[s]);
+      ++ai;
+    };
+    Walk w;
+    for (bool more = w.first(P); more; more = w.next(P)) {
+      if (w.new_item) {
+        if (ok && w.n >= 1 && !mbar_wait_bounded(&kfree, static_cast<uint32_t>(w.n - 1) & 1u)) {
+          ok = false;
+          *fail = 1;
+        }
+        tc_fence_after();
+        for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&kready);
+      }
+      if (w.new_head && P.r > 0)
+        for (int i = 0; i < w.halves * P.hpt; ++i, ++zi) {
+          const int sl = zi % kPwZ;
+          if (ok && zi >= kPwZ && !mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(zi / kPwZ - 1) & 1u)) {
+            ok = false;
+            *fail = 1;
+          }
+          tc_fence_after();
+          move(kColZ + sl * 32);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&zready[sl]);
+        }
+    }
+  } else if (warp >= 8) {
+    // ---- epilogue: key (TMEM lane) 32 quad + lane of a half; 32-column chunks of
+    // parity `odd` of the tile ---------------------------------------------------
+    const int quad = warp & 3, odd = (warp - 8) >> 2, key = 32 * quad + lane, et = tid - 256;
     // log2-domain log-sum-exp of column et of a unit; +inf where the column
     // holds no query of the window or its query saw nothing (weight 0)
     auto lse_of = [&](const Walk& w) {
@@ -388,66 +468,78 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     bool more = w.first(P), ok = true;
     if (more && et < kPwCols) s_lse[0][et] = lse_of(w);
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    float total = 0.f;
+    float total[2] = {0.f, 0.f};
+    int x = 0;
     for (int u = 0; more; ++u) {
       Walk nx = w;
       const bool more_next = nx.next(P);
       float lse_next = 0.f;
       if (more_next && et < kPwCols) lse_next = lse_of(nx);
-      if (w.new_item) total = 0.f;
-      const int row = w.kt * kPwKeys + key;
-      if (ok && *fail) ok = false;
-      if (ok) {
-        ok = mbar_wait_bounded(&accf[u % kPwAcc], static_cast<uint32_t>(u / kPwAcc) & 1u);
-        if (!ok) *fail = 1;
-      }
-      if (ok) {
-        tc_fence_after();
-        // query t of the tile sees this key when t >= t_min
-        const int t_min = row - (w.L - P.window) - w.qt * P.wt;
-        const bool masked = w.kt * kPwKeys + kPwKeys - 1 > w.L - P.window + w.qt * P.wt;
-        const float* lse = s_lse[u & 1];
-        for (int c = half; 32 * c < ncols; c += 2) {
-          float sc = P.scale_log2;
-          uint32_t v[32];
-          tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + (u % kPwAcc) * kPwCols + 32 * c, v);
-          float ks[2] = {1.f, 1.f};
-          if (P.key_scale && row < w.L) {  // (a chunk spans at most two heads: wt >= 16)
-            const size_t at = (static_cast<size_t>(w.b) * P.H + w.hs + 32 * c / P.wt) * P.max_len + row;
-            ks[0] = ks[1] = P.key_scale[at];
-            if (P.wt == 16) ks[1] = P.key_scale[at + P.max_len];
-          }
-          tmem_wait_ld();
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      if (w.new_item) total[0] = total[1] = 0.f;
+      const float* lse = s_lse[u & 1];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse + 32 * c + e);
-            const float s2 = sc * ks[e >> 4];
-            float x[4] = {exp2_fast(fmaf(__uint_as_float(v[e]), s2, -l4.x)),
-                          exp2_fast(fmaf(__uint_as_float(v[e + 1]), s2, -l4.y)),
-                          exp2_fast(fmaf(__uint_as_float(v[e + 2]), s2, -l4.z)),
-                          exp2_fast(fmaf(__uint_as_float(v[e + 3]), s2, -l4.w))};
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (((32 * c + e + k) & (P.wt - 1)) < t_min) x[k] = 0.f;
+      for (int m = 0; m < 2; ++m) {
+        if (m >= w.halves) break;
+        const int row = w.kt * kPwKeys + m * kPwHalf + key;
+        ok = ok && !*fail && mbar_wait_bounded(&accf[x & 1], static_cast<uint32_t>(x / kPwAcc) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          *fail = 1;
+        } else {
+          tc_fence_after();
+          // query t of the tile sees this key when t >= t_min
+          const int t_min = row - (w.L - P.window) - w.qt * P.wt;
+          const bool masked = w.kt * kPwKeys + m * kPwHalf + kPwHalf - 1 > w.L - P.window + w.qt * P.wt;
+          for (int c = odd; 32 * c < ncols; c += 2) {
+            uint32_t v[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + (x & 1) * kPwCols + 32 * c, v);
+            float ks[2] = {P.scale_log2, P.scale_log2};
+            if (P.key_scale && row < w.L) {  // (a chunk spans at most two heads: wt >= 16)
+              const size_t at = (static_cast<size_t>(w.b) * P.H + w.hs + 32 * c / P.wt) * P.max_len + row;
+              ks[0] = ks[1] = P.scale_log2 * P.key_scale[at];
+              if (P.wt == 16) ks[1] = P.scale_log2 * P.key_scale[at + P.max_len];
             }
+            tmem_wait_ld();
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum[k] += x[k];
+            for (int e = 0; e < 32; e += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(lse + 32 * c + e);
+              const float s2 = ks[e >> 4];
+              float y[4] = {exp2_fast(fmaf(__uint_as_float(v[e]), s2, -l4.x)),
+                            exp2_fast(fmaf(__uint_as_float(v[e + 1]), s2, -l4.y)),
+                            exp2_fast(fmaf(__uint_as_float(v[e + 2]), s2, -l4.z)),
+                            exp2_fast(fmaf(__uint_as_float(v[e + 3]), s2, -l4.w))};
+              if (masked) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (((32 * c + e + k) & (P.wt - 1)) < t_min) y[k] = 0.f;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sum[k] += y[k];
+            }
+            total[m] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
-          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc_fence_before();
         }
-        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&acce[x & 1]);
+        ++x;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&acce[u % kPwAcc]);
       // (written again two items later, past a barrier its reader passed too)
-      if (w.last_of_item && half == 1) s_part[w.n & 1][key] = total;
+      if (w.last_of_item && odd == 1) {
+        s_part[w.n & 1][0][key] = total[0];
+        s_part[w.n & 1][1][key] = total[1];
+      }
       if (more_next && et < kPwCols) s_lse[(u + 1) & 1][et] = lse_next;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (w.last_of_item && half == 0 && row < w.L)
-        P.partial[(static_cast<size_t>(w.h0 / P.hg) * P.B + w.b) * P.max_len + row] =
-            ok ? total + s_part[w.n & 1][key] : __int_as_float(0x7fc00000);
+      if (w.last_of_item && odd == 0) {
+        float* out = P.partial + (static_cast<size_t>(w.h0 / P.hg) * P.B + w.b) * P.max_len;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int row = w.kt * kPwKeys + m * kPwHalf + key;
+          if (row < w.L) out[row] = ok ? total[m] + s_part[w.n & 1][m][key] : __int_as_float(0x7fc00000);
+        }
+      }
       w = nx;
       more = more_next;
     }
@@ -457,10 +549,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   __syncthreads();
   if (tid == 0) {
     bool done = true;
-    for (int i = max(0, s_k - 2); i < s_k; ++i)
-      done = mbar_wait_bounded(&kfull[i & 1], static_cast<uint32_t>(i / 2) & 1u) && done;
-    for (int i = max(0, s_z - kPwZ); i < s_z; ++i)
-      done = mbar_wait_bounded(&zfull[i % kPwZ], static_cast<uint32_t>(i / kPwZ) & 1u) && done;
+    for (int i = max(0, s_a - kPwA); i < s_a; ++i)
+      done = mbar_wait_bounded(&afull[i % kPwA], static_cast<uint32_t>(i / kPwA) & 1u) && done;
     for (int i = max(0, s_q - kPwQ); i < s_q; ++i)
       done = mbar_wait_bounded(&qfull[i % kPwQ], static_cast<uint32_t>(i / kPwQ) & 1u) && done;
     for (int i = max(0, s_acc - kPwAcc); i < s_acc; ++i)
@@ -470,7 +560,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kPwAcc * kPwCols);
+  if (warp == 1) tmem_dealloc(tmem, kPwTmem);
 }
 
 // weights_out = decay * earlier weight (rows before the prompt's own) + the
@@ -541,9 +631,9 @@ PromptLayout prompt_plan(const lrkv_dims& d, int window, int sms, PromptParams& 
   P.nqt = (window + P.wt - 1) / P.wt;
   P.kr = (P.r + 15) / 16;
   P.nkt = (P.max_len + kPwKeys - 1) / kPwKeys;
-  // head groups: until there are four items per SM
+  // head groups: until there are three items per SM
   P.hg = P.H;
-  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < 4LL * sms) P.hg /= 2;
+  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < 3LL * sms) P.hg /= 2;
   P.nhg = P.H / P.hg;
   P.items = static_cast<long long>(P.nkt) * P.B * P.nhg;
   P.grid = static_cast<int>(std::min<long long>(sms, P.items));
@@ -614,7 +704,7 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
   P.page_shift = shift;
   P.num_pages = num_pages;
   P.max_blocks = block_table ? P.max_len / page_size : 0;
-  P.box_rows = block_table ? std::min(page_size, kPwKeys) : kPwKeys;
+  P.box_rows = block_table ? std::min(page_size, kPwHalf) : kPwHalf;
   P.seq_lens = seq_lens; P.lse = lse; P.key_scale = key_scale;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.b_k = static_cast<const __nv_bfloat16*>(b_k);
@@ -624,25 +714,26 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
   const uint64_t dh = P.dh, H = P.H, r = P.r, B = P.B, Q = q_len;
   const uint64_t rows = block_table ? page_size : P.max_len, seqs = block_table ? num_pages : P.B;
   const uint64_t wp = static_cast<uint64_t>(P.nqt) * P.wt;
-  const uint64_t qd[4] = {dh, Q, H, B}, qs[3] = {H * dh * 2, dh * 2, Q * H * dh * 2};
-  const uint32_t qb[4] = {64u, static_cast<uint32_t>(P.wt), static_cast<uint32_t>(P.hpt), 1u};
+  const uint32_t nb = P.dh / 64, wt = P.wt, hpt = P.hpt;
+  const uint64_t qd[5] = {64, Q, H, nb, B}, qs[4] = {H * dh * 2, dh * 2, 128, Q * H * dh * 2};
+  const uint32_t qb[5] = {64u, wt, hpt, nb, 1u}, pb[5] = {64u, wt, hpt, 2u, 1u};
   if (!make_tmap_3d_bf16(&m.k, k_s, dh, rows, seqs, 64u, P.box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_4d_bf16_swizzled(&m.q, q, qd, qs, qb))
+      !make_tmap_5d_bf16_swizzled(&m.q, q, qd, qs, qb))
     return LRKV_ERR_CUDA;
   if (P.r > 0) {
     const uint64_t zd[4] = {r, H, rows, seqs}, zs[3] = {r * 2, H * r * 2, rows * H * r * 2};
     const uint32_t zb[4] = {64u, 1u, static_cast<uint32_t>(P.box_rows), 1u};
-    const uint64_t pd[4] = {128, wp, H, B}, ps[3] = {256, wp * 256, H * wp * 256};
-    if (!make_tmap_4d_bf16_swizzled(&m.z, z_k, zd, zs, zb) || !make_tmap_4d_bf16_swizzled(&m.p, P.p, pd, ps, qb))
+    const uint64_t pd[5] = {64, wp, H, 2, B}, ps[4] = {256, wp * 256, 128, H * wp * 256};
+    if (!make_tmap_4d_bf16_swizzled(&m.z, z_k, zd, zs, zb) || !make_tmap_5d_bf16_swizzled(&m.p, P.p, pd, ps, pb))
       return LRKV_ERR_CUDA;
   }
   using Fn = void (*)(const PromptParams, const PromptMaps);
   const Fn kern = P.dh == 128 ? lrkv_prefill_weights_kernel<128> : lrkv_prefill_weights_kernel<64>;
-  const int smem = 1024 + (2 * (P.dh / 64) + kPwZ + kPwQ) * kPwSlot;
+  const int smem = 1024 + (kPwA + kPwQ * (P.dh / 64 + 2)) * kPwBox;
   if (ensure_kernel_smem(reinterpret_cast<const void*>(kern), smem, true) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (P.r > 0) {
-    const int ab_smem = P.dh * (P.kr * 16 + 8) * 2;
+    const int ab_smem = (P.dh * (P.kr * 16 + 8) + 64 * 136) * 2;  // (d_h + 8 <= 136)
     lrkv_prefill_absorb_kernel<<<dim3(static_cast<unsigned>((wp + 63) / 64), P.H, P.B), kAbThreads, ab_smem, s>>>(P);
     if (cudaGetLastError() != cudaSuccess) return LRKV_ERR_CUDA;
   }

@@ -659,22 +659,49 @@ def _size_of(call: str, *args) -> int:
     return int(n.value)
 
 
-def _check(named: dict, shapes: dict, device) -> None:
-    """Every given tensor contiguous and on `device`; the named ones of the
-    given (dtype, shape), None standing for any type."""
-    for name, t in named.items():
-        if t is None:
-            continue
-        if not t.is_contiguous():
-            raise ValueError(f"LRKV tensors must be contiguous: {name}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if name in shapes:
-            dtype, shape = shapes[name]
-            if dtype is not None and t.dtype != dtype:
+def _check(device: int, *specs) -> None:
+    """Each spec (name, tensor or None, dtype, shape): type, shape, layout and
+    CUDA device of the given tensors.  Written for a decode step's host time: a
+    tight loop, the message only when something is wrong."""
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                              or t.get_device() != device):
+            if t.dtype is not dtype:
                 raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-            if tuple(t.shape) != tuple(shape):
+            if t.shape != shape:
                 raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"LRKV tensors must be contiguous: {name}")
+            raise ValueError(f"{name} is on {t.device}, the call's first tensor on device {device}")
+    if device < 0:
+        raise ValueError("LRKV tensors must be on a CUDA device")
+
+
+class _On:
+    """The CUDA device `device` made current for a call (left alone when it is)."""
+
+    __slots__ = ("device", "before")
+
+    def __init__(self, device: int):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before != self.device:
+            torch.cuda.set_device(self.before)
+
+
+def _stream_on(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_U8, _F32, _I32 = torch.uint8, torch.float32, torch.int32
 
 
 def _cache_rows(k_s, block_table, batch: int):
@@ -708,22 +735,22 @@ def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: f
         out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
     if lse is None:
         lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    f32, dt = torch.float32, q.dtype
-    _check(dict(q=q, k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, b_k=b_k, b_v=b_v, seq_lens=seq_lens, weights=weights,
-                weights_out=weights_out, key_scale=key_scale, block_table=block_table, out=out, lse=lse, ws=ws),
-           dict(k_s=(dt, rows + (dh,)), v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)),
-                b_k=(dt, (H, dh, r)), b_v=(dt, (H, dh, r)), seq_lens=(torch.int32, (B,)),
-                weights=(f32, (B, max_len)), weights_out=(f32, (B, max_len)), key_scale=(f32, (B, H, max_len)),
-                block_table=(torch.int32, (B, max_len // page_size if page_size else 0)), out=(f32, (B, H, dh)),
-                lse=(f32, (B, H))), q.device)
-    with torch.cuda.device(q.device):
+    dt, dev, flat, z, basis = q.dtype, q.get_device(), (B, max_len), rows + (H, r), (H, dh, r)
+    _check(dev, ("q", q, dt, (B, H, dh)), ("k_s", k_s, dt, rows + (dh,)), ("v_s", v_s, dt, rows + (dh,)),
+           ("z_k", z_k, dt, z), ("z_v", z_v, dt, z), ("b_k", b_k, dt, basis), ("b_v", b_v, dt, basis),
+           ("seq_lens", seq_lens, _I32, (B,)), ("weights", weights, _F32, flat),
+           ("weights_out", weights_out, _F32, flat), ("key_scale", key_scale, _F32, (B, H, max_len)),
+           ("block_table", block_table, _I32, (B, max_len // (page_size or 1))), ("out", out, _F32, (B, H, dh)),
+           ("lse", lse, _F32, (B, H)))
+    with _On(dev):
         if ws is None:
             ws = decode_weighted_workspace(dims, q.device)
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_decode_weighted(
             ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s), _ptr(v_s),
             _ptr(z_k) if r else None, _ptr(z_v) if r else None, _ptr(b_k) if r else None, _ptr(b_v) if r else None,
             _ptr(key_scale), _ptr(seq_lens), float(decay), _ptr(weights), _ptr(weights_out), _ptr(out), _ptr(lse),
-            _ptr(ws), ws.numel(), _stream_handle(stream)))
+            _ptr(ws), ws.numel(), _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_decode_weighted")
     return out, lse, weights_out, ws
@@ -748,20 +775,20 @@ def prefill_weights(q, k_s, z_k, b_k, lse, seq_lens, weights, window: int = 0, d
     if weights_out is None:
         weights_out = weights if weights is not None else torch.zeros((B, max_len), dtype=torch.float32,
                                                                       device=q.device)
-    f32, dt = torch.float32, q.dtype
-    _check(dict(q=q, k_s=k_s, z_k=z_k, b_k=b_k, lse=lse, seq_lens=seq_lens, weights=weights,
-                weights_out=weights_out, key_scale=key_scale, block_table=block_table, ws=ws),
-           dict(k_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), b_k=(dt, (H, dh, r)), lse=(f32, (B, H, Tq)),
-                seq_lens=(torch.int32, (B,)), weights=(f32, (B, max_len)), weights_out=(f32, (B, max_len)),
-                key_scale=(f32, (B, H, max_len)),
-                block_table=(torch.int32, (B, max_len // page_size if page_size else 0))), q.device)
-    with torch.cuda.device(q.device):
+    dt, dev, flat = q.dtype, q.get_device(), (B, max_len)
+    _check(dev, ("q", q, dt, (B, Tq, H, dh)), ("k_s", k_s, dt, rows + (dh,)), ("z_k", z_k, dt, rows + (H, r)),
+           ("b_k", b_k, dt, (H, dh, r)), ("lse", lse, _F32, (B, H, Tq)), ("seq_lens", seq_lens, _I32, (B,)),
+           ("weights", weights, _F32, flat), ("weights_out", weights_out, _F32, flat),
+           ("key_scale", key_scale, _F32, (B, H, max_len)),
+           ("block_table", block_table, _I32, (B, max_len // (page_size or 1))))
+    with _On(dev):
         if ws is None:
             ws = prefill_weights_workspace(dims, window, q.device)
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_prefill_weights(
             ctypes.byref(dims), Tq, window, _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s),
             _ptr(z_k) if r else None, _ptr(b_k) if r else None, _ptr(key_scale), _ptr(lse), _ptr(seq_lens),
-            float(decay), _ptr(weights), _ptr(weights_out), _ptr(ws), ws.numel(), _stream_handle(stream)))
+            float(decay), _ptr(weights), _ptr(weights_out), _ptr(ws), ws.numel(), _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_prefill_weights")
     return weights_out, ws
@@ -792,24 +819,23 @@ def evict(k_s, v_s, z_k, z_v, weights, seq_lens, budget: int, sink: int = 0, rec
     order_out = order if order_out is None else order_out
     new_lens = seq_lens if new_lens is None else new_lens
     axes = positions.shape[-1] if positions is not None else 0
-    f32, i32, dt = torch.float32, torch.int32, k_s.dtype
-    flat = (B, max_len)
-    _check(dict(k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, weights=weights, seq_lens=seq_lens, order=order,
-                key_scale=key_scale, positions=positions, block_table=block_table, weights_out=weights_out,
-                order_out=order_out, new_lens=new_lens, kept=kept, ws=ws),
-           dict(v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)), weights=(f32, flat),
-                seq_lens=(i32, (B,)), order=(i32, flat), key_scale=(f32, (B, H, max_len)),
-                positions=(i32, flat + (axes,)), weights_out=(f32, flat), order_out=(i32, flat),
-                new_lens=(i32, (B,)), kept=(i32, (B, int(budget))),
-                block_table=(i32, (B, max_len // page_size if page_size else 0))), k_s.device)
-    with torch.cuda.device(k_s.device):
+    dt, dev, flat, z = k_s.dtype, k_s.get_device(), (B, max_len), rows + (H, r)
+    _check(dev, ("k_s", k_s, dt, rows + (dh,)), ("v_s", v_s, dt, rows + (dh,)), ("z_k", z_k, dt, z),
+           ("z_v", z_v, dt, z), ("weights", weights, _F32, flat), ("seq_lens", seq_lens, _I32, (B,)),
+           ("order", order, _I32, flat), ("key_scale", key_scale, _F32, (B, H, max_len)),
+           ("positions", positions, _I32, flat + (axes,)), ("weights_out", weights_out, _F32, flat),
+           ("order_out", order_out, _I32, flat), ("new_lens", new_lens, _I32, (B,)),
+           ("kept", kept, _I32, (B, int(budget))),
+           ("block_table", block_table, _I32, (B, max_len // (page_size or 1))))
+    with _On(dev):
         if ws is None:
             ws = evict_workspace(B, max_len, budget, k_s.device)
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_evict(
             ctypes.byref(dims), int(budget), int(sink), int(recent), _ptr(weights), _ptr(order), _ptr(seq_lens),
             page_size, num_pages, _ptr(block_table), _ptr(k_s), _ptr(v_s), _ptr(z_k) if r else None,
             _ptr(z_v) if r else None, _ptr(key_scale), _ptr(positions), axes, _ptr(weights_out), _ptr(order_out),
-            _ptr(new_lens), _ptr(kept), _ptr(ws), ws.numel(), _stream_handle(stream)))
+            _ptr(new_lens), _ptr(kept), _ptr(ws), ws.numel(), _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_evict")
     return new_lens, weights_out, order_out, ws
@@ -829,13 +855,14 @@ def rope_rotate(x, positions, cos_sin, sections, out=None, ws=None, stream=None)
     dims = make_dims(B, H, dh, 0, 1, x.dtype)
     if out is None:
         out = torch.empty_like(x)
-    _check(dict(x=x, positions=positions, cos_sin=cos_sin, out=out, ws=ws),
-           dict(positions=(torch.int32, (B, n, axes)), cos_sin=(torch.float32, (cos_sin.shape[0], dh)),
-                out=(x.dtype, x.shape)), x.device)
-    with torch.cuda.device(x.device):
+    dev, max_pos = x.get_device(), cos_sin.shape[0]
+    _check(dev, ("x", x, x.dtype, x.shape), ("positions", positions, _I32, (B, n, axes)),
+           ("cos_sin", cos_sin, _F32, (max_pos, dh)), ("out", out, x.dtype, x.shape),
+           ("ws", ws, _U8, ws.shape if ws is not None else None))
+    with _On(dev):
         st = int(load().lrkv_rope_rotate(
             ctypes.byref(dims), n, _ptr(x), _ptr(positions), axes, _sections(sections), _ptr(cos_sin),
-            cos_sin.shape[0], _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(), _stream_handle(stream)))
+            max_pos, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(), _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_rope_rotate")
     return out
@@ -860,22 +887,22 @@ def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, se
         out = torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device)
     if lse is None:
         lse = torch.empty((B, H), dtype=torch.float32, device=q_rot.device)
-    f32, dt, rows = torch.float32, q_rot.dtype, (B, max_len)
-    _check(dict(q_rot=q_rot, k_s=k_s, v_s=v_s, z_k=z_k, z_v=z_v, b_k=b_k, b_v=b_v, cos_sin=cos_sin,
-                positions=positions, seq_lens=seq_lens, weights=weights, weights_out=weights_out, out=out, lse=lse,
-                ws=ws),
-           dict(k_s=(dt, rows + (dh,)), v_s=(dt, rows + (dh,)), z_k=(dt, rows + (H, r)), z_v=(dt, rows + (H, r)),
-                b_k=(dt, (H, dh, r)), b_v=(dt, (H, dh, r)), cos_sin=(f32, (cos_sin.shape[0], dh)),
-                positions=(torch.int32, rows + (axes,)), seq_lens=(torch.int32, (B,)), weights=(f32, rows),
-                weights_out=(f32, rows), out=(f32, (B, H, dh)), lse=(f32, (B, H))), q_rot.device)
-    with torch.cuda.device(q_rot.device):
+    dt, dev, flat, z, basis = q_rot.dtype, q_rot.get_device(), (B, max_len), (B, max_len, H, r), (H, dh, r)
+    _check(dev, ("q_rot", q_rot, dt, (B, H, dh)), ("k_s", k_s, dt, (B, max_len, dh)),
+           ("v_s", v_s, dt, (B, max_len, dh)), ("z_k", z_k, dt, z), ("z_v", z_v, dt, z), ("b_k", b_k, dt, basis),
+           ("b_v", b_v, dt, basis), ("cos_sin", cos_sin, _F32, (cos_sin.shape[0], dh)),
+           ("positions", positions, _I32, (B, max_len, axes)), ("seq_lens", seq_lens, _I32, (B,)),
+           ("weights", weights, _F32, flat), ("weights_out", weights_out, _F32, flat),
+           ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
+    with _On(dev):
         if ws is None:
             ws = decode_rope_axes_workspace(dims, q_rot.device)
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_decode_rope_axes(
             ctypes.byref(dims), _ptr(q_rot), _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(b_k), _ptr(b_v),
             _ptr(cos_sin), cos_sin.shape[0], _ptr(positions), axes, _sections(sections), _ptr(seq_lens),
             float(decay), _ptr(weights), _ptr(weights_out), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-            _stream_handle(stream)))
+            _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_decode_rope_axes")
     return out, lse, weights_out, ws

@@ -191,11 +191,12 @@ def test_the_binding_checks_tensors():
     refused(lrkv.decode_weighted, *good[:7], lens.long(), w, match="seq_lens")
     refused(lrkv.decode_weighted, *good[:8], w[:, :39].contiguous(), match="weights")
     refused(lrkv.decode_weighted, *good[:8], w.double(), match="weights")
-    refused(lrkv.decode_weighted, q, k.transpose(0, 1), *good[2:], match="contiguous")
+    refused(lrkv.decode_weighted, q, torch.zeros(2, 64, 40, dtype=q.dtype).transpose(1, 2), *good[2:],
+            match="contiguous")
     refused(lrkv.decode_weighted, q, k.float(), *good[2:], match="k_s")
     refused(lrkv.decode_weighted, *good[:5], b[:8].contiguous(), b, lens, w, match="b_k")
     refused(lrkv.decode_weighted, *good, match="key_scale", key_scale=torch.zeros(2, 16, 41))
-    refused(lrkv.decode_weighted, *good, match="key_scale", key_scale=torch.zeros(2, 16, 40, device="meta"))
+    refused(lrkv.decode_weighted, *good, match="CUDA")                 # right in all but the device
     refused(lrkv.prefill_weights, q[:, None], k, z, b, torch.zeros(2, 16, 2), lens, w, match="lse")
     refused(lrkv.prefill_weights, q[:, None], k, z, b, torch.zeros(2, 16, 1), lens, w.to(torch.float16), match="weights")
     refused(lrkv.evict, k, k, z, z, w, lens, 8, match="order", order=torch.zeros(2, 40))
