@@ -29,7 +29,7 @@
 // first keys) first and dealt in a snake; the rings run on across items.
 // Warp 0 copies the keys' boxes (TMA), warps 4-7 move them to TMEM, warp 2
 // copies the query tiles, one thread of warp 1 issues the MMAs into two
-// accumulators, warps 8-15 read them back.  Each item leaves one partial sum
+// accumulators, warps 8-23 read them back.  Each item leaves one partial sum
 // per key; the last kernel adds the head groups' partials in order.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -55,15 +55,17 @@ using namespace dec;
 
 namespace {
 
-constexpr int kPwThreads = 512;   // 16 warps (roles above)
+constexpr int kPwThreads = 800;   // 25 warps (roles above)
+constexpr int kPwEpi = 16;        // epilogue warps: four per lane quadrant, a 32-column chunk each
 constexpr int kPwHalf = 128;      // keys of an M half (TMEM lanes)
 constexpr int kPwKeys = 256;      // keys of an item
 constexpr int kPwCols = 128;      // query columns of a tile
 constexpr int kPwBox = 16384;     // one 128-row x 64-column operand box
 constexpr int kPwA = 4;           // ring of key boxes in shared memory
 constexpr int kPwQ = 2;           // ring of query tiles (64 KB: queries, absorbed high and low parts)
-constexpr int kPwZ = 4;           // ring of latent boxes in TMEM (32 columns each)
+constexpr int kPwZ = 4;           // latent boxes in TMEM (32 columns each): a ring of two per M half
 constexpr int kPwAcc = 2;         // accumulators (128 columns each)
+constexpr int kPwL = 4;           // ring of log-sum-exp tiles in shared memory
 constexpr int kColK = kPwAcc * kPwCols;         // TMEM: accumulators | k_s of two halves | latents
 constexpr int kColZ = kColK + 128;
 constexpr int kPwTmem = 512;
@@ -71,7 +73,7 @@ constexpr int kAbThreads = 128;   // absorb: four warps of 16 queries each
 
 struct PromptParams {
   int B, H, dh, r, max_len, q_len, window;
-  int wt, hpt, nqt;          // queries and heads of a tile, tiles of the window
+  int wt, wt_log, hpt, nqt;  // queries (2^wt_log) and heads of a tile, tiles of the window
   int hg, nhg, nkt;          // heads of an item, head groups, key tiles
   int kr;                    // 16-wide steps over the latents
   int box_rows;              // rows of one key copy: 128, or the page size when smaller
@@ -97,17 +99,16 @@ struct PromptMaps {
   CUtensorMap p;  // p: (64, nqt wt, H, 2, B), box (64, wt, hpt, 2, 1)
 };
 
-// The units (query tiles) a CTA works through, in the same order for every
-// role: round k takes item k G + c, or k G + G - 1 - c in odd rounds (items
-// fall in work, so the CTAs' totals stay level), and in it its heads and their
-// tiles.
+// The items a CTA works through, in the same order for every role: round k takes
+// item k G + c, or k G + G - 1 - c in odd rounds (items fall in work, so the
+// CTAs' totals stay level).  An item's units: its heads hpt at a time, for each
+// the query tiles qt0 .. nqt - 1.
 struct Walk {
   int round;
-  int b, h0, kt, L;     // item: sequence, first head of the group, key tile, length
+  int b, h0, kt, L;     // sequence, first head of the group, key tile, length
   int halves;           // M halves that hold visible keys
-  int hs, qt, qt0;      // unit: first head, query tile; first tile that sees the keys
+  int qt0;              // first tile that sees the keys
   int n;                // items begun, minus one
-  bool new_item, new_head, last_of_item, last_of_head;
 
   __device__ __forceinline__ bool open(const PromptParams& P) {
     const int G = gridDim.x, c = blockIdx.x;
@@ -126,16 +127,8 @@ struct Walk {
     }
     halves = kt * kPwKeys + kPwHalf < L ? 2 : 1;
     qt0 = max(0, kt * kPwKeys - (L - P.window)) / P.wt;
-    hs = h0;
-    qt = qt0;
     ++n;
-    new_item = new_head = true;
-    marks(P);
     return true;
-  }
-  __device__ __forceinline__ void marks(const PromptParams& P) {
-    last_of_head = qt + 1 == P.nqt;
-    last_of_item = last_of_head && hs + P.hpt == h0 + P.hg;
   }
   __device__ __forceinline__ bool first(const PromptParams& P) {
     round = 0;
@@ -143,27 +136,69 @@ struct Walk {
     return open(P);
   }
   __device__ __forceinline__ bool next(const PromptParams& P) {
-    if (last_of_item) {
-      ++round;
-      return open(P);
-    }
-    new_item = false;
-    new_head = last_of_head;
-    if (last_of_head) {
-      hs += P.hpt;
-      qt = qt0;
-    } else {
-      ++qt;
-    }
-    marks(P);
-    return true;
+    ++round;
+    return open(P);
   }
 };
+
+// Two fp32 values in one 64-bit register, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Sum over a 32-column chunk of 2^(score s - lse), nlse holding -lse (log2
+// domain, -inf where a column counts for nothing); with MASKED only the columns
+// whose query index (column modulo wt) is at least t_min.  s0 scales the first
+// 16 columns, s1 the others.
+template <bool MASKED>
+__device__ __forceinline__ float chunk_sum(const uint32_t (&v)[32], const float* nlse, float s0, float s1, int col,
+                                           int wt, int t_min) {
+  uint64_t sum[2] = {0ull, 0ull};
+  const uint64_t sa = pair(s0, s0), sb = pair(s1, s1);
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nlse + e);
+    const uint64_t s2 = e < 16 ? sa : sb;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = e + 2 * k;
+      const uint64_t x = fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2, k ? l.y : l.x);
+      float a, b;
+      unpair(x, a, b);
+      a = exp2_fast(a);
+      b = exp2_fast(b);
+      if (MASKED) {
+        a = ((col + i) & (wt - 1)) < t_min ? 0.f : a;
+        b = ((col + i + 1) & (wt - 1)) < t_min ? 0.f : b;
+      }
+      sum[k] = add2(sum[k], pair(a, b));
+    }
+  }
+  float a, b, c, d;
+  unpair(sum[0], a, b);
+  unpair(sum[1], c, d);
+  return (a + b) + (c + d);
 }
 
 }  // namespace
@@ -257,12 +292,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   constexpr int kStage = (NB + 2) * kPwBox;
   extern __shared__ __align__(16) unsigned char pw_raw[];
   __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready, kfree, zready[kPwZ], zfree[kPwZ],
-      accf[kPwAcc], acce[kPwAcc];
+      accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL];
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad;
-  __shared__ int s_a, s_q, s_acc;  // boxes and tiles issued, half units committed
-  __shared__ __align__(16) float s_lse[2][kPwCols];  // read four columns at a time
-  __shared__ float s_part[2][2][kPwHalf];
+  __shared__ int s_a, s_q, s_acc[kPwAcc];  // boxes and tiles issued, half units committed
+  __shared__ __align__(16) float s_lse[kPwL][kPwCols];  // read four columns at a time
+  __shared__ float s_part[2][4][2][kPwHalf];
   unsigned char* smem = pw_raw + ((1024u - (smem_u32(pw_raw) & 1023u)) & 1023u);
   unsigned char* s_aring = smem;                          // [kPwA] boxes
   unsigned char* s_qring = s_aring + kPwA * kPwBox;       // [kPwQ] tiles
@@ -271,12 +306,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kPwA; ++i) { mbar_init(&afull[i], 1); mbar_init(&aempty[i], 4); }
-    for (int i = 0; i < kPwQ; ++i) { mbar_init(&qfull[i], 1); mbar_init(&qempty[i], 1); }
+    for (int i = 0; i < kPwQ; ++i) { mbar_init(&qfull[i], 1); mbar_init(&qempty[i], 2); }
     for (int i = 0; i < kPwZ; ++i) { mbar_init(&zready[i], 4); mbar_init(&zfree[i], 1); }
-    for (int i = 0; i < kPwAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], 8); }
+    for (int i = 0; i < kPwAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], kPwEpi); }
+    for (int i = 0; i < kPwL; ++i) { mbar_init(&lfull[i], 1); mbar_init(&lempty[i], kPwEpi); }
     mbar_init(&kready, 4);
-    mbar_init(&kfree, 1);
-    s_fail = s_bad = s_a = s_q = s_acc = 0;
+    mbar_init(&kfree, 2);
+    s_fail = s_bad = s_a = s_q = s_acc[0] = s_acc[1] = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, kPwTmem);
@@ -292,24 +328,26 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (lane == 0) {
       // ---- key boxes: k_s of both halves per item, z_k,h of both per head -------
       int ai = 0;
+      bool live = true;
       Walk w;
-      for (bool more = w.first(P); more && !*fail; more = w.next(P)) {
-        const int nk = w.new_item ? w.halves * NB : 0, nz = w.new_head && P.r > 0 ? w.halves * P.hpt : 0;
-        bool live = true;
-        for (int i = 0; i < nk + nz && live; ++i) {
+      for (bool more = w.first(P); more && live && !*fail; more = w.next(P)) {
+        const int nk = w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
+        for (int i = 0; i < nk + nz; ++i) {
           const int s = ai % kPwA;
-          if (ai >= kPwA && !mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(ai / kPwA - 1) & 1u)) {
-            live = false;
+          live = ai < kPwA || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(ai / kPwA - 1) & 1u);
+          if (!live) {
+            *fail = 1;
             break;
           }
+          // the heads' latents one after another, both halves of each
           const bool is_k = i < nk;
-          const int m = is_k ? i / NB : (i - nk) / P.hpt;
+          const int m = is_k ? i / NB : (i - nk) % w.halves;
           const int row = w.kt * kPwKeys + m * kPwHalf;
           const int boxes = (min(kPwHalf, w.L - row) + P.box_rows - 1) / P.box_rows;  // copies of the visible rows
           const uint32_t box_bytes = static_cast<uint32_t>(P.box_rows) * 128u;
           mbar_arrive_expect_tx(&afull[s], box_bytes * boxes);
-          for (int j = 0; j < boxes; ++j) {
-            int seq = w.b, r0 = row + j * P.box_rows;  // tensor-map coordinates of the copy
+          for (int k = 0; k < boxes; ++k) {
+            int seq = w.b, r0 = row + k * P.box_rows;  // tensor-map coordinates of the copy
             if (P.block_table) {
               seq = P.block_table[static_cast<size_t>(w.b) * P.max_blocks + (r0 >> P.page_shift)];
               r0 &= (1 << P.page_shift) - 1;
@@ -318,17 +356,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 seq = P.num_pages;
               }
             }
-            unsigned char* dst = s_aring + s * kPwBox + j * box_bytes;
+            unsigned char* dst = s_aring + s * kPwBox + k * box_bytes;
             if (is_k)
               tma_load_3d(dst, &maps.k, 64 * (i % NB), r0, seq, &afull[s]);
             else
-              tma_load_4d(dst, &maps.z, 0, w.hs + (i - nk) % P.hpt, r0, seq, &afull[s]);
+              tma_load_4d(dst, &maps.z, 0, w.h0 + (i - nk) / w.halves, r0, seq, &afull[s]);
           }
           s_a = ++ai;
-        }
-        if (!live) {
-          *fail = 1;
-          break;
         }
       }
     }
@@ -336,71 +370,115 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (lane == 0) {
       // ---- query tiles -----------------------------------------------------------
       int qi = 0;
+      bool live = true;
       Walk w;
-      for (bool more = w.first(P); more && !*fail; more = w.next(P), ++qi) {
-        const int s = qi % kPwQ;
-        if (qi >= kPwQ && !mbar_wait_bounded(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u)) {
-          *fail = 1;
-          break;
-        }
-        unsigned char* st = s_qring + s * kStage;
-        mbar_arrive_expect_tx(&qfull[s], static_cast<uint32_t>(ncols) * 128u * (NB + (P.r > 0 ? 2 : 0)));
-        tma_load_5d(st, &maps.q, 0, P.q_len - P.window + w.qt * P.wt, w.hs, 0, w.b, &qfull[s]);
-        if (P.r > 0) tma_load_5d(st + NB * kPwBox, &maps.p, 0, w.qt * P.wt, w.hs, 0, w.b, &qfull[s]);
-        s_q = qi + 1;
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMAs: half unit x into accumulator x % 2 --------------------------------
-      const uint32_t id_all = idesc_bf16(128, ncols, 0, 0), id_head = idesc_bf16(128, P.wt, 0, 0);
-      int x = 0, qi = 0, zi = 0;
-      Walk w;
-      for (bool more = w.first(P); more && !*fail; more = w.next(P), ++qi) {
-        const int s = qi % kPwQ;
-        bool ok = !w.new_item || mbar_wait_bounded(&kready, static_cast<uint32_t>(w.n) & 1u);
-        ok = ok && mbar_wait_bounded(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u);
-        const uint32_t qa = smem_u32(s_qring + s * kStage), pa = qa + NB * kPwBox;
-        for (int m = 0; m < w.halves && ok; ++m, ++x) {
-          const uint32_t acc = tmem + (x & 1) * kPwCols;
-          ok = x < kPwAcc || mbar_wait_bounded(&acce[x & 1], static_cast<uint32_t>(x / kPwAcc - 1) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          for (int c = 0; c < NB; ++c) {
-            const uint32_t ka = tmem + kColK + (m * NB + c) * 32, qc = qa + c * ncols * 128;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_ts(acc, ka + kk * 8, smem_desc(qc + kk * 32, 16, 1024, 2), id_all, c + kk > 0 ? 1u : 0u);
-          }
-          for (int i = 0; P.r > 0 && i < P.hpt && ok; ++i) {
-            const int z = zi + m * P.hpt + i, sl = z % kPwZ;
-            if (w.new_head) ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / kPwZ) & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t za = tmem + kColZ + sl * 32, hi = pa + i * P.wt * 128, lo = hi + ncols * 128;
-            for (int kk = 0; kk < P.kr; ++kk) {
-              tc_mma_ts(acc + i * P.wt, za + kk * 8, smem_desc(hi + kk * 32, 16, 1024, 2), id_head, 1u);
-              tc_mma_ts(acc + i * P.wt, za + kk * 8, smem_desc(lo + kk * 32, 16, 1024, 2), id_head, 1u);
+      for (bool more = w.first(P); more && live && !*fail; more = w.next(P))
+        for (int hs = w.h0; hs < w.h0 + P.hg && live; hs += P.hpt)
+          for (int qt = w.qt0; qt < P.nqt; ++qt, ++qi) {
+            const int s = qi % kPwQ;
+            live = qi < kPwQ || mbar_wait_bounded(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u);
+            if (!live) {
+              *fail = 1;
+              break;
             }
-            if (w.last_of_head) tc_commit(&zfree[sl]);
+            unsigned char* st = s_qring + s * kStage;
+            mbar_arrive_expect_tx(&qfull[s], static_cast<uint32_t>(ncols) * 128u * (NB + (P.r > 0 ? 2 : 0)));
+            tma_load_5d(st, &maps.q, 0, P.q_len - P.window + qt * P.wt, hs, 0, w.b, &qfull[s]);
+            if (P.r > 0) tma_load_5d(st + NB * kPwBox, &maps.p, 0, qt * P.wt, hs, 0, w.b, &qfull[s]);
+            s_q = qi + 1;
           }
-          if (!ok) break;
-          tc_commit(&accf[x & 1]);
-          s_acc = x + 1;
-        }
-        if (!ok) {
-          *fail = 1;
-          break;
-        }
-        if (P.r > 0 && w.last_of_head) zi += w.halves * P.hpt;
-        tc_commit(&qempty[s]);
-        if (w.last_of_item) tc_commit(&kfree);
-      }
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp == 1 || warp == 24) {
+    if (lane == 0) {
+      // ---- MMAs of M half m into accumulator m: a thread each, since issuing an
+      // instruction takes a thread ~95 cycles for 64 of tensor work ------------------
+      const int m = warp == 24;
+      const uint32_t id_all = idesc_bf16(128, ncols, 0, 0), id_head = idesc_bf16(128, P.wt, 0, 0);
+      const uint64_t d0 = smem_desc(smem_u32(s_qring), 16, 1024, 2);  // address field: 16-byte units, low bits
+      const uint32_t box = static_cast<uint32_t>(ncols) * 8u, head = static_cast<uint32_t>(P.wt) * 8u;
+      const uint32_t acc = tmem + m * kPwCols, ka = tmem + kColK + m * (NB * 32);
+      int x = 0, qi = 0, zi = 0;
+      bool ok = true;
+      Walk w;
+      for (bool more = w.first(P); more && ok && !*fail; more = w.next(P)) {
+        ok = mbar_wait_bounded(&kready, static_cast<uint32_t>(w.n) & 1u);
+        const bool on = m < w.halves;
+        for (int hs = 0; hs < P.hg && ok; hs += P.hpt) {
+          for (int qt = w.qt0; qt < P.nqt && ok; ++qt, ++qi) {
+            const int s = qi % kPwQ;
+            ok = mbar_wait_bounded(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u) &&
+                 (!on || x < 1 || mbar_wait_bounded(&acce[m], static_cast<uint32_t>(x - 1) & 1u));
+            if (!ok) break;
+            if (on) {
+              tc_fence_after();
+              const uint64_t qd = d0 + static_cast<uint32_t>(s * (kStage / 16));
+#pragma unroll
+              for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_ts(acc, ka + c * 32 + kk * 8, qd + c * box + kk * 2, id_all, c + kk > 0 ? 1u : 0u);
+              uint64_t hd = qd + NB * (kPwBox / 16);
+              for (int i = 0; P.r > 0 && i < P.hpt; ++i, hd += head) {
+                const int z = zi + i, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
+                if (qt == w.qt0) {
+                  ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / (kPwZ / 2)) & 1u);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                const uint32_t za = tmem + kColZ + sl * 32, at = acc + i * P.wt;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  if (kk < P.kr) {
+                    tc_mma_ts(at, za + kk * 8, hd + kk * 2, id_head, 1u);
+                    tc_mma_ts(at, za + kk * 8, hd + box + kk * 2, id_head, 1u);
+                  }
+                if (qt + 1 == P.nqt) tc_commit(&zfree[sl]);
+              }
+              if (!ok) break;
+              tc_commit(&accf[m]);
+              s_acc[m] = ++x;
+            }
+            tc_commit(&qempty[s]);
+          }
+          if (on) zi += P.hpt;
+        }
+        if (ok) tc_commit(&kfree);
+      }
+      if (!ok) *fail = 1;
+    }
+  } else if (warp == 3) {
+    // ---- minus the log2-domain log-sum-exp of a tile's columns; -inf where a
+    // column holds no query of the window or its query saw nothing (weight 0) ----
+    bool ok = true;
+    int u = 0;
+    Walk w;
+    for (bool more = w.first(P); more && ok; more = w.next(P))
+      for (int hs = w.h0; hs < w.h0 + P.hg && ok; hs += P.hpt)
+        for (int qt = w.qt0; qt < P.nqt; ++qt, ++u) {
+          const int s = u % kPwL;
+          ok = ok && !*fail && (u < kPwL || mbar_wait_bounded(&lempty[s], static_cast<uint32_t>(u / kPwL - 1) & 1u));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            *fail = 1;
+            break;
+          }
+#pragma unroll
+          for (int k = 0; k < kPwCols / 32; ++k) {
+            const int col = lane + 32 * k, i = qt * P.wt + (col & (P.wt - 1)), h = hs + (col >> P.wt_log);
+            float v = -INFINITY;
+            if (col < ncols && i < P.window) {
+              v = P.lse[(static_cast<size_t>(w.b) * P.H + h) * P.q_len + P.q_len - P.window + i];
+              v = v == -INFINITY ? v : -v * kLog2e;
+            }
+            s_lse[s][col] = v;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&lfull[s]);
+        }
+  } else if (warp < 8) {
     // ---- key boxes to TMEM: lane = row of the half, two columns per 32-bit word ----
     const int quad = warp & 3, row = 32 * quad + lane;
-    int ai = 0, zi = 0;
+    int ai = 0, zi[2] = {0, 0};
     bool ok = true;
     auto move = [&](uint32_t col) {
       const int s = ai % kPwA;
@@ -426,122 +504,86 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     };
     Walk w;
     for (bool more = w.first(P); more; more = w.next(P)) {
-      if (w.new_item) {
-        if (ok && w.n >= 1 && !mbar_wait_bounded(&kfree, static_cast<uint32_t>(w.n - 1) & 1u)) {
-          ok = false;
-          *fail = 1;
-        }
+      ok = ok && (w.n < 1 || mbar_wait_bounded(&kfree, static_cast<uint32_t>(w.n - 1) & 1u));
+      tc_fence_after();
+      for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&kready);
+      for (int i = 0; P.r > 0 && i < w.halves * P.hg; ++i) {
+        const int m = i % w.halves, z = zi[m]++, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
+        ok = ok && (z < kPwZ / 2 || mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(z / (kPwZ / 2) - 1) & 1u));
         tc_fence_after();
-        for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
+        move(kColZ + sl * 32);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cta(&kready);
+        if (lane == 0) mbar_arrive_cta(&zready[sl]);
       }
-      if (w.new_head && P.r > 0)
-        for (int i = 0; i < w.halves * P.hpt; ++i, ++zi) {
-          const int sl = zi % kPwZ;
-          if (ok && zi >= kPwZ && !mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(zi / kPwZ - 1) & 1u)) {
-            ok = false;
-            *fail = 1;
-          }
-          tc_fence_after();
-          move(kColZ + sl * 32);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta(&zready[sl]);
-        }
     }
-  } else if (warp >= 8) {
-    // ---- epilogue: key (TMEM lane) 32 quad + lane of a half; 32-column chunks of
-    // parity `odd` of the tile ---------------------------------------------------
-    const int quad = warp & 3, odd = (warp - 8) >> 2, key = 32 * quad + lane, et = tid - 256;
-    // log2-domain log-sum-exp of column et of a unit; +inf where the column
-    // holds no query of the window or its query saw nothing (weight 0)
-    auto lse_of = [&](const Walk& w) {
-      if (et >= ncols) return INFINITY;
-      const int i = w.qt * P.wt + (et & (P.wt - 1)), h = w.hs + et / P.wt;
-      if (i >= P.window) return INFINITY;
-      const float v = P.lse[(static_cast<size_t>(w.b) * P.H + h) * P.q_len + P.q_len - P.window + i];
-      return v == -INFINITY ? INFINITY : v * kLog2e;
-    };
-    Walk w;
-    bool more = w.first(P), ok = true;
-    if (more && et < kPwCols) s_lse[0][et] = lse_of(w);
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+  } else if (warp < 24) {
+    // ---- epilogue: key (TMEM lane) 32 quad + lane of a half, columns 32 part ..
+    // 32 part + 31 of the tile ---------------------------------------------------
+    const int quad = warp & 3, part = (warp - 8) >> 2, key = 32 * quad + lane;
+    const bool mine = 32 * part < ncols;
     float total[2] = {0.f, 0.f};
-    int x = 0;
-    for (int u = 0; more; ++u) {
-      Walk nx = w;
-      const bool more_next = nx.next(P);
-      float lse_next = 0.f;
-      if (more_next && et < kPwCols) lse_next = lse_of(nx);
-      if (w.new_item) total[0] = total[1] = 0.f;
-      const float* lse = s_lse[u & 1];
+    int x[2] = {0, 0}, u = 0;
+    bool ok = true;
+    Walk w;
+    for (bool more = w.first(P); more; more = w.next(P)) {
+      total[0] = total[1] = 0.f;
+      for (int hs = w.h0; hs < w.h0 + P.hg; hs += P.hpt)
+        for (int qt = w.qt0; qt < P.nqt; ++qt, ++u) {
+          const float* lse = s_lse[u % kPwL] + 32 * part;
+          ok = ok && !*fail && mbar_wait_bounded(&lfull[u % kPwL], static_cast<uint32_t>(u / kPwL) & 1u);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m >= w.halves) break;
-        const int row = w.kt * kPwKeys + m * kPwHalf + key;
-        ok = ok && !*fail && mbar_wait_bounded(&accf[x & 1], static_cast<uint32_t>(x / kPwAcc) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          *fail = 1;
-        } else {
-          tc_fence_after();
-          // query t of the tile sees this key when t >= t_min
-          const int t_min = row - (w.L - P.window) - w.qt * P.wt;
-          const bool masked = w.kt * kPwKeys + m * kPwHalf + kPwHalf - 1 > w.L - P.window + w.qt * P.wt;
-          for (int c = odd; 32 * c < ncols; c += 2) {
+          for (int m = 0; m < 2; ++m) {
+            if (m >= w.halves) break;
+            const int row = w.kt * kPwKeys + m * kPwHalf + key;
+            ok = ok && !*fail && mbar_wait_bounded(&accf[m], static_cast<uint32_t>(x[m]) & 1u);
+            ok = __all_sync(0xffffffffu, ok);
             uint32_t v[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + (x & 1) * kPwCols + 32 * c, v);
-            float ks[2] = {P.scale_log2, P.scale_log2};
-            if (P.key_scale && row < w.L) {  // (a chunk spans at most two heads: wt >= 16)
-              const size_t at = (static_cast<size_t>(w.b) * P.H + w.hs + 32 * c / P.wt) * P.max_len + row;
-              ks[0] = ks[1] = P.scale_log2 * P.key_scale[at];
-              if (P.wt == 16) ks[1] = P.scale_log2 * P.key_scale[at + P.max_len];
+            if (!ok) {
+              *fail = 1;
+            } else if (mine) {
+              tc_fence_after();
+              tmem_ld32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + m * kPwCols + 32 * part, v);
+              tmem_wait_ld();
+              tc_fence_before();
             }
-            tmem_wait_ld();
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(lse + 32 * c + e);
-              const float s2 = ks[e >> 4];
-              float y[4] = {exp2_fast(fmaf(__uint_as_float(v[e]), s2, -l4.x)),
-                            exp2_fast(fmaf(__uint_as_float(v[e + 1]), s2, -l4.y)),
-                            exp2_fast(fmaf(__uint_as_float(v[e + 2]), s2, -l4.z)),
-                            exp2_fast(fmaf(__uint_as_float(v[e + 3]), s2, -l4.w))};
-              if (masked) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (((32 * c + e + k) & (P.wt - 1)) < t_min) y[k] = 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cta(&acce[m]);  // the accumulator is free
+            ++x[m];
+            if (ok && mine) {
+              float s0 = P.scale_log2, s1 = P.scale_log2;
+              if (P.key_scale && row < w.L) {  // (the chunk spans at most two heads: wt >= 16)
+                const float* kp = P.key_scale + (static_cast<size_t>(w.b) * P.H + hs) * P.max_len + row;
+                s0 *= kp[static_cast<size_t>((32 * part) >> P.wt_log) * P.max_len];
+                s1 *= kp[static_cast<size_t>((32 * part + 16) >> P.wt_log) * P.max_len];
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) sum[k] += y[k];
+              // query t of the tile sees this key when t >= t_min
+              const int first = w.L - P.window + qt * P.wt;
+              if (w.kt * kPwKeys + m * kPwHalf + kPwHalf - 1 > first)
+                total[m] += chunk_sum<true>(v, lse, s0, s1, 32 * part, P.wt, row - first);
+              else
+                total[m] += chunk_sum<false>(v, lse, s0, s1, 0, 0, 0);
             }
-            total[m] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&lempty[u % kPwL]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cta(&acce[x & 1]);
-        ++x;
+      // the four column parts meet (the array of an item's parity is written again
+      // two items later, past a barrier its readers passed too)
+      float (*sp)[2][kPwHalf] = s_part[w.n & 1];
+      sp[part][0][key] = total[0];
+      sp[part][1][key] = total[1];
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (part < 2) {
+        const int row = w.kt * kPwKeys + part * kPwHalf + key;  // part 0 finishes half 0, part 1 half 1
+        const float sum = (sp[0][part][key] + sp[1][part][key]) + (sp[2][part][key] + sp[3][part][key]);
+        if (row < w.L)
+          P.partial[(static_cast<size_t>(w.h0 / P.hg) * P.B + w.b) * P.max_len + row] =
+              ok ? sum : __int_as_float(0x7fc00000);
       }
-      // (written again two items later, past a barrier its reader passed too)
-      if (w.last_of_item && odd == 1) {
-        s_part[w.n & 1][0][key] = total[0];
-        s_part[w.n & 1][1][key] = total[1];
-      }
-      if (more_next && et < kPwCols) s_lse[(u + 1) & 1][et] = lse_next;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (w.last_of_item && odd == 0) {
-        float* out = P.partial + (static_cast<size_t>(w.h0 / P.hg) * P.B + w.b) * P.max_len;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int row = w.kt * kPwKeys + m * kPwHalf + key;
-          if (row < w.L) out[row] = ok ? total[m] + s_part[w.n & 1][m][key] : __int_as_float(0x7fc00000);
-        }
-      }
-      w = nx;
-      more = more_next;
     }
   }
   // every copy and MMA issued is complete before the block gives up its shared
@@ -553,8 +595,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       done = mbar_wait_bounded(&afull[i % kPwA], static_cast<uint32_t>(i / kPwA) & 1u) && done;
     for (int i = max(0, s_q - kPwQ); i < s_q; ++i)
       done = mbar_wait_bounded(&qfull[i % kPwQ], static_cast<uint32_t>(i / kPwQ) & 1u) && done;
-    for (int i = max(0, s_acc - kPwAcc); i < s_acc; ++i)
-      done = mbar_wait_bounded(&accf[i % kPwAcc], static_cast<uint32_t>(i / kPwAcc) & 1u) && done;
+    for (int i = 0; i < kPwAcc; ++i)
+      if (s_acc[i] > 0) done = mbar_wait_bounded(&accf[i], static_cast<uint32_t>(s_acc[i] - 1) & 1u) && done;
     P.cta_status[blockIdx.x] = (s_fail || !done ? kDevTimeout : 0u) | (s_bad ? kDevBounds : 0u);
   }
   tc_fence_before();
@@ -628,6 +670,8 @@ PromptLayout prompt_plan(const lrkv_dims& d, int window, int sms, PromptParams& 
   P.hpt = 1;
   while (2 * P.hpt * P.wt <= kPwCols && P.H % (2 * P.hpt) == 0) P.hpt *= 2;
   if (P.wt * P.hpt < 32) P.wt = 32;
+  P.wt_log = 0;
+  while ((1 << P.wt_log) < P.wt) ++P.wt_log;
   P.nqt = (window + P.wt - 1) / P.wt;
   P.kr = (P.r + 15) / 16;
   P.nkt = (P.max_len + kPwKeys - 1) / kPwKeys;
