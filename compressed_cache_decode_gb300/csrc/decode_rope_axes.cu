@@ -11,9 +11,19 @@
 // entry k of the table's row of that position, so a row's rotation is gathered
 // from up to `axes` table rows.
 //
-// Grid (range CTAs, groups of 8 heads), one warp per head, 16-token tiles of
-// k_s, v_s and the group's z_k, z_v in a ring of TMA stages.  Per tile the CTA
-// gathers the 16 rows' cos and sin into shared memory together.
+// Grid (range CTAs, groups of 8 heads), one warp per head (B_h's MMA fragments
+// live in its registers), 16-token tiles of k_s, v_s and the group's z_k, z_v
+// in a ring of TMA stages.  Per tile and warp: K = Z_h B_h^T on the tensor
+// cores (mma.sync, fp32 accumulation), plus the shared row, dotted with the
+// query turned back by the row's angles,
+//   q~ . (k D) = x0 (qa cos + qb sin) + x1 (qb cos - qa sin)   per pair,
+// three two-wide fp32 instructions; the values O^T += V^T p with the
+// probabilities as a bf16 high part in one column of the B operand and the low
+// part in the next, so that one MMA takes both.  The 16 rows' cos and sin are
+// gathered by the whole CTA into one of two shared buffers: the table entries
+// of tile j + 2 and the positions of tile j + 3 are loaded while tile j is
+// computed, since the two dependent loads' latency in every tile took most of
+// the time at first (4 x 32K rows, 32 heads: 950 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -42,6 +52,36 @@ constexpr int kRHeads = 8;                   // heads per CTA, one consumer warp
 constexpr int kRThreads = 32 * kRHeads;
 constexpr int kRHeader = 1024;               // barriers and stage records
 constexpr int kRMaxStages = 16;
+constexpr float kRRescaleLog2 = 8.f;         // raise the reference max only past 2^8
+
+// Two fp32 values in one 64-bit register, for the two-wide fp32 instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 struct AxesArgs {
   RopeAxes ax;
@@ -53,14 +93,18 @@ struct AxesArgs {
 template <int DH, int R>
 __global__ void __launch_bounds__(kRThreads, 1)
     lrkv_decode_rope_axes_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_zk,
-                            const __grid_constant__ CUtensorMap tm_zv, const __grid_constant__ AxesArgs A) {
-  constexpr int NT = DH / 8;   // 8-column tiles of the rebuilt key
-  constexpr int KS = R / 16;   // 16-wide steps over a head's latents
-  constexpr int CW = DH / 32;  // shared value columns per lane
+                                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_zk,
+                                 const __grid_constant__ CUtensorMap tm_zv, const __grid_constant__ AxesArgs A) {
+  constexpr int NT = DH / 8;    // 8-column tiles of the rebuilt key
+  constexpr int KS = R / 16;    // 16-wide steps over a head's latents
+  constexpr int MV = DH / 16;   // 16-row tiles of the shared values
+  constexpr int MZ = R / 16;    // 16-row tiles of the private values
+  constexpr int NP = DH / 32;   // pairs a thread gathers per tile (one token, 16 threads)
+  constexpr int CSR = DH + 4;   // floats per gathered row (padded)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ int s_timeout, s_badpos;
-  __shared__ __align__(16) float s_cs[kRT * (DH + 4)];
+  __shared__ __align__(16) float s_cs[2][kRT * CSR];            // (cos, sin) per pair of the tile's rows
+  __shared__ __align__(16) float4 s_q[kRHeads][DH / 2];         // (qa, qb, qb, -qa) per pair
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
 
   pdl_trigger();  // the merge may launch: it waits for this grid before it reads
@@ -68,7 +112,6 @@ __global__ void __launch_bounds__(kRThreads, 1)
   const int g = lane >> 2, q4 = lane & 3;
   const int B = P.B, H = P.H;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  int* cons = reinterpret_cast<int*>(smem + 128);    // [16] warps done with each stage (all uses)
   int* issued = reinterpret_cast<int*>(smem + 256);  // [16] last tile issued into each stage
   int* pre = reinterpret_cast<int*>(smem + kRHeader);
 
@@ -78,7 +121,6 @@ __global__ void __launch_bounds__(kRThreads, 1)
     s_badpos = 0;
     for (int s = 0; s < P.stages; ++s) {
       mbar_init(&full[s], 1);
-      cons[s] = 0;
       issued[s] = -1;
     }
     fence_barrier_init();
@@ -128,8 +170,9 @@ __global__ void __launch_bounds__(kRThreads, 1)
 
   const int zseg0 = blockIdx.y * P.nsb;
   const uint32_t tx = static_cast<uint32_t>(2 * (DH / 64) * kRT * 128 + 2 * P.zt_bytes);
-  // the copies of tile (sequence b, rows t0 ..) into stage s (one thread)
-  auto issue = [&](int s, int j, const TileWalk& t) {
+  // the copies of tile j (sequence b, rows t0 ..) into its stage (one thread)
+  auto issue = [&](int j, const TileWalk& t) {
+    const int s = j % P.stages;
     unsigned char* ks = smem + P.off_kv + static_cast<size_t>(s) * P.stage_bytes;
     unsigned char* vs = ks + P.kv_bytes;
     unsigned char* zk = vs + P.kv_bytes;
@@ -148,210 +191,270 @@ __global__ void __launch_bounds__(kRThreads, 1)
   TileWalk ahead;
   bool ahead_more = walk_first(ahead, pre, B, g0, g1);
   for (int j = 0; j < P.stages && ahead_more; ++j) {
-    if (tid == 0) issue(j, j, ahead);
+    if (tid == 0) issue(j, ahead);
     ahead_more = walk_next(ahead, pre, B, g1, kRT);
   }
-  {
-    // ================================================ consumers: head h ====
-    const int h = blockIdx.y * kRHeads + warp;
-    // B_h^K as the B operand of K = Z_h B_h^T (k = latent column, n = head
-    // dim): lane (g, q4) holds B_h[8 n + g][16 kk + 2 q4 (+1)] and [.. + 8 (+9)]
-    uint32_t bf[NT][KS][2];
-    {
-      const __nv_bfloat16* bk = static_cast<const __nv_bfloat16*>(P.b_k) + static_cast<size_t>(h) * DH * R;
+
+  // ---- 2. the gather's roles: token tid / 16 of a tile, pairs NP (tid % 16) ..
+  const int gt = tid >> 4, gk = NP * (tid & 15);
+  int gaxis[NP];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+  for (int u = 0; u < NP; ++u) gaxis[u] = A.ax.axis(gk + u);
+  auto positions_of = [&](const TileWalk& t, int (&pos)[NP]) {
+    const bool there = t.t0 + gt < t.t_end;
+    const int32_t* row = A.positions + (static_cast<size_t>(t.b) * P.max_len + t.t0 + gt) * A.ax.n;
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          const __nv_bfloat16* row = bk + (8 * n + g) * R + 16 * kk + 2 * q4;
-          bf[n][kk][0] = *reinterpret_cast<const uint32_t*>(row);
-          bf[n][kk][1] = *reinterpret_cast<const uint32_t*>(row + 8);
-        }
+    for (int u = 0; u < NP; ++u) pos[u] = there ? __ldg(row + gaxis[u]) : 0;
+  };
+  auto entries_of = [&](const int (&pos)[NP], float2 (&cs)[NP]) {
+#pragma unroll
+    for (int u = 0; u < NP; ++u) {
+      const int p = min(max(pos[u], 0), P.rope_max_pos - 1);
+      if (p != pos[u]) *reinterpret_cast<volatile int*>(&s_badpos) = 1;
+      cs[u] = __ldg(reinterpret_cast<const float2*>(P.rope_cs + static_cast<size_t>(p) * DH + 2 * (gk + u)));
     }
-    const int zoff = (warp / P.hs) * (kRT * segrow) + (warp % P.hs) * R * 2;  // this head in a latent tile
-    // value columns of this lane: shared d0 .. d0 + CW - 1, private lane (+ 32)
-    const int d0 = CW * lane;
-    const int vcb = d0 >> 6, vch = (d0 & 63) >> 3, voff = (d0 & 7) * 2;
+  };
+  auto put = [&](int buf, const float2 (&cs)[NP]) {
+#pragma unroll
+    for (int u = 0; u < NP; u += 2)
+      *reinterpret_cast<float4*>(&s_cs[buf][gt * CSR + 2 * (gk + u)]) =
+          make_float4(cs[u].x, cs[u].y, cs[u + 1].x, cs[u + 1].y);
+  };
 
-    TileWalk w;
-    bool more = walk_first(w, pre, B, g0, g1);
-    bool ok = true, waited = false;
-    int cur_b = -1;
-    float m = -INFINITY, l = 0.f;
-    float os[CW], oz[2] = {0.f, 0.f};
+  // ---- 3. this warp's head ------------------------------------------------------
+  const int h = blockIdx.y * kRHeads + warp;
+  // B_h^K as the B operand of K = Z_h B_h^T (k = latent column, n = head
+  // dim): lane (g, q4) holds B_h[8 n + g][16 kk + 2 q4 (+1)] and [.. + 8 (+9)]
+  uint32_t bf[NT][KS][2];
+  {
+    const __nv_bfloat16* bk = static_cast<const __nv_bfloat16*>(P.b_k) + static_cast<size_t>(h) * DH * R;
 #pragma unroll
-    for (int e = 0; e < CW; ++e) os[e] = 0.f;
-    uint32_t qv[NT];  // q~ of head h: columns 8 n + 2 q4, + 1 (bf16 pairs)
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        const __nv_bfloat16* row = bk + (8 * n + g) * R + 16 * kk + 2 * q4;
+        bf[n][kk][0] = *reinterpret_cast<const uint32_t*>(row);
+        bf[n][kk][1] = *reinterpret_cast<const uint32_t*>(row + 8);
+      }
+  }
+  const int zoff = (warp / P.hs) * (kRT * segrow) + (warp % P.hs) * R * 2;  // this head in a latent tile
+  const int trow = (lane & 7) + 8 * (lane >> 4), tcol = (lane >> 3) & 1;    // transposed A operand (values)
 
-    // this head's partial of sequence b: (m, l) and the unnormalised
-    // [O_s | O_z] at slot b + c (the merge takes every CTA's)
-    auto write_partial = [&](int b) {
-      if (!waited) {
-        pdl_wait();  // the launch before may still read the workspace
-        waited = true;
+  // tiles j (w), j + 2 (table entries) and j + 3 (positions)
+  TileWalk w, wt;
+  bool more = walk_first(w, pre, B, g0, g1);
+  float2 cs[NP];
+  int pos[NP];
+  int known = 0;  // tiles seen ahead: cs holds tile 1's entries, pos tile 2's positions
+  {
+    wt = w;
+    positions_of(wt, pos);
+    entries_of(pos, cs);
+    put(0, cs);
+    if (walk_next(wt, pre, B, g1, kRT)) {
+      known = 1;
+      positions_of(wt, pos);
+      entries_of(pos, cs);
+      if (walk_next(wt, pre, B, g1, kRT)) {
+        known = 2;
+        positions_of(wt, pos);
       }
-      const size_t slot = static_cast<size_t>(b + c);
-      if (lane == 0) {
-        float* pml = P.part_ml + (slot * H + h) * 2;
-        pml[0] = m;
-        pml[1] = l;
-      }
-      float* o = P.part_acc + (slot * H + h) * (DH + R);
-#pragma unroll
-      for (int e = 0; e < CW; ++e) o[d0 + e] = os[e];
-      if (lane < R) o[DH + lane] = oz[0];
-      if (lane + 32 < R) o[DH + lane + 32] = oz[1];
-    };
+    }
+  }
+  bool ok = true, waited = false;
+  int cur_b = -1;
+  float m = -INFINITY, l = 0.f;
+  // O_s^T and O_z^T: rows as in the accumulator layout, column 0 (lanes q4 = 0)
+  // the high parts' sum, column 1 the low parts'
+  float os[MV][4], oz[MZ][4];
 
-    for (int j = 0; more; ++j) {
-      if (w.b != cur_b) {
-        if (cur_b >= 0) write_partial(cur_b);
-        cur_b = w.b;
-        m = -INFINITY;
-        l = 0.f;
+  // this head's partial of sequence b: (m, l) and the unnormalised
+  // [O_s | O_z] at slot b + c (the merge takes every CTA's)
+  auto write_partial = [&](int b) {
+    if (!waited) {
+      pdl_wait();  // the launch before may still read the workspace
+      waited = true;
+    }
+    const size_t slot = static_cast<size_t>(b + c);
+    if (lane == 0) {
+      float* pml = P.part_ml + (slot * H + h) * 2;
+      pml[0] = m;
+      pml[1] = l;
+    }
+    float* o = P.part_acc + (slot * H + h) * (DH + R);
+    if (q4 == 0) {
 #pragma unroll
-        for (int e = 0; e < CW; ++e) os[e] = 0.f;
-        oz[0] = oz[1] = 0.f;
-        const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(P.q) + (static_cast<size_t>(w.b) * H + h) * DH;
+      for (int e = 0; e < MV; ++e) {
+        o[16 * e + g] = os[e][0] + os[e][1];
+        o[16 * e + g + 8] = os[e][2] + os[e][3];
+      }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) qv[n] = *reinterpret_cast<const uint32_t*>(qh + 8 * n + 2 * q4);
+      for (int e = 0; e < MZ; ++e) {
+        o[DH + 16 * e + g] = oz[e][0] + oz[e][1];
+        o[DH + 16 * e + g + 8] = oz[e][2] + oz[e][3];
       }
-      const int s = j % P.stages;
-      const int nvalid = min(kRT, w.t_end - w.t0);
-      // the tile's rotations: pair k of token i at cs[i][2 k]
-      __syncthreads();  // the previous tile's readers are done
-      for (int e = tid; e < kRT * (DH / 2); e += kRThreads) {
-        const int i = e / (DH / 2), k = e % (DH / 2);
-        float2 v = make_float2(1.f, 0.f);
-        if (i < nvalid) {
-          int pos = A.positions[(static_cast<size_t>(w.b) * P.max_len + w.t0 + i) * A.ax.n + A.ax.axis(k)];
-          if (pos < 0 || pos >= P.rope_max_pos) {
-            *reinterpret_cast<volatile int*>(&s_badpos) = 1;
-            pos = min(max(pos, 0), P.rope_max_pos - 1);
-          }
-          v = *reinterpret_cast<const float2*>(P.rope_cs + static_cast<size_t>(pos) * DH + 2 * k);
-        }
-        *reinterpret_cast<float2*>(s_cs + i * (DH + 4) + 2 * k) = v;
+    }
+  };
+
+  __syncthreads();  // the first tile's rotations
+  for (int j = 0; more; ++j) {
+    // rotations ahead: tile j + 1's into the other buffer, j + 2's entries, j + 3's positions
+    if (known >= 1) put((j + 1) & 1, cs);
+    if (known >= 2) {
+      entries_of(pos, cs);
+      known = walk_next(wt, pre, B, g1, kRT) ? 2 : 1;
+      if (known == 2) positions_of(wt, pos);
+    } else {
+      known = 0;
+    }
+    if (w.b != cur_b) {
+      if (cur_b >= 0) write_partial(cur_b);
+      cur_b = w.b;
+      m = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < MV; ++e) os[e][0] = os[e][1] = os[e][2] = os[e][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < MZ; ++e) oz[e][0] = oz[e][1] = oz[e][2] = oz[e][3] = 0.f;
+      const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(P.q) + (static_cast<size_t>(w.b) * H + h) * DH;
+      __syncwarp();
+      for (int k = lane; k < DH / 2; k += 32) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(qh + 2 * k);
+        s_q[warp][k] = make_float4(bf_lo(v), bf_hi(v), bf_hi(v), -bf_lo(v));
       }
-      __syncthreads();
-      if (ok && *reinterpret_cast<volatile int*>(&s_timeout)) ok = false;  // another warp gave up
-      if (ok) {
-        ok = mbar_wait_bounded(&full[s], static_cast<uint32_t>(j / P.stages) & 1u, P.wait_limit);
-        if (!ok) *reinterpret_cast<volatile int*>(&s_timeout) = 1;
-      }
-      if (ok) {
-        const unsigned char* ks = smem + P.off_kv + static_cast<size_t>(s) * P.stage_bytes;
-        const unsigned char* vs = ks + P.kv_bytes;
-        const unsigned char* zk = vs + P.kv_bytes;
-        const unsigned char* zv = zk + P.zt_bytes;
-        // ---- rebuilt, rotated key . q~ : tokens g (part0) and g + 8 (part1) ----
-        uint32_t a[KS][4];
+      __syncwarp();
+    }
+    const int s = j % P.stages;
+    const int nvalid = min(kRT, w.t_end - w.t0);
+    ok = ok && !*reinterpret_cast<volatile int*>(&s_timeout) &&
+         mbar_wait_bounded(&full[s], static_cast<uint32_t>(j / P.stages) & 1u, P.wait_limit);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      *reinterpret_cast<volatile int*>(&s_timeout) = 1;
+    } else {
+      const unsigned char* ks = smem + P.off_kv + static_cast<size_t>(s) * P.stage_bytes;
+      const unsigned char* vs = ks + P.kv_bytes;
+      const unsigned char* zk = vs + P.kv_bytes;
+      const unsigned char* zv = zk + P.zt_bytes;
+      // ---- rebuilt key . turned query: tokens g and g + 8 ----
+      uint32_t a[KS][4];
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk)
+        ldsm_x4(a[kk][0], a[kk][1], a[kk][2], a[kk][3],
+                zk + zoff + (lane & 15) * segrow + (16 * kk + 8 * (lane >> 4)) * 2);
+      const float* cs0 = &s_cs[j & 1][g * CSR + 2 * q4];
+      const float* cs1 = cs0 + 8 * CSR;
+      const ulonglong2* qp = reinterpret_cast<const ulonglong2*>(&s_q[warp][q4]);
+      uint64_t part0 = 0ull, part1 = 0ull;  // even and odd coordinates' sums
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += 4) {
+        float acc[4][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk)
-          ldsm_x4(a[kk][0], a[kk][1], a[kk][2], a[kk][3],
-                  zk + zoff + (lane & 15) * segrow + (16 * kk + 8 * (lane >> 4)) * 2);
-        const float* cs0 = s_cs + g * (DH + 4);
-        const float* cs1 = cs0 + 8 * (DH + 4);
-        float part0 = 0.f, part1 = 0.f;
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += 4) {
-          float acc[4][4];
+          for (int u = 0; u < 4; ++u)
+            mma_bf16_16816(acc[u], a[kk][0], a[kk][1], a[kk][2], a[kk][3], bf[n0 + u][kk][0], bf[n0 + u][kk][1]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-              mma_bf16_16816(acc[u], a[kk][0], a[kk][1], a[kk][2], a[kk][3], bf[n0 + u][kk][0], bf[n0 + u][kk][1]);
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int n = n0 + u, d = 8 * n + 2 * q4;
-            const unsigned char* kb = ks + (d >> 6) * (kRT * 128);
-            const uint32_t s0 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g, (d & 63) >> 3, 128) + 4 * q4);
-            const uint32_t s1 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g + 8, (d & 63) >> 3, 128) + 4 * q4);
-            const float2 c0 = *reinterpret_cast<const float2*>(cs0 + d);  // (cos, sin) of pair d / 2
-            const float2 c1 = *reinterpret_cast<const float2*>(cs1 + d);
-            const float x0 = acc[u][0] + bf_lo(s0), x1 = acc[u][1] + bf_hi(s0);
-            const float y0 = acc[u][2] + bf_lo(s1), y1 = acc[u][3] + bf_hi(s1);
-            const float qa = bf_lo(qv[n]), qb = bf_hi(qv[n]);
-            part0 = fmaf(qa, fmaf(x0, c0.x, -x1 * c0.y), fmaf(qb, fmaf(x0, c0.y, x1 * c0.x), part0));
-            part1 = fmaf(qa, fmaf(y0, c1.x, -y1 * c1.y), fmaf(qb, fmaf(y0, c1.y, y1 * c1.x), part1));
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int n = n0 + u, d = 8 * n + 2 * q4;
+          const unsigned char* kb = ks + (d >> 6) * (kRT * 128);
+          const uint32_t s0 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g, (d & 63) >> 3, 128) + 4 * q4);
+          const uint32_t s1 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g + 8, (d & 63) >> 3, 128) + 4 * q4);
+          const float2 c0 = *reinterpret_cast<const float2*>(cs0 + 8 * n);  // (cos, sin) of pair d / 2
+          const float2 c1 = *reinterpret_cast<const float2*>(cs1 + 8 * n);
+          const ulonglong2 qv = qp[4 * n];  // (qa, qb), (qb, -qa)
+          const uint64_t x = add2(pair(acc[u][0], acc[u][1]), pair(bf_lo(s0), bf_hi(s0)));
+          const uint64_t y = add2(pair(acc[u][2], acc[u][3]), pair(bf_lo(s1), bf_hi(s1)));
+          part0 = fma2(x, fma2(pair(c0.x, c0.x), qv.x, mul2(pair(c0.y, c0.y), qv.y)), part0);
+          part1 = fma2(y, fma2(pair(c1.x, c1.x), qv.x, mul2(pair(c1.y, c1.y), qv.y)), part1);
         }
-        part0 += __shfl_xor_sync(0xffffffffu, part0, 1);
-        part0 += __shfl_xor_sync(0xffffffffu, part0, 2);
-        part1 += __shfl_xor_sync(0xffffffffu, part1, 1);
-        part1 += __shfl_xor_sync(0xffffffffu, part1, 2);
-        // ---- one online softmax over the tile (log2 domain) ----
-        const float sc0 = g < nvalid ? part0 * P.scale_log2 : -INFINITY;
-        const float sc1 = g + 8 < nvalid ? part1 * P.scale_log2 : -INFINITY;
-        if (P.scores && q4 == 0) {
-          if (!waited) {
-            pdl_wait();  // the launch before may still read the workspace
-            waited = true;
-          }
-          float* srow = P.scores + (static_cast<size_t>(w.b) * H + h) * P.max_len + w.t0;
-          if (g < nvalid) srow[g] = sc0;
-          if (g + 8 < nvalid) srow[g + 8] = sc1;
-        }
-        float mx = fmaxf(sc0, sc1);
-#pragma unroll
-        for (int o2 = 4; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-        const float mn = fmaxf(m, mx);
-        const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float p0 = exp2f(sc0 - mn), p1 = exp2f(sc1 - mn);
-        float ps = p0 + p1;
-#pragma unroll
-        for (int o2 = 4; o2 < 32; o2 <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o2);
-        l = fmaf(l, alpha, ps);
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < CW; ++e) os[e] *= alpha;
-        oz[0] *= alpha;
-        oz[1] *= alpha;
-        // ---- values, unrotated: rows of the history only (rows past it may hold anything) ----
-        const unsigned char* vb = vs + vcb * (kRT * 128);
-        const unsigned char* zvh = zv + zoff;
-        for (int t = 0; t < nvalid; ++t) {
-          const float pt = __shfl_sync(0xffffffffu, t < 8 ? p0 : p1, (t & 7) * 4);
-          const unsigned char* vrow = vb + swz_off(t, vch, 128) + voff;
-          if constexpr (CW == 4) {
-            const uint2 v = *reinterpret_cast<const uint2*>(vrow);
-            os[0] = fmaf(pt, bf_lo(v.x), os[0]);
-            os[1] = fmaf(pt, bf_hi(v.x), os[1]);
-            os[2] = fmaf(pt, bf_lo(v.y), os[2]);
-            os[3] = fmaf(pt, bf_hi(v.y), os[3]);
-          } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(vrow);
-            os[0] = fmaf(pt, bf_lo(v), os[0]);
-            os[1] = fmaf(pt, bf_hi(v), os[1]);
-          }
-          const __nv_bfloat16* zr = reinterpret_cast<const __nv_bfloat16*>(zvh + t * segrow);
-          if (lane < R) oz[0] = fmaf(pt, __bfloat162float(zr[lane]), oz[0]);
-          if (lane + 32 < R) oz[1] = fmaf(pt, __bfloat162float(zr[lane + 32]), oz[1]);
-        }
-        // the stage is free once all eight heads are done with it: the last
-        // warp to finish refills it with the tile `stages` ahead (a warp
-        // counts only after it saw the stage's copy land, so a refill never
-        // joins a pending phase)
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          __threadfence_block();
-          const bool last = (atomicAdd(&cons[s], 1) % kRHeads) == kRHeads - 1;
-          __threadfence_block();
-          if (last && ahead_more && !*reinterpret_cast<volatile int*>(&s_timeout)) {
-            fence_proxy_async_smem();
-            issue(s, j + P.stages, ahead);
-          }
-        }
-        __syncwarp();
       }
-      more = walk_next(w, pre, B, g1, kRT);
-      if (ahead_more) ahead_more = walk_next(ahead, pre, B, g1, kRT);
+      float e0, e1, f0, f1;
+      unpair(part0, e0, f0);
+      unpair(part1, e1, f1);
+      e0 += f0;
+      e1 += f1;
+      e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
+      e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
+      e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
+      e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
+      // ---- one online softmax over the tile (log2 domain) ----
+      const float sc0 = g < nvalid ? e0 * P.scale_log2 : -INFINITY;
+      const float sc1 = g + 8 < nvalid ? e1 * P.scale_log2 : -INFINITY;
+      if (P.scores && q4 == 0) {
+        if (!waited) {
+          pdl_wait();  // the launch before may still read the workspace
+          waited = true;
+        }
+        float* srow = P.scores + (static_cast<size_t>(w.b) * H + h) * P.max_len + w.t0;
+        if (g < nvalid) srow[g] = sc0;
+        if (g + 8 < nvalid) srow[g + 8] = sc1;
+      }
+      float mx = fmaxf(sc0, sc1);
+#pragma unroll
+      for (int o2 = 4; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+      if (mx > m + kRRescaleLog2) {  // (the same for every lane)
+        const float alpha = m == -INFINITY ? 0.f : exp2f(m - mx);
+        m = mx;
+        l *= alpha;
+#pragma unroll
+        for (int e = 0; e < MV; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) os[e][k] *= alpha;
+#pragma unroll
+        for (int e = 0; e < MZ; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) oz[e][k] *= alpha;
+      }
+      const float p0 = exp2f(sc0 - m), p1 = exp2f(sc1 - m);
+      l += p0 + p1;  // this lane's tokens; the lanes meet at the end of the piece
+      // P as the B operand: column 0 the bf16 high parts, column 1 the low parts
+      // (lanes g = 0 and 1 hold tokens 2 q4, 2 q4 + 1 and + 8)
+      uint32_t b0, b1;
+      {
+        const float ta = __shfl_sync(0xffffffffu, p0, 8 * q4), tb = __shfl_sync(0xffffffffu, p0, 8 * q4 + 4);
+        const float tc = __shfl_sync(0xffffffffu, p1, 8 * q4), td = __shfl_sync(0xffffffffu, p1, 8 * q4 + 4);
+        const uint32_t hi0 = pack_bf16(ta, tb), hi1 = pack_bf16(tc, td);
+        const uint32_t lo0 = pack_bf16(ta - bf_lo(hi0), tb - bf_hi(hi0));
+        const uint32_t lo1 = pack_bf16(tc - bf_lo(hi1), td - bf_hi(hi1));
+        b0 = g == 0 ? hi0 : g == 1 ? lo0 : 0u;
+        b1 = g == 0 ? hi1 : g == 1 ? lo1 : 0u;
+      }
+      // ---- values, unrotated: rows past the piece (which may hold anything)
+      // must not meet their zero probabilities as 0 x NaN ----
+      const uint32_t k0 = (2 * q4 < nvalid ? 0x0000ffffu : 0u) | (2 * q4 + 1 < nvalid ? 0xffff0000u : 0u);
+      const uint32_t k1 = (2 * q4 + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * q4 + 9 < nvalid ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int e = 0; e < MV; ++e) {
+        uint32_t v0, v1, v2, v3;
+        const int ch = 2 * e + tcol;  // 16-byte chunk along the head dim
+        ldsm_x4_trans(v0, v1, v2, v3, vs + (ch >> 3) * (kRT * 128) + swz_off(trow, ch & 7, 128));
+        mma_bf16_16816(os[e], v0 & k0, v1 & k0, v2 & k1, v3 & k1, b0, b1);
+      }
+#pragma unroll
+      for (int e = 0; e < MZ; ++e) {
+        uint32_t v0, v1, v2, v3;
+        ldsm_x4_trans(v0, v1, v2, v3, zv + zoff + trow * segrow + (16 * e + 8 * tcol) * 2);
+        mma_bf16_16816(oz[e], v0 & k0, v1 & k0, v2 & k1, v3 & k1, b0, b1);
+      }
     }
-    if (cur_b >= 0) write_partial(cur_b);
+    more = walk_next(w, pre, B, g1, kRT);
+    if (!more || w.b != cur_b) {  // the piece ends here: the lanes' denominators meet (each token on four lanes)
+#pragma unroll
+      for (int o2 = 4; o2 < 32; o2 <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+    }
+    // the tile's readers are done (its stage is refilled with the tile `stages`
+    // ahead) and the next tile's rotations are in place
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (ahead_more) {
+      if (tid == 0 && !*reinterpret_cast<volatile int*>(&s_timeout)) issue(j + P.stages, ahead);
+      ahead_more = walk_next(ahead, pre, B, g1, kRT);
+    }
   }
+  if (cur_b >= 0) write_partial(cur_b);
 
   // ---- every copy this CTA issued has landed before it exits ----
   __syncthreads();
@@ -367,7 +470,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
       P.meta[0] = N;
       P.meta[1] = G;
     }
-    *cta_status = (bad || *reinterpret_cast<volatile int*>(&s_badpos) ? kDevBounds : 0u) | (*reinterpret_cast<volatile int*>(&s_timeout) ? kDevTimeout : 0u);
+    *cta_status = (bad || *reinterpret_cast<volatile int*>(&s_badpos) ? kDevBounds : 0u) |
+                  (*reinterpret_cast<volatile int*>(&s_timeout) ? kDevTimeout : 0u);
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     pdl_wait();
@@ -436,7 +540,8 @@ lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_
   P.stage_bytes = round_up(2 * P.kv_bytes + 2 * P.zt_bytes, 1024);
   P.off_prefix = kRHeader;
   P.off_kv = round_up(kRHeader + (P.B + 1) * 4, 1024);
-  const int budget = 226 * 1024 - kRT * (P.dh + 4) * 4;  // less the static tables
+  // less the static tables: two tiles of rotations, the queries
+  const int budget = 226 * 1024 - 2 * kRT * (P.dh + 4) * 4 - kRHeads * (P.dh / 2) * 16;
   P.stages = std::min(kRMaxStages, (budget - P.off_kv - 1024) / P.stage_bytes);
   if (P.stages < 2) return LRKV_ERR_UNSUPPORTED;
   P.smem_bytes = P.off_kv + P.stages * P.stage_bytes + 1024;
