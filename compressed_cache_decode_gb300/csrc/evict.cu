@@ -13,6 +13,11 @@
 // k-th into the k-th.  That moves the fewest rows there can be, no row is both
 // read and written, and all moves run at once.
 //
+// Measured: 32 x 4097 rows to 4096 22 us a call (17 us of the selection's
+// dependent passes); 8 x 9-16K rows to 4096 95 us, 304 MB of moves at 4.7 TB/s
+// behind a 21 us selection; 256K rows to 32K 113 us, half of it the selection,
+// whose 16 CTAs spend most on the first counting pass and on the lists.
+//
 // 1. lrkv_evict_select_kernel, one cluster of CTAs per sequence: a radix
 //    selection (11 + 11 + 10 bits) of the order-preserving integer image of
 //    the weights finds the smallest kept value, each CTA counting its rows in
@@ -28,6 +33,8 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <map>
+#include <mutex>
 
 #include "decode_plan.h"
 #include "host_cache.h"
@@ -44,9 +51,11 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;          // 11 bits a level (the last level uses 1024)
-constexpr int kEvMaxCluster = 8;       // portable cluster size
+constexpr int kEvMaxCluster = 16;      // (more than 8 needs the kernel's opt-in)
 constexpr int kEvCacheRows = 40 * 1024;  // rows whose keys a CTA keeps in shared memory
+constexpr int kEvUnroll = 4;             // rows a thread has in flight per pass
 constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 4;             // rows a CTA moves at a time
 constexpr uint32_t kKeyHeld = 0xffffffffu;  // above every weight's key
 constexpr uint32_t kKeyOut = 0u;            // below every weight's key
 
@@ -86,6 +95,22 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Adds each lane's bin (where `on`) to a table in shared memory.  Weights tie
+// (rows nothing looked at), so the lanes that share the first one's bin are
+// added at once; the others add for themselves.  (Grouping all lanes by a
+// match instruction took longer than the additions it saved.)
+__device__ __forceinline__ void tally(int* hist, bool on, uint32_t bin) {
+  const unsigned active = __ballot_sync(0xffffffffu, on);
+  if (!active) return;
+  const int first = __ffs(active) - 1;
+  const uint32_t lead = __shfl_sync(0xffffffffu, bin, first);
+  const unsigned same = __ballot_sync(0xffffffffu, on && bin == lead);
+  if (on) {
+    if (bin != lead) atomicAdd(&hist[bin], 1);
+    else if ((threadIdx.x & 31) == first) atomicAdd(&hist[bin], __popc(same));
+  }
+}
+
 // Exclusive prefix over the CTA's warps of a per-warp count (the same value
 // on every lane of a warp); total receives the CTA's sum.
 __device__ __forceinline__ int warp_prefix(int count, int* s_warp, int& total) {
@@ -102,6 +127,18 @@ __device__ __forceinline__ int warp_prefix(int count, int* s_warp, int& total) {
   total = __shfl_sync(0xffffffffu, v, kEvWarps - 1);
   const int mine = __shfl_sync(0xffffffffu, v, warp);
   return mine - count;
+}
+
+// The cluster's values of one shared integer: lane c holds CTA c's (c < ncta,
+// at most 16), so that the remote reads are all in flight at once.
+__device__ __forceinline__ int from_cluster(const cg::cluster_group& cluster, int* value, int ncta) {
+  const int lane = threadIdx.x & 31;
+  return lane < ncta ? *cluster.map_shared_rank(value, lane) : 0;
+}
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // Physical cache row of logical row t (page * page_size + offset), or -1 when
@@ -122,6 +159,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   extern __shared__ uint32_t s_keys[];          // [rows_per_cta] when cached
   __shared__ int s_hist[3][kEvBins];            // one table per level: no level waits to clear another's
+  __shared__ int s_sum[kEvBins / 2];            // this CTA's share of a level's cluster-wide counts
   __shared__ int s_warp[kEvWarps];
   __shared__ int s_cta[4];                      // this CTA's max age + 1, held rows, equal rows, holes
   __shared__ int s_cta2;                        // ... moved rows
@@ -154,44 +192,58 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     return a < P.sink || a >= newest - P.recent;
   };
   auto key_of = [&](int t) -> uint32_t {
+    const uint32_t k = weight_key(w[t]);
     const bool hd = held(t);
-    if (among_held) return hd ? weight_key(w[t]) : kKeyOut;
-    return hd ? kKeyHeld : weight_key(w[t]);
+    return among_held ? (hd ? k : kKeyOut) : (hd ? kKeyHeld : k);
   };
   auto key_at = [&](int t) -> uint32_t { return P.cached ? s_keys[t - lo] : key_of(t); };
 
   if (!all) {
     if (age) {
       int m = 0;
-      for (int t = wlo + lane; t < whi; t += 32) m = max(m, age[t] + 1);
+      for (int t = wlo + lane; t < whi; t += 32 * kEvUnroll) {
+#pragma unroll
+        for (int u = 0; u < kEvUnroll; ++u)
+          if (t + 32 * u < whi) m = max(m, age[t + 32 * u] + 1);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (lane == 0) atomicMax(&s_cta[0], m);
       cluster.sync();
-      int all_max = 0;
-      for (int c = 0; c < ncta; ++c) all_max = max(all_max, *cluster.map_shared_rank(&s_cta[0], c));
-      newest = all_max;
+      newest = __reduce_max_sync(0xffffffffu, from_cluster(cluster, &s_cta[0], ncta));
     }
+    // keys, and the counts of their highest 11 bits
     int count = 0;
-    for (int t = wlo + lane; t < whi; t += 32) {
-      const uint32_t k = key_of(t);
-      if (P.cached) s_keys[t - lo] = k;
-      count += k == kKeyHeld;
+    for (int t = wlo + lane; t - lane < whi; t += 32 * kEvUnroll) {
+      uint32_t k[kEvUnroll];
+#pragma unroll
+      for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? key_of(t + 32 * u) : kKeyOut;
+#pragma unroll
+      for (int u = 0; u < kEvUnroll; ++u) {
+        if (t - lane + 32 * u >= whi) break;
+        if (P.cached && t + 32 * u < whi) s_keys[t + 32 * u - lo] = k[u];
+        count += k[u] == kKeyHeld;
+        tally(s_hist[0], k[u] != kKeyHeld && k[u] != kKeyOut, k[u] >> 21);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
     if (lane == 0) atomicAdd(&s_cta[1], count);
     cluster.sync();
-    int nheld = 0;
-    for (int c = 0; c < ncta; ++c) nheld += *cluster.map_shared_rank(&s_cta[1], c);
-    int need = n - nheld;
+    int need = n - warp_sum(from_cluster(cluster, &s_cta[1], ncta));
     if (need < 0) {
       among_held = true;
       need = n;
-      if (P.cached) {
-        for (int t = wlo + lane; t < whi; t += 32) s_keys[t - lo] = key_of(t);
-        __syncwarp();
+      // counted again over the held rows alone (every CTA has read the others' first counts)
+      cluster.sync();
+      for (int i = tid; i < kEvBins; i += kEvThreads) s_hist[0][i] = 0;
+      __syncthreads();
+      for (int t = wlo + lane; t - lane < whi; t += 32) {
+        const uint32_t k = t < whi ? key_of(t) : kKeyOut;
+        if (P.cached && t < whi) s_keys[t - lo] = k;
+        tally(s_hist[0], k != kKeyOut, k >> 21);
       }
+      cluster.sync();
     }
     if (need == 0) {
       threshold = kKeyHeld;  // exactly the held rows
@@ -203,26 +255,37 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
       for (int level = 0; level < 3; ++level) {
         const int bits = level < 2 ? 11 : 10, shift = 32 - width - bits;
         int* hist = s_hist[level];
-        for (int t = wlo + lane; t - lane < whi; t += 32) {
-          bool on = t < whi;
-          uint32_t k = 0;
-          if (on) {
-            k = key_at(t);
-            on = k != kKeyHeld && k != kKeyOut && (width == 0 || (k >> (32 - width)) == prefix);
+        if (level > 0) {
+          for (int t = wlo + lane; t - lane < whi; t += 32 * kEvUnroll) {
+            uint32_t k[kEvUnroll];
+#pragma unroll
+            for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? key_at(t + 32 * u) : kKeyOut;
+#pragma unroll
+            for (int u = 0; u < kEvUnroll; ++u) {
+              if (t - lane + 32 * u >= whi) break;
+              tally(hist, k[u] != kKeyHeld && k[u] != kKeyOut && (k[u] >> (32 - width)) == prefix,
+                    (k[u] >> shift) & ((1u << bits) - 1u));
+            }
           }
-          // one count per distinct bin of the warp (weights cluster in few bins)
-          const int bin = on ? static_cast<int>((k >> shift) & ((1u << bits) - 1u)) : -1;
-          const unsigned peers = __match_any_sync(0xffffffffu, bin);
-          if (on && lane == __ffs(peers) - 1) atomicAdd(&hist[bin], __popc(peers));
+          cluster.sync();
         }
-        cluster.sync();
         // bins from the top: thread i owns bins 2047 - 2 i and 2046 - 2 i
         const int b0 = kEvBins - 1 - 2 * tid, b1 = b0 - 1;
-        int c0 = 0, c1 = 0;
-        for (int c = 0; c < ncta; ++c) {
-          const int* other = cluster.map_shared_rank(hist, c);
-          c0 += other[b0];
-          c1 += other[b1];
+        int c0 = hist[b0], c1 = hist[b1];
+        if (ncta > 1) {
+          // CTA r adds up its share of the bins over the cluster, then every CTA
+          // reads the sums: 2 + 2 remote reads a thread, not 2 per CTA
+          const int share = kEvBins / ncta, part = kEvThreads / share;  // threads per bin (ncta / 2)
+          const int bin = rank * share + tid % share;
+          int sum = 0;
+          for (int c = tid / share; c < ncta; c += part) sum += cluster.map_shared_rank(hist, c)[bin];
+          if (tid < share) s_sum[tid] = 0;
+          __syncthreads();
+          if (part > 1) atomicAdd(&s_sum[tid % share], sum);
+          else s_sum[tid] = sum;
+          cluster.sync();
+          c0 = cluster.map_shared_rank(s_sum, b0 / share)[b0 % share];
+          c1 = cluster.map_shared_rank(s_sum, b1 / share)[b1 % share];
         }
         int v = c0 + c1;
 #pragma unroll
@@ -261,7 +324,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     eq_before = warp_prefix(eq, s_warp, total);
     if (tid == 0) s_cta[2] = total;
     cluster.sync();
-    for (int c = 0; c < rank; ++c) eq_before += *cluster.map_shared_rank(&s_cta[2], c);
+    const int v = from_cluster(cluster, &s_cta[2], ncta);
+    eq_before += warp_sum(lane < rank ? v : 0);
   }
   // walks this warp's rows in order: f(row, valid, kept mask of the 32 rows)
   auto walk = [&](auto f) {
@@ -301,15 +365,10 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     s_cta2 = move_total;
   }
   cluster.sync();
-  int moves = 0;
-  for (int c = 0; c < ncta; ++c) {
-    const int hc = *cluster.map_shared_rank(&s_cta[3], c), mc = *cluster.map_shared_rank(&s_cta2, c);
-    if (c < rank) {
-      hole_at += hc;
-      move_at += mc;
-    }
-    moves += mc;
-  }
+  const int holes_of = from_cluster(cluster, &s_cta[3], ncta), moves_of = from_cluster(cluster, &s_cta2, ncta);
+  const int moves = warp_sum(moves_of);
+  hole_at += warp_sum(lane < rank ? holes_of : 0);
+  move_at += warp_sum(lane < rank ? moves_of : 0);
   // ---- lists, and the rows that stay where they are
   const size_t row0 = static_cast<size_t>(b) * P.max_len;
   bool no_page = false;
@@ -350,8 +409,9 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   cluster.sync();
 }
 
-// One moved row per CTA turn: its 16-byte pieces across the four cache
-// tensors, up to four in flight per thread, then the per-row data.
+// Four moved rows per CTA turn: their 16-byte pieces across the four cache
+// tensors, eight in flight per thread (one row at a time kept too few bytes in
+// flight: 2.7 TB/s), and the per-row data by a thread each.
 // It lets no dependent start early: a decode launched next reads the cache at
 // once, before it waits for the launch before it.
 __global__ void __launch_bounds__(kMoveThreads) lrkv_evict_move_kernel(const EvictParams P) {
@@ -360,38 +420,67 @@ __global__ void __launch_bounds__(kMoveThreads) lrkv_evict_move_kernel(const Evi
   const int m = P.moves[b];
   const int n0 = P.n16[0], n1 = n0 + P.n16[1], n2 = n1 + P.n16[2], n3 = n2 + P.n16[3];
   const size_t row0 = static_cast<size_t>(b) * P.max_len;
-  for (int k = blockIdx.x; k < m; k += gridDim.x) {
-    const int2 from = P.src[static_cast<size_t>(b) * P.cap + k], to = P.dst[static_cast<size_t>(b) * P.cap + k];
-    if (from.y >= 0 && to.y >= 0) {
-      for (int i0 = tid; i0 < n3; i0 += 4 * kMoveThreads) {
-        uint4 v[4];
-        unsigned char* out[4];
+  const int2* src = P.src + static_cast<size_t>(b) * P.cap;
+  const int2* dst = P.dst + static_cast<size_t>(b) * P.cap;
+  for (int k0 = blockIdx.x * kMoveRows; k0 < m; k0 += gridDim.x * kMoveRows) {
+    const int rows = min(kMoveRows, m - k0);
+    int2 from[kMoveRows], to[kMoveRows];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = i0 + u * kMoveThreads;
-          if (i < n3) {
-            const int s = i < n0 ? 0 : i < n1 ? 1 : i < n2 ? 2 : 3;
-            const int p = i - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2);
-            const size_t width = static_cast<size_t>(P.n16[s]) * 16;
-            v[u] = *reinterpret_cast<const uint4*>(P.base[s] + from.y * width + 16 * static_cast<size_t>(p));
-            out[u] = P.base[s] + to.y * width + 16 * static_cast<size_t>(p);
-          }
+    for (int i = 0; i < kMoveRows; ++i) {
+      from[i] = to[i] = make_int2(-1, -1);
+      if (i < rows) {
+        from[i] = src[k0 + i];
+        to[i] = dst[k0 + i];
+      }
+    }
+    // piece p of a row, for every row: the same tensor and offset
+    for (int p0 = tid; p0 < n3; p0 += 2 * kMoveThreads) {
+      uint4 v[2][kMoveRows];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int p = p0 + u * kMoveThreads;
+        if (p < n3) {
+          const int s = p < n0 ? 0 : p < n1 ? 1 : p < n2 ? 2 : 3;
+          const size_t width = static_cast<size_t>(P.n16[s]) * 16;
+          const unsigned char* at = P.base[s] + 16 * static_cast<size_t>(p - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2));
+#pragma unroll
+          for (int i = 0; i < kMoveRows; ++i)
+            if (from[i].y >= 0 && to[i].y >= 0) v[u][i] = *reinterpret_cast<const uint4*>(at + from[i].y * width);
         }
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (i0 + u * kMoveThreads < n3) *reinterpret_cast<uint4*>(out[u]) = v[u];
+      for (int u = 0; u < 2; ++u) {
+        const int p = p0 + u * kMoveThreads;
+        if (p < n3) {
+          const int s = p < n0 ? 0 : p < n1 ? 1 : p < n2 ? 2 : 3;
+          const size_t width = static_cast<size_t>(P.n16[s]) * 16;
+          unsigned char* at = P.base[s] + 16 * static_cast<size_t>(p - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2));
+#pragma unroll
+          for (int i = 0; i < kMoveRows; ++i)
+            if (from[i].y >= 0 && to[i].y >= 0) *reinterpret_cast<uint4*>(at + to[i].y * width) = v[u][i];
+        }
       }
     }
     if (P.key_scale)
       for (int h = tid; h < P.H; h += kMoveThreads) {
         float* row = P.key_scale + (static_cast<size_t>(b) * P.H + h) * P.max_len;
-        row[to.x] = row[from.x];
+        float v[kMoveRows];
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i)
+          if (i < rows) v[i] = row[from[i].x];
+#pragma unroll
+        for (int i = 0; i < kMoveRows; ++i)
+          if (i < rows) row[to[i].x] = v[i];
       }
-    if (P.positions && tid < P.axes)
-      P.positions[(row0 + to.x) * P.axes + tid] = P.positions[(row0 + from.x) * P.axes + tid];
-    if (tid == 32) P.weights_out[row0 + to.x] = P.weights[row0 + from.x];
-    if (tid == 64 && P.order_out) P.order_out[row0 + to.x] = P.order ? P.order[row0 + from.x] : from.x;
-    if (tid == 96 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + to.x] = from.x;
+#pragma unroll
+    for (int i = 0; i < kMoveRows; ++i) {
+      if (i >= rows) break;
+      const int f = from[i].x, d = to[i].x;
+      if (P.positions && tid < P.axes) P.positions[(row0 + d) * P.axes + tid] = P.positions[(row0 + f) * P.axes + tid];
+      if (tid == 32) P.weights_out[row0 + d] = P.weights[row0 + f];
+      if (tid == 64 && P.order_out) P.order_out[row0 + d] = P.order ? P.order[row0 + f] : f;
+      if (tid == 96 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + d] = f;
+    }
   }
   if (blockIdx.x == 0 && b == 0 && tid < 32) {
     uint32_t bits = 0u;
@@ -433,6 +522,37 @@ size_t evict_layout(EvictParams& P, void* ws) {
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+constexpr int select_smem_max = kEvCacheRows * 4;
+
+// Whether a cluster of kEvMaxCluster selection CTAs (more than the portable 8:
+// the kernel's opt-in is set here) can run on the current device.
+bool wide_clusters_fit(int smem) {
+  static std::mutex mu;
+  static std::map<int, bool> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = known.find(dev);
+  if (it != known.end()) return it->second;
+  const void* select = reinterpret_cast<const void*>(&lrkv_evict_select_kernel);
+  int n = 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kEvMaxCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kEvMaxCluster);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool fits = ensure_kernel_smem(select, smem) == cudaSuccess &&
+                    cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, select, &cfg) == cudaSuccess && n >= 1;
+  known[dev] = fits;
+  return fits;
+}
 
 }  // namespace
 
@@ -501,16 +621,20 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   if (sms < 1) return LRKV_ERR_CUDA;
 
   // CTAs per sequence: more while the sequences leave SMs idle and a CTA has
-  // more than 8192 rows
+  // more than 6144 rows.  8 x 16K rows: 99 us with 2 CTAs each (8192 rows),
+  // 95 us with 4, 94 us with 8, 120 us with 16; 32 x 4.3K rows: 22.0 us with
+  // one, 24 us with 2 or 4 (the cluster's exchanges cost more than the passes).
   int ncta = 1;
-  while (ncta < kEvMaxCluster && 2LL * ncta * P.B <= sms && P.max_len > 8192 * ncta) ncta *= 2;
+  while (ncta < kEvMaxCluster && 2LL * ncta * P.B <= sms && P.max_len > 6144LL * ncta) ncta *= 2;
+  // 16 CTAs need an SM group that holds them all: asked once per device
+  if (ncta > 8 && !wide_clusters_fit(select_smem_max)) ncta = 8;
   const int step = 32 * kEvWarps;
   P.rows_per_cta = ((P.max_len + ncta - 1) / ncta + step - 1) / step * step;
   P.cached = P.rows_per_cta <= kEvCacheRows;
   const int smem = P.cached ? P.rows_per_cta * 4 : 0;
   const void* select = reinterpret_cast<const void*>(&lrkv_evict_select_kernel);
   // (the kernel's static tables count towards the 48 KB that need no attribute)
-  if (ensure_kernel_smem(select, kEvCacheRows * 4) != cudaSuccess) return LRKV_ERR_CUDA;
+  if (ensure_kernel_smem(select, select_smem_max) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -527,7 +651,8 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   if (cudaLaunchKernelEx(&cfg, lrkv_evict_select_kernel, P) != cudaSuccess) return LRKV_ERR_CUDA;
   // enough CTAs to fill the SMs eight times over, at least one per sequence
   const long long per_seq = std::max(1LL, (8LL * sms + P.B - 1) / P.B);
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1LL, std::min<long long>(P.cap, per_seq))), P.B);
+  const long long turns = (P.cap + kMoveRows - 1) / kMoveRows;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1LL, std::min(turns, per_seq))), P.B);
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
