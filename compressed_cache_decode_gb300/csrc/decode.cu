@@ -1052,8 +1052,9 @@ lrkv_status launch_all(const DecodePlan& P, cudaStream_t stream, cudaEvent_t ev_
 
 }  // namespace
 
-lrkv_status decode_make_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* ws_bytes) {
+lrkv_status decode_make_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* ws_bytes, bool weighted) {
   std::memset(&P, 0, sizeof(P));
+  P.weighted = weighted;
   P.B = d.batch; P.H = d.heads; P.dh = d.head_dim; P.r = d.rank; P.max_len = d.max_len;
   P.map_len = d.max_len; P.map_seqs = d.batch;  // contiguous cache (a paged call overrides)
   const float scale = d.scale > 0.f ? d.scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));

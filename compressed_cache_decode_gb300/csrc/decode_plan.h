@@ -112,6 +112,7 @@ struct DecodePlan {
   int map_len, map_seqs;
   float* out;
   float* lse;
+  int weighted;   // 1: planned for a weighted decode (the p table holds a third part)
   float* scores;  // [B][H][max_len] scaled scores (log2 domain) of a weighted decode, or NULL
   // full-RoPE decode: the cos/sin table [max_pos][dh] (pairs (cos, sin) per
   // frequency) and its staged tile ([16][cs_row] fp32 per ring stage)
@@ -120,7 +121,7 @@ struct DecodePlan {
 };
 
 // Fills everything but the operand pointers; returns the workspace size.
-lrkv_status decode_make_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* ws_bytes);
+lrkv_status decode_make_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* ws_bytes, bool weighted = false);
 lrkv_status key_scale_launch(const lrkv_dims& dm, float eps, int n_new, const void* k_s, const void* z_k,
                              const void* b_k, const int32_t* start_pos, float* key_scale, void* stream);
 lrkv_status step_append_launch(const lrkv_dims& dm, int d_model, const void* x, const void* w_sk,

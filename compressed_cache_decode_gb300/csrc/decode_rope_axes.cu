@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
   constexpr int MV = DH / 16;   // 16-row tiles of the shared values
   constexpr int MZ = R / 16;    // 16-row tiles of the private values
   constexpr int NP = DH / 32;   // pairs a thread gathers per tile (one token, 16 threads)
-  constexpr int CSR = DH + 4;   // floats per gathered row (padded)
+  constexpr int CSR = DH + 8;   // floats per gathered row (rows 8 banks apart: no conflicts)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ int s_timeout, s_badpos;
   __shared__ __align__(16) float s_cs[2][kRT * CSR];            // (cos, sin) per pair of the tile's rows
@@ -541,7 +541,7 @@ lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_
   P.off_prefix = kRHeader;
   P.off_kv = round_up(kRHeader + (P.B + 1) * 4, 1024);
   // less the static tables: two tiles of rotations, the queries
-  const int budget = 226 * 1024 - 2 * kRT * (P.dh + 4) * 4 - kRHeads * (P.dh / 2) * 16;
+  const int budget = 226 * 1024 - 2 * kRT * (P.dh + 8) * 4 - kRHeads * (P.dh / 2) * 16;
   P.stages = std::min(kRMaxStages, (budget - P.off_kv - 1024) / P.stage_bytes);
   if (P.stages < 2) return LRKV_ERR_UNSUPPORTED;
   P.smem_bytes = P.off_kv + P.stages * P.stage_bytes + 1024;

@@ -71,7 +71,7 @@ static lrkv_status stream_plan_impl(DecodePlan& P) {
     for (int h2 = 0; h2 < 2; ++h2)
       for (int n = 0; n < 32; ++n) P.zo[h2][n] = 0;
   }
-  P.pq_bytes = round_up(16 * dh * 2 + 16 * r * 4, 128);
+  P.pq_bytes = round_up(16 * dh * 2 + 16 * r * (P.weighted ? 6 : 4), 128);
   // absorb roles: 16 heads x r/4 column groups x bk_dsplit head-dim parts
   P.bk_dsplit = 1;
   while (r > 0 && 16 * (r / 4) * P.bk_dsplit * 2 <= kThreadsS && P.bk_dsplit * 2 <= dh / 4) P.bk_dsplit *= 2;

@@ -38,9 +38,9 @@
 // (log2 domain, fp32) at P.scores[b][h][row], from which the weights of the
 // rows are summed over the heads once the merge knows the log-sum-exp: 4 H
 // bytes a row beside 4 (d_h + H r) of cache, instead of a second pass over the
-// key half of the cache.  The outputs are held to fp32 accuracy then, so the
-// probabilities enter the value products as bf16 high + low parts (16 bits).
-// The plain scan rounds them once to bf16.
+// key half of the cache.  Its outputs are held to fp32 accuracy: p and the
+// probabilities enter their products as three bf16 parts (24 bits), where the
+// plain scan takes two of p and one of the probabilities.
 #pragma once
 
 #include <cuda.h>
@@ -221,16 +221,28 @@ __device__ __forceinline__ void bk_load(const DecodePlan& P, int m0, const BkRol
 // holds {hi(p[c]), hi(p[c+1])}, {lo(p[c]), lo(p[c+1])} (bf16 high parts and
 // the bf16 of what they leave), the same 8 bytes per column pair as the fp32
 // row would take: one 16-byte store of two entries.
-__device__ __forceinline__ void store_p_entries(float* prow, const float (&a)[4]) {
-  float h[4];
+// W: a third part, what the two leave, at word hl r/2 + c/2 of a second table
+// behind the 16 r words of the first.
+template <bool W>
+__device__ __forceinline__ void store_p_entries(float* table, int r, int hl, int c, const float (&a)[4]) {
+  float h[4], l[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) h[u] = __bfloat162float(__float2bfloat16_rn(a[u]));
-  *reinterpret_cast<uint4*>(prow) = make_uint4(pack_bf16(h[0], h[1]), pack_bf16(a[0] - h[0], a[1] - h[1]),
-                                               pack_bf16(h[2], h[3]), pack_bf16(a[2] - h[2], a[3] - h[3]));
+  for (int u = 0; u < 4; ++u) {
+    h[u] = __bfloat162float(__float2bfloat16_rn(a[u]));
+    l[u] = a[u] - h[u];
+  }
+  *reinterpret_cast<uint4*>(table + hl * r + c) =
+      make_uint4(pack_bf16(h[0], h[1]), pack_bf16(l[0], l[1]), pack_bf16(h[2], h[3]), pack_bf16(l[2], l[3]));
+  if constexpr (W) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) l[u] -= __bfloat162float(__float2bfloat16_rn(l[u]));
+    *reinterpret_cast<uint2*>(table + 16 * r + (hl * r + c) / 2) = make_uint2(pack_bf16(l[0], l[1]), pack_bf16(l[2], l[3]));
+  }
 }
 
 // The same from a shared-memory copy of the row tile's B^K: head hl's
 // [dh][r] bf16 block at hl * bk_head_bytes, head-dim rows d = i bk_dsplit + dp.
+template <bool W>
 __device__ __forceinline__ void absorb_rows_smem(const DecodePlan& P, const BkRole& R,
                                                  const unsigned char* bks, const __nv_bfloat16* qa,
                                                  const __nv_bfloat16* qb, float* pa, float* pb) {
@@ -261,13 +273,14 @@ __device__ __forceinline__ void absorb_rows_smem(const DecodePlan& P, const BkRo
     }
   // heads past H get zero entries
   if (R.hl < 16 && R.dp == 0) {
-    store_p_entries(pa + R.hl * P.r + 4 * R.cg, aa);
-    if (pb) store_p_entries(pb + R.hl * P.r + 4 * R.cg, ab);
+    store_p_entries<W>(pa, P.r, R.hl, 4 * R.cg, aa);
+    if (pb) store_p_entries<W>(pb, P.r, R.hl, 4 * R.cg, ab);
   }
 }
 
 // p rows of up to two sequences (q rows qa, qb: [16][dh] bf16; p rows pa, pb:
 // [16][r] private-score table entries); v holds the first chunk of B^K already.
+template <bool W>
 __device__ __forceinline__ void absorb_rows(const DecodePlan& P, int m0, const BkRole& R, uint2 (&v)[kBkChunk],
                                             const __nv_bfloat16* qa, const __nv_bfloat16* qb, float* pa, float* pb) {
   float aa[4] = {0.f, 0.f, 0.f, 0.f}, ab[4] = {0.f, 0.f, 0.f, 0.f};
@@ -298,8 +311,8 @@ __device__ __forceinline__ void absorb_rows(const DecodePlan& P, int m0, const B
     }
   // heads past H get zero entries
   if (R.hl < 16 && R.dp == 0) {
-    store_p_entries(pa + R.hl * P.r + 4 * R.cg, aa);
-    if (pb) store_p_entries(pb + R.hl * P.r + 4 * R.cg, ab);
+    store_p_entries<W>(pa, P.r, R.hl, 4 * R.cg, aa);
+    if (pb) store_p_entries<W>(pb, P.r, R.hl, 4 * R.cg, ab);
   }
 }
 
@@ -600,10 +613,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     if (P.bk_stages > 0) {
       const bool bk_in = ok && mbar_wait_bounded(bkbar, 0u, P.wait_limit);  // drained before exit in any case
       ok = ok && bk_in;
-      absorb_rows_smem(P, bkr, smem + P.off_kv + static_cast<size_t>(first_burst) * P.stage_bytes, qa, qb2, pa,
+      absorb_rows_smem<W>(P, bkr, smem + P.off_kv + static_cast<size_t>(first_burst) * P.stage_bytes, qa, qb2, pa,
                        pb);
     } else {
-      absorb_rows(P, m0, bkr, bkv, qa, qb2, pa, pb);
+      absorb_rows<W>(P, m0, bkr, bkv, qa, qb2, pa, pb);
     }
     if (!ok) *reinterpret_cast<volatile int*>(&s_timeout) = 1;
   }
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     if (MZMAX > 0 && kp >= 2) {  // p of a third or later piece (the first two came before)
       uint2 v[kBkChunk];
       bk_load(P, m0, bkr, 0, v);
-      absorb_rows(P, m0, bkr, v, reinterpret_cast<const __nv_bfloat16*>(pqb), nullptr,
+      absorb_rows<W>(P, m0, bkr, v, reinterpret_cast<const __nv_bfloat16*>(pqb), nullptr,
                   reinterpret_cast<float*>(pqb + 16 * dh * 2), nullptr);
       named_sync(1, kThreadsS);  // p rows ready
     }
@@ -814,15 +827,22 @@ __global__ void __launch_bounds__(kThreadsS, 1)
           const unsigned char* z0 = zk + arow * zrow + ahalf * 16;
           const int* zoh = zo + 32 * hf;
           const uint2* pt = reinterpret_cast<const uint2*>(pqcur + 16 * dh * 2) + 4 * hf * r + q4;
+          [[maybe_unused]] const uint32_t* pt3 =
+              reinterpret_cast<const uint32_t*>(pqcur + 16 * dh * 2 + 16 * r * 4) + 4 * hf * r + q4;
           // (6 batches unrolled with the per-group values: measured faster than none
           // or all of them, which runs out of registers)
 #pragma unroll (PH ? 6 : 1)
           for (int kk = 0; kk < kst; kk += BS) {  // batches of BS steps (kst is even)
             uint32_t a[BS][4];
             uint2 f0[BS], f1[BS];
+            [[maybe_unused]] uint32_t t0[BS], t1[BS];
 #pragma unroll
             for (int u = 0; u < BS; ++u)
               if (kk + u < kst) {
+                if constexpr (W) {
+                  t0[u] = pt3[8 * (kk + u)];
+                  t1[u] = pt3[8 * (kk + u) + 4];
+                }
                 ldsm_x4(a[u][0], a[u][1], a[u][2], a[u][3], z0 + zoh[kk + u]);
                 f0[u] = pt[8 * (kk + u)];
                 f1[u] = pt[8 * (kk + u) + 4];
@@ -835,6 +855,9 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                 const uint32_t h1 = k1v ? f1[u].x : 0u, l1 = k1v ? f1[u].y : 0u;
                 mma_bf16_16816((u & 1) ? sb : sa, a[u][0], a[u][1], a[u][2], a[u][3], h0, h1);
                 mma_bf16_16816((u & 1) ? lb : la, a[u][0], a[u][1], a[u][2], a[u][3], l0, l1);
+                if constexpr (W)
+                  mma_bf16_16816((u & 1) ? lb : la, a[u][0], a[u][1], a[u][2], a[u][3], k0v ? t0[u] : 0u,
+                                 k1v ? t1[u] : 0u);
               }
           }
         }
@@ -894,11 +917,15 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         const uint32_t ph0 = pack_bf16(p0, p1), ph1 = pack_bf16(p2, p3);
         const uint32_t pb0 = movmatrix_trans(ph0);  // tokens 0-7
         const uint32_t pb1 = movmatrix_trans(ph1);  // tokens 8-15
-        // W: what the bf16 probabilities leave, as a second operand
-        uint32_t pl0 = 0u, pl1 = 0u;
+        // W: what the bf16 probabilities leave, as a second and a third operand
+        [[maybe_unused]] uint32_t pl0 = 0u, pl1 = 0u, pm0 = 0u, pm1 = 0u;
         if constexpr (W) {
-          pl0 = movmatrix_trans(pack_bf16(p0 - bf_lo(ph0), p1 - bf_hi(ph0)));
-          pl1 = movmatrix_trans(pack_bf16(p2 - bf_lo(ph1), p3 - bf_hi(ph1)));
+          const float r0 = p0 - bf_lo(ph0), r1 = p1 - bf_hi(ph0), r2 = p2 - bf_lo(ph1), r3 = p3 - bf_hi(ph1);
+          const uint32_t lo0 = pack_bf16(r0, r1), lo1 = pack_bf16(r2, r3);
+          pl0 = movmatrix_trans(lo0);
+          pl1 = movmatrix_trans(lo1);
+          pm0 = movmatrix_trans(pack_bf16(r0 - bf_lo(lo0), r1 - bf_hi(lo0)));
+          pm1 = movmatrix_trans(pack_bf16(r2 - bf_lo(lo1), r3 - bf_hi(lo1)));
         }
 
         // Values.  The A operands of tokens outside [lo, nvalid) meet zero
@@ -922,7 +949,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                 a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
               }
               mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
-              if constexpr (W) mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
+              if constexpr (W) {
+                mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
+                mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pm0, pm1);
+              }
             }
           }
           // private values, per head group: O_z,grp^T += Z_v,grp^T P^T with
@@ -933,7 +963,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
             for (int h = 0; h < 8; h += GH) {
               const bool own = g / GH == h / GH;
               const uint32_t b0 = own ? pb0 : 0u, b1 = own ? pb1 : 0u;
-              const uint32_t c0 = W && own ? pl0 : 0u, c1 = W && own ? pl1 : 0u;
+              [[maybe_unused]] const uint32_t c0 = own ? pl0 : 0u, c1 = own ? pl1 : 0u;
+              [[maybe_unused]] const uint32_t e0 = own ? pm0 : 0u, e1 = own ? pm1 : 0u;
               const unsigned char* zb = zvb + zhead[hb + h];
               uint32_t a[NZH][4];
 #pragma unroll
@@ -944,7 +975,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                   a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
                 }
                 mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
-                if constexpr (W) mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], c0, c1);
+                if constexpr (W) {
+                  mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], c0, c1);
+                  mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], e0, e1);
+                }
               }
             }
           } else if (MZMAX > 0) {
@@ -964,7 +998,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                     a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
                   }
                   mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
-                  if constexpr (W) mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
+                  if constexpr (W) {
+                    mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
+                    mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pm0, pm1);
+                  }
                 }
             }
           }

@@ -207,7 +207,7 @@ lrkv_status weighted_plan(const lrkv_dims* dims, lrkv::DecodePlan& P, size_t* sc
   int sms = 0;
   if ((st = current_sm_count(&sms)) != LRKV_OK) return st;
   size_t need = 0;
-  if ((st = lrkv::decode_make_plan(*dims, sms, P, &need)) != LRKV_OK) return st;
+  if ((st = lrkv::decode_make_plan(*dims, sms, P, &need, true)) != LRKV_OK) return st;
   if (!P.stream) return LRKV_ERR_UNSUPPORTED;  // the bf16 streaming scan leaves the scores
   *score_off = (need + 255) / 256 * 256;
   *bytes = *score_off + static_cast<size_t>(dims->batch) * dims->heads * dims->max_len * sizeof(float);
