@@ -9,21 +9,33 @@
 // query, and one online softmax per head runs over the rows; the values are
 // not rotated.  Pair k turns by positions[axis(k)] theta_k: its (cos, sin) is
 // entry k of the table's row of that position, so a row's rotation is gathered
-// from up to `axes` table rows.
+// from up to `axes` table rows.  Per pair
+//   q~ . (k D) = qa (x0 cos - x1 sin) + qb (x0 sin + x1 cos).
 //
-// Grid (range CTAs, groups of 8 heads), one warp per head (B_h's MMA fragments
-// live in its registers), 16-token tiles of k_s, v_s and the group's z_k, z_v
-// in a ring of TMA stages.  Per tile and warp: K = Z_h B_h^T on the tensor
-// cores (mma.sync, fp32 accumulation), plus the shared row, dotted with the
-// query turned back by the row's angles,
-//   q~ . (k D) = x0 (qa cos + qb sin) + x1 (qb cos - qa sin)   per pair,
-// three two-wide fp32 instructions; the values O^T += V^T p with the
-// probabilities as a bf16 high part in one column of the B operand and the low
-// part in the next, so that one MMA takes both.  The 16 rows' cos and sin are
-// gathered by the whole CTA into one of two shared buffers: the table entries
-// of tile j + 2 and the positions of tile j + 3 are loaded while tile j is
-// computed, since the two dependent loads' latency in every tile took most of
-// the time at first (4 x 32K rows, 32 heads: 950 us).
+// The cache's bytes bound it; the rebuild's d_h r multiply-adds per (row, head)
+// do so as well when the warps do them (the mma.sync form of this kernel took
+// 800 instructions per 16 rows and head, 495 us on 4 x 32K rows of 32 heads).
+// So K = Z_h B_h^T runs on tcgen05, 128 rows by d_h columns into one of four
+// TMEM accumulators, with a thread per row and half of the pairs behind it: the
+// thread keeps its row's cos, sin and shared part in registers for all heads
+// of the CTA and spends nine two-wide fp32 instructions on two pairs.  B_h's rows
+// are stored in the order x0, x0', x1, x1' of neighbouring pairs, so that two
+// pairs' halves lie side by side in TMEM.
+//
+// Grid (range CTAs, groups of 4 heads), 16 warps: warp 0 copies (TMA: k_s and
+// each head's z_k per 128 rows, v_s and z_v per 32 rows), warp 1 issues the
+// MMAs, warps 4-11 form the scores (TMEM lane quadrant x half of the pairs; they
+// take the registers that the other warps give up), warps 12-15 the softmax and
+// the values: each takes a quarter of the shared value
+// columns for the four heads and the latents of one head (mma.sync; the
+// probabilities as three bf16 parts in free columns of the B operand).
+//
+// Measured on 4 x 32K rows (32 heads, rank 48): 403 us, the cache at 2.2 TB/s,
+// 13.5K cycles a tile and CTA where its bytes need 4.6K.  What bounds it is the
+// score warps' latency: a tile's gather (positions, table entries, the exchange
+// through shared memory) takes 4.4K cycles in a row and a head's 32 pairs 1.4K
+// for ~220 instructions, with two such warps per scheduler and no registers left
+// to overlap them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -47,12 +59,29 @@ using namespace dec;
 
 namespace {
 
-constexpr int kRT = 16;                      // tokens per tile
-constexpr int kRHeads = 8;                   // heads per CTA, one consumer warp each
-constexpr int kRThreads = 32 * kRHeads;
-constexpr int kRHeader = 1024;               // barriers and stage records
-constexpr int kRMaxStages = 16;
+constexpr int kRT = 128;                     // rows of a tile (TMEM lanes)
+constexpr int kRSub = 32;                    // rows of a value copy
+constexpr int kRHeads = 4;                   // heads per CTA
+constexpr int kRScore = 8;                   // score warps
+constexpr int kRValue = 4;                   // value warps
+constexpr int kRThreads = 32 * (4 + kRScore + kRValue);
+// registers per thread after the split: 512 at most over the four warpgroups, 128 each at launch
+constexpr int kRRegsCopy = 56, kRRegsScore = 168, kRRegsValue = 120;
+static_assert(kRRegsCopy + 2 * kRRegsScore + kRRegsValue <= 512, "more registers than the block has");
+constexpr int kRAcc = 4;                     // TMEM accumulators
+constexpr int kRMaxZ = 4, kRMaxV = 8;        // ring depths (at most)
+constexpr int kRBox = 16384;                 // 128 rows x 64 columns
+constexpr int kRStage = 80;                  // bytes of a row of the gather's staging (64 and a pad)
 constexpr float kRRescaleLog2 = 8.f;         // raise the reference max only past 2^8
+
+struct AxesArgs {
+  RopeAxes ax;
+  int even;                  // 1: no section boundary splits pairs 2 i, 2 i + 1
+  const int32_t* positions;  // [B][max_len][axes]
+  int nz, nv;                // ring depths: latent boxes, value copies
+  int vt_bytes, zv_off;      // bytes of a value copy's slot; offset of its latents
+  int off_b, off_k, off_z, off_v, off_st, off_sc, off_q;  // shared memory
+};
 
 // Two fp32 values in one 64-bit register, for the two-wide fp32 instructions.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -82,11 +111,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-struct AxesArgs {
-  RopeAxes ax;
-  const int32_t* positions;  // [B][max_len][axes]
-};
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// 32 lanes x 16 columns of TMEM.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void bar_named(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 }  // namespace
 
@@ -95,36 +149,37 @@ __global__ void __launch_bounds__(kRThreads, 1)
     lrkv_decode_rope_axes_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_zk,
                                  const __grid_constant__ CUtensorMap tm_zv, const __grid_constant__ AxesArgs A) {
-  constexpr int NT = DH / 8;    // 8-column tiles of the rebuilt key
-  constexpr int KS = R / 16;    // 16-wide steps over a head's latents
-  constexpr int MV = DH / 16;   // 16-row tiles of the shared values
-  constexpr int MZ = R / 16;    // 16-row tiles of the private values
-  constexpr int NP = DH / 32;   // pairs a thread gathers per tile (one token, 16 threads)
-  constexpr int CSR = DH + 8;   // floats per gathered row (rows 8 banks apart: no conflicts)
+  constexpr int NB = DH / 64;        // 64-column boxes of a shared row
+  constexpr int HP = DH / 4;         // pairs of a score thread (half of the head's)
+  constexpr int MS = DH / 64;        // 16-row tiles of the shared values per value warp
+  constexpr int MZ = R / 16;         // 16-row tiles of a head's private values
+  constexpr uint32_t kTmemCols = kRAcc * DH;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ int s_timeout, s_badpos;
-  __shared__ __align__(16) float s_cs[2][kRT * CSR];            // (cos, sin) per pair of the tile's rows
-  __shared__ __align__(16) float4 s_q[kRHeads][DH / 2];         // (qa, qb, qb, -qa) per pair
+  __shared__ uint64_t kfull, kempty, zfull[kRMaxZ], zempty[kRMaxZ], vfull[kRMaxV], vempty[kRMaxV], accf[kRAcc],
+      acce[kRAcc], scf[2], sce[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_timeout, s_badpos, s_k, s_z, s_v, s_mma;  // copies and MMAs issued
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  volatile int* fail = &s_timeout;
 
   pdl_trigger();  // the merge may launch: it waits for this grid before it reads
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
-  const int B = P.B, H = P.H;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  int* issued = reinterpret_cast<int*>(smem + 256);  // [16] last tile issued into each stage
-  int* pre = reinterpret_cast<int*>(smem + kRHeader);
+  const int B = P.B, H = P.H, h0 = blockIdx.y * kRHeads;
+  int* pre = reinterpret_cast<int*>(smem);
 
-  // ---- 1. barriers, sequence starts (clamped lengths) ----------------------
+  // ---- 1. barriers, TMEM, sequence starts (clamped lengths), B_h -------------------
   if (tid == 0) {
-    s_timeout = 0;
-    s_badpos = 0;
-    for (int s = 0; s < P.stages; ++s) {
-      mbar_init(&full[s], 1);
-      issued[s] = -1;
-    }
+    mbar_init(&kfull, 1);
+    mbar_init(&kempty, kRScore);
+    for (int i = 0; i < kRMaxZ; ++i) { mbar_init(&zfull[i], 1); mbar_init(&zempty[i], 1); }
+    for (int i = 0; i < kRMaxV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], kRValue); }
+    for (int i = 0; i < kRAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], kRScore); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&scf[i], kRScore); mbar_init(&sce[i], kRValue); }
+    s_timeout = s_badpos = s_k = s_z = s_v = s_mma = 0;
     fence_barrier_init();
   }
+  if (warp == 1) tmem_alloc(&tmem_base, kTmemCols);
   int bad = 0;
   for (int b = tid; b < B; b += blockDim.x) {
     int L = P.seq_lens[b];
@@ -150,333 +205,485 @@ __global__ void __launch_bounds__(kRThreads, 1)
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
   const int N = pre[B];
   const int G = max(1, min(static_cast<int>(gridDim.x), (N + P.min_tokens - 1) / max(P.min_tokens, 1)));
-  uint32_t* cta_status = P.cta_status + blockIdx.y * gridDim.x + blockIdx.x;
-  if (N == 0 || static_cast<int>(blockIdx.x) >= G) {
-    pdl_wait();  // the launch before may still read the workspace
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      for (int b = tid; b <= B; b += blockDim.x) P.prefix[b] = pre[b];
-      if (tid == 0) { P.meta[0] = N; P.meta[1] = G; }
-    }
-    if (tid == 0) *cta_status = bad ? kDevBounds : 0u;
-    return;
-  }
   const int c = blockIdx.x;
-  const int g0 = static_cast<int>(static_cast<long long>(c) * N / G);
-  const int g1 = static_cast<int>(static_cast<long long>(c + 1) * N / G);
-  const int segrow = P.segp * 2;  // bytes per latent segment row
-
-  const int zseg0 = blockIdx.y * P.nsb;
-  const uint32_t tx = static_cast<uint32_t>(2 * (DH / 64) * kRT * 128 + 2 * P.zt_bytes);
-  // the copies of tile j (sequence b, rows t0 ..) into its stage (one thread)
-  auto issue = [&](int j, const TileWalk& t) {
-    const int s = j % P.stages;
-    unsigned char* ks = smem + P.off_kv + static_cast<size_t>(s) * P.stage_bytes;
-    unsigned char* vs = ks + P.kv_bytes;
-    unsigned char* zk = vs + P.kv_bytes;
-    unsigned char* zv = zk + P.zt_bytes;
-    mbar_arrive_expect_tx(&full[s], tx);
-#pragma unroll
-    for (int cb = 0; cb < DH / 64; ++cb) {
-      tma_load_3d(ks + cb * kRT * 128, &tm_k, cb * 64, t.t0, t.b, &full[s]);
-      tma_load_3d(vs + cb * kRT * 128, &tm_v, cb * 64, t.t0, t.b, &full[s]);
+  uint32_t* cta_status = P.cta_status + blockIdx.y * gridDim.x + blockIdx.x;
+  const bool work = N > 0 && c < G;
+  const int g0 = work ? static_cast<int>(static_cast<long long>(c) * N / G) : 0;
+  const int g1 = work ? static_cast<int>(static_cast<long long>(c + 1) * N / G) : 0;
+  if (work) {
+    // row n of head i's operand is B_h's row 4 (n / 4) + {0, 2, 1, 3}[n % 4] (the
+    // copy's 128-byte swizzle by hand)
+    const __nv_bfloat16* bk = static_cast<const __nv_bfloat16*>(P.b_k) + static_cast<size_t>(h0) * DH * R;
+    for (int e = tid; e < kRHeads * DH * (R / 8); e += kRThreads) {
+      const int ch = e % (R / 8), n = e / (R / 8) % DH, i = e / (R / 8) / DH;
+      const int d = (n & ~3) | ((n & 1) << 1) | ((n >> 1) & 1);
+      *reinterpret_cast<uint4*>(smem + A.off_b + (i * DH + n) * 128 + ((ch ^ (n & 7)) << 4)) =
+          *reinterpret_cast<const uint4*>(bk + (static_cast<size_t>(i) * DH + d) * R + 8 * ch);
     }
-    tma_load_4d(zk, &tm_zk, 0, t.t0, zseg0, t.b, &full[s]);
-    tma_load_4d(zv, &tm_zv, 0, t.t0, zseg0, t.b, &full[s]);
-    *reinterpret_cast<volatile int*>(&issued[s]) = j;
-  };
-  // the walk `stages` tiles ahead: the first stages' tiles go out now
-  TileWalk ahead;
-  bool ahead_more = walk_first(ahead, pre, B, g0, g1);
-  for (int j = 0; j < P.stages && ahead_more; ++j) {
-    if (tid == 0) issue(j, ahead);
-    ahead_more = walk_next(ahead, pre, B, g1, kRT);
+    fence_proxy_async_smem();  // read by the tensor core's own path
   }
+  __syncthreads();
 
-  // ---- 2. the gather's roles: token tid / 16 of a tile, pairs NP (tid % 16) ..
-  const int gt = tid >> 4, gk = NP * (tid & 15);
-  int gaxis[NP];
-#pragma unroll
-  for (int u = 0; u < NP; ++u) gaxis[u] = A.ax.axis(gk + u);
-  auto positions_of = [&](const TileWalk& t, int (&pos)[NP]) {
-    const bool there = t.t0 + gt < t.t_end;
-    const int32_t* row = A.positions + (static_cast<size_t>(t.b) * P.max_len + t.t0 + gt) * A.ax.n;
-#pragma unroll
-    for (int u = 0; u < NP; ++u) pos[u] = there ? __ldg(row + gaxis[u]) : 0;
-  };
-  auto entries_of = [&](const int (&pos)[NP], float2 (&cs)[NP]) {
-#pragma unroll
-    for (int u = 0; u < NP; ++u) {
-      const int p = min(max(pos[u], 0), P.rope_max_pos - 1);
-      if (p != pos[u]) *reinterpret_cast<volatile int*>(&s_badpos) = 1;
-      cs[u] = __ldg(reinterpret_cast<const float2*>(P.rope_cs + static_cast<size_t>(p) * DH + 2 * (gk + u)));
-    }
-  };
-  auto put = [&](int buf, const float2 (&cs)[NP]) {
-#pragma unroll
-    for (int u = 0; u < NP; u += 2)
-      *reinterpret_cast<float4*>(&s_cs[buf][gt * CSR + 2 * (gk + u)]) =
-          make_float4(cs[u].x, cs[u].y, cs[u + 1].x, cs[u + 1].y);
-  };
-
-  // ---- 3. this warp's head ------------------------------------------------------
-  const int h = blockIdx.y * kRHeads + warp;
-  // B_h^K as the B operand of K = Z_h B_h^T (k = latent column, n = head
-  // dim): lane (g, q4) holds B_h[8 n + g][16 kk + 2 q4 (+1)] and [.. + 8 (+9)]
-  uint32_t bf[NT][KS][2];
-  {
-    const __nv_bfloat16* bk = static_cast<const __nv_bfloat16*>(P.b_k) + static_cast<size_t>(h) * DH * R;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        const __nv_bfloat16* row = bk + (8 * n + g) * R + 16 * kk + 2 * q4;
-        bf[n][kk][0] = *reinterpret_cast<const uint32_t*>(row);
-        bf[n][kk][1] = *reinterpret_cast<const uint32_t*>(row + 8);
+  TileWalk w;
+  if (!work) {
+    // nothing to do
+  } else if (warp < 4) {
+    regs_down<kRRegsCopy>();
+    if (warp == 0 && lane == 0) {
+      // ---- copies: the keys' and the values' queues, whichever has a free slot ------
+      TileWalk kw, vw;
+      bool km = walk_first(kw, pre, B, g0, g1), vm = walk_first(vw, pre, B, g0, g1);
+      int kt = 0, ki = 0, zi = 0, vi = 0, vs = 0;  // tile, box within it (0: k_s), boxes, value copies, copy within a tile
+      long long idle = clock64();
+      while ((km || vm) && !*fail) {
+        bool did = false;
+        if (km) {
+          const int s = zi % A.nz;
+          if (ki == 0) {
+            if (kt < 1 || mbar_test(&kempty, static_cast<uint32_t>(kt - 1) & 1u)) {
+              mbar_arrive_expect_tx(&kfull, NB * kRBox);
+              for (int cb = 0; cb < NB; ++cb)
+                tma_load_3d(smem + A.off_k + cb * kRBox, &tm_k, 64 * cb, kw.t0, kw.b, &kfull);
+              s_k = ++kt;
+              ki = 1;
+              did = true;
+            }
+          } else if (zi < A.nz || mbar_test(&zempty[s], static_cast<uint32_t>(zi / A.nz - 1) & 1u)) {
+            mbar_arrive_expect_tx(&zfull[s], kRBox);
+            tma_load_4d(smem + A.off_z + s * kRBox, &tm_zk, 0, h0 + ki - 1, kw.t0, kw.b, &zfull[s]);
+            s_z = ++zi;
+            if (++ki > kRHeads) {
+              ki = 0;
+              km = walk_next(kw, pre, B, g1, kRT);
+            }
+            did = true;
+          }
+        }
+        if (vm) {
+          const int s = vi % A.nv;
+          if (vi < A.nv || mbar_test(&vempty[s], static_cast<uint32_t>(vi / A.nv - 1) & 1u)) {
+            unsigned char* dst = smem + A.off_v + s * A.vt_bytes;
+            mbar_arrive_expect_tx(&vfull[s], NB * kRSub * 128 + P.zt_bytes);
+            for (int cb = 0; cb < NB; ++cb)
+              tma_load_3d(dst + cb * kRSub * 128, &tm_v, 64 * cb, vw.t0 + vs * kRSub, vw.b, &vfull[s]);
+            tma_load_4d(dst + A.zv_off, &tm_zv, 0, vw.t0 + vs * kRSub, blockIdx.y * P.nsb, vw.b, &vfull[s]);
+            s_v = ++vi;
+            if (++vs * kRSub >= min(kRT, vw.t_end - vw.t0)) {  // copies with rows of the piece only
+              vs = 0;
+              vm = walk_next(vw, pre, B, g1, kRT);
+            }
+            did = true;
+          }
+        }
+        if (did) idle = clock64();
+        else if (clock64() - idle > P.wait_limit) *fail = 1;
       }
-  }
-  const int zoff = (warp / P.hs) * (kRT * segrow) + (warp % P.hs) * R * 2;  // this head in a latent tile
-  const int trow = (lane & 7) + 8 * (lane >> 4), tcol = (lane >> 3) & 1;    // transposed A operand (values)
-
-  // tiles j (w), j + 2 (table entries) and j + 3 (positions)
-  TileWalk w, wt;
-  bool more = walk_first(w, pre, B, g0, g1);
-  float2 cs[NP];
-  int pos[NP];
-  int known = 0;  // tiles seen ahead: cs holds tile 1's entries, pos tile 2's positions
-  {
-    wt = w;
-    positions_of(wt, pos);
-    entries_of(pos, cs);
-    put(0, cs);
-    if (walk_next(wt, pre, B, g1, kRT)) {
-      known = 1;
-      positions_of(wt, pos);
-      entries_of(pos, cs);
-      if (walk_next(wt, pre, B, g1, kRT)) {
-        known = 2;
-        positions_of(wt, pos);
+    } else if (warp == 1 && lane == 0) {
+      // ---- MMAs: K = Z_h B_h^T of (tile, head) u into accumulator u % 4 ---------------
+      constexpr uint32_t idesc = idesc_bf16(128, DH, 0, 0);
+      const uint64_t bd = smem_desc(smem_u32(smem + A.off_b), 16, 1024, 2);
+      const uint64_t zd = smem_desc(smem_u32(smem + A.off_z), 16, 1024, 2);
+      int u = 0;
+      bool ok = true;
+      for (bool more = walk_first(w, pre, B, g0, g1); more && ok && !*fail; more = walk_next(w, pre, B, g1, kRT))
+        for (int i = 0; i < kRHeads; ++i, ++u) {
+          const int s = u % A.nz, a = u % kRAcc;
+          ok = mbar_wait_bounded(&zfull[s], static_cast<uint32_t>(u / A.nz) & 1u, P.wait_limit) &&
+               (u < kRAcc || mbar_wait_bounded(&acce[a], static_cast<uint32_t>(u / kRAcc - 1) & 1u, P.wait_limit));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < R / 16; ++kk)
+            tc_mma_ss(tmem + a * DH, zd + static_cast<uint32_t>(s * (kRBox / 16)) + kk * 2,
+                      bd + static_cast<uint32_t>(i * DH * 8) + kk * 2, idesc, kk > 0 ? 1u : 0u);
+          tc_commit(&zempty[s]);
+          tc_commit(&accf[a]);
+          s_mma = u + 1;
+        }
+      if (!ok) *fail = 1;
+    }
+  } else if (warp < 4 + kRScore) {
+    regs_up<kRRegsScore>();
+    // ---- scores: row 32 quad + lane of the tile, pairs half HP .. + HP - 1 -------------
+    const int quad = warp & 3, half = (warp - 4) >> 2, row = 32 * quad + lane;
+    unsigned char* stage = smem + A.off_st + (warp - 4) * 32 * kRStage;
+    float* sq = reinterpret_cast<float*>(smem + A.off_q);              // [4][DH / 4][4]: qa qa' qb qb'
+    bool ok = true;
+    int cur_b = -1, j = 0, u = 0;
+    uint64_t cc[HP / 2], ss[HP / 2];  // cos and sin of pairs 2 i, 2 i + 1 of this thread's half
+    int pos[kMaxAxes];
+    auto positions_of = [&](const TileWalk& t) {
+      const int32_t* at = A.positions + (static_cast<size_t>(t.b) * P.max_len + t.t0 + row) * A.ax.n;
+      const bool there = t.t0 + row < t.t_end;
+#pragma unroll
+      for (int x = 0; x < kMaxAxes; ++x) pos[x] = there && x < A.ax.n ? __ldg(at + x) : 0;
+    };
+    bool more = walk_first(w, pre, B, g0, g1);
+    if (more) positions_of(w);
+    for (; more; ++j) {
+      if (w.b != cur_b) {
+        cur_b = w.b;
+        bar_named(1, 32 * kRScore);  // every score warp is done with the last query
+        const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(P.q) + (static_cast<size_t>(w.b) * H + h0) * DH;
+        for (int e = tid - 128; e < kRHeads * DH / 4; e += 32 * kRScore) {
+          const uint2 v = *reinterpret_cast<const uint2*>(qh + 4 * e);
+          const float qa = bf_lo(v.x), qb = bf_hi(v.x), ra = bf_lo(v.y), rb = bf_hi(v.y);
+          *reinterpret_cast<float4*>(sq + 4 * e) = make_float4(qa, ra, qb, rb);
+        }
+        bar_named(1, 32 * kRScore);
       }
-    }
-  }
-  bool ok = true, waited = false;
-  int cur_b = -1;
-  float m = -INFINITY, l = 0.f;
-  // O_s^T and O_z^T: rows as in the accumulator layout, column 0 (lanes q4 = 0)
-  // the high parts' sum, column 1 the low parts'
-  float os[MV][4], oz[MZ][4];
-
-  // this head's partial of sequence b: (m, l) and the unnormalised
-  // [O_s | O_z] at slot b + c (the merge takes every CTA's)
-  auto write_partial = [&](int b) {
-    if (!waited) {
-      pdl_wait();  // the launch before may still read the workspace
-      waited = true;
-    }
-    const size_t slot = static_cast<size_t>(b + c);
-    if (lane == 0) {
-      float* pml = P.part_ml + (slot * H + h) * 2;
-      pml[0] = m;
-      pml[1] = l;
-    }
-    float* o = P.part_acc + (slot * H + h) * (DH + R);
-    if (q4 == 0) {
+      // the rotations, 8 pairs of the warp's 32 rows at a time: 4 lanes load a row's
+      // 64 bytes, the row's own lane takes them from shared memory
 #pragma unroll
-      for (int e = 0; e < MV; ++e) {
-        o[16 * e + g] = os[e][0] + os[e][1];
-        o[16 * e + g + 8] = os[e][2] + os[e][3];
-      }
-#pragma unroll
-      for (int e = 0; e < MZ; ++e) {
-        o[DH + 16 * e + g] = oz[e][0] + oz[e][1];
-        o[DH + 16 * e + g + 8] = oz[e][2] + oz[e][3];
-      }
-    }
-  };
-
-  __syncthreads();  // the first tile's rotations
-  for (int j = 0; more; ++j) {
-    // rotations ahead: tile j + 1's into the other buffer, j + 2's entries, j + 3's positions
-    if (known >= 1) put((j + 1) & 1, cs);
-    if (known >= 2) {
-      entries_of(pos, cs);
-      known = walk_next(wt, pre, B, g1, kRT) ? 2 : 1;
-      if (known == 2) positions_of(wt, pos);
-    } else {
-      known = 0;
-    }
-    if (w.b != cur_b) {
-      if (cur_b >= 0) write_partial(cur_b);
-      cur_b = w.b;
-      m = -INFINITY;
-      l = 0.f;
-#pragma unroll
-      for (int e = 0; e < MV; ++e) os[e][0] = os[e][1] = os[e][2] = os[e][3] = 0.f;
-#pragma unroll
-      for (int e = 0; e < MZ; ++e) oz[e][0] = oz[e][1] = oz[e][2] = oz[e][3] = 0.f;
-      const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(P.q) + (static_cast<size_t>(w.b) * H + h) * DH;
-      __syncwarp();
-      for (int k = lane; k < DH / 2; k += 32) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(qh + 2 * k);
-        s_q[warp][k] = make_float4(bf_lo(v), bf_hi(v), bf_hi(v), -bf_lo(v));
-      }
-      __syncwarp();
-    }
-    const int s = j % P.stages;
-    const int nvalid = min(kRT, w.t_end - w.t0);
-    ok = ok && !*reinterpret_cast<volatile int*>(&s_timeout) &&
-         mbar_wait_bounded(&full[s], static_cast<uint32_t>(j / P.stages) & 1u, P.wait_limit);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) {
-      *reinterpret_cast<volatile int*>(&s_timeout) = 1;
-    } else {
-      const unsigned char* ks = smem + P.off_kv + static_cast<size_t>(s) * P.stage_bytes;
-      const unsigned char* vs = ks + P.kv_bytes;
-      const unsigned char* zk = vs + P.kv_bytes;
-      const unsigned char* zv = zk + P.zt_bytes;
-      // ---- rebuilt key . turned query: tokens g and g + 8 ----
-      uint32_t a[KS][4];
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk)
-        ldsm_x4(a[kk][0], a[kk][1], a[kk][2], a[kk][3],
-                zk + zoff + (lane & 15) * segrow + (16 * kk + 8 * (lane >> 4)) * 2);
-      const float* cs0 = &s_cs[j & 1][g * CSR + 2 * q4];
-      const float* cs1 = cs0 + 8 * CSR;
-      const ulonglong2* qp = reinterpret_cast<const ulonglong2*>(&s_q[warp][q4]);
-      uint64_t part0 = 0ull, part1 = 0ull;  // even and odd coordinates' sums
-#pragma unroll
-      for (int n0 = 0; n0 < NT; n0 += 4) {
-        float acc[4][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mma_bf16_16816(acc[u], a[kk][0], a[kk][1], a[kk][2], a[kk][3], bf[n0 + u][kk][0], bf[n0 + u][kk][1]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int n = n0 + u, d = 8 * n + 2 * q4;
-          const unsigned char* kb = ks + (d >> 6) * (kRT * 128);
-          const uint32_t s0 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g, (d & 63) >> 3, 128) + 4 * q4);
-          const uint32_t s1 = *reinterpret_cast<const uint32_t*>(kb + swz_off(g + 8, (d & 63) >> 3, 128) + 4 * q4);
-          const float2 c0 = *reinterpret_cast<const float2*>(cs0 + 8 * n);  // (cos, sin) of pair d / 2
-          const float2 c1 = *reinterpret_cast<const float2*>(cs1 + 8 * n);
-          const ulonglong2 qv = qp[4 * n];  // (qa, qb), (qb, -qa)
-          const uint64_t x = add2(pair(acc[u][0], acc[u][1]), pair(bf_lo(s0), bf_hi(s0)));
-          const uint64_t y = add2(pair(acc[u][2], acc[u][3]), pair(bf_lo(s1), bf_hi(s1)));
-          part0 = fma2(x, fma2(pair(c0.x, c0.x), qv.x, mul2(pair(c0.y, c0.y), qv.y)), part0);
-          part1 = fma2(y, fma2(pair(c1.x, c1.x), qv.x, mul2(pair(c1.y, c1.y), qv.y)), part1);
+      for (int x = 0; x < kMaxAxes; ++x) {
+        if (pos[x] < 0 || pos[x] >= P.rope_max_pos) {
+          s_badpos = 1;
+          pos[x] = min(max(pos[x], 0), P.rope_max_pos - 1);
         }
       }
-      float e0, e1, f0, f1;
-      unpair(part0, e0, f0);
-      unpair(part1, e1, f1);
-      e0 += f0;
-      e1 += f1;
-      e0 += __shfl_xor_sync(0xffffffffu, e0, 1);
-      e1 += __shfl_xor_sync(0xffffffffu, e1, 1);
-      e0 += __shfl_xor_sync(0xffffffffu, e0, 2);
-      e1 += __shfl_xor_sync(0xffffffffu, e1, 2);
-      // ---- one online softmax over the tile (log2 domain) ----
-      const float sc0 = g < nvalid ? e0 * P.scale_log2 : -INFINITY;
-      const float sc1 = g + 8 < nvalid ? e1 * P.scale_log2 : -INFINITY;
-      if (P.scores && q4 == 0) {
-        if (!waited) {
-          pdl_wait();  // the launch before may still read the workspace
-          waited = true;
+      __syncwarp();
+      *reinterpret_cast<int4*>(stage + lane * kRStage) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      __syncwarp();
+      float4 e[HP / 8][4];
+#pragma unroll
+      for (int ch = 0; ch < HP / 8; ++ch) {
+        const int k = half * HP + 8 * ch + 2 * q4;  // this lane's two pairs
+        const unsigned char* pa = stage + g * kRStage + 4 * A.ax.axis(k);
+        const unsigned char* pb = stage + g * kRStage + 4 * A.ax.axis(k + 1);
+#pragma unroll
+        for (int r8 = 0; r8 < 4; ++r8) {
+          const float* ta = P.rope_cs + static_cast<size_t>(*reinterpret_cast<const int*>(pa + 8 * r8 * kRStage)) * DH + 2 * k;
+          if (A.even) {
+            e[ch][r8] = __ldg(reinterpret_cast<const float4*>(ta));
+          } else {
+            const float* tb = P.rope_cs + static_cast<size_t>(*reinterpret_cast<const int*>(pb + 8 * r8 * kRStage)) * DH + 2 * k;
+            const float2 a = __ldg(reinterpret_cast<const float2*>(ta));
+            const float2 b = __ldg(reinterpret_cast<const float2*>(tb + 2));
+            e[ch][r8] = make_float4(a.x, a.y, b.x, b.y);
+          }
         }
-        float* srow = P.scores + (static_cast<size_t>(w.b) * H + h) * P.max_len + w.t0;
-        if (g < nvalid) srow[g] = sc0;
-        if (g + 8 < nvalid) srow[g + 8] = sc1;
       }
-      float mx = fmaxf(sc0, sc1);
+      // (the next tile's positions load meanwhile)
+      more = walk_next(w, pre, B, g1, kRT);
+      if (more) positions_of(w);
 #pragma unroll
-      for (int o2 = 4; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-      if (mx > m + kRRescaleLog2) {  // (the same for every lane)
-        const float alpha = m == -INFINITY ? 0.f : exp2f(m - mx);
-        m = mx;
-        l *= alpha;
+      for (int ch = 0; ch < HP / 8; ++ch) {
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < MV; ++e)
+        for (int r8 = 0; r8 < 4; ++r8)
+          *reinterpret_cast<float4*>(stage + (8 * r8 + g) * kRStage + 16 * q4) =
+              make_float4(e[ch][r8].x, e[ch][r8].z, e[ch][r8].y, e[ch][r8].w);
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) os[e][k] *= alpha;
-#pragma unroll
-        for (int e = 0; e < MZ; ++e)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) oz[e][k] *= alpha;
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(stage + lane * kRStage + 16 * i);
+          cc[4 * ch + i] = v.x;
+          ss[4 * ch + i] = v.y;
+        }
       }
-      const float p0 = exp2f(sc0 - m), p1 = exp2f(sc1 - m);
-      l += p0 + p1;  // this lane's tokens; the lanes meet at the end of the piece
-      // P as the B operand: column 0 the bf16 high parts, column 1 the low parts
-      // (lanes g = 0 and 1 hold tokens 2 q4, 2 q4 + 1 and + 8)
-      uint32_t b0, b1;
-      {
-        const float ta = __shfl_sync(0xffffffffu, p0, 8 * q4), tb = __shfl_sync(0xffffffffu, p0, 8 * q4 + 4);
-        const float tc = __shfl_sync(0xffffffffu, p1, 8 * q4), td = __shfl_sync(0xffffffffu, p1, 8 * q4 + 4);
-        const uint32_t hi0 = pack_bf16(ta, tb), hi1 = pack_bf16(tc, td);
-        const uint32_t lo0 = pack_bf16(ta - bf_lo(hi0), tb - bf_hi(hi0));
-        const uint32_t lo1 = pack_bf16(tc - bf_lo(hi1), td - bf_hi(hi1));
-        b0 = g == 0 ? hi0 : g == 1 ? lo0 : 0u;
-        b1 = g == 0 ? hi1 : g == 1 ? lo1 : 0u;
-      }
-      // ---- values, unrotated: rows past the piece (which may hold anything)
-      // must not meet their zero probabilities as 0 x NaN ----
-      const uint32_t k0 = (2 * q4 < nvalid ? 0x0000ffffu : 0u) | (2 * q4 + 1 < nvalid ? 0xffff0000u : 0u);
-      const uint32_t k1 = (2 * q4 + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * q4 + 9 < nvalid ? 0xffff0000u : 0u);
+      // the row's shared part, two columns per word
+      ok = ok && !*fail && mbar_wait_bounded(&kfull, static_cast<uint32_t>(j) & 1u, P.wait_limit);
+      ok = __all_sync(0xffffffffu, ok);
+      uint32_t sk[HP];
+      if (ok) {
+        const unsigned char* kr = smem + A.off_k + (DH == 128 ? half * kRBox : 0) + row * 128;
 #pragma unroll
-      for (int e = 0; e < MV; ++e) {
-        uint32_t v0, v1, v2, v3;
-        const int ch = 2 * e + tcol;  // 16-byte chunk along the head dim
-        ldsm_x4_trans(v0, v1, v2, v3, vs + (ch >> 3) * (kRT * 128) + swz_off(trow, ch & 7, 128));
-        mma_bf16_16816(os[e], v0 & k0, v1 & k0, v2 & k1, v3 & k1, b0, b1);
+        for (int i = 0; i < HP / 4; ++i) {
+          const int chunk = (DH == 128 ? 0 : half * (HP / 4)) + i;
+          const uint4 v = *reinterpret_cast<const uint4*>(kr + ((chunk ^ (row & 7)) << 4));
+          sk[4 * i] = v.x; sk[4 * i + 1] = v.y; sk[4 * i + 2] = v.z; sk[4 * i + 3] = v.w;
+        }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&kempty);
+      // the score buffer of tile j - 2 is free
+      ok = ok && (j < 2 || mbar_wait_bounded(&sce[j & 1], static_cast<uint32_t>(j / 2 - 1) & 1u, P.wait_limit));
+      float* sc = reinterpret_cast<float*>(smem + A.off_sc) + ((j & 1) * 2 + half) * kRHeads * kRT + row;
+#pragma unroll 1
+      for (int i = 0; i < kRHeads; ++i, ++u) {
+        const int a = u % kRAcc;
+        ok = ok && !*fail && mbar_wait_bounded(&accf[a], static_cast<uint32_t>(u / kRAcc) & 1u, P.wait_limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          *fail = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&acce[a]);
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16) + a * DH + half * (DH / 2);
+        const float* qa = sq + i * DH + half * (DH / 2);
+        uint64_t acc0 = 0ull, acc1 = 0ull, acc2 = 0ull;  // qa x0 cos, qb (x0 sin + x1 cos), qa x1 sin
+        uint32_t v[DH / 32][16];
 #pragma unroll
-      for (int e = 0; e < MZ; ++e) {
-        uint32_t v0, v1, v2, v3;
-        ldsm_x4_trans(v0, v1, v2, v3, zv + zoff + trow * segrow + (16 * e + 8 * tcol) * 2);
-        mma_bf16_16816(oz[e], v0 & k0, v1 & k0, v2 & k1, v3 & k1, b0, b1);
+        for (int c16 = 0; c16 < DH / 32; c16 += 2) {
+          tmem_ld16(at + 16 * c16, v[c16]);
+          tmem_ld16(at + 16 * c16 + 16, v[c16 + 1]);
+          tmem_wait_ld();
+          if (c16 + 2 == DH / 32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cta(&acce[a]);  // the accumulator is free
+          }
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const int dp = 4 * c16 + p;  // pairs 2 dp, 2 dp + 1 of the half
+            const uint32_t* x = &v[c16 + p / 4][4 * (p & 3)];
+            const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(qa + 4 * dp);
+            const uint32_t sa = sk[2 * dp], sb = sk[2 * dp + 1];
+            const uint64_t x0 = add2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), pair(bf_lo(sa), bf_lo(sb)));
+            const uint64_t x1 = add2(pair(__uint_as_float(x[2]), __uint_as_float(x[3])), pair(bf_hi(sa), bf_hi(sb)));
+            acc0 = fma2(qv.x, mul2(cc[dp], x0), acc0);
+            acc2 = fma2(qv.x, mul2(ss[dp], x1), acc2);
+            acc1 = fma2(qv.y, fma2(ss[dp], x0, mul2(cc[dp], x1)), acc1);
+          }
+        }
+        {
+          float u0, u1, v0, v1;
+          unpair(acc0, u0, u1);
+          unpair(acc2, v0, v1);
+          acc0 = pair(u0 - v0, u1 - v1);
+        }
+        float a0, a1, b0, b1;
+        unpair(acc0, a0, a1);
+        unpair(acc1, b0, b1);
+        sc[i * kRT] = (a0 + a1) + (b0 + b1);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&scf[j & 1]);
     }
-    more = walk_next(w, pre, B, g1, kRT);
-    if (!more || w.b != cur_b) {  // the piece ends here: the lanes' denominators meet (each token on four lanes)
+    if (!ok) *fail = 1;
+  } else {
+    regs_down<kRRegsValue>();
+    // ---- softmax and values: shared columns 16 MS v .. of the four heads, latents of
+    // head v -----------------------------------------------------------------------
+    const int v = warp - 4 - kRScore, hd = g & 3;  // this lane's softmax: head hd
+    const int trow = (lane & 7) + 8 * (lane >> 4), tcol = (lane >> 3) & 1;
+    const int zoff = (v / P.hs) * (kRSub * P.segp * 2) + (v % P.hs) * R * 2;
+    pdl_wait();  // the launch before may still read the workspace
+    bool ok = true;
+    int cur_b = -1, j = 0, vi = 0;
+    float m = -INFINITY, l = 0.f;
+    // columns 0-3 the heads' high and third parts, 4-7 their low parts (of oz
+    // only head v's two columns mean anything)
+    float os[MS][4], oz[MZ][4];
+    // the tensor cores cut each sum short of fp32 rounding (1e-5 off after 800
+    // steps): a tile's products get accumulators of their own
+    float ts[MS][4], tz[MZ][4];
+    auto write_partial = [&](int b) {
+      const size_t slot = static_cast<size_t>(b + c);
+      float lsum = l;
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+      lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+      if (lane == 4 * v) {
+        float* pml = P.part_ml + (slot * H + h0 + v) * 2;
+        pml[0] = m;
+        pml[1] = lsum;
+      }
 #pragma unroll
-      for (int o2 = 4; o2 < 32; o2 <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+      for (int e = 0; e < MS; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) os[e][k] += __shfl_xor_sync(0xffffffffu, os[e][k], 2);
+#pragma unroll
+      for (int e = 0; e < MZ; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oz[e][k] += __shfl_xor_sync(0xffffffffu, oz[e][k], 2);
+      if (q4 < 2) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float* o = P.part_acc + (slot * H + h0 + 2 * q4 + x) * (DH + R) + 16 * MS * v;
+#pragma unroll
+          for (int e = 0; e < MS; ++e) {
+            o[16 * e + g] = os[e][x];
+            o[16 * e + g + 8] = os[e][2 + x];
+          }
+        }
+      }
+      if (q4 == v >> 1) {
+        float* o = P.part_acc + (slot * H + h0 + v) * (DH + R) + DH;
+#pragma unroll
+        for (int e = 0; e < MZ; ++e) {
+          o[16 * e + g] = (v & 1) ? oz[e][1] : oz[e][0];
+          o[16 * e + g + 8] = (v & 1) ? oz[e][3] : oz[e][2];
+        }
+      }
+    };
+    bool more = walk_first(w, pre, B, g0, g1);
+    for (; more; ++j) {
+      if (w.b != cur_b) {
+        if (cur_b >= 0) write_partial(cur_b);
+        cur_b = w.b;
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int e = 0; e < MS; ++e) os[e][0] = os[e][1] = os[e][2] = os[e][3] = 0.f;
+#pragma unroll
+        for (int e = 0; e < MZ; ++e) oz[e][0] = oz[e][1] = oz[e][2] = oz[e][3] = 0.f;
+      }
+      const int nvalid = min(kRT, w.t_end - w.t0);
+      ok = ok && !*fail && mbar_wait_bounded(&scf[j & 1], static_cast<uint32_t>(j / 2) & 1u, P.wait_limit);
+      ok = __all_sync(0xffffffffu, ok);
+      float s[32];  // scores of head hd: s[4 t + {0, 1, 2, 3}] rows 16 t + 2 q4 + {0, 1, 8, 9}
+      if (ok) {
+        const float* lo = reinterpret_cast<const float*>(smem + A.off_sc) + (j & 1) * 2 * kRHeads * kRT;
+        const float* hi = lo + kRHeads * kRT;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = 16 * t + 8 * k + 2 * q4;
+            const float2 a = *reinterpret_cast<const float2*>(lo + hd * kRT + r);
+            const float2 b = *reinterpret_cast<const float2*>(hi + hd * kRT + r);
+            s[4 * t + 2 * k] = r < nvalid ? (a.x + b.x) * P.scale_log2 : -INFINITY;
+            s[4 * t + 2 * k + 1] = r + 1 < nvalid ? (a.y + b.y) * P.scale_log2 : -INFINITY;
+          }
+        if (P.scores) {
+          float* out = P.scores + (static_cast<size_t>(w.b) * H + h0 + v) * P.max_len + w.t0;
+#pragma unroll
+          for (int k = 0; k < kRT / 32; ++k) {
+            const int r = 32 * k + lane;
+            if (r < nvalid) out[r] = (lo[v * kRT + r] + hi[v * kRT + r]) * P.scale_log2;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&sce[j & 1]);
+      if (ok) {
+        // one online softmax per head (log2 domain), the reference raised lazily
+        float mx = s[0];
+#pragma unroll
+        for (int k = 1; k < 32; ++k) mx = fmaxf(mx, s[k]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool up = mx > m + kRRescaleLog2;
+        if (__any_sync(0xffffffffu, up)) {
+          const float alpha = !up ? 1.f : m == -INFINITY ? 0.f : exp2f(m - mx);
+          if (up) m = mx;
+          l *= alpha;
+          const float a0 = __shfl_sync(0xffffffffu, alpha, 4 * ((2 * q4) & 3));  // columns 2 q4, 2 q4 + 1
+          const float a1 = __shfl_sync(0xffffffffu, alpha, 4 * ((2 * q4 + 1) & 3));
+#pragma unroll
+          for (int e = 0; e < MS; ++e) {
+            os[e][0] *= a0; os[e][1] *= a1; os[e][2] *= a0; os[e][3] *= a1;
+          }
+#pragma unroll
+          for (int e = 0; e < MZ; ++e) {
+            oz[e][0] *= a0; oz[e][1] *= a1; oz[e][2] *= a0; oz[e][3] *= a1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          s[k] = exp2f(s[k] - m);
+          l += s[k];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < MS; ++e) ts[e][0] = ts[e][1] = ts[e][2] = ts[e][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < MZ; ++e) tz[e][0] = tz[e][1] = tz[e][2] = tz[e][3] = 0.f;
+#pragma unroll
+      for (int sub = 0; sub < kRT / kRSub; ++sub) {
+        if (sub * kRSub >= nvalid) break;
+        const int slot = vi % A.nv;
+        ok = ok && !*fail && mbar_wait_bounded(&vfull[slot], static_cast<uint32_t>(vi / A.nv) & 1u, P.wait_limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          const unsigned char* vsm = smem + A.off_v + slot * A.vt_bytes;
+          const unsigned char* zsm = vsm + A.zv_off + zoff;
+#pragma unroll
+          for (int t2 = 0; t2 < 2; ++t2) {
+            const int t = 2 * sub + t2;  // 16 rows
+            // three bf16 parts of the probabilities of rows 2 q4, + 1 (first word), + 8, + 9 (second)
+            uint32_t p1[2], p2[2], p3[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float x = s[4 * t + 2 * k], y = s[4 * t + 2 * k + 1];
+              p1[k] = pack_bf16(x, y);
+              const float x2 = x - bf_lo(p1[k]), y2 = y - bf_hi(p1[k]);
+              p2[k] = pack_bf16(x2, y2);
+              p3[k] = pack_bf16(x2 - bf_lo(p2[k]), y2 - bf_hi(p2[k]));
+            }
+            // column g: the high part of head g, the low part of head g - 4; then the third parts
+            const uint32_t b0 = g < 4 ? p1[0] : p2[0], b1 = g < 4 ? p1[1] : p2[1];
+            const uint32_t c0 = g < 4 ? p3[0] : 0u, c1 = g < 4 ? p3[1] : 0u;
+            // rows past the piece (which may hold anything) must not meet their
+            // zero probabilities as 0 x NaN
+            const int left = nvalid - 16 * t;
+            const uint32_t k0 = (2 * q4 < left ? 0x0000ffffu : 0u) | (2 * q4 + 1 < left ? 0xffff0000u : 0u);
+            const uint32_t k1 = (2 * q4 + 8 < left ? 0x0000ffffu : 0u) | (2 * q4 + 9 < left ? 0xffff0000u : 0u);
+            const int r = 16 * t2 + trow;
+#pragma unroll
+            for (int e = 0; e < MS; ++e) {
+              uint32_t x0, x1, x2, x3;
+              const int ch = 2 * (MS * v + e) + tcol;  // 16-byte chunk along the head dim
+              ldsm_x4_trans(x0, x1, x2, x3, vsm + (ch >> 3) * (kRSub * 128) + swz_off(r, ch & 7, 128));
+              x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
+              mma_bf16_16816(ts[e], x0, x1, x2, x3, b0, b1);
+              mma_bf16_16816(ts[e], x0, x1, x2, x3, c0, c1);
+            }
+#pragma unroll
+            for (int e = 0; e < MZ; ++e) {
+              uint32_t x0, x1, x2, x3;
+              ldsm_x4_trans(x0, x1, x2, x3, zsm + r * (P.segp * 2) + (16 * e + 8 * tcol) * 2);
+              x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
+              mma_bf16_16816(tz[e], x0, x1, x2, x3, b0, b1);
+              mma_bf16_16816(tz[e], x0, x1, x2, x3, c0, c1);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&vempty[slot]);
+        ++vi;
+      }
+#pragma unroll
+      for (int e = 0; e < MS; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) os[e][k] += ts[e][k];
+#pragma unroll
+      for (int e = 0; e < MZ; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oz[e][k] += tz[e][k];
+      more = walk_next(w, pre, B, g1, kRT);
     }
-    // the tile's readers are done (its stage is refilled with the tile `stages`
-    // ahead) and the next tile's rotations are in place
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (ahead_more) {
-      if (tid == 0 && !*reinterpret_cast<volatile int*>(&s_timeout)) issue(j + P.stages, ahead);
-      ahead_more = walk_next(ahead, pre, B, g1, kRT);
-    }
+    if (cur_b >= 0) write_partial(cur_b);
+    if (!ok) *fail = 1;
   }
-  if (cur_b >= 0) write_partial(cur_b);
 
-  // ---- every copy this CTA issued has landed before it exits ----
+  // ---- every copy and MMA this CTA issued is complete before it exits ----
   __syncthreads();
   if (tid == 0) {
-    pdl_wait();
-    bool drained = true;
-    for (int st = 0; st < P.stages; ++st) {
-      const int j = *reinterpret_cast<volatile int*>(&issued[st]);
-      if (j >= 0) drained = mbar_wait_bounded(&full[st], static_cast<uint32_t>(j / P.stages) & 1u) && drained;
-    }
-    if (!drained) *reinterpret_cast<volatile int*>(&s_timeout) = 1;
+    bool done = true;
+    if (s_k > 0) done = mbar_wait_bounded(&kfull, static_cast<uint32_t>(s_k - 1) & 1u);
+    for (int i = max(0, s_z - A.nz); i < s_z; ++i)
+      done = mbar_wait_bounded(&zfull[i % A.nz], static_cast<uint32_t>(i / A.nz) & 1u) && done;
+    for (int i = max(0, s_v - A.nv); i < s_v; ++i)
+      done = mbar_wait_bounded(&vfull[i % A.nv], static_cast<uint32_t>(i / A.nv) & 1u) && done;
+    for (int i = max(0, s_mma - kRAcc); i < s_mma; ++i)
+      done = mbar_wait_bounded(&accf[i % kRAcc], static_cast<uint32_t>(i / kRAcc) & 1u) && done;
+    if (!done) *fail = 1;
+    pdl_wait();  // the launch before may still read the workspace
     if (blockIdx.x == 0 && blockIdx.y == 0) {
       P.meta[0] = N;
       P.meta[1] = G;
     }
-    *cta_status = (bad || *reinterpret_cast<volatile int*>(&s_badpos) ? kDevBounds : 0u) |
-                  (*reinterpret_cast<volatile int*>(&s_timeout) ? kDevTimeout : 0u);
+    *cta_status = (bad || s_badpos ? kDevBounds : 0u) | (*fail ? kDevTimeout : 0u);
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     pdl_wait();
     for (int b = tid; b <= B; b += blockDim.x) P.prefix[b] = pre[b];
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ======================================================================= host
@@ -507,14 +714,16 @@ lrkv_status rope_axes_check(const lrkv_dims* d) {
   if (d->batch < 1 || d->heads < 1 || d->head_dim < 1 || d->rank < 0 || d->max_len < 1) return LRKV_ERR_INVALID_ARG;
   if (d->dtype != LRKV_BF16 && d->dtype != LRKV_F32) return LRKV_ERR_INVALID_ARG;
   if (!(d->scale == d->scale)) return LRKV_ERR_INVALID_ARG;
-  if (d->dtype != LRKV_BF16 || !rope_fn(d->head_dim, d->rank) || d->heads % kRHeads != 0) return LRKV_ERR_UNSUPPORTED;
+  if (d->dtype != LRKV_BF16 || !rope_fn(d->head_dim, d->rank) || d->heads % 8 != 0) return LRKV_ERR_UNSUPPORTED;
   if (d->batch > kMaxBatch || static_cast<long long>(d->batch) * d->max_len > (1LL << 31) - 1)
     return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }
 
-lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* score_off, size_t* ws_bytes) {
+lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, AxesArgs& A, size_t* score_off,
+                           size_t* ws_bytes) {
   std::memset(&P, 0, sizeof(P));
+  std::memset(&A, 0, sizeof(A));
   P.B = d.batch; P.H = d.heads; P.dh = d.head_dim; P.r = d.rank; P.max_len = d.max_len;
   P.map_len = d.max_len; P.map_seqs = d.batch;
   const float scale = d.scale > 0.f ? d.scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
@@ -528,24 +737,35 @@ lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_
   P.mt = P.H / kRHeads;
   P.grid = std::max(1, num_sms / P.mt);
   P.ngw = 1;
-  P.hs = 0;
-  for (int hs = kRHeads; hs >= 1; hs >>= 1)
-    if (P.H % hs == 0 && (hs * P.r) % 16 == 0 && hs * P.r + 8 <= 256) { P.hs = hs; break; }
-  if (P.hs == 0) return LRKV_ERR_UNSUPPORTED;
+  // value latents: segments of hs heads, rows padded to an odd number of 16-byte chunks
+  P.hs = 4 * P.r + 8 <= 256 ? 4 : 2;
   P.segw = P.hs * P.r;
   P.segp = P.segw + 8;
   P.nsb = kRHeads / P.hs;
-  P.zt_bytes = P.nsb * kRT * P.segp * 2;
-  P.kv_bytes = round_up(kRT * P.dh * 2, 1024);
-  P.stage_bytes = round_up(2 * P.kv_bytes + 2 * P.zt_bytes, 1024);
-  P.off_prefix = kRHeader;
-  P.off_kv = round_up(kRHeader + (P.B + 1) * 4, 1024);
-  // less the static tables: two tiles of rotations, the queries
-  const int budget = 226 * 1024 - 2 * kRT * (P.dh + 8) * 4 - kRHeads * (P.dh / 2) * 16;
-  P.stages = std::min(kRMaxStages, (budget - P.off_kv - 1024) / P.stage_bytes);
-  if (P.stages < 2) return LRKV_ERR_UNSUPPORTED;
-  P.smem_bytes = P.off_kv + P.stages * P.stage_bytes + 1024;
-  P.min_tokens = 8 * kRT;
+  P.zt_bytes = P.nsb * kRSub * P.segp * 2;
+  // shared memory: sequence starts | B_h | k_s | latent ring | value ring | staging | scores | queries;
+  // the value ring takes what is left
+  const int nb = P.dh / 64;
+  A.zv_off = nb * kRSub * 128;
+  A.vt_bytes = round_up(A.zv_off + P.zt_bytes, 1024);
+  const int budget = 224 * 1024;  // (3 KB of the 227 for the static part and the alignment)
+  const int fixed = round_up((P.B + 1) * 4, 1024) + kRHeads * P.dh * 128 + nb * kRBox + kRScore * 32 * kRStage +
+                    2 * 2 * kRHeads * kRT * 4 + kRHeads * P.dh * 4;
+  for (A.nz = 3; A.nz >= 1; --A.nz) {
+    A.nv = std::min(kRMaxV, (budget - fixed - A.nz * kRBox) / A.vt_bytes);
+    if (A.nv >= 2) break;
+  }
+  if (A.nz < 1) return LRKV_ERR_UNSUPPORTED;
+  int off = round_up((P.B + 1) * 4, 1024);
+  A.off_b = off; off += kRHeads * P.dh * 128;
+  A.off_k = off; off += nb * kRBox;
+  A.off_z = off; off += A.nz * kRBox;
+  A.off_v = off; off += A.nv * A.vt_bytes;
+  A.off_st = off; off += kRScore * 32 * kRStage;
+  A.off_sc = off; off += 2 * 2 * kRHeads * kRT * 4;
+  A.off_q = off; off += kRHeads * P.dh * 4;
+  P.smem_bytes = off + 1024;
+  P.min_tokens = kRT;
   P.wide_merge = 1;
   P.wide_warps = 8;
   P.combine_ctas = static_cast<int>(std::min<long long>(static_cast<long long>(P.B) * P.H, 4ll * num_sms));
@@ -571,8 +791,9 @@ lrkv_status lrkv_decode_rope_axes_workspace_size(const lrkv_dims* dims, size_t* 
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
   lrkv::DecodePlan P;
+  lrkv::AxesArgs A;
   size_t off = 0;
-  return lrkv::rope_axes_plan(*dims, sms, P, &off, bytes);
+  return lrkv::rope_axes_plan(*dims, sms, P, A, &off, bytes);
 }
 
 lrkv_status lrkv_decode_rope_axes(const lrkv_dims* dims, const void* q_rot, const void* k_s, const void* v_s,
@@ -594,36 +815,41 @@ lrkv_status lrkv_decode_rope_axes(const lrkv_dims* dims, const void* q_rot, cons
     if (!lse) return LRKV_ERR_INVALID_ARG;  // the weights need the log-sum-exp
     if ((st = lrkv::weights_check(decay, weights, weights_out)) != LRKV_OK) return st;
   }
-  lrkv::AxesArgs A;
-  if (!lrkv::rope_axes_make(axes, sections, dims->head_dim, A.ax)) return LRKV_ERR_INVALID_ARG;
-  A.positions = positions;
+  lrkv::RopeAxes ax;
+  if (!lrkv::rope_axes_make(axes, sections, dims->head_dim, ax)) return LRKV_ERR_INVALID_ARG;
   if (!ws) return LRKV_ERR_WORKSPACE;
   if (!lrkv::a16(ws)) return LRKV_ERR_INVALID_ARG;
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
   lrkv::DecodePlan P;
+  lrkv::AxesArgs A;
   size_t score_off = 0, need = 0;
-  if ((st = lrkv::rope_axes_plan(*dims, sms, P, &score_off, &need)) != LRKV_OK) return st;
+  if ((st = lrkv::rope_axes_plan(*dims, sms, P, A, &score_off, &need)) != LRKV_OK) return st;
   if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
   lrkv::decode_bind_workspace(P, ws);
   if (weights_out) P.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + score_off);
   P.q = q_rot; P.k_s = k_s; P.v_s = v_s; P.z_k = z_k; P.z_v = z_v; P.b_k = b_k; P.b_v = b_v;
   P.seq_lens = seq_lens; P.out = out; P.lse = lse;
   P.rope_cs = cos_sin; P.rope_max_pos = max_pos;
+  A.ax = ax;
+  A.positions = positions;
+  A.even = 1;
+  for (int a = 0; a < axes; ++a) A.even = A.even && ax.end[a] % 2 == 0;
 
   CUtensorMap tm_k, tm_v, tm_zk, tm_zv;
   std::memset(&tm_k, 0, sizeof(tm_k)); std::memset(&tm_v, 0, sizeof(tm_v));
   std::memset(&tm_zk, 0, sizeof(tm_zk)); std::memset(&tm_zv, 0, sizeof(tm_zv));
-  const uint64_t row = static_cast<uint64_t>(P.H) * P.r * 2;
-  const uint64_t zdims[4] = {static_cast<uint64_t>(P.segw), static_cast<uint64_t>(P.max_len),
-                             static_cast<uint64_t>(P.H / P.hs), static_cast<uint64_t>(P.B)};
-  const uint64_t zstr[3] = {row, static_cast<uint64_t>(P.segw) * 2, row * P.max_len};
-  const uint32_t zbox[4] = {static_cast<uint32_t>(P.segp), static_cast<uint32_t>(lrkv::kRT),
+  const uint64_t r = P.r, H = P.H, L = P.max_len, B = P.B;
+  const uint64_t kdims[4] = {r, H, L, B}, kstr[3] = {r * 2, H * r * 2, L * H * r * 2};
+  const uint32_t kbox[4] = {64u, 1u, static_cast<uint32_t>(lrkv::kRT), 1u};
+  const uint64_t vdims[4] = {static_cast<uint64_t>(P.segw), L, H / P.hs, B};
+  const uint64_t vstr[3] = {H * r * 2, static_cast<uint64_t>(P.segw) * 2, L * H * r * 2};
+  const uint32_t vbox[4] = {static_cast<uint32_t>(P.segp), static_cast<uint32_t>(lrkv::kRSub),
                             static_cast<uint32_t>(P.nsb), 1u};
-  if (!lrkv::make_tmap_3d_bf16(&tm_k, k_s, P.dh, P.max_len, P.B, 64, lrkv::kRT, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !lrkv::make_tmap_3d_bf16(&tm_v, v_s, P.dh, P.max_len, P.B, 64, lrkv::kRT, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !lrkv::make_tmap_4d_bf16_strided(&tm_zk, z_k, zdims, zstr, zbox) ||
-      !lrkv::make_tmap_4d_bf16_strided(&tm_zv, z_v, zdims, zstr, zbox))
+  if (!lrkv::make_tmap_3d_bf16(&tm_k, k_s, P.dh, L, B, 64, lrkv::kRT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !lrkv::make_tmap_3d_bf16(&tm_v, v_s, P.dh, L, B, 64, lrkv::kRSub, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !lrkv::make_tmap_4d_bf16_swizzled(&tm_zk, z_k, kdims, kstr, kbox) ||
+      !lrkv::make_tmap_4d_bf16_strided(&tm_zv, z_v, vdims, vstr, vbox))
     return LRKV_ERR_CUDA;
   const lrkv::RopeFn kern = lrkv::rope_fn(P.dh, P.r);
   if (lrkv::ensure_kernel_smem(reinterpret_cast<const void*>(kern), P.smem_bytes, true) != cudaSuccess)
