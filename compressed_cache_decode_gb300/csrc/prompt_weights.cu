@@ -285,34 +285,37 @@ __global__ void __launch_bounds__(kAbThreads) lrkv_prefill_absorb_kernel(const P
   }
 }
 
-template <int DH>
+template <int DH, bool ONE>
 __global__ void __launch_bounds__(kPwThreads, 1)
     lrkv_prefill_weights_kernel(const __grid_constant__ PromptParams P, const __grid_constant__ PromptMaps maps) {
   constexpr int NB = DH / 64;  // 64-column boxes of a shared row
   constexpr int kStage = (NB + 2) * kPwBox;
+  constexpr int KB = ONE ? 2 : 1;  // k_s buffers in TMEM
   extern __shared__ __align__(16) unsigned char pw_raw[];
-  __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready, kfree, zready[kPwZ], zfree[kPwZ],
+  __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready[KB], kfree[KB], kfull, zready[kPwZ], zfree[kPwZ],
       accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL];
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad;
-  __shared__ int s_a, s_q, s_acc[kPwAcc];  // boxes and tiles issued, half units committed
+  __shared__ int s_use[kPwA], s_k, s_q, s_acc[kPwAcc];  // boxes and tiles issued, half units committed
   __shared__ __align__(16) float s_lse[kPwL][kPwCols];  // read four columns at a time
   __shared__ float s_part[2][4][2][kPwHalf];
   unsigned char* smem = pw_raw + ((1024u - (smem_u32(pw_raw) & 1023u)) & 1023u);
   unsigned char* s_aring = smem;                          // [kPwA] boxes
-  unsigned char* s_qring = s_aring + kPwA * kPwBox;       // [kPwQ] tiles
+  unsigned char* s_kbox = s_aring + kPwA * kPwBox;        // ONE: the k_s box on its way to TMEM
+  unsigned char* s_qring = s_kbox + (ONE ? kPwBox : 0);   // [kPwQ] tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* fail = &s_fail;
 
   if (tid == 0) {
-    for (int i = 0; i < kPwA; ++i) { mbar_init(&afull[i], 1); mbar_init(&aempty[i], 4); }
+    for (int i = 0; i < kPwA; ++i) { mbar_init(&afull[i], 1); mbar_init(&aempty[i], ONE ? 1 : 4); }
     for (int i = 0; i < kPwQ; ++i) { mbar_init(&qfull[i], 1); mbar_init(&qempty[i], 2); }
     for (int i = 0; i < kPwZ; ++i) { mbar_init(&zready[i], 4); mbar_init(&zfree[i], 1); }
     for (int i = 0; i < kPwAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], kPwEpi); }
     for (int i = 0; i < kPwL; ++i) { mbar_init(&lfull[i], 1); mbar_init(&lempty[i], kPwEpi); }
-    mbar_init(&kready, 4);
-    mbar_init(&kfree, 2);
-    s_fail = s_bad = s_a = s_q = s_acc[0] = s_acc[1] = 0;
+    for (int i = 0; i < KB; ++i) { mbar_init(&kready[i], 4); mbar_init(&kfree[i], 2); }
+    mbar_init(&kfull, 1);
+    for (int i = 0; i < kPwA; ++i) s_use[i] = 0;
+    s_fail = s_bad = s_k = s_q = s_acc[0] = s_acc[1] = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, kPwTmem);
@@ -324,45 +327,53 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   pdl_trigger();
   pdl_wait();
 
+  // one thread's copy of a key box of half m: k_s columns 64 c .. (c >= 0), or the
+  // latents of head -1 - c
+  auto copy_box = [&](const Walk& w, int m, int c, unsigned char* dst, uint64_t* full) {
+    const int row = w.kt * kPwKeys + m * kPwHalf;
+    const int boxes = (min(kPwHalf, w.L - row) + P.box_rows - 1) / P.box_rows;  // copies of the visible rows
+    const uint32_t box_bytes = static_cast<uint32_t>(P.box_rows) * 128u;
+    mbar_arrive_expect_tx(full, box_bytes * boxes);
+    for (int k = 0; k < boxes; ++k, dst += box_bytes) {
+      int seq = w.b, r0 = row + k * P.box_rows;  // tensor-map coordinates of the copy
+      if (P.block_table) {
+        seq = P.block_table[static_cast<size_t>(w.b) * P.max_blocks + (r0 >> P.page_shift)];
+        r0 &= (1 << P.page_shift) - 1;
+        if (seq < 0 || seq >= P.num_pages) {  // no page of the pool: the copy fills zeros
+          s_bad = 1;
+          seq = P.num_pages;
+        }
+      }
+      if (c >= 0)
+        tma_load_3d(dst, &maps.k, 64 * c, r0, seq, full);
+      else
+        tma_load_4d(dst, &maps.z, 0, -1 - c, r0, seq, full);
+    }
+  };
+
   if (warp == 0) {
     if (lane == 0) {
-      // ---- key boxes: k_s of both halves per item, z_k,h of both per head -------
-      int ai = 0;
+      // ---- key boxes: k_s of both halves per item (ONE: not here), then the
+      // heads' latents one after another, both halves of each -----------------------
+      int ai = 0, zi[2] = {0, 0};
       bool live = true;
       Walk w;
       for (bool more = w.first(P); more && live && !*fail; more = w.next(P)) {
-        const int nk = w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
+        const int nk = ONE ? 0 : w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
         for (int i = 0; i < nk + nz; ++i) {
-          const int s = ai % kPwA;
-          live = ai < kPwA || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(ai / kPwA - 1) & 1u);
+          const bool is_k = i < nk;
+          const int m = is_k ? i / NB : (i - nk) % w.halves;
+          const int s = ONE ? m * (kPwA / 2) + zi[m] % (kPwA / 2) : ai % kPwA;
+          const int u = ONE ? zi[m] / (kPwA / 2) : ai / kPwA;  // use of the slot
+          live = u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u);
           if (!live) {
             *fail = 1;
             break;
           }
-          // the heads' latents one after another, both halves of each
-          const bool is_k = i < nk;
-          const int m = is_k ? i / NB : (i - nk) % w.halves;
-          const int row = w.kt * kPwKeys + m * kPwHalf;
-          const int boxes = (min(kPwHalf, w.L - row) + P.box_rows - 1) / P.box_rows;  // copies of the visible rows
-          const uint32_t box_bytes = static_cast<uint32_t>(P.box_rows) * 128u;
-          mbar_arrive_expect_tx(&afull[s], box_bytes * boxes);
-          for (int k = 0; k < boxes; ++k) {
-            int seq = w.b, r0 = row + k * P.box_rows;  // tensor-map coordinates of the copy
-            if (P.block_table) {
-              seq = P.block_table[static_cast<size_t>(w.b) * P.max_blocks + (r0 >> P.page_shift)];
-              r0 &= (1 << P.page_shift) - 1;
-              if (seq < 0 || seq >= P.num_pages) {  // no page of the pool: the copy fills zeros
-                s_bad = 1;
-                seq = P.num_pages;
-              }
-            }
-            unsigned char* dst = s_aring + s * kPwBox + k * box_bytes;
-            if (is_k)
-              tma_load_3d(dst, &maps.k, 64 * (i % NB), r0, seq, &afull[s]);
-            else
-              tma_load_4d(dst, &maps.z, 0, w.h0 + (i - nk) / w.halves, r0, seq, &afull[s]);
-          }
-          s_a = ++ai;
+          copy_box(w, m, is_k ? i % NB : -1 - (w.h0 + (i - nk) / w.halves), s_aring + s * kPwBox, &afull[s]);
+          ++ai;
+          ++zi[m];
+          s_use[s] = u + 1;
         }
       }
     }
@@ -396,12 +407,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const uint32_t id_all = idesc_bf16(128, ncols, 0, 0), id_head = idesc_bf16(128, P.wt, 0, 0);
       const uint64_t d0 = smem_desc(smem_u32(s_qring), 16, 1024, 2);  // address field: 16-byte units, low bits
       const uint32_t box = static_cast<uint32_t>(ncols) * 8u, head = static_cast<uint32_t>(P.wt) * 8u;
-      const uint32_t acc = tmem + m * kPwCols, ka = tmem + kColK + m * (NB * 32);
+      const uint32_t acc = tmem + m * kPwCols;
+      const uint64_t a0 = smem_desc(smem_u32(s_aring + m * (kPwA / 2) * kPwBox), 16, 1024, 2);
       int x = 0, qi = 0, zi = 0;
       bool ok = true;
       Walk w;
       for (bool more = w.first(P); more && ok && !*fail; more = w.next(P)) {
-        ok = mbar_wait_bounded(&kready, static_cast<uint32_t>(w.n) & 1u);
+        ok = mbar_wait_bounded(&kready[w.n % KB], static_cast<uint32_t>(w.n / KB) & 1u);
+        const uint32_t ka = tmem + kColK + (w.n % KB) * 128 + m * (NB * 32);
         const bool on = m < w.halves;
         for (int hs = 0; hs < P.hg && ok; hs += P.hpt) {
           for (int qt = w.qt0; qt < P.nqt && ok; ++qt, ++qi) {
@@ -419,20 +432,36 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                   tc_mma_ts(acc, ka + c * 32 + kk * 8, qd + c * box + kk * 2, id_all, c + kk > 0 ? 1u : 0u);
               uint64_t hd = qd + NB * (kPwBox / 16);
               for (int i = 0; P.r > 0 && i < P.hpt; ++i, hd += head) {
-                const int z = zi + i, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
-                if (qt == w.qt0) {
-                  ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / (kPwZ / 2)) & 1u);
+                const int z = zi + i;
+                const uint32_t at = acc + i * P.wt;
+                if (ONE) {
+                  const int sl = z % (kPwA / 2), bar = m * (kPwA / 2) + sl;
+                  ok = mbar_wait_bounded(&afull[bar], static_cast<uint32_t>(z / (kPwA / 2)) & 1u);
                   if (!ok) break;
-                  tc_fence_after();
-                }
-                const uint32_t za = tmem + kColZ + sl * 32, at = acc + i * P.wt;
+                  const uint64_t ad = a0 + static_cast<uint32_t>(sl * (kPwBox / 16));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  if (kk < P.kr) {
-                    tc_mma_ts(at, za + kk * 8, hd + kk * 2, id_head, 1u);
-                    tc_mma_ts(at, za + kk * 8, hd + box + kk * 2, id_head, 1u);
+                  for (int kk = 0; kk < 4; ++kk)
+                    if (kk < P.kr) {
+                      tc_mma_ss(at, ad + kk * 2, hd + kk * 2, id_head, 1u);
+                      tc_mma_ss(at, ad + kk * 2, hd + box + kk * 2, id_head, 1u);
+                    }
+                  tc_commit(&aempty[bar]);
+                } else {
+                  const int sl = m * (kPwZ / 2) + z % (kPwZ / 2);
+                  if (qt == w.qt0) {
+                    ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / (kPwZ / 2)) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
                   }
-                if (qt + 1 == P.nqt) tc_commit(&zfree[sl]);
+                  const uint32_t za = tmem + kColZ + sl * 32;
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    if (kk < P.kr) {
+                      tc_mma_ts(at, za + kk * 8, hd + kk * 2, id_head, 1u);
+                      tc_mma_ts(at, za + kk * 8, hd + box + kk * 2, id_head, 1u);
+                    }
+                  if (qt + 1 == P.nqt) tc_commit(&zfree[sl]);
+                }
               }
               if (!ok) break;
               tc_commit(&accf[m]);
@@ -442,7 +471,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           }
           if (on) zi += P.hpt;
         }
-        if (ok) tc_commit(&kfree);
+        if (ok) tc_commit(&kfree[w.n % KB]);
       }
       if (!ok) *fail = 1;
     }
@@ -480,37 +509,59 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const int quad = warp & 3, row = 32 * quad + lane;
     int ai = 0, zi[2] = {0, 0};
     bool ok = true;
+    auto to_tmem = [&](const unsigned char* src, uint32_t col) {
+      src += row * 128;
+      uint32_t v[32];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+        v[4 * c] = u.x; v[4 * c + 1] = u.y; v[4 * c + 2] = u.z; v[4 * c + 3] = u.w;
+      }
+      tmem_st32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + col, v);
+      tmem_wait_st();
+      fence_proxy_async_smem();  // the reads above before the slot's next copy
+      __syncwarp();
+    };
     auto move = [&](uint32_t col) {
       const int s = ai % kPwA;
       ok = ok && !*fail && mbar_wait_bounded(&afull[s], static_cast<uint32_t>(ai / kPwA) & 1u);
       ok = __all_sync(0xffffffffu, ok);  // the warp moves together
-      if (!ok) {
+      if (ok)
+        to_tmem(s_aring + s * kPwBox, col);
+      else
         *fail = 1;
-      } else {
-        const unsigned char* src = s_aring + s * kPwBox + row * 128;
-        uint32_t v[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
-          v[4 * c] = u.x; v[4 * c + 1] = u.y; v[4 * c + 2] = u.z; v[4 * c + 3] = u.w;
-        }
-        tmem_st32(tmem + (static_cast<uint32_t>(32 * quad) << 16) + col, v);
-        tmem_wait_st();
-      }
-      fence_proxy_async_smem();  // the reads above before the slot's next copy
-      __syncwarp();
       if (lane == 0) mbar_arrive_cta(&aempty[s]);
       ++ai;
     };
     Walk w;
     for (bool more = w.first(P); more; more = w.next(P)) {
-      ok = ok && (w.n < 1 || mbar_wait_bounded(&kfree, static_cast<uint32_t>(w.n - 1) & 1u));
+      const int buf = w.n % KB;
+      ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
       tc_fence_after();
-      for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
+      for (int i = 0; i < w.halves * NB; ++i) {
+        if (ONE) {
+          // one box at a time, an item ahead of the MMAs: copied by the first of
+          // these warps once all four have read the one before
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (warp == 4 && lane == 0 && ok && !*fail) {
+            copy_box(w, i / NB, i % NB, s_kbox, &kfull);
+            s_k = ai + 1;
+          }
+          ok = ok && !*fail && mbar_wait_bounded(&kfull, static_cast<uint32_t>(ai) & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok)
+            to_tmem(s_kbox, kColK + buf * 128 + i * 32);
+          else
+            *fail = 1;
+          ++ai;
+        } else {
+          move(kColK + i * 32);
+        }
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&kready);
-      for (int i = 0; P.r > 0 && i < w.halves * P.hg; ++i) {
+      if (lane == 0) mbar_arrive_cta(&kready[buf]);
+      for (int i = 0; !ONE && P.r > 0 && i < w.halves * P.hg; ++i) {
         const int m = i % w.halves, z = zi[m]++, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
         ok = ok && (z < kPwZ / 2 || mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(z / (kPwZ / 2) - 1) & 1u));
         tc_fence_after();
@@ -591,8 +642,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   __syncthreads();
   if (tid == 0) {
     bool done = true;
-    for (int i = max(0, s_a - kPwA); i < s_a; ++i)
-      done = mbar_wait_bounded(&afull[i % kPwA], static_cast<uint32_t>(i / kPwA) & 1u) && done;
+    for (int i = 0; i < kPwA; ++i)
+      if (s_use[i] > 0) done = mbar_wait_bounded(&afull[i], static_cast<uint32_t>(s_use[i] - 1) & 1u) && done;
+    if (s_k > 0) done = mbar_wait_bounded(&kfull, static_cast<uint32_t>(s_k - 1) & 1u) && done;
     for (int i = max(0, s_q - kPwQ); i < s_q; ++i)
       done = mbar_wait_bounded(&qfull[i % kPwQ], static_cast<uint32_t>(i / kPwQ) & 1u) && done;
     for (int i = 0; i < kPwAcc; ++i)
@@ -677,7 +729,7 @@ PromptLayout prompt_plan(const lrkv_dims& d, int window, int sms, PromptParams& 
   P.nkt = (P.max_len + kPwKeys - 1) / kPwKeys;
   // head groups: until there are three items per SM
   P.hg = P.H;
-  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < 3LL * sms) P.hg /= 2;
+  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < (P.nqt == 1 ? 6LL : 3LL) * sms) P.hg /= 2;
   P.nhg = P.H / P.hg;
   P.items = static_cast<long long>(P.nkt) * P.B * P.nhg;
   P.grid = static_cast<int>(std::min<long long>(sms, P.items));
@@ -772,8 +824,10 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
       return LRKV_ERR_CUDA;
   }
   using Fn = void (*)(const PromptParams, const PromptMaps);
-  const Fn kern = P.dh == 128 ? lrkv_prefill_weights_kernel<128> : lrkv_prefill_weights_kernel<64>;
-  const int smem = 1024 + (kPwA + kPwQ * (P.dh / 64 + 2)) * kPwBox;
+  const bool one = P.nqt == 1;
+  const Fn kern = P.dh == 128 ? (one ? lrkv_prefill_weights_kernel<128, true> : lrkv_prefill_weights_kernel<128, false>)
+                              : (one ? lrkv_prefill_weights_kernel<64, true> : lrkv_prefill_weights_kernel<64, false>);
+  const int smem = 1024 + (kPwA + one + kPwQ * (P.dh / 64 + 2)) * kPwBox;
   if (ensure_kernel_smem(reinterpret_cast<const void*>(kern), smem, true) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (P.r > 0) {
