@@ -30,7 +30,7 @@
 // columns for the four heads and the latents of one head (mma.sync; the
 // probabilities as three bf16 parts in free columns of the B operand).
 //
-// Measured on 4 x 32K rows (32 heads, rank 48): 403 us, the cache at 2.2 TB/s,
+// Measured on 4 x 32K rows (32 heads, rank 48): 393 us, the cache at 2.2 TB/s,
 // 13.5K cycles a tile and CTA where its bytes need 4.6K.  What bounds it is the
 // score warps' latency: a tile's gather (positions, table entries, the exchange
 // through shared memory) takes 4.4K cycles in a row and a head's 32 pairs 1.4K

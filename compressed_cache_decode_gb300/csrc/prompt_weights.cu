@@ -15,22 +15,37 @@
 // high + low parts (lrkv_prefill_absorb_kernel), two MMAs over the same
 // latents, as the prefill's own scores do.
 //
-// Bound by the tensor pipe and, close behind, by what feeds it.  The keys are
-// the A operand from TMEM: they are the same for every query of the item
-// (k_s) or of the head (z_k,h), and with both operands in shared memory an
-// N = 128 instruction reads 8 KB for 64 cycles of work and took ~95.  CTA item
-// = (sequence, 256 keys as two halves of 128 lanes, group of heads), so that a
-// tile of queries (64 KB with its absorbed parts) is copied once for two M
+// What bounds it: the rate at which one SM takes the MMAs.  For all the queries
+// of 2 x 4K prompts (32 heads, d_h 128, rank 64: 108.6 us of tensor work at the
+// rate of a large bf16 product, p's two parts counted) the call takes 258 us:
+// 33 for p, 217 for the scores.  What was tried, at that shape:
+//   - both operands in shared memory: an N = 128 instruction reads 8 KB for 64
+//     cycles of work and took ~95.  So the keys, the same for every query of the
+//     item (k_s) or of the head (z_k,h), are the A operand from TMEM: 548 -> 312 us.
+//   - one issuing thread takes ~95 cycles an instruction: a thread per M half,
+//     each with its accumulator and its ring of latents: 312 -> 253 us.
+//   - a cluster of two sharing the query tiles by multicast (345 us) and query
+//     copies of 32 KB in a deeper ring (350 us) were slower than one CTA's 312.
+// An item is (sequence, 256 keys as two halves of 128 lanes, group of heads), so
+// that a tile of queries (64 KB with its absorbed parts) is copied once for two
 // halves: with one half the copies alone took longer than the MMAs.  A tile is
 // `wt` queries of `hpt` heads, 128 columns at most: short windows put several
 // heads side by side, whose shared part is one MMA.
 //
+// A window of one tile (ONE) uses each latent box once: it stays in shared memory
+// as the A operand, and its TMEM takes a second k_s buffer, so the next item's
+// keys are moved during this one.  4 x 16K keys of 32 heads, rank 64, window 32
+// (277 MB, 41.5 us at the copy rate): 115 us with the boxes moved, 95 us so.  There
+// the N = 32 products of one head each bound it; four issuing threads, each with
+// half of a tile's heads, took 106 us.
+//
 // Persistent: one CTA per SM walks the items, those with the most queries (the
 // first keys) first and dealt in a snake; the rings run on across items.
-// Warp 0 copies the keys' boxes (TMA), warps 4-7 move them to TMEM, warp 2
-// copies the query tiles, one thread of warp 1 issues the MMAs into two
-// accumulators, warps 8-23 read them back.  Each item leaves one partial sum
-// per key; the last kernel adds the head groups' partials in order.
+// Warp 0 copies the keys' boxes (TMA), warp 2 the query tiles; warps 4-7 move
+// keys to TMEM; one thread of warp 1 and one of warp 24 issue the MMAs of a half
+// each; warp 3 lays down the log-sum-exps; warps 8-23 read the accumulators back.
+// Each item leaves one partial sum per key; the last kernel adds the head groups'
+// partials in order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -355,7 +370,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (lane == 0) {
       // ---- key boxes: k_s of both halves per item (ONE: not here), then the
       // heads' latents one after another, both halves of each -----------------------
-      int ai = 0, zi[2] = {0, 0};
+      int ai = 0, z0 = 0, z1 = 0;  // boxes issued; ONE: of either half
       bool live = true;
       Walk w;
       for (bool more = w.first(P); more && live && !*fail; more = w.next(P)) {
@@ -363,8 +378,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         for (int i = 0; i < nk + nz; ++i) {
           const bool is_k = i < nk;
           const int m = is_k ? i / NB : (i - nk) % w.halves;
-          const int s = ONE ? m * (kPwA / 2) + zi[m] % (kPwA / 2) : ai % kPwA;
-          const int u = ONE ? zi[m] / (kPwA / 2) : ai / kPwA;  // use of the slot
+          const int z = m ? z1 : z0;
+          const int s = ONE ? m * (kPwA / 2) + z % (kPwA / 2) : ai % kPwA;
+          const int u = ONE ? z / (kPwA / 2) : ai / kPwA;  // use of the slot
           live = u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u);
           if (!live) {
             *fail = 1;
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           }
           copy_box(w, m, is_k ? i % NB : -1 - (w.h0 + (i - nk) / w.halves), s_aring + s * kPwBox, &afull[s]);
           ++ai;
-          ++zi[m];
+          (m ? z1 : z0) = z + 1;
           s_use[s] = u + 1;
         }
       }
@@ -507,7 +523,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   } else if (warp < 8) {
     // ---- key boxes to TMEM: lane = row of the half, two columns per 32-bit word ----
     const int quad = warp & 3, row = 32 * quad + lane;
-    int ai = 0, zi[2] = {0, 0};
+    int ai = 0, z0 = 0, z1 = 0;
     bool ok = true;
     auto to_tmem = [&](const unsigned char* src, uint32_t col) {
       src += row * 128;
@@ -562,7 +578,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&kready[buf]);
       for (int i = 0; !ONE && P.r > 0 && i < w.halves * P.hg; ++i) {
-        const int m = i % w.halves, z = zi[m]++, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
+        const int m = i % w.halves, z = m ? z1++ : z0++, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
         ok = ok && (z < kPwZ / 2 || mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(z / (kPwZ / 2) - 1) & 1u));
         tc_fence_after();
         move(kColZ + sl * 32);
@@ -727,9 +743,12 @@ PromptLayout prompt_plan(const lrkv_dims& d, int window, int sms, PromptParams& 
   P.nqt = (window + P.wt - 1) / P.wt;
   P.kr = (P.r + 15) / 16;
   P.nkt = (P.max_len + kPwKeys - 1) / kPwKeys;
-  // head groups: until there are three items per SM
+  // head groups: until there are three items per SM, or six when a window is one
+  // tile, where the items are equal and the last round's idle SMs cost most (4 x
+  // 16K keys of 32 heads: three 100 us, six 95)
+  const long long want = (P.nqt == 1 ? 6LL : 3LL) * sms;
   P.hg = P.H;
-  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < (P.nqt == 1 ? 6LL : 3LL) * sms) P.hg /= 2;
+  while (P.hg % (2 * P.hpt) == 0 && static_cast<long long>(P.nkt) * P.B * (P.H / P.hg) < want) P.hg /= 2;
   P.nhg = P.H / P.hg;
   P.items = static_cast<long long>(P.nkt) * P.B * P.nhg;
   P.grid = static_cast<int>(std::min<long long>(sms, P.items));

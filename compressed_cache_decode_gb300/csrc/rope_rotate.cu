@@ -11,6 +11,10 @@
 // A thread owns 16 bytes of a head's row (4 pairs of bf16, 2 of fp32) for
 // every n-th head of one token, so its cos and sin come from the table once
 // per token and stay in registers across the heads.
+//
+// Measured: 2 x 4096 tokens of 32 heads, d_h 128, bf16, three axes (134 MB read
+// and written, 20.1 us at the copy rate) 33 us, 4.1 TB/s; one token of 32
+// sequences 9.7 us a call, which is the launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -460,8 +460,8 @@ lrkv_status lrkv_decode_rope(const lrkv_dims* dims, const void* q_rot, const voi
  * accumulates
  *   sum over the heads of a_{h,j}
  * into row j; its new token is row L_b - 1.  The cache is read once.  out is
- * held to fp32 accuracy (the probabilities enter the value products as two
- * bf16 parts, not one).  lse must not be NULL.  Supported: the shapes on which
+ * held to fp32 accuracy (q B^K and the probabilities enter their products as
+ * three bf16 parts).  lse must not be NULL.  Supported: the shapes on which
  * lrkv_decode streams bf16 (others return LRKV_ERR_UNSUPPORTED).  Workspace:
  * lrkv_decode_weighted_workspace_size() bytes (the decode's and the scores,
  * 4 batch heads max_len).
@@ -498,8 +498,8 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
  * Eviction.  Sequence b keeps n = min(L_b, budget) of its L_b = seq_lens[b]
  * rows:
  *   - the held rows: age < sink (the first tokens) or age >= newest - recent,
- *     where the age of a row is order[b][j] (its token's number; NULL: the row
- *     index) and newest is one past the largest age;
+ *     where the age of a row is order[b][j] (its token's number, >= 0; NULL:
+ *     the row index) and newest is one past the largest age;
  *   - then the rows of the largest weights, equal weights by the lower row,
  *     NaN as -infinity.  (If the ages given hold more than n rows, these
  *     compete by weight among themselves.)
