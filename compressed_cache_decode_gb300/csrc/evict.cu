@@ -79,6 +79,7 @@ struct EvictParams {
   int32_t* moves;          // [B] moved rows
   int2* src;               // [B][cap] (logical, physical) row of the k-th moved row
   int2* dst;               // [B][cap] (logical, physical) row of the k-th hole
+  uint32_t* masks;         // [B][2][ceil(max_len / 32)] row masks (when not in shared memory)
   // moved data
   int n16[4];              // 16-byte pieces of a row of each cache tensor
   unsigned char* base[4];
@@ -129,11 +130,14 @@ __device__ __forceinline__ int warp_prefix(int count, int* s_warp, int& total) {
   return mine - count;
 }
 
-// The cluster's values of one shared integer: lane c holds CTA c's (c < ncta,
-// at most 16), so that the remote reads are all in flight at once.
-__device__ __forceinline__ int from_cluster(const cg::cluster_group& cluster, int* value, int ncta) {
+// The cluster's values of one shared integer: lane c of every warp holds CTA c's
+// (c < ncta, at most 16).  One warp fetches them, all remote reads in flight at
+// once (every warp for itself took 3K cycles more); s_all is this gather's own.
+__device__ __forceinline__ int from_cluster(const cg::cluster_group& cluster, int* value, int ncta, int* s_all) {
+  if (threadIdx.x < static_cast<unsigned>(ncta)) s_all[threadIdx.x] = *cluster.map_shared_rank(value, threadIdx.x);
+  __syncthreads();
   const int lane = threadIdx.x & 31;
-  return lane < ncta ? *cluster.map_shared_rank(value, lane) : 0;
+  return lane < ncta ? s_all[lane] : 0;
 }
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
@@ -157,13 +161,14 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   const int rank = static_cast<int>(cluster.block_rank()), ncta = static_cast<int>(cluster.num_blocks());
   const int b = blockIdx.x / ncta;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  extern __shared__ uint32_t s_keys[];          // [rows_per_cta] when cached
+  extern __shared__ uint32_t s_keys[];          // when cached: [rows_per_cta], then two bits a row
   __shared__ int s_hist[3][kEvBins];            // one table per level: no level waits to clear another's
   __shared__ int s_sum[kEvBins / 2];            // this CTA's share of a level's cluster-wide counts
   __shared__ int s_warp[kEvWarps];
   __shared__ int s_cta[4];                      // this CTA's max age + 1, held rows, equal rows, holes
   __shared__ int s_cta2;                        // ... moved rows
   __shared__ int s_bin, s_above, s_bad;
+  __shared__ int s_all[5][kEvMaxCluster];
 
   pdl_trigger();
   for (int i = tid; i < 3 * kEvBins; i += kEvThreads) (&s_hist[0][0])[i] = 0;
@@ -187,16 +192,36 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   bool among_held = false;         // more held rows than n: they compete among themselves
   const bool all = L <= n;         // nothing goes
   int newest = L;                  // tokens seen: one past the largest age
-  auto held = [&](int t) {
-    const int a = age ? age[t] : t;
-    return a < P.sink || a >= newest - P.recent;
-  };
-  auto key_of = [&](int t) -> uint32_t {
-    const uint32_t k = weight_key(w[t]);
-    const bool hd = held(t);
+  auto key = [&](float x, int a) -> uint32_t {  // of weight x and age a
+    const uint32_t k = weight_key(x);
+    const bool hd = a < P.sink || a >= newest - P.recent;
     return among_held ? (hd ? k : kKeyOut) : (hd ? kKeyHeld : k);
   };
-  auto key_at = [&](int t) -> uint32_t { return P.cached ? s_keys[t - lo] : key_of(t); };
+  // Keys of rows t, t + 32, ... (kKeyOut past whi; some row of the warp must be
+  // below it).  Every load is made, of the last row where there is none: loads
+  // behind a condition wait for one another (22K cycles of 16K rows, against 6K).
+  auto make_keys = [&](int t, uint32_t (&k)[kEvUnroll]) {
+    float x[kEvUnroll];
+    int a[kEvUnroll];
+#pragma unroll
+    for (int u = 0; u < kEvUnroll; ++u) {
+      const int at = min(t + 32 * u, whi - 1);
+      x[u] = w[at];
+      a[u] = age ? age[at] : at;
+    }
+#pragma unroll
+    for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? key(x[u], a[u]) : kKeyOut;
+  };
+  auto keys_at = [&](int t, uint32_t (&k)[kEvUnroll]) {
+    if (P.cached) {
+#pragma unroll
+      for (int u = 0; u < kEvUnroll; ++u) k[u] = s_keys[min(t + 32 * u, whi - 1) - lo];
+#pragma unroll
+      for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? k[u] : kKeyOut;
+    } else {
+      make_keys(t, k);
+    }
+  };
 
   if (!all) {
     if (age) {
@@ -204,33 +229,38 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
       for (int t = wlo + lane; t < whi; t += 32 * kEvUnroll) {
 #pragma unroll
         for (int u = 0; u < kEvUnroll; ++u)
-          if (t + 32 * u < whi) m = max(m, age[t + 32 * u] + 1);
+          m = max(m, age[min(t + 32 * u, whi - 1)] + 1);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (lane == 0) atomicMax(&s_cta[0], m);
       cluster.sync();
-      newest = __reduce_max_sync(0xffffffffu, from_cluster(cluster, &s_cta[0], ncta));
+      newest = __reduce_max_sync(0xffffffffu, from_cluster(cluster, &s_cta[0], ncta, s_all[0]));
     }
-    // keys, and the counts of their highest 11 bits
+    // keys, and the counts of their highest 11 bits (few bins hold most rows, so
+    // neighbouring lanes count in three tables)
     int count = 0;
     for (int t = wlo + lane; t - lane < whi; t += 32 * kEvUnroll) {
       uint32_t k[kEvUnroll];
-#pragma unroll
-      for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? key_of(t + 32 * u) : kKeyOut;
+      make_keys(t, k);
 #pragma unroll
       for (int u = 0; u < kEvUnroll; ++u) {
         if (t - lane + 32 * u >= whi) break;
         if (P.cached && t + 32 * u < whi) s_keys[t + 32 * u - lo] = k[u];
         count += k[u] == kKeyHeld;
-        tally(s_hist[0], k[u] != kKeyHeld && k[u] != kKeyOut, k[u] >> 21);
+        tally(s_hist[lane % 3], k[u] != kKeyHeld && k[u] != kKeyOut, k[u] >> 21);
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
     if (lane == 0) atomicAdd(&s_cta[1], count);
+    __syncthreads();
+    for (int i = tid; i < kEvBins; i += kEvThreads) {
+      s_hist[0][i] += s_hist[1][i] + s_hist[2][i];
+      s_hist[1][i] = s_hist[2][i] = 0;
+    }
     cluster.sync();
-    int need = n - warp_sum(from_cluster(cluster, &s_cta[1], ncta));
+    int need = n - warp_sum(from_cluster(cluster, &s_cta[1], ncta, s_all[1]));
     if (need < 0) {
       among_held = true;
       need = n;
@@ -238,10 +268,15 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
       cluster.sync();
       for (int i = tid; i < kEvBins; i += kEvThreads) s_hist[0][i] = 0;
       __syncthreads();
-      for (int t = wlo + lane; t - lane < whi; t += 32) {
-        const uint32_t k = t < whi ? key_of(t) : kKeyOut;
-        if (P.cached && t < whi) s_keys[t - lo] = k;
-        tally(s_hist[0], k != kKeyOut, k >> 21);
+      for (int t = wlo + lane; t - lane < whi; t += 32 * kEvUnroll) {
+        uint32_t k[kEvUnroll];
+        make_keys(t, k);
+#pragma unroll
+        for (int u = 0; u < kEvUnroll; ++u) {
+          if (t - lane + 32 * u >= whi) break;
+          if (P.cached && t + 32 * u < whi) s_keys[t + 32 * u - lo] = k[u];
+          tally(s_hist[0], k[u] != kKeyOut, k[u] >> 21);
+        }
       }
       cluster.sync();
     }
@@ -258,8 +293,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
         if (level > 0) {
           for (int t = wlo + lane; t - lane < whi; t += 32 * kEvUnroll) {
             uint32_t k[kEvUnroll];
-#pragma unroll
-            for (int u = 0; u < kEvUnroll; ++u) k[u] = t + 32 * u < whi ? key_at(t + 32 * u) : kKeyOut;
+            keys_at(t, k);
 #pragma unroll
             for (int u = 0; u < kEvUnroll; ++u) {
               if (t - lane + 32 * u >= whi) break;
@@ -313,44 +347,69 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     }
   }
 
-  // ---- ranks: equal keys first (the lower rows stay), then holes and moves
-  int eq_before = 0;
-  if (!all && threshold_need > 0) {
-    int eq = 0;
-    for (int t = wlo + lane; t < whi; t += 32) eq += key_at(t) == threshold;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    int total;
-    eq_before = warp_prefix(eq, s_warp, total);
-    if (tid == 0) s_cta[2] = total;
-    cluster.sync();
-    const int v = from_cluster(cluster, &s_cta[2], ncta);
-    eq_before += warp_sum(lane < rank ? v : 0);
-  }
-  // walks this warp's rows in order: f(row, valid, kept mask of the 32 rows)
-  auto walk = [&](auto f) {
-    int eqs = eq_before;
-    for (int t0 = wlo; t0 < whi; t0 += 32) {
-      const int t = t0 + lane;
-      const bool there = t < whi;
-      bool keep = there;
-      if (!all) {
-        const uint32_t k = there ? key_at(t) : kKeyOut;
-        const bool same = there && threshold_need > 0 && k == threshold;
-        const unsigned m = __ballot_sync(0xffffffffu, same);
-        const int r = eqs + __popc(m & ((1u << lane) - 1u));
-        keep = there && (same ? r < threshold_need : k > threshold || (threshold_need == 0 && k == threshold));
-        eqs += __popc(m);
-      }
-      f(t, there, keep);
-    }
+  // ---- ranks.  A word per 32 rows: the rows above the threshold, and those at it
+  const int words = (whi - wlo + 31) / 32;
+  const size_t mask_words = (static_cast<size_t>(P.max_len) + 31) / 32;
+  uint32_t* keep_w = P.cached ? s_keys + P.rows_per_cta + (wlo - lo) / 32
+                              : P.masks + static_cast<size_t>(b) * 2 * mask_words + wlo / 32;
+  uint32_t* equal_w = keep_w + (P.cached ? P.rows_per_cta / 32 : mask_words);
+  // the lowest bits of the word of rows t0 .. t0 + 31 up to row `end`
+  auto rows_below = [](int t0, int end) -> uint32_t {
+    const int k = min(max(end - t0, 0), 32);
+    return k == 32 ? 0xffffffffu : (1u << k) - 1u;
   };
   int hole = 0, move = 0;  // this lane's, then its warp's
   if (!all) {
-    walk([&](int t, bool there, bool keep) {
-      hole += there && t < n && !keep;
-      move += there && t >= n && keep;
-    });
+    const bool ties = threshold_need > 0;
+    int eq = 0;
+    for (int t = wlo + lane, i = 0; i < words; t += 32 * kEvUnroll, i += kEvUnroll) {
+      uint32_t k[kEvUnroll];
+      keys_at(t, k);
+#pragma unroll
+      for (int u = 0; u < kEvUnroll; ++u) {
+        const unsigned m = __ballot_sync(0xffffffffu, k[u] > threshold || (!ties && k[u] == threshold));
+        const unsigned e = __ballot_sync(0xffffffffu, ties && k[u] == threshold);
+        eq += __popc(e);
+        if (lane == u && i + u < words) {
+          keep_w[i + u] = m;
+          equal_w[i + u] = e;
+        }
+      }
+    }
+    __syncwarp();
+    int eq_before = 0;
+    if (ties) {  // equal keys: the lower rows stay
+      int total;
+      eq_before = warp_prefix(eq, s_warp, total);
+      if (tid == 0) s_cta[2] = total;
+      cluster.sync();
+      const int v = from_cluster(cluster, &s_cta[2], ncta, s_all[2]);
+      eq_before += warp_sum(lane < rank ? v : 0);
+    }
+    for (int i0 = 0; i0 < words; i0 += 32) {
+      const int i = i0 + lane, t0 = wlo + 32 * i;
+      uint32_t keep = i < words ? keep_w[i] : 0u, e = i < words ? equal_w[i] : 0u;
+      const int mine = __popc(e);
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+      }
+      const int sum = __shfl_sync(0xffffffffu, before, 31);
+      int take = min(max(threshold_need - (eq_before + before - mine), 0), mine);
+      if (take == mine) {
+        keep |= e;
+      } else {
+        for (; take > 0; --take, e &= e - 1u) keep |= e & (0u - e);
+      }
+      eq_before += sum;
+      if (i < words) keep_w[i] = keep;
+      const uint32_t front = rows_below(t0, n);
+      hole += __popc(rows_below(t0, whi) & front & ~keep);
+      move += __popc(keep & ~front);
+    }
+    __syncwarp();
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -365,33 +424,35 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     s_cta2 = move_total;
   }
   cluster.sync();
-  const int holes_of = from_cluster(cluster, &s_cta[3], ncta), moves_of = from_cluster(cluster, &s_cta2, ncta);
+  const int holes_of = from_cluster(cluster, &s_cta[3], ncta, s_all[3]), moves_of = from_cluster(cluster, &s_cta2, ncta, s_all[4]);
   const int moves = warp_sum(moves_of);
   hole_at += warp_sum(lane < rank ? holes_of : 0);
   move_at += warp_sum(lane < rank ? moves_of : 0);
   // ---- lists, and the rows that stay where they are
   const size_t row0 = static_cast<size_t>(b) * P.max_len;
   bool no_page = false;
-  walk([&](int t, bool there, bool keep) {
-    const bool is_hole = there && t < n && !keep, is_move = there && t >= n && keep;
-    const unsigned hm = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_move);
-    const unsigned below = (1u << lane) - 1u;
-    if (is_hole || is_move) {
+  const bool copies = P.weights_out != P.weights || (P.order_out && P.order_out != P.order) || P.kept;
+  const unsigned below = (1u << lane) - 1u;
+  for (int i = 0; i < words; ++i) {
+    const int t0 = wlo + 32 * i, t = t0 + lane;
+    const uint32_t there = rows_below(t0, whi), front = rows_below(t0, n), keep = all ? there : keep_w[i];
+    const uint32_t hm = there & front & ~keep, mm = keep & ~front;
+    if (((hm | mm) >> lane) & 1u) {
       const int phys = physical_row(P, b, t);
       no_page |= phys < 0;
-      if (is_hole)
+      if ((hm >> lane) & 1u)
         P.dst[static_cast<size_t>(b) * P.cap + hole_at + __popc(hm & below)] = make_int2(t, phys);
       else
         P.src[static_cast<size_t>(b) * P.cap + move_at + __popc(mm & below)] = make_int2(t, phys);
     }
     hole_at += __popc(hm);
     move_at += __popc(mm);
-    if (there && t < n && keep) {
+    if (copies && ((keep & front) >> lane) & 1u) {
       if (P.weights_out != P.weights) P.weights_out[row0 + t] = w[t];
       if (P.order_out && P.order_out != P.order) P.order_out[row0 + t] = age ? age[t] : t;
       if (P.kept) P.kept[static_cast<size_t>(b) * P.budget + t] = t;
     }
-  });
+  }
   if (P.kept)
     for (int t = n + rank * kEvThreads + tid; t < P.budget; t += ncta * kEvThreads)
       P.kept[static_cast<size_t>(b) * P.budget + t] = -1;
@@ -399,12 +460,14 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   // every CTA has read seq_lens (new_lens may be the same array) and s_bad,
   // s_cta of its neighbours before any of them goes
   cluster.sync();
-  if (rank == 0 && tid == 0) {
-    uint32_t bits = bad_len ? kDevBounds : 0u;
-    for (int c = 0; c < ncta; ++c) bits |= *cluster.map_shared_rank(&s_bad, c) ? kDevBounds : 0u;
-    P.flags[b] = bits;
-    P.moves[b] = moves;
-    P.new_lens[b] = n;
+  if (rank == 0 && warp == 0) {
+    const bool bad = lane < ncta && *cluster.map_shared_rank(&s_bad, lane);
+    const bool any = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      P.flags[b] = bad_len || any ? kDevBounds : 0u;
+      P.moves[b] = moves;
+      P.new_lens[b] = n;
+    }
   }
   cluster.sync();
 }
@@ -498,7 +561,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 lrkv_status evict_check(int batch, int max_len, int budget) {
   if (batch < 1 || max_len < 1 || budget < 1 || budget > max_len) return LRKV_ERR_INVALID_ARG;
-  if (batch > kMaxBatch || static_cast<long long>(batch) * max_len > (1LL << 31) - 1) return LRKV_ERR_UNSUPPORTED;
+  if (batch > kMaxBatch || static_cast<long long>(batch) * max_len > (1LL << 31) - (1 << 16))  // row numbers rounded up stay in 32 bits return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }
 
@@ -511,19 +574,23 @@ size_t evict_layout(EvictParams& P, void* ws) {
   const size_t off_moves = off; off += up256(static_cast<size_t>(P.B) * 4);
   const size_t off_src = off; off += list;
   const size_t off_dst = off; off += list;
+  const size_t off_masks = off; off += up256(static_cast<size_t>(P.B) * 2 * ((static_cast<size_t>(P.max_len) + 31) / 32) * 4);
   if (ws) {
     P.status = reinterpret_cast<uint32_t*>(base);
     P.flags = reinterpret_cast<uint32_t*>(base + off_flags);
     P.moves = reinterpret_cast<int32_t*>(base + off_moves);
     P.src = reinterpret_cast<int2*>(base + off_src);
     P.dst = reinterpret_cast<int2*>(base + off_dst);
+    P.masks = reinterpret_cast<uint32_t*>(base + off_masks);
   }
   return off;
 }
 
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int select_smem_max = kEvCacheRows * 4;
+// Shared memory of the selection for `rows` cached rows: a key and two bits each.
+constexpr int select_smem(int rows) { return rows * 4 + rows / 16 * 4; }
+constexpr int select_smem_max = select_smem(kEvCacheRows);
 
 // Whether a cluster of kEvMaxCluster selection CTAs (more than the portable 8:
 // the kernel's opt-in is set here) can run on the current device.
@@ -631,7 +698,7 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   const int step = 32 * kEvWarps;
   P.rows_per_cta = ((P.max_len + ncta - 1) / ncta + step - 1) / step * step;
   P.cached = P.rows_per_cta <= kEvCacheRows;
-  const int smem = P.cached ? P.rows_per_cta * 4 : 0;
+  const int smem = P.cached ? select_smem(P.rows_per_cta) : 0;
   const void* select = reinterpret_cast<const void*>(&lrkv_evict_select_kernel);
   // (the kernel's static tables count towards the 48 KB that need no attribute)
   if (ensure_kernel_smem(select, select_smem_max) != cudaSuccess) return LRKV_ERR_CUDA;
