@@ -13,19 +13,21 @@
 // k-th into the k-th.  That moves the fewest rows there can be, no row is both
 // read and written, and all moves run at once.
 //
-// Measured: 32 x 4097 rows to 4096 22 us a call (17 us of the selection's
-// dependent passes); 8 x 9-16K rows to 4096 95 us, 304 MB of moves at 4.7 TB/s
-// behind a 21 us selection; 256K rows to 32K 113 us, half of it the selection,
-// whose 16 CTAs spend most on the first counting pass and on the lists.
+// Measured: 32 x 4097 rows to 4096 22 us a call (the selection's dependent
+// passes and the call's own host time); 8 x 9-16K rows to 4096 79 us, 304 MB of
+// moves at 5.3 TB/s behind a 22 us selection; 256K rows to 32K 86 us, half of it
+// the selection: three cluster-wide counts at ~6.5K cycles each, the rest its
+// passes over 16K rows a CTA.
 //
 // 1. lrkv_evict_select_kernel, one cluster of CTAs per sequence: a radix
 //    selection (11 + 11 + 10 bits) of the order-preserving integer image of
 //    the weights finds the smallest kept value, each CTA counting its rows in
 //    shared memory and the cluster adding the counts up through distributed
-//    shared memory; then ballots and one prefix over the warps of the cluster
-//    rank equal values, holes and moved rows.
-// 2. lrkv_evict_move_kernel copies each moved row: 4 cache tensors, key
-//    scales, positions, weight, age.
+//    shared memory; then a bit per row and prefixes over words, warps and the
+//    cluster rank equal values, holes and moved rows.
+// 2. lrkv_evict_move_kernel copies each moved row: 4 cache tensors (bulk copies
+//    through shared memory; through registers, 16 bytes a thread, the same moves
+//    ran at 4.2 TB/s), key scales, positions, weight, age.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,8 +56,9 @@ constexpr int kEvBins = 2048;          // 11 bits a level (the last level uses 1
 constexpr int kEvMaxCluster = 16;      // (more than 8 needs the kernel's opt-in)
 constexpr int kEvCacheRows = 40 * 1024;  // rows whose keys a CTA keeps in shared memory
 constexpr int kEvUnroll = 4;             // rows a thread has in flight per pass
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;             // rows a CTA moves at a time
+constexpr int kMoveWarps = 32;           // warps of a moving CTA at most, a slot of shared memory each
+constexpr int kMoveSmem = 216 * 1024;    // of the slots
+constexpr int kMoveSlotMax = 27 * 1024;  // bytes of a slot at most (longer rows go in parts)
 constexpr uint32_t kKeyHeld = 0xffffffffu;  // above every weight's key
 constexpr uint32_t kKeyOut = 0u;            // below every weight's key
 
@@ -81,6 +84,7 @@ struct EvictParams {
   int2* dst;               // [B][cap] (logical, physical) row of the k-th hole
   uint32_t* masks;         // [B][2][ceil(max_len / 32)] row masks (when not in shared memory)
   // moved data
+  int slot;                // bytes of a moving warp's slot (a multiple of 128)
   int n16[4];              // 16-byte pieces of a row of each cache tensor
   unsigned char* base[4];
   int H, axes;
@@ -464,6 +468,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
     const bool bad = lane < ncta && *cluster.map_shared_rank(&s_bad, lane);
     const bool any = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
+      if (b == 0) *P.status = 0u;
       P.flags[b] = bad_len || any ? kDevBounds : 0u;
       P.moves[b] = moves;
       P.new_lens[b] = n;
@@ -472,85 +477,113 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   cluster.sync();
 }
 
-// Four moved rows per CTA turn: their 16-byte pieces across the four cache
-// tensors, eight in flight per thread (one row at a time kept too few bytes in
-// flight: 2.7 TB/s), and the per-row data by a thread each.
-// It lets no dependent start early: a decode launched next reads the cache at
-// once, before it waits for the launch before it.
-__global__ void __launch_bounds__(kMoveThreads) lrkv_evict_move_kernel(const EvictParams P) {
+// Bulk copies by one thread: shared -> global, and the waits for its stores to
+// have been read out of shared memory, and to be complete.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src_smem)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// A warp per moved row and turn: its cache rows go through the warp's slot of
+// shared memory as bulk copies (no registers hold them, and up to 216 KB of an SM
+// are under way), its per-row data by the lanes meanwhile.  A row longer than a
+// slot goes in parts.  It lets no dependent start early: a decode launched next
+// reads the cache at once, before it waits for the launch before it.
+__global__ void __launch_bounds__(32 * kMoveWarps, 1) lrkv_evict_move_kernel(const EvictParams P) {
+  extern __shared__ __align__(128) unsigned char s_rows[];  // [warps][slot]
+  __shared__ uint64_t full[kMoveWarps];
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) {
+    mbar_init(&full[warp], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
   pdl_wait();
-  const int b = blockIdx.y, tid = threadIdx.x;
+  asm volatile("fence.proxy.async.global;" ::: "memory");  // rows of earlier kernels' plain stores, read by bulk copies
   const int m = P.moves[b];
-  const int n0 = P.n16[0], n1 = n0 + P.n16[1], n2 = n1 + P.n16[2], n3 = n2 + P.n16[3];
+  long long at[5] = {0};  // where each tensor's part of a row begins, in bytes
+#pragma unroll
+  for (int s = 0; s < 4; ++s) at[s + 1] = at[s] + 16ll * P.n16[s];
   const size_t row0 = static_cast<size_t>(b) * P.max_len;
   const int2* src = P.src + static_cast<size_t>(b) * P.cap;
   const int2* dst = P.dst + static_cast<size_t>(b) * P.cap;
-  for (int k0 = blockIdx.x * kMoveRows; k0 < m; k0 += gridDim.x * kMoveRows) {
-    const int rows = min(kMoveRows, m - k0);
-    int2 from[kMoveRows], to[kMoveRows];
+  unsigned char* slot = s_rows + static_cast<size_t>(warp) * P.slot;
+  uint32_t phase = 0;
+  bool ok = true;
+  const int stride = gridDim.x * warps;
+  int k = blockIdx.x * warps + warp;
+  int2 from = make_int2(-1, -1), to = from;
+  if (k < m) {
+    from = src[k];
+    to = dst[k];
+  }
+  while (k < m && ok) {
+    const int f = from.x, d = to.x;
+    const bool paged_in = from.y >= 0 && to.y >= 0;
+    const size_t fp = static_cast<size_t>(max(from.y, 0)), dp = static_cast<size_t>(max(to.y, 0));
+    k += stride;
+    bool rest = true;  // the per-row data and the next row's numbers are to do
+    for (long long c0 = 0; c0 < at[4] && ok; c0 += P.slot) {
+      const long long c1 = min(c0 + P.slot, at[4]);
+      if (paged_in && lane == 0) {
+        bulk_wait_read();
+        mbar_arrive_expect_tx(&full[warp], static_cast<uint32_t>(c1 - c0));
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-      from[i] = to[i] = make_int2(-1, -1);
-      if (i < rows) {
-        from[i] = src[k0 + i];
-        to[i] = dst[k0 + i];
-      }
-    }
-    // piece p of a row, for every row: the same tensor and offset
-    for (int p0 = tid; p0 < n3; p0 += 2 * kMoveThreads) {
-      uint4 v[2][kMoveRows];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int p = p0 + u * kMoveThreads;
-        if (p < n3) {
-          const int s = p < n0 ? 0 : p < n1 ? 1 : p < n2 ? 2 : 3;
-          const size_t width = static_cast<size_t>(P.n16[s]) * 16;
-          const unsigned char* at = P.base[s] + 16 * static_cast<size_t>(p - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2));
-#pragma unroll
-          for (int i = 0; i < kMoveRows; ++i)
-            if (from[i].y >= 0 && to[i].y >= 0) v[u][i] = *reinterpret_cast<const uint4*>(at + from[i].y * width);
+        for (int s = 0; s < 4; ++s) {
+          const long long a = max(c0, at[s]), e = min(c1, at[s + 1]);
+          if (a < e)
+            tma_load_1d(slot + (a - c0), P.base[s] + fp * (at[s + 1] - at[s]) + (a - at[s]),
+                        static_cast<uint32_t>(e - a), &full[warp]);
         }
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int p = p0 + u * kMoveThreads;
-        if (p < n3) {
-          const int s = p < n0 ? 0 : p < n1 ? 1 : p < n2 ? 2 : 3;
-          const size_t width = static_cast<size_t>(P.n16[s]) * 16;
-          unsigned char* at = P.base[s] + 16 * static_cast<size_t>(p - (s == 0 ? 0 : s == 1 ? n0 : s == 2 ? n1 : n2));
-#pragma unroll
-          for (int i = 0; i < kMoveRows; ++i)
-            if (from[i].y >= 0 && to[i].y >= 0) *reinterpret_cast<uint4*>(at + to[i].y * width) = v[u][i];
+      if (rest) {
+        rest = false;
+        if (k < m) {
+          from = src[k];
+          to = dst[k];
         }
+        if (P.key_scale)
+          for (int h = lane; h < P.H; h += 32) {
+            float* row = P.key_scale + (static_cast<size_t>(b) * P.H + h) * P.max_len;
+            row[d] = row[f];
+          }
+        if (P.positions && lane < P.axes) P.positions[(row0 + d) * P.axes + lane] = P.positions[(row0 + f) * P.axes + lane];
+        if (lane == 4) P.weights_out[row0 + d] = P.weights[row0 + f];
+        if (lane == 5 && P.order_out) P.order_out[row0 + d] = P.order ? P.order[row0 + f] : f;
+        if (lane == 6 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + d] = f;
       }
-    }
-    if (P.key_scale)
-      for (int h = tid; h < P.H; h += kMoveThreads) {
-        float* row = P.key_scale + (static_cast<size_t>(b) * P.H + h) * P.max_len;
-        float v[kMoveRows];
+      if (!paged_in) break;
+      ok = mbar_wait_bounded(&full[warp], phase & 1u);
+      ok = __all_sync(0xffffffffu, ok);
+      ++phase;
+      if (ok && lane == 0) {
 #pragma unroll
-        for (int i = 0; i < kMoveRows; ++i)
-          if (i < rows) v[i] = row[from[i].x];
-#pragma unroll
-        for (int i = 0; i < kMoveRows; ++i)
-          if (i < rows) row[to[i].x] = v[i];
+        for (int s = 0; s < 4; ++s) {
+          const long long a = max(c0, at[s]), e = min(c1, at[s + 1]);
+          if (a < e)
+            bulk_store(P.base[s] + dp * (at[s + 1] - at[s]) + (a - at[s]), slot + (a - c0), static_cast<uint32_t>(e - a));
+        }
+        bulk_commit();
       }
-#pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-      if (i >= rows) break;
-      const int f = from[i].x, d = to[i].x;
-      if (P.positions && tid < P.axes) P.positions[(row0 + d) * P.axes + tid] = P.positions[(row0 + f) * P.axes + tid];
-      if (tid == 32) P.weights_out[row0 + d] = P.weights[row0 + f];
-      if (tid == 64 && P.order_out) P.order_out[row0 + d] = P.order ? P.order[row0 + f] : f;
-      if (tid == 96 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + d] = f;
     }
   }
-  if (blockIdx.x == 0 && b == 0 && tid < 32) {
+  if (lane == 0) {
+    bulk_wait_all();
+    if (!ok) {
+      mbar_wait_bounded(&full[warp], (phase - 1u) & 1u);  // a late copy lands before the block ends
+      atomicOr(P.status, kDevTimeout);
+    }
+  }
+  if (blockIdx.x == 0 && b == 0 && warp == 0) {
     uint32_t bits = 0u;
-    for (int i = tid; i < P.B; i += 32) bits |= P.flags[i];
+    for (int i = lane; i < P.B; i += 32) bits |= P.flags[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
-    if (tid == 0) *P.status = bits;
+    if (lane == 0 && bits) atomicOr(P.status, bits);  // (the selection cleared it)
   }
 }
 
@@ -561,7 +594,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 lrkv_status evict_check(int batch, int max_len, int budget) {
   if (batch < 1 || max_len < 1 || budget < 1 || budget > max_len) return LRKV_ERR_INVALID_ARG;
-  if (batch > kMaxBatch || static_cast<long long>(batch) * max_len > (1LL << 31) - (1 << 16))  // row numbers rounded up stay in 32 bits return LRKV_ERR_UNSUPPORTED;
+  // row numbers rounded up to a CTA's stay in 32 bits
+  if (batch > kMaxBatch || static_cast<long long>(batch) * max_len > (1LL << 31) - (1 << 16)) return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }
 
@@ -688,9 +722,10 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   if (sms < 1) return LRKV_ERR_CUDA;
 
   // CTAs per sequence: more while the sequences leave SMs idle and a CTA has
-  // more than 6144 rows.  8 x 16K rows: 99 us with 2 CTAs each (8192 rows),
-  // 95 us with 4, 94 us with 8, 120 us with 16; 32 x 4.3K rows: 22.0 us with
-  // one, 24 us with 2 or 4 (the cluster's exchanges cost more than the passes).
+  // more than 6144 rows.  8 x 16K rows (when the moves took 72 us of it): 99 us
+  // with 2 CTAs each (8192 rows), 95 us with 4, 94 us with 8, 120 us with 16; 32 x
+  // 4.3K rows: 22.0 us with one, 24 us with 2 or 4 (the cluster's exchanges cost
+  // more than the passes).
   int ncta = 1;
   while (ncta < kEvMaxCluster && 2LL * ncta * P.B <= sms && P.max_len > 6144LL * ncta) ncta *= 2;
   // 16 CTAs need an SM group that holds them all: asked once per device
@@ -716,12 +751,18 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, lrkv_evict_select_kernel, P) != cudaSuccess) return LRKV_ERR_CUDA;
-  // enough CTAs to fill the SMs eight times over, at least one per sequence
-  const long long per_seq = std::max(1LL, (8LL * sms + P.B - 1) / P.B);
-  const long long turns = (P.cap + kMoveRows - 1) / kMoveRows;
+  // the move: as many warps as slots of a whole row fit, two CTAs per SM over all
+  // sequences (one runs at a time, the second evens out the sequences)
+  const long long row_bytes = 2 * (shared + latent);
+  P.slot = static_cast<int>(std::min<long long>(kMoveSlotMax, (row_bytes + 127) / 128 * 128));
+  const int warps = std::min(kMoveWarps, kMoveSmem / P.slot);
+  if (ensure_kernel_smem(reinterpret_cast<const void*>(&lrkv_evict_move_kernel), kMoveSmem) != cudaSuccess)
+    return LRKV_ERR_CUDA;
+  const long long per_seq = std::max(1LL, (2LL * sms + P.B - 1) / P.B);
+  const long long turns = (P.cap + warps - 1) / warps;
   cfg.gridDim = dim3(static_cast<unsigned>(std::max(1LL, std::min(turns, per_seq))), P.B);
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = warps * P.slot;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, lrkv_evict_move_kernel, P) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
 }

@@ -717,7 +717,7 @@ lrkv_status prompt_check(const lrkv_dims* d, int window) {
   if (d->dtype != LRKV_BF16 || (d->head_dim != 64 && d->head_dim != 128) || d->rank % 8 != 0 || d->rank > 64)
     return LRKV_ERR_UNSUPPORTED;
   if (d->batch > kMaxBatch || d->heads > 256 || window > d->max_len ||
-      static_cast<long long>(d->batch) * d->max_len > (1LL << 31) - 1)
+      static_cast<long long>(d->batch) * d->max_len > (1LL << 31) - (1 << 16))  // rows rounded up stay in 32 bits
     return LRKV_ERR_UNSUPPORTED;
   return LRKV_OK;
 }
