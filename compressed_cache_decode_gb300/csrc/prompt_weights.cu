@@ -35,9 +35,11 @@
 // A window of one tile (ONE) uses each latent box once: it stays in shared memory
 // as the A operand, and its TMEM takes a second k_s buffer, so the next item's
 // keys are moved during this one.  4 x 16K keys of 32 heads, rank 64, window 32
-// (277 MB, 41.5 us at the copy rate): 115 us with the boxes moved, 95 us so.  There
+// (277 MB, 41.5 us at the copy rate): 115 us with the boxes moved, 82 us so.  There
 // the N = 32 products of one head each bound it; four issuing threads, each with
-// half of a tile's heads, took 106 us.
+// half of a tile's heads, took 106 us where two took 95.  For the long windows the
+// boxes moved to TMEM are better: read from shared memory for each of a head's
+// tiles, even with the TMEM they free as a third accumulator, 233 us for 217.
 //
 // Persistent: one CTA per SM walks the items, those with the most queries (the
 // first keys) first and dealt in a snake; the rings run on across items.
@@ -367,28 +369,44 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- key boxes: k_s of both halves per item (ONE: not here), then the
-      // heads' latents one after another, both halves of each -----------------------
-      int ai = 0, z0 = 0, z1 = 0;  // boxes issued; ONE: of either half
+    if (ONE && lane == 0) {
+      // ---- the heads' latents one after another, both halves of each --------------
+      int zi[2] = {0, 0};
+      bool live = true;
+      Walk w;
+      for (bool more = w.first(P); more && live && !*fail; more = w.next(P))
+        for (int i = 0; P.r > 0 && i < P.hg && live; ++i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (m >= w.halves) break;
+            const int s = m * (kPwA / 2) + zi[m] % (kPwA / 2), u = zi[m] / (kPwA / 2);  // slot, use of it
+            live = live && (u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u));
+            if (!live) {
+              *fail = 1;
+              break;
+            }
+            copy_box(w, m, -1 - (w.h0 + i), s_aring + s * kPwBox, &afull[s]);
+            ++zi[m];
+            s_use[s] = u + 1;
+          }
+    } else if (lane == 0) {
+      // ---- key boxes: k_s of both halves per item, then the heads' latents --------
+      int ai = 0;
       bool live = true;
       Walk w;
       for (bool more = w.first(P); more && live && !*fail; more = w.next(P)) {
-        const int nk = ONE ? 0 : w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
+        const int nk = w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
         for (int i = 0; i < nk + nz; ++i) {
-          const bool is_k = i < nk;
-          const int m = is_k ? i / NB : (i - nk) % w.halves;
-          const int z = m ? z1 : z0;
-          const int s = ONE ? m * (kPwA / 2) + z % (kPwA / 2) : ai % kPwA;
-          const int u = ONE ? z / (kPwA / 2) : ai / kPwA;  // use of the slot
+          const int s = ai % kPwA, u = ai / kPwA;  // slot, use of it
           live = u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u);
           if (!live) {
             *fail = 1;
             break;
           }
-          copy_box(w, m, is_k ? i % NB : -1 - (w.h0 + (i - nk) / w.halves), s_aring + s * kPwBox, &afull[s]);
+          const bool is_k = i < nk;
+          copy_box(w, is_k ? i / NB : (i - nk) % w.halves, is_k ? i % NB : -1 - (w.h0 + (i - nk) / w.halves),
+                   s_aring + s * kPwBox, &afull[s]);
           ++ai;
-          (m ? z1 : z0) = z + 1;
           s_use[s] = u + 1;
         }
       }
@@ -552,16 +570,18 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     Walk w;
     for (bool more = w.first(P); more; more = w.next(P)) {
       const int buf = w.n % KB;
-      ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
-      tc_fence_after();
-      for (int i = 0; i < w.halves * NB; ++i) {
-        if (ONE) {
-          // one box at a time, an item ahead of the MMAs: copied by the first of
-          // these warps once all four have read the one before
+      if (ONE) {
+        for (int i = 0; i < w.halves * NB; ++i, ++ai) {
+          // one box at a time, copied by the first of these warps once all four have
+          // read the one before; the first is under way before its place in TMEM is free
           asm volatile("bar.sync 2, 128;" ::: "memory");
           if (warp == 4 && lane == 0 && ok && !*fail) {
             copy_box(w, i / NB, i % NB, s_kbox, &kfull);
             s_k = ai + 1;
+          }
+          if (i == 0) {
+            ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
+            tc_fence_after();
           }
           ok = ok && !*fail && mbar_wait_bounded(&kfull, static_cast<uint32_t>(ai) & 1u);
           ok = __all_sync(0xffffffffu, ok);
@@ -569,10 +589,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             to_tmem(s_kbox, kColK + buf * 128 + i * 32);
           else
             *fail = 1;
-          ++ai;
-        } else {
-          move(kColK + i * 32);
         }
+      } else {
+        ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
+        tc_fence_after();
+        for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
       }
       tc_fence_before();
       __syncwarp();
