@@ -933,6 +933,17 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         // hold non-finite bits there (unwritten rows), where 0 x NaN must not
         // reach the sums: that tile (and the warm-up pass) zeroes those
         // tokens' operand halves, every other tile runs unmasked.
+        // (W: a tile's three parts are summed apart, the smallest first, and added to
+        // the running sums by an fp32 addition: the tensor cores' sums are cut short,
+        // which over some hundred tiles cost 1.5e-6 to 3e-6 of the outputs; so 4e-7)
+        [[maybe_unused]] auto mma_parts = [&](float (&acc)[4], const uint32_t (&a)[4]) {
+          float t[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_bf16_16816(t, a[0], a[1], a[2], a[3], pm0, pm1);
+          mma_bf16_16816(t, a[0], a[1], a[2], a[3], pl0, pl1);
+          mma_bf16_16816(t, a[0], a[1], a[2], a[3], pb0, pb1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += t[e];
+        };
         auto values = [&](auto masked) {
           constexpr bool M = decltype(masked)::value;
           const uint32_t k0 = M ? keep0 : 0xffffffffu, k1 = M ? keep1 : 0xffffffffu;
@@ -948,17 +959,18 @@ __global__ void __launch_bounds__(kThreadsS, 1)
               if (M) {
                 a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
               }
-              mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
-              if constexpr (W) {
-                mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
-                mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pm0, pm1);
-              }
+              if constexpr (W)
+                mma_parts(acc_v[n0 + u], a[u]);
+              else
+                mma_bf16_16816(acc_v[n0 + u], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
             }
           }
           // private values, per head group: O_z,grp^T += Z_v,grp^T P^T with
           // P^T kept in the group's columns only (this lane's column g)
           if (PH) {
             const unsigned char* zvb = zv + trow * zrow + tcol * 16;
+            // W: the tile's sums (each column belongs to one group)
+            [[maybe_unused]] float tz[W ? NZH : 1][4] = {};
 #pragma unroll
             for (int h = 0; h < 8; h += GH) {
               const bool own = g / GH == h / GH;
@@ -974,12 +986,20 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                 if (M) {
                   a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
                 }
-                mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
                 if constexpr (W) {
-                  mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], c0, c1);
-                  mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], e0, e1);
+                  mma_bf16_16816(tz[u], a[u][0], a[u][1], a[u][2], a[u][3], e0, e1);
+                  mma_bf16_16816(tz[u], a[u][0], a[u][1], a[u][2], a[u][3], c0, c1);
+                  mma_bf16_16816(tz[u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
+                } else {
+                  mma_bf16_16816(acc_z[u], a[u][0], a[u][1], a[u][2], a[u][3], b0, b1);
                 }
               }
+            }
+            if constexpr (W) {
+#pragma unroll
+              for (int u = 0; u < NZH; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc_z[u][e] += tz[u][e];
             }
           } else if (MZMAX > 0) {
             // private values: O_z^T += Z_v^T P^T over this half's latent columns
@@ -997,11 +1017,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
                   if (M) {
                     a[u][0] &= k0; a[u][1] &= k0; a[u][2] &= k1; a[u][3] &= k1;
                   }
-                  mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
-                  if constexpr (W) {
-                    mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pl0, pl1);
-                    mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pm0, pm1);
-                  }
+                  if constexpr (W)
+                    mma_parts(acc_z[(n0 + u) % NZV], a[u]);
+                  else
+                    mma_bf16_16816(acc_z[(n0 + u) % NZV], a[u][0], a[u][1], a[u][2], a[u][3], pb0, pb1);
                 }
             }
           }
