@@ -324,6 +324,13 @@ __global__ void __launch_bounds__(kRThreads, 1)
 #pragma unroll
       for (int x = 0; x < kMaxAxes; ++x) pos[x] = there && x < A.ax.n ? __ldg(at + x) : 0;
     };
+    // byte offsets, 4 bits each, of the axes of this lane's two pairs of every chunk
+    uint32_t axis_at = 0u;
+#pragma unroll
+    for (int ch = 0; ch < HP / 8; ++ch) {
+      const int k = half * HP + 8 * ch + 2 * q4;
+      axis_at |= static_cast<uint32_t>(4 * A.ax.axis(k) | 4 * A.ax.axis(k + 1) << 4) << (8 * ch);
+    }
     bool more = walk_first(w, pre, B, g0, g1);
     if (more) positions_of(w);
     for (; more; ++j) {
@@ -351,20 +358,27 @@ __global__ void __launch_bounds__(kRThreads, 1)
       *reinterpret_cast<int4*>(stage + lane * kRStage) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       __syncwarp();
       float4 e[HP / 8][4];
+      const float* table = P.rope_cs + 2 * (half * HP + 2 * q4);  // this lane's two pairs of chunk 0
+      if (A.even) {
 #pragma unroll
-      for (int ch = 0; ch < HP / 8; ++ch) {
-        const int k = half * HP + 8 * ch + 2 * q4;  // this lane's two pairs
-        const unsigned char* pa = stage + g * kRStage + 4 * A.ax.axis(k);
-        const unsigned char* pb = stage + g * kRStage + 4 * A.ax.axis(k + 1);
+        for (int ch = 0; ch < HP / 8; ++ch) {
+          const unsigned char* pa = stage + g * kRStage + (axis_at >> (8 * ch) & 0xfu);
 #pragma unroll
-        for (int r8 = 0; r8 < 4; ++r8) {
-          const float* ta = P.rope_cs + static_cast<size_t>(*reinterpret_cast<const int*>(pa + 8 * r8 * kRStage)) * DH + 2 * k;
-          if (A.even) {
-            e[ch][r8] = __ldg(reinterpret_cast<const float4*>(ta));
-          } else {
-            const float* tb = P.rope_cs + static_cast<size_t>(*reinterpret_cast<const int*>(pb + 8 * r8 * kRStage)) * DH + 2 * k;
-            const float2 a = __ldg(reinterpret_cast<const float2*>(ta));
-            const float2 b = __ldg(reinterpret_cast<const float2*>(tb + 2));
+          for (int r8 = 0; r8 < 4; ++r8)
+            e[ch][r8] = __ldg(reinterpret_cast<const float4*>(
+                table + static_cast<size_t>(*reinterpret_cast<const int*>(pa + 8 * r8 * kRStage)) * DH + 16 * ch));
+        }
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < HP / 8; ++ch) {
+          const unsigned char* pa = stage + g * kRStage + (axis_at >> (8 * ch) & 0xfu);
+          const unsigned char* pb = stage + g * kRStage + (axis_at >> (8 * ch + 4) & 0xfu);
+#pragma unroll
+          for (int r8 = 0; r8 < 4; ++r8) {
+            const size_t ra = static_cast<size_t>(*reinterpret_cast<const int*>(pa + 8 * r8 * kRStage)) * DH;
+            const size_t rb = static_cast<size_t>(*reinterpret_cast<const int*>(pb + 8 * r8 * kRStage)) * DH;
+            const float2 a = __ldg(reinterpret_cast<const float2*>(table + ra + 16 * ch));
+            const float2 b = __ldg(reinterpret_cast<const float2*>(table + rb + 16 * ch + 2));
             e[ch][r8] = make_float4(a.x, a.y, b.x, b.y);
           }
         }
