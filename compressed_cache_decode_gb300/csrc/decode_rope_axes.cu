@@ -30,18 +30,21 @@
 // columns for the four heads and the latents of one head (mma.sync; the
 // probabilities as three bf16 parts in free columns of the B operand).
 //
-// Measured on 4 x 32K rows (32 heads, rank 48): 393 us, the cache at 2.2 TB/s,
-// 13.5K cycles a tile and CTA where its bytes need 4.6K.  What bounds it is the
-// score warps' latency: a tile's gather (positions, table entries, the exchange
-// through shared memory) takes 4.4K cycles in a row and a head's 32 pairs 1.4K
-// for ~220 instructions, with two such warps per scheduler and no registers left
-// to overlap them.
+// Measured on 4 x 32K rows (32 heads, rank 48): 364 us, the cache at 2.4 TB/s,
+// ~12K cycles a tile and CTA where its bytes need 4.6K.  The score warps and the
+// value warps are both at work nearly all of that time, each waiting on its own
+// chains: the scores' gather (positions, table entries, the exchange through
+// shared memory) takes 3K cycles of a tile and a head's 32 pairs ~2K, the values
+// 900 per 16 rows for ten dependent mma.sync.  What was tried and was slower: the
+// shared part added by the tensor core (a unit operand, 411 us for 375), TMEM read
+// 16 columns ahead of the sums (401 for 375), masks on every tile's values (375).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "decode_common.cuh"
 #include "decode_plan.h"
@@ -602,61 +605,73 @@ __global__ void __launch_bounds__(kRThreads, 1)
       for (int e = 0; e < MS; ++e) ts[e][0] = ts[e][1] = ts[e][2] = ts[e][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < MZ; ++e) tz[e][0] = tz[e][1] = tz[e][2] = tz[e][3] = 0.f;
+      auto products = [&](auto masked) {
+        constexpr bool M = decltype(masked)::value;
 #pragma unroll
-      for (int sub = 0; sub < kRT / kRSub; ++sub) {
-        if (sub * kRSub >= nvalid) break;
-        const int slot = vi % A.nv;
-        ok = ok && !*fail && mbar_wait_bounded(&vfull[slot], static_cast<uint32_t>(vi / A.nv) & 1u, P.wait_limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          const unsigned char* vsm = smem + A.off_v + slot * A.vt_bytes;
-          const unsigned char* zsm = vsm + A.zv_off + zoff;
+        for (int sub = 0; sub < kRT / kRSub; ++sub) {
+          if (sub * kRSub >= nvalid) break;
+          const int slot = vi % A.nv;
+          ok = ok && !*fail && mbar_wait_bounded(&vfull[slot], static_cast<uint32_t>(vi / A.nv) & 1u, P.wait_limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const unsigned char* vsm = smem + A.off_v + slot * A.vt_bytes;
+            const unsigned char* zsm = vsm + A.zv_off + zoff;
 #pragma unroll
-          for (int t2 = 0; t2 < 2; ++t2) {
-            const int t = 2 * sub + t2;  // 16 rows
-            // three bf16 parts of the probabilities of rows 2 q4, + 1 (first word), + 8, + 9 (second)
-            uint32_t p1[2], p2[2], p3[2];
+            for (int t2 = 0; t2 < 2; ++t2) {
+              const int t = 2 * sub + t2;  // 16 rows
+              // three bf16 parts of the probabilities of rows 2 q4, + 1 (first word), + 8, + 9 (second)
+              uint32_t p1[2], p2[2], p3[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float x = s[4 * t + 2 * k], y = s[4 * t + 2 * k + 1];
-              p1[k] = pack_bf16(x, y);
-              const float x2 = x - bf_lo(p1[k]), y2 = y - bf_hi(p1[k]);
-              p2[k] = pack_bf16(x2, y2);
-              p3[k] = pack_bf16(x2 - bf_lo(p2[k]), y2 - bf_hi(p2[k]));
-            }
-            // column g: the high part of head g, the low part of head g - 4; then the third parts
-            const uint32_t b0 = g < 4 ? p1[0] : p2[0], b1 = g < 4 ? p1[1] : p2[1];
-            const uint32_t c0 = g < 4 ? p3[0] : 0u, c1 = g < 4 ? p3[1] : 0u;
-            // rows past the piece (which may hold anything) must not meet their
-            // zero probabilities as 0 x NaN
-            const int left = nvalid - 16 * t;
-            const uint32_t k0 = (2 * q4 < left ? 0x0000ffffu : 0u) | (2 * q4 + 1 < left ? 0xffff0000u : 0u);
-            const uint32_t k1 = (2 * q4 + 8 < left ? 0x0000ffffu : 0u) | (2 * q4 + 9 < left ? 0xffff0000u : 0u);
-            const int r = 16 * t2 + trow;
+              for (int k = 0; k < 2; ++k) {
+                const float x = s[4 * t + 2 * k], y = s[4 * t + 2 * k + 1];
+                p1[k] = pack_bf16(x, y);
+                const float x2 = x - bf_lo(p1[k]), y2 = y - bf_hi(p1[k]);
+                p2[k] = pack_bf16(x2, y2);
+                p3[k] = pack_bf16(x2 - bf_lo(p2[k]), y2 - bf_hi(p2[k]));
+              }
+              // column g: the high part of head g, the low part of head g - 4; then the third parts
+              const uint32_t b0 = g < 4 ? p1[0] : p2[0], b1 = g < 4 ? p1[1] : p2[1];
+              const uint32_t c0 = g < 4 ? p3[0] : 0u, c1 = g < 4 ? p3[1] : 0u;
+              // rows past the piece (which may hold anything) must not meet their
+              // zero probabilities as 0 x NaN
+              const int left = nvalid - 16 * t;
+              const uint32_t k0 = !M ? 0u : (2 * q4 < left ? 0x0000ffffu : 0u) | (2 * q4 + 1 < left ? 0xffff0000u : 0u);
+              const uint32_t k1 =
+                  !M ? 0u : (2 * q4 + 8 < left ? 0x0000ffffu : 0u) | (2 * q4 + 9 < left ? 0xffff0000u : 0u);
+              const int r = 16 * t2 + trow;
 #pragma unroll
-            for (int e = 0; e < MS; ++e) {
-              uint32_t x0, x1, x2, x3;
-              const int ch = 2 * (MS * v + e) + tcol;  // 16-byte chunk along the head dim
-              ldsm_x4_trans(x0, x1, x2, x3, vsm + (ch >> 3) * (kRSub * 128) + swz_off(r, ch & 7, 128));
-              x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
-              mma_bf16_16816(ts[e], x0, x1, x2, x3, b0, b1);
-              mma_bf16_16816(ts[e], x0, x1, x2, x3, c0, c1);
-            }
+              for (int e = 0; e < MS; ++e) {
+                uint32_t x0, x1, x2, x3;
+                const int ch = 2 * (MS * v + e) + tcol;  // 16-byte chunk along the head dim
+                ldsm_x4_trans(x0, x1, x2, x3, vsm + (ch >> 3) * (kRSub * 128) + swz_off(r, ch & 7, 128));
+                if (M) {
+                  x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
+                }
+                mma_bf16_16816(ts[e], x0, x1, x2, x3, b0, b1);
+                mma_bf16_16816(ts[e], x0, x1, x2, x3, c0, c1);
+              }
 #pragma unroll
-            for (int e = 0; e < MZ; ++e) {
-              uint32_t x0, x1, x2, x3;
-              ldsm_x4_trans(x0, x1, x2, x3, zsm + r * (P.segp * 2) + (16 * e + 8 * tcol) * 2);
-              x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
-              mma_bf16_16816(tz[e], x0, x1, x2, x3, b0, b1);
-              mma_bf16_16816(tz[e], x0, x1, x2, x3, c0, c1);
+              for (int e = 0; e < MZ; ++e) {
+                uint32_t x0, x1, x2, x3;
+                ldsm_x4_trans(x0, x1, x2, x3, zsm + r * (P.segp * 2) + (16 * e + 8 * tcol) * 2);
+                if (M) {
+                  x0 &= k0; x1 &= k0; x2 &= k1; x3 &= k1;
+                }
+                mma_bf16_16816(tz[e], x0, x1, x2, x3, b0, b1);
+                mma_bf16_16816(tz[e], x0, x1, x2, x3, c0, c1);
+              }
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(&vempty[slot]);
+          ++vi;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cta(&vempty[slot]);
-        ++vi;
-      }
+      };
+      if (nvalid < kRT)
+        products(std::true_type{});
+      else
+        products(std::false_type{});
 #pragma unroll
       for (int e = 0; e < MS; ++e)
 #pragma unroll
