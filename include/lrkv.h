@@ -522,7 +522,8 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
  * whose block names no page of the pool is not moved (its weight, age and
  * kept entry are) and sets LRKV_ERR_DEVICE_BOUNDS, as a length outside
  * [0, max_len], which is clamped, does.
- * dtype BF16 or F32; rows of a multiple of 16 bytes; 1 <= budget <= max_len;
+ * dtype BF16 or F32; rows of a multiple of 16 bytes; batch max_len at most
+ * 2^31 - 2^16 (for lrkv_prefill_weights too); 1 <= budget <= max_len;
  * sink, recent >= 0 and sink + recent <= budget; axes 1 .. 4 with positions, 0
  * without.  z_k, z_v may be NULL when rank == 0.  Workspace:
  * lrkv_evict_workspace_size() bytes, its status word set afresh.

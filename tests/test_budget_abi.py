@@ -168,6 +168,11 @@ def test_workspace_sizes():
     assert size("lrkv_evict_workspace_size", 2, 256, 0)[0] == BAD
     assert size("lrkv_evict_workspace_size", 2, 256, 257)[0] == BAD
     assert size("lrkv_evict_workspace_size", 5000, 256, 100)[0] == NO
+    # row numbers, rounded up to what a CTA takes, stay in 32 bits
+    assert size("lrkv_evict_workspace_size", 1, 2 ** 31 - 2 ** 16, 100)[0] == 0
+    assert size("lrkv_evict_workspace_size", 1, 2 ** 31 - 2 ** 16 + 1, 100)[0] == NO
+    assert size("lrkv_evict_workspace_size", 2, 2 ** 30, 100)[0] == NO
+    assert size("lrkv_prefill_weights_workspace_size", ctypes.byref(bf(B=1, r=0, L=2 ** 31 - 1)), 16)[0] == NO
     assert size("lrkv_decode_rope_axes_workspace_size", d)[0] == 0
     assert size("lrkv_decode_rope_axes_workspace_size", ctypes.byref(bf(r=28)))[0] == NO
     # a size that passes 32 bits

@@ -1,7 +1,7 @@
 """Around the calls that keep a cache inside a token budget: guard regions on
 every buffer they write, a captured graph of them replayed on other contents,
-two calls at once, waits that run out, and prompt windows of every tile shape
-and over many items per SM."""
+two calls at once, waits that run out, prompt windows of every tile shape and
+over many items per SM, evictions of long rows and from long sequences."""
 import pytest
 import torch
 
@@ -42,6 +42,23 @@ WINDOWS = [
 @pytest.mark.parametrize("shape", WINDOWS)
 def test_prefill_weights_of_every_tile_shape(shape):
     base.test_prefill_weights(shape)
+
+
+EVICTIONS = [
+    # B, H, d_h, r, max_len, lengths, budget, sink, recent, dtype, axes
+    (2, 64, 128, 64, 40, [40, 33], 12, 1, 2, "f32", 2),          # rows of 33 KB, moved in two parts
+    (1, 256, 64, 64, 24, [24], 10, 0, 3, "f32", 0),              # rows of 128 KB, moved in five
+    (3, 1, 8, 0, 5000, [5000, 4097, 2], 4096, 4, 16, "bf16", 0),  # rows of 32 bytes, no latents
+    (1, 1, 64, 8, 700000, [699999], 1000, 0, 10, "bf16", 0),     # 16 CTAs, more rows each than keys they keep
+    (80, 1, 16, 8, 42000, [42000 - 523 * b for b in range(80)], 40, 1, 9, "bf16", 1),  # the same, a CTA each
+]
+
+
+@pytest.mark.parametrize("shape", EVICTIONS)
+@pytest.mark.parametrize("ordered", [False, True])
+@pytest.mark.parametrize("page", [0, 1])
+def test_evict_long_rows_and_long_sequences(shape, ordered, page):
+    base.test_evict(shape, ordered, page)
 
 
 def _state(B=2, H=8, dh=128, r=48, Lm=400, lens=(400, 217), seed=5):
