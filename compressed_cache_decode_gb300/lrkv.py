@@ -677,28 +677,51 @@ def _check(device: int, *specs) -> None:
         raise ValueError("LRKV tensors must be on a CUDA device")
 
 
+def _raw_stream(stream) -> int:
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 class _On:
-    """The CUDA device `device` made current for a call (left alone when it is)."""
+    """The device of tensor `t` made current for a call, and the call's own
+    `stream` (None: the current one) for what the call allocates and fills: a
+    block of another stream's pool may still be in use there, and a fill on
+    another stream is in no order with the call."""
 
-    __slots__ = ("device", "before")
+    __slots__ = ("device", "before", "stream", "caller", "inner")
 
-    def __init__(self, device: int):
-        self.device = device
+    def __init__(self, t, stream=None):
+        self.device, self.stream = t.get_device(), stream
 
     def __enter__(self):
         self.before = torch.cuda.current_device()
         if self.before != self.device:
             torch.cuda.set_device(self.device)
+        self.inner = None
+        if self.stream is not None:
+            raw = _raw_stream(self.stream)
+            if raw != torch._C._cuda_getCurrentRawStream(self.device):
+                self.caller = torch.cuda.current_stream(self.device)
+                # (0 and 1 are the handles of the default stream)
+                self.inner = torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device) if raw > 1 else
+                                               torch.cuda.default_stream(self.device))
+                self.inner.__enter__()
+        return self
 
     def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
         if self.before != self.device:
             torch.cuda.set_device(self.before)
 
+    def own(self, t: torch.Tensor) -> torch.Tensor:
+        """t, made within this context, to be used on the caller's stream too."""
+        if self.inner is not None:
+            t.record_stream(self.caller)
+        return t
+
 
 def _stream_on(stream, device: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _raw_stream(stream)
 
 
 _U8, _F32, _I32 = torch.uint8, torch.float32, torch.int32
@@ -728,9 +751,7 @@ def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: f
     r = z_k.shape[-1] if z_k is not None else 0
     max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
     dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
-    if weights_out is None:
-        weights_out = weights if weights is not None else torch.zeros((B, max_len), dtype=torch.float32,
-                                                                      device=q.device)
+    weights_out = weights if weights_out is None else weights_out
     if out is None:
         out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
     if lse is None:
@@ -742,7 +763,9 @@ def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: f
            ("weights_out", weights_out, _F32, flat), ("key_scale", key_scale, _F32, (B, H, max_len)),
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))), ("out", out, _F32, (B, H, dh)),
            ("lse", lse, _F32, (B, H)))
-    with _On(dev):
+    with _On(q, stream) as on:
+        if weights_out is None:
+            weights_out = on.own(torch.zeros((B, max_len), dtype=torch.float32, device=q.device))
         if ws is None:
             ws = decode_weighted_workspace(dims, q.device)
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
@@ -772,16 +795,16 @@ def prefill_weights(q, k_s, z_k, b_k, lse, seq_lens, weights, window: int = 0, d
     max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
     dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
     window = int(window) or Tq
-    if weights_out is None:
-        weights_out = weights if weights is not None else torch.zeros((B, max_len), dtype=torch.float32,
-                                                                      device=q.device)
+    weights_out = weights if weights_out is None else weights_out
     dt, dev, flat = q.dtype, q.get_device(), (B, max_len)
     _check(dev, ("q", q, dt, (B, Tq, H, dh)), ("k_s", k_s, dt, rows + (dh,)), ("z_k", z_k, dt, rows + (H, r)),
            ("b_k", b_k, dt, (H, dh, r)), ("lse", lse, _F32, (B, H, Tq)), ("seq_lens", seq_lens, _I32, (B,)),
            ("weights", weights, _F32, flat), ("weights_out", weights_out, _F32, flat),
            ("key_scale", key_scale, _F32, (B, H, max_len)),
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))))
-    with _On(dev):
+    with _On(q, stream) as on:
+        if weights_out is None:
+            weights_out = on.own(torch.zeros((B, max_len), dtype=torch.float32, device=q.device))
         if ws is None:
             ws = prefill_weights_workspace(dims, window, q.device)
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
@@ -827,7 +850,7 @@ def evict(k_s, v_s, z_k, z_v, weights, seq_lens, budget: int, sink: int = 0, rec
            ("order_out", order_out, _I32, flat), ("new_lens", new_lens, _I32, (B,)),
            ("kept", kept, _I32, (B, int(budget))),
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))))
-    with _On(dev):
+    with _On(k_s):
         if ws is None:
             ws = evict_workspace(B, max_len, budget, k_s.device)
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
@@ -859,7 +882,7 @@ def rope_rotate(x, positions, cos_sin, sections, out=None, ws=None, stream=None)
     _check(dev, ("x", x, x.dtype, x.shape), ("positions", positions, _I32, (B, n, axes)),
            ("cos_sin", cos_sin, _F32, (max_pos, dh)), ("out", out, x.dtype, x.shape),
            ("ws", ws, _U8, ws.shape if ws is not None else None))
-    with _On(dev):
+    with _On(x):
         st = int(load().lrkv_rope_rotate(
             ctypes.byref(dims), n, _ptr(x), _ptr(positions), axes, _sections(sections), _ptr(cos_sin),
             max_pos, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(), _stream_on(stream, dev)))
@@ -894,7 +917,7 @@ def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, se
            ("positions", positions, _I32, (B, max_len, axes)), ("seq_lens", seq_lens, _I32, (B,)),
            ("weights", weights, _F32, flat), ("weights_out", weights_out, _F32, flat),
            ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
-    with _On(dev):
+    with _On(q_rot):
         if ws is None:
             ws = decode_rope_axes_workspace(dims, q_rot.device)
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
