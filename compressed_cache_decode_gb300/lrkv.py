@@ -752,10 +752,6 @@ def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: f
     max_len, page_size, num_pages, rows = _cache_rows(k_s, block_table, B)
     dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
     weights_out = weights if weights_out is None else weights_out
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     dt, dev, flat, z, basis = q.dtype, q.get_device(), (B, max_len), rows + (H, r), (H, dh, r)
     _check(dev, ("q", q, dt, (B, H, dh)), ("k_s", k_s, dt, rows + (dh,)), ("v_s", v_s, dt, rows + (dh,)),
            ("z_k", z_k, dt, z), ("z_v", z_v, dt, z), ("b_k", b_k, dt, basis), ("b_v", b_v, dt, basis),
@@ -766,8 +762,12 @@ def decode_weighted(q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, weights, decay: f
     with _On(q, stream) as on:
         if weights_out is None:
             weights_out = on.own(torch.zeros((B, max_len), dtype=torch.float32, device=q.device))
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
         if ws is None:
-            ws = decode_weighted_workspace(dims, q.device)
+            ws = on.own(decode_weighted_workspace(dims, q.device))
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_decode_weighted(
             ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s), _ptr(v_s),
@@ -806,7 +806,7 @@ def prefill_weights(q, k_s, z_k, b_k, lse, seq_lens, weights, window: int = 0, d
         if weights_out is None:
             weights_out = on.own(torch.zeros((B, max_len), dtype=torch.float32, device=q.device))
         if ws is None:
-            ws = prefill_weights_workspace(dims, window, q.device)
+            ws = on.own(prefill_weights_workspace(dims, window, q.device))
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_prefill_weights(
             ctypes.byref(dims), Tq, window, _ptr(q), page_size, num_pages, _ptr(block_table), _ptr(k_s),
@@ -850,9 +850,9 @@ def evict(k_s, v_s, z_k, z_v, weights, seq_lens, budget: int, sink: int = 0, rec
            ("order_out", order_out, _I32, flat), ("new_lens", new_lens, _I32, (B,)),
            ("kept", kept, _I32, (B, int(budget))),
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))))
-    with _On(k_s):
+    with _On(k_s, stream) as on:
         if ws is None:
-            ws = evict_workspace(B, max_len, budget, k_s.device)
+            ws = on.own(evict_workspace(B, max_len, budget, k_s.device))
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_evict(
             ctypes.byref(dims), int(budget), int(sink), int(recent), _ptr(weights), _ptr(order), _ptr(seq_lens),
@@ -876,13 +876,13 @@ def rope_rotate(x, positions, cos_sin, sections, out=None, ws=None, stream=None)
     B, n, H, dh = x.shape
     axes = len(sections)
     dims = make_dims(B, H, dh, 0, 1, x.dtype)
-    if out is None:
-        out = torch.empty_like(x)
     dev, max_pos = x.get_device(), cos_sin.shape[0]
     _check(dev, ("x", x, x.dtype, x.shape), ("positions", positions, _I32, (B, n, axes)),
            ("cos_sin", cos_sin, _F32, (max_pos, dh)), ("out", out, x.dtype, x.shape),
            ("ws", ws, _U8, ws.shape if ws is not None else None))
-    with _On(x):
+    with _On(x, stream) as on:
+        if out is None:
+            out = on.own(torch.empty_like(x))
         st = int(load().lrkv_rope_rotate(
             ctypes.byref(dims), n, _ptr(x), _ptr(positions), axes, _sections(sections), _ptr(cos_sin),
             max_pos, _ptr(out), _ptr(ws), 0 if ws is None else ws.numel(), _stream_on(stream, dev)))
@@ -906,10 +906,6 @@ def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, se
     r, max_len, axes = z_k.shape[-1], k_s.shape[1], len(sections)
     dims = make_dims(B, H, dh, r, max_len, q_rot.dtype, scale)
     weights_out = weights if weights_out is None else weights_out
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q_rot.device)
     dt, dev, flat, z, basis = q_rot.dtype, q_rot.get_device(), (B, max_len), (B, max_len, H, r), (H, dh, r)
     _check(dev, ("q_rot", q_rot, dt, (B, H, dh)), ("k_s", k_s, dt, (B, max_len, dh)),
            ("v_s", v_s, dt, (B, max_len, dh)), ("z_k", z_k, dt, z), ("z_v", z_v, dt, z), ("b_k", b_k, dt, basis),
@@ -917,9 +913,13 @@ def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, se
            ("positions", positions, _I32, (B, max_len, axes)), ("seq_lens", seq_lens, _I32, (B,)),
            ("weights", weights, _F32, flat), ("weights_out", weights_out, _F32, flat),
            ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
-    with _On(q_rot):
+    with _On(q_rot, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q_rot.device))
         if ws is None:
-            ws = decode_rope_axes_workspace(dims, q_rot.device)
+            ws = on.own(decode_rope_axes_workspace(dims, q_rot.device))
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_decode_rope_axes(
             ctypes.byref(dims), _ptr(q_rot), _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(b_k), _ptr(b_v),

@@ -2,7 +2,10 @@
 
 A call given `stream` while another stream is current: the weights that its
 caller did not pass are cleared on the call's stream (a fill on the current
-one is in no order with the kernels and may land after them).
+one is in no order with the kernels and may land after them), and its
+workspace and outputs come from that stream's pool (a block of the current
+stream's pool may still be read or written there, and is handed out again
+there as soon as the caller lets go of it, while the call still uses it).
 
 On the CPU the streams are fakes: a stack of raw handles stands for the
 current stream, and every allocation notes the handle it is made under."""
@@ -108,6 +111,26 @@ def test_weights_not_given_are_cleared_on_the_call_s_stream(fake, call, stream, 
     assert [s for _, s in fake.lib.calls] == [want] and fake.current == [HERE]
 
 
+CALLS = dict(
+    decode_weighted=(weighted, 4), prefill_weights=(prompt, 2),    # calls and the allocations of each
+    evict=(lambda t, s: lrkv.evict(t.k, t.k, t.z, t.z, t.weights, t.lens, 8, stream=s), 1),
+    rope_rotate=(lambda t, s: lrkv.rope_rotate(t.prompt, t.pos[:, :4].contiguous(), t.table, [16, 16], stream=s), 1),
+    decode_rope_axes=(lambda t, s: lrkv.decode_rope_axes(*t.decode, t.table, t.pos, [16, 16], t.lens, stream=s), 3))
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("stream, want", [(None, HERE), (HERE, HERE), (OWN, OWN)])
+def test_allocations_belong_to_the_call_s_stream(fake, call, stream, want):
+    t = _tensors()
+    fake.made.clear()
+    run, n = CALLS[call]
+    run(t, stream)
+    assert [on for _, _, on in fake.made] == [want] * n
+    assert [s for _, s in fake.lib.calls] == [want] and fake.current == [HERE]
+    # ... and are known to the allocator as used on the caller's stream too
+    assert fake.shared == ([(x.data_ptr(), HERE) for _, x, _ in fake.made] if want == OWN else [])
+
+
 # ------------------------------------------------------------------ on the GPU --
 
 @pytest.fixture
@@ -143,3 +166,33 @@ def test_weights_are_whole_while_the_current_stream_is_busy(case, call, raw):
         early = got.clone()
     torch.cuda.synchronize()
     assert torch.equal(early, want) and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+def test_a_dropped_workspace_is_not_handed_out_while_the_call_uses_it():
+    """Calls queued behind a busy stream of their own, their workspaces dropped at
+    once, while blocks of the same size are taken and filled on the current one."""
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    ensure_built()
+    B, H, dh, r, Lm, budget = 4, 8, 64, 32, 3000, 900
+    case = T.cuda(inputs.random_decode_case(seed=5, batch=B, heads=H, head_dim=dh, rank=r, max_len=Lm, dtype="bf16",
+                                            lens=[3000, 2999, 1500, 900]))
+    weights = torch.rand((B, Lm), generator=torch.Generator().manual_seed(1)).cuda()
+
+    def state():
+        return [case[k].clone() for k in ("k_s", "v_s", "z_k", "z_v")] + [weights.clone(), case["seq_lens"].clone()]
+
+    want, got = state(), state()
+    lrkv.evict(*want, budget, sink=1, recent=3)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    size = lrkv.evict_workspace(B, Lm, budget).numel()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    lrkv.evict(*got, budget, sink=1, recent=3, stream=s)
+    others = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    del others
