@@ -103,6 +103,18 @@ lrkv_status check_paging(const lrkv_dims* dims, const PagedCache& pc) {
 }
 
 
+// Whether the bases lie where the planned kernels read them in wide pieces: the
+// streaming scan takes b_k in bulk copies (16 bytes) or, where its ring has no
+// room for them, in 8-byte loads; the narrow merge reads short rows of b_v as
+// 32-bit words.  The other paths load single elements.
+bool bases_aligned(const lrkv::DecodePlan& P, const void* b_k, const void* b_v) {
+  auto on = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+  if (P.r == 0) return true;
+  const int k_bytes = !P.stream ? P.esz : P.bk_stages > 0 ? 16 : 8;
+  const int v_bytes = P.bf16 && !P.wide_merge && P.dh <= 64 && P.r <= 32 ? 4 : P.esz;
+  return on(b_k, k_bytes) && on(b_v, v_bytes);
+}
+
 lrkv_status decode_common(const lrkv_dims* dims, const void* q, const void* k_s, const void* v_s,
                           const void* z_k, const void* z_v, const void* b_k, const void* b_v,
                           const int32_t* seq_lens, float* out, float* lse, void* ws, size_t ws_bytes,
@@ -121,6 +133,7 @@ lrkv_status decode_common(const lrkv_dims* dims, const void* q, const void* k_s,
   lrkv::DecodePlan P;
   size_t need = 0;
   if ((st = lrkv::decode_make_plan(*dims, sms, P, &need)) != LRKV_OK) return st;
+  if (!bases_aligned(P, b_k, b_v)) return LRKV_ERR_INVALID_ARG;
   if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
   // post-projection RMSNorm and the paged cache: the streaming scan only
   if ((key_scale || paged) && !P.stream) return LRKV_ERR_UNSUPPORTED;
@@ -239,6 +252,7 @@ lrkv_status lrkv_decode_weighted(const lrkv_dims* dims, const void* q, int page_
   if (dims->rank > 0 && (!z_k || !z_v || !b_k || !b_v)) return LRKV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_s) || !aligned16(v_s)) return LRKV_ERR_INVALID_ARG;
   if (dims->rank > 0 && (!aligned16(z_k) || !aligned16(z_v))) return LRKV_ERR_INVALID_ARG;
+  if (!bases_aligned(P, b_k, b_v)) return LRKV_ERR_INVALID_ARG;
   if ((st = lrkv::weights_check(decay, weights, weights_out)) != LRKV_OK) return st;
   const PagedCache pc{block_table, page_size, num_pages};
   if (block_table && (st = check_paging(dims, pc)) != LRKV_OK) return st;
@@ -283,6 +297,7 @@ lrkv_status decode_step_common(const lrkv_dims* dims, int d_model, const void* x
   lrkv::DecodePlan P;
   size_t need = 0;
   if ((st = lrkv::decode_make_plan(*dims, sms, P, &need)) != LRKV_OK) return st;
+  if (!bases_aligned(P, b_k, b_v)) return LRKV_ERR_INVALID_ARG;
   if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
   if (paged && !P.stream) return LRKV_ERR_UNSUPPORTED;
   if (paged) set_paging(P, *dims, *paged);

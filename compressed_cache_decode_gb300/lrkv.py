@@ -213,10 +213,53 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _raw_stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_handle(stream) -> Optional[int]:
+    return _raw_stream(torch.cuda.current_stream() if stream is None else stream)
+
+
+class _On:
+    """The device of tensor `t` made current for a call, and the call's own
+    `stream` (None: the current one) for what the call allocates and fills: a
+    block of another stream's pool may still be in use there, and a fill on
+    another stream is in no order with the call."""
+
+    __slots__ = ("device", "before", "stream", "caller", "inner")
+
+    def __init__(self, t, stream=None):
+        self.device, self.stream = t.get_device(), stream
+
+    def __enter__(self):
+        self.inner = None
+        if self.device < 0:  # (not a CUDA tensor: the call refuses it)
+            return self
+        self.before = torch.cuda.current_device()
+        if self.before != self.device:
+            torch.cuda.set_device(self.device)
+        if self.stream is not None:
+            raw = _raw_stream(self.stream)
+            if raw != torch._C._cuda_getCurrentRawStream(self.device):
+                self.caller = torch.cuda.current_stream(self.device)
+                # (0 and 1 are the handles of the default stream)
+                self.inner = torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device) if raw > 1 else
+                                               torch.cuda.default_stream(self.device))
+                self.inner.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
+        if self.device >= 0 and self.before != self.device:
+            torch.cuda.set_device(self.before)
+
+    def own(self, t: torch.Tensor) -> torch.Tensor:
+        """t, made within this context, to be used on the caller's stream too."""
+        if self.inner is not None:
+            t.record_stream(self.caller)
+        return t
 
 
 def make_dims(batch: int, heads: int, head_dim: int, rank: int, max_len: int, dtype,
@@ -310,12 +353,13 @@ def decode(q: torch.Tensor, k_s: torch.Tensor, v_s: torch.Tensor, z_k: torch.Ten
     max_len = k_s.shape[1]
     r = z_k.shape[-1] if z_k is not None else 0
     dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(dims, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode_workspace(dims, q.device))
     for t in (q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens):
         if t is not None and not t.is_contiguous():
             raise ValueError("LRKV tensors must be contiguous")
@@ -347,7 +391,8 @@ def append(x: torch.Tensor, w_sk: torch.Tensor, w_sv: torch.Tensor, u_k: torch.T
     B, n_new, d = x.shape
     H, r = z_k.shape[2], z_k.shape[3]
     dims = make_dims(B, H, k_s.shape[2], r, k_s.shape[1], x.dtype)
-    ws = torch.zeros(16, dtype=torch.uint8, device=x.device)
+    with _On(x, stream) as on:
+        ws = on.own(torch.zeros(16, dtype=torch.uint8, device=x.device))
     st = lrkv_append(dims, d, n_new, x, w_sk, w_sv, u_k, u_v, start_pos, k_s, v_s, z_k, z_v, ws,
                      ws.numel(), stream)
     if st != LRKV_OK:
@@ -381,12 +426,13 @@ def decode_normed(q, k_s, v_s, z_k, z_v, b_k, b_v, key_scale, seq_lens, scale: f
     """decode with the keys' post-projection RMSNorm scales applied to the scores."""
     B, H, dh = q.shape
     dims = make_dims(B, H, dh, z_k.shape[-1], k_s.shape[1], q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(dims, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode_workspace(dims, q.device))
     st = lrkv_decode_normed(dims, q, k_s, v_s, z_k, z_v, b_k, b_v, key_scale, seq_lens, out, lse, ws,
                             ws.numel(), stream)
     if st != LRKV_OK:
@@ -414,12 +460,13 @@ def decode_step(x: torch.Tensor, w_sk: torch.Tensor, w_sv: torch.Tensor, u_k: to
     B, H, dh = q.shape
     d = x.shape[-1]
     dims = make_dims(B, H, dh, z_k.shape[-1], k_s.shape[1], q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(dims, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode_workspace(dims, q.device))
     for t in (x, w_sk, w_sv, u_k, u_v, q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens):
         if not t.is_contiguous():
             raise ValueError("LRKV tensors must be contiguous")
@@ -465,12 +512,13 @@ def prefill(q: torch.Tensor, k_s: torch.Tensor, v_s: torch.Tensor, z_k: torch.Te
     B, Tq, H, dh = q.shape
     r = z_k.shape[-1]
     dims = make_dims(B, H, dh, r, k_s.shape[1], q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H, Tq), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device))
     st = lrkv_prefill(dims, Tq, q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens, out, lse, ws, ws.numel(),
                       stream)
     if st != LRKV_OK:
@@ -487,12 +535,13 @@ def prefill_normed(q: torch.Tensor, k_s: torch.Tensor, v_s: torch.Tensor, z_k: t
     B, Tq, H, dh = q.shape
     r = z_k.shape[-1]
     dims = make_dims(B, H, dh, r, k_s.shape[1], q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H, Tq), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device))
     st = lrkv_prefill_normed(dims, Tq, q, k_s, v_s, z_k, z_v, b_k, b_v, key_scale, seq_lens, out, lse, ws,
                              ws.numel(), stream)
     if st != LRKV_OK:
@@ -517,12 +566,13 @@ def decode_paged(q, k_s, v_s, z_k, z_v, b_k, b_v, block_table, seq_lens, scale: 
     num_pages, page_size = k_s.shape[0], k_s.shape[1]
     r = z_k.shape[-1]
     dims = make_dims(B, H, dh, r, block_table.shape[1] * page_size, q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(dims, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode_workspace(dims, q.device))
     st = lrkv_decode_paged(dims, page_size, num_pages, block_table, q, k_s, v_s, z_k, z_v, b_k, b_v, seq_lens,
                            out, lse, ws, ws.numel(), stream)
     if st != LRKV_OK:
@@ -539,8 +589,9 @@ def append_paged(x, w_sk, w_sv, u_k, u_v, start_pos, block_table, k_s, v_s, z_k,
     num_pages, page_size, dh = k_s.shape
     r = z_k.shape[-1]
     dims = make_dims(B, heads, dh, r, block_table.shape[1] * page_size, x.dtype)
-    if ws is None:
-        ws = torch.zeros(16, dtype=torch.uint8, device=x.device)
+    with _On(x, stream) as on:
+        if ws is None:
+            ws = on.own(torch.zeros(16, dtype=torch.uint8, device=x.device))
     st = int(load().lrkv_append_paged(ctypes.byref(dims), d, n_new, _ptr(x), _ptr(w_sk), _ptr(w_sv), _ptr(u_k),
                                       _ptr(u_v), _ptr(start_pos), page_size, num_pages, _ptr(block_table),
                                       _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(ws), ws.numel(),
@@ -557,12 +608,13 @@ def decode_step_paged(x, w_sk, w_sv, u_k, u_v, q, k_s, v_s, z_k, z_v, b_k, b_v, 
     num_pages, page_size = k_s.shape[0], k_s.shape[1]
     r = z_k.shape[-1]
     dims = make_dims(B, H, dh, r, block_table.shape[1] * page_size, q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(dims, q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode_workspace(dims, q.device))
     st = int(load().lrkv_decode_step_paged(ctypes.byref(dims), x.shape[-1], _ptr(x), _ptr(w_sk), _ptr(w_sv),
                                            _ptr(u_k), _ptr(u_v), _ptr(q), page_size, num_pages,
                                            _ptr(block_table), _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v),
@@ -582,12 +634,13 @@ def prefill_paged(q, k_s, v_s, z_k, z_v, b_k, b_v, block_table, seq_lens, scale:
     num_pages, page_size = k_s.shape[0], k_s.shape[1]
     r = z_k.shape[-1]
     dims = make_dims(B, H, dh, r, block_table.shape[1] * page_size, q.dtype, scale)
-    if out is None:
-        out = torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, Tq, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H, Tq), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(torch.zeros(lrkv_prefill_workspace_size(dims, Tq), dtype=torch.uint8, device=q.device))
     st = int(load().lrkv_prefill_paged(ctypes.byref(dims), Tq, _ptr(q), page_size, num_pages, _ptr(block_table),
                                        _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(b_k), _ptr(b_v),
                                        _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
@@ -602,7 +655,8 @@ def prefill_paged(q, k_s, v_s, z_k, z_v, b_k, b_v, block_table, seq_lens, scale:
 def rope_table(max_pos: int, head_dim: int, base: float = 10000.0, device="cuda", stream=None) -> torch.Tensor:
     """The rotation table [max_pos, head_dim] fp32 (cos, sin pairs) computed
     by the library."""
-    t = torch.empty((max_pos, head_dim), dtype=torch.float32, device=device)
+    with _On(torch.empty(0, device=device), stream) as on:
+        t = on.own(torch.empty((max_pos, head_dim), dtype=torch.float32, device=device))
     st = int(load().lrkv_rope_table(int(max_pos), int(head_dim), float(base), _ptr(t), _stream_handle(stream)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_rope_table")
@@ -633,12 +687,13 @@ def decode_rope(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, seq_lens, scale: f
     table from rope_table().  Returns (out, lse)."""
     B, H, dh = q_rot.shape
     dims = make_dims(B, H, dh, z_k.shape[-1], k_s.shape[1], q_rot.dtype, scale)
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q_rot.device)
-    if ws is None:
-        ws = torch.empty(lrkv_decode_rope_workspace_size(dims), dtype=torch.uint8, device=q_rot.device)
+    with _On(q_rot, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q_rot.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q_rot.device))
+        if ws is None:
+            ws = on.own(torch.empty(lrkv_decode_rope_workspace_size(dims), dtype=torch.uint8, device=q_rot.device))
     for t in (q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, seq_lens):
         if not t.is_contiguous():
             raise ValueError("LRKV tensors must be contiguous")
@@ -675,49 +730,6 @@ def _check(device: int, *specs) -> None:
             raise ValueError(f"{name} is on {t.device}, the call's first tensor on device {device}")
     if device < 0:
         raise ValueError("LRKV tensors must be on a CUDA device")
-
-
-def _raw_stream(stream) -> int:
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-class _On:
-    """The device of tensor `t` made current for a call, and the call's own
-    `stream` (None: the current one) for what the call allocates and fills: a
-    block of another stream's pool may still be in use there, and a fill on
-    another stream is in no order with the call."""
-
-    __slots__ = ("device", "before", "stream", "caller", "inner")
-
-    def __init__(self, t, stream=None):
-        self.device, self.stream = t.get_device(), stream
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device:
-            torch.cuda.set_device(self.device)
-        self.inner = None
-        if self.stream is not None:
-            raw = _raw_stream(self.stream)
-            if raw != torch._C._cuda_getCurrentRawStream(self.device):
-                self.caller = torch.cuda.current_stream(self.device)
-                # (0 and 1 are the handles of the default stream)
-                self.inner = torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device) if raw > 1 else
-                                               torch.cuda.default_stream(self.device))
-                self.inner.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
-        if self.before != self.device:
-            torch.cuda.set_device(self.before)
-
-    def own(self, t: torch.Tensor) -> torch.Tensor:
-        """t, made within this context, to be used on the caller's stream too."""
-        if self.inner is not None:
-            t.record_stream(self.caller)
-        return t
 
 
 def _stream_on(stream, device: int) -> int:
@@ -938,16 +950,17 @@ def dense_decode(q, k, v, seq_lens, scale: float = 0.0, out=None, lse=None, ws=N
     [B, L, H_kv, d] bf16.  Returns (out, lse, ws)."""
     B, H, d = q.shape
     dims = lrkv_dense_dims(B, H, k.shape[2], d, k.shape[1], float(scale))
-    if out is None:
-        out = torch.empty((B, H, d), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        n = ctypes.c_size_t(0)
-        st = load().lrkv_dense_decode_workspace_size(ctypes.byref(dims), ctypes.byref(n))
-        if st != LRKV_OK:
-            raise LRKVError(st, "lrkv_dense_decode_workspace_size")
-        ws = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, d), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            n = ctypes.c_size_t(0)
+            st = load().lrkv_dense_decode_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+            if st != LRKV_OK:
+                raise LRKVError(st, "lrkv_dense_decode_workspace_size")
+            ws = on.own(torch.empty(int(n.value), dtype=torch.uint8, device=q.device))
     st = int(load().lrkv_dense_decode(ctypes.byref(dims), _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), _ptr(out),
                                       _ptr(lse), _ptr(ws), ws.numel(), _stream_handle(stream)))
     if st != LRKV_OK:
@@ -960,16 +973,17 @@ def mla_decode(q, c, w_uk, w_uv, seq_lens, scale: float = 0.0, out=None, lse=Non
     [H, d_h, d_c] bf16.  Returns (out, lse, ws)."""
     B, H, dh = q.shape
     dims = lrkv_mla_dims(B, H, dh, c.shape[2], c.shape[1], float(scale))
-    if out is None:
-        out = torch.empty((B, H, dh), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    if ws is None:
-        n = ctypes.c_size_t(0)
-        st = load().lrkv_mla_decode_workspace_size(ctypes.byref(dims), ctypes.byref(n))
-        if st != LRKV_OK:
-            raise LRKVError(st, "lrkv_mla_decode_workspace_size")
-        ws = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            n = ctypes.c_size_t(0)
+            st = load().lrkv_mla_decode_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+            if st != LRKV_OK:
+                raise LRKVError(st, "lrkv_mla_decode_workspace_size")
+            ws = on.own(torch.empty(int(n.value), dtype=torch.uint8, device=q.device))
     st = int(load().lrkv_mla_decode(ctypes.byref(dims), _ptr(q), _ptr(c), _ptr(w_uk), _ptr(w_uv), _ptr(seq_lens),
                                     _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream_handle(stream)))
     if st != LRKV_OK:

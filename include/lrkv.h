@@ -34,7 +34,9 @@
  *  * Alignment.  Cache pointers, q, x and the append weights must be 16-byte
  *    aligned, and head_dim*sizeof(elem) and heads*rank*sizeof(elem) must be
  *    multiples of 16 bytes (every row is moved by the Tensor Memory
- *    Accelerator, which copies 16-byte-aligned spans).
+ *    Accelerator, which copies 16-byte-aligned spans).  Keep b_k and b_v
+ *    16-byte aligned as well: the calls refuse a base that lies where their
+ *    kernels' wide reads of it cannot start.
  *  * Errors.  Arguments are checked on the host before anything is enqueued;
  *    a failed check returns a status and enqueues nothing.  A CUDA launch
  *    failure returns LRKV_ERR_CUDA.  Problems only the device can see (a

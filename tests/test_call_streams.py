@@ -32,7 +32,7 @@ class FakeLibrary:
             if name.endswith("_workspace_size"):
                 args[-1]._obj.value = 64
             else:
-                self.calls.append((name, args[-1]))
+                self.calls.append((name, args[-1]))    # (append also reads its status word back)
             return 0
         return call
 
@@ -55,7 +55,8 @@ class Fake:
         def stream_of(raw, device=None):
             return types.SimpleNamespace(cuda_stream=raw)
 
-        mp.setattr(torch.cuda, "current_device", lambda: -1)   # what a CPU tensor answers for its device
+        mp.setattr(torch.cuda, "current_device", lambda: 0)
+        mp.setattr(torch.Tensor, "get_device", lambda t: 0)
         mp.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: self.current[-1], raising=False)
         mp.setattr(torch.cuda, "current_stream", lambda device=None: stream_of(self.current[-1]))
         mp.setattr(torch.cuda, "ExternalStream", stream_of)
@@ -89,7 +90,8 @@ def _tensors():
     q, k, z, b = bf(B, H, DH), bf(B, L, DH), bf(B, L, H, R), bf(H, DH, R)
     return types.SimpleNamespace(q=q, k=k, z=z, b=b, lens=i(B), weights=torch.ones(B, L), pos=i(B, L, 2),
                                  table=torch.ones(L, DH), lse=torch.ones(B, H, 4), prompt=bf(B, 4, H, DH),
-                                 decode=(q, k, k, z, z, b, b))
+                                 decode=(q, k, k, z, z, b, b),
+                                 append=(bf(B, 8),) + (bf(DH, 8),) * 2 + (bf(H * R, 8),) * 2)
 
 
 def weighted(t, stream):
@@ -115,7 +117,22 @@ CALLS = dict(
     decode_weighted=(weighted, 4), prefill_weights=(prompt, 2),    # calls and the allocations of each
     evict=(lambda t, s: lrkv.evict(t.k, t.k, t.z, t.z, t.weights, t.lens, 8, stream=s), 1),
     rope_rotate=(lambda t, s: lrkv.rope_rotate(t.prompt, t.pos[:, :4].contiguous(), t.table, [16, 16], stream=s), 1),
-    decode_rope_axes=(lambda t, s: lrkv.decode_rope_axes(*t.decode, t.table, t.pos, [16, 16], t.lens, stream=s), 3))
+    decode_rope_axes=(lambda t, s: lrkv.decode_rope_axes(*t.decode, t.table, t.pos, [16, 16], t.lens, stream=s), 3),
+    decode=(lambda t, s: lrkv.decode(*t.decode, t.lens, stream=s), 3),
+    decode_normed=(lambda t, s: lrkv.decode_normed(*t.decode, t.lse, t.lens, stream=s), 3),
+    decode_paged=(lambda t, s: lrkv.decode_paged(*t.decode, t.pos[..., 0], t.lens, stream=s), 3),
+    decode_rope=(lambda t, s: lrkv.decode_rope(*t.decode, t.table, t.lens, stream=s), 3),
+    decode_step=(lambda t, s: lrkv.decode_step(*t.append, *t.decode, t.lens, stream=s), 3),
+    decode_step_paged=(lambda t, s: lrkv.decode_step_paged(*t.append, *t.decode, t.pos[..., 0], t.lens, stream=s), 3),
+    prefill=(lambda t, s: lrkv.prefill(t.prompt, *t.decode[1:], t.lens, stream=s), 3),
+    prefill_normed=(lambda t, s: lrkv.prefill_normed(t.prompt, *t.decode[1:], t.lse, t.lens, stream=s), 3),
+    prefill_paged=(lambda t, s: lrkv.prefill_paged(t.prompt, *t.decode[1:], t.pos[..., 0], t.lens, stream=s), 3),
+    append=(lambda t, s: lrkv.append(t.q, *t.append[1:], t.lens, *t.decode[1:5], stream=s), 1),
+    append_paged=(lambda t, s: lrkv.append_paged(t.q, *t.append[1:], t.lens, t.pos[..., 0], *t.decode[1:5], H,
+                                                 stream=s), 1),
+    dense_decode=(lambda t, s: lrkv.dense_decode(t.q, t.z, t.z, t.lens, stream=s), 3),
+    mla_decode=(lambda t, s: lrkv.mla_decode(t.q, t.k, t.b, t.b, t.lens, stream=s), 3),
+    rope_table=(lambda t, s: lrkv.rope_table(L, DH, device="cpu", stream=s), 1))
 
 
 @pytest.mark.parametrize("call", CALLS)
@@ -125,8 +142,9 @@ def test_allocations_belong_to_the_call_s_stream(fake, call, stream, want):
     fake.made.clear()
     run, n = CALLS[call]
     run(t, stream)
+    fake.made[:] = [m for m in fake.made if m[1].numel()]
     assert [on for _, _, on in fake.made] == [want] * n
-    assert [s for _, s in fake.lib.calls] == [want] and fake.current == [HERE]
+    assert fake.lib.calls[0][1] == want and fake.current == [HERE]
     # ... and are known to the allocator as used on the caller's stream too
     assert fake.shared == ([(x.data_ptr(), HERE) for _, x, _ in fake.made] if want == OWN else [])
 
