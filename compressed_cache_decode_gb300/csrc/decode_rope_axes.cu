@@ -159,9 +159,9 @@ __global__ void __launch_bounds__(kRThreads, 1)
   constexpr uint32_t kTmemCols = kRAcc * DH;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ uint64_t kfull, kempty, zfull[kRMaxZ], zempty[kRMaxZ], vfull[kRMaxV], vempty[kRMaxV], accf[kRAcc],
-      acce[kRAcc], scf[2], sce[2];
+      acce[kRAcc], scf[2], sce[2], mdone;
   __shared__ uint32_t tmem_base;
-  __shared__ int s_timeout, s_badpos, s_k, s_z, s_v, s_mma;  // copies and MMAs issued
+  __shared__ int s_timeout, s_badpos, s_k, s_z, s_v;  // copies issued
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   volatile int* fail = &s_timeout;
 
@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
     for (int i = 0; i < kRMaxV; ++i) { mbar_init(&vfull[i], 1); mbar_init(&vempty[i], kRValue); }
     for (int i = 0; i < kRAcc; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], kRScore); }
     for (int i = 0; i < 2; ++i) { mbar_init(&scf[i], kRScore); mbar_init(&sce[i], kRValue); }
-    s_timeout = s_badpos = s_k = s_z = s_v = s_mma = 0;
+    mbar_init(&mdone, 1);
+    s_timeout = s_badpos = s_k = s_z = s_v = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, kTmemCols);
@@ -239,7 +240,14 @@ __global__ void __launch_bounds__(kRThreads, 1)
   } else if (warp < 4) {
     regs_down<kRRegsCopy>();
     if (warp == 0 && lane == 0) {
-      // ---- copies: the keys' and the values' queues, whichever has a free slot ------
+      // ---- copies: the keys' and the values' queues, whichever has a free slot: let go
+      // by its readers and, since readers that gave up let go too, landed (a second copy
+      // must never join a phase that is still pending; latent slots are let go by the
+      // MMAs that read them) -----------------------------------------------------------
+      auto again = [&](uint64_t* empty, uint64_t* full, int use) {  // whether use `use` of a slot may begin
+        const uint32_t last = static_cast<uint32_t>(use - 1) & 1u;
+        return use < 1 || (mbar_test(empty, last) && mbar_test(full, last));
+      };
       TileWalk kw, vw;
       bool km = walk_first(kw, pre, B, g0, g1), vm = walk_first(vw, pre, B, g0, g1);
       int kt = 0, ki = 0, zi = 0, vi = 0, vs = 0;  // tile, box within it (0: k_s), boxes, value copies, copy within a tile
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
         if (km) {
           const int s = zi % A.nz;
           if (ki == 0) {
-            if (kt < 1 || mbar_test(&kempty, static_cast<uint32_t>(kt - 1) & 1u)) {
+            if (again(&kempty, &kfull, kt)) {
               mbar_arrive_expect_tx(&kfull, NB * kRBox);
               for (int cb = 0; cb < NB; ++cb)
                 tma_load_3d(smem + A.off_k + cb * kRBox, &tm_k, 64 * cb, kw.t0, kw.b, &kfull);
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
         }
         if (vm) {
           const int s = vi % A.nv;
-          if (vi < A.nv || mbar_test(&vempty[s], static_cast<uint32_t>(vi / A.nv - 1) & 1u)) {
+          if (again(&vempty[s], &vfull[s], vi / A.nv)) {
             unsigned char* dst = smem + A.off_v + s * A.vt_bytes;
             mbar_arrive_expect_tx(&vfull[s], NB * kRSub * 128 + P.zt_bytes);
             for (int cb = 0; cb < NB; ++cb)
@@ -307,8 +315,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
                       bd + static_cast<uint32_t>(i * DH * 8) + kk * 2, idesc, kk > 0 ? 1u : 0u);
           tc_commit(&zempty[s]);
           tc_commit(&accf[a]);
-          s_mma = u + 1;
         }
+      tc_commit(&mdone);  // every MMA issued, also by a pass that gave up
       if (!ok) *fail = 1;
     }
   } else if (warp < 4 + kRScore) {
@@ -695,8 +703,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
       done = mbar_wait_bounded(&zfull[i % A.nz], static_cast<uint32_t>(i / A.nz) & 1u) && done;
     for (int i = max(0, s_v - A.nv); i < s_v; ++i)
       done = mbar_wait_bounded(&vfull[i % A.nv], static_cast<uint32_t>(i / A.nv) & 1u) && done;
-    for (int i = max(0, s_mma - kRAcc); i < s_mma; ++i)
-      done = mbar_wait_bounded(&accf[i % kRAcc], static_cast<uint32_t>(i / kRAcc) & 1u) && done;
+    if (work) done = mbar_wait_bounded(&mdone, 0u) && done;
     if (!done) *fail = 1;
     pdl_wait();  // the launch before may still read the workspace
     if (blockIdx.x == 0 && blockIdx.y == 0) {

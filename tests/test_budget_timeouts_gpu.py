@@ -1,0 +1,70 @@
+"""Waits that run out in the calls that keep a cache inside a token budget.
+
+With the bound of the waits cut short (LRKV_WAIT_LIMIT_CYCLES; caches larger
+than L2 and L2 flushed, so that copies are under way) a call gives up
+somewhere: at one cycle at its first waits, at larger bounds in the middle of its
+work, with some warps gone on and others not.  It must end, wait at the full
+bound for every copy and MMA that it issued, and say so in its status word; the
+next call on the same workspace is whole."""
+import pytest
+import torch
+
+import _budget_util as T
+from _lib_util import ensure_built
+from compressed_cache_decode_gb300 import inputs, lrkv
+
+pytestmark = pytest.mark.gpu
+
+LIMITS = [1, 300, 1000, 2000, 4000, 10000]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    ensure_built()
+    lrkv.load()
+
+
+def _give_up_and_recover(run, ws, monkeypatch):
+    """run() under every limit and whole again after each; its results as a list."""
+    want = run()
+    torch.cuda.synchronize()
+    assert lrkv.lrkv_read_device_status(ws) == lrkv.LRKV_OK
+    flush = torch.empty(512 << 20, dtype=torch.uint8, device="cuda")
+    seen = []
+    for limit in LIMITS:
+        flush.fill_(1)
+        monkeypatch.setenv("LRKV_WAIT_LIMIT_CYCLES", str(limit))
+        run()
+        torch.cuda.synchronize()
+        seen.append(lrkv.lrkv_read_device_status(ws))
+        monkeypatch.delenv("LRKV_WAIT_LIMIT_CYCLES")
+        got = run()
+        torch.cuda.synchronize()
+        assert lrkv.lrkv_read_device_status(ws) == lrkv.LRKV_OK
+        for g, t in zip(got, want):
+            assert torch.equal(g, t), limit
+    assert seen[0] == lrkv.LRKV_ERR_TIMEOUT
+    assert set(seen) <= {lrkv.LRKV_OK, lrkv.LRKV_ERR_TIMEOUT}
+
+
+def _decode_case(B=2, H=32, dh=128, r=48, Lm=32768, lens=(32768, 20000)):
+    d = T.cuda(inputs.random_decode_case(seed=5, batch=B, heads=H, head_dim=dh, rank=r, max_len=Lm, dtype="bf16",
+                                         lens=list(lens)))
+    return d, lrkv.make_dims(B, H, dh, r, Lm, torch.bfloat16)
+
+
+@pytest.mark.parametrize("heads, head_dim, rank", [(32, 128, 48), (16, 64, 64)])
+def test_decode_rope_axes(heads, head_dim, rank, monkeypatch):
+    d, dims = _decode_case(H=heads, dh=head_dim, r=rank)
+    ws = lrkv.decode_rope_axes_workspace(dims)
+    table = lrkv.rope_table(32768, head_dim)
+    pos = torch.arange(32768, dtype=torch.int32, device="cuda").expand(2, 32768)[..., None].contiguous()
+
+    def run():
+        w = torch.zeros((2, 32768), device="cuda")
+        return lrkv.decode_rope_axes(*[d[k] for k in T.NAMES[:7]], table, pos, [head_dim // 2], d["seq_lens"],
+                                     weights=w, ws=ws)[:3]
+
+    _give_up_and_recover(run, ws, monkeypatch)
