@@ -904,20 +904,17 @@ __global__ void __launch_bounds__(32 * NW) lrkv_decode_merge_wide_kernel(const D
 }
 
 // ======================================================================= host
+long long wait_limit_cycles() {
+  const char* v = std::getenv("LRKV_WAIT_LIMIT_CYCLES");
+  const long long x = (v && *v) ? std::atoll(v) : 0;
+  return x > 0 ? x : kWaitLimitCycles;
+}
+
 namespace {
 
 int env_int(const char* name, int dflt) {
   const char* v = std::getenv(name);
   return (v && *v) ? std::atoi(v) : dflt;
-}
-
-// The bound of the decode's waits for its copies (SM cycles): the
-// environment variable LRKV_WAIT_LIMIT_CYCLES when it holds a positive
-// number (for tests of the timeout path), else kWaitLimitCycles.
-long long wait_limit_cycles() {
-  const char* v = std::getenv("LRKV_WAIT_LIMIT_CYCLES");
-  const long long x = (v && *v) ? std::atoll(v) : 0;
-  return x > 0 ? x : kWaitLimitCycles;
 }
 
 using SplitFn = void (*)(const DecodePlan, const CUtensorMap, const CUtensorMap);

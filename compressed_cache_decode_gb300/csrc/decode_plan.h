@@ -120,6 +120,11 @@ struct DecodePlan {
   int cs_row, cs_bytes, rope_max_pos;
 };
 
+// The bound of the kernels' waits (SM cycles): the environment variable
+// LRKV_WAIT_LIMIT_CYCLES when it holds a positive number (for tests of the
+// timeout path), else kWaitLimitCycles.
+long long wait_limit_cycles();
+
 // Fills everything but the operand pointers; returns the workspace size.
 lrkv_status decode_make_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, size_t* ws_bytes, bool weighted = false);
 lrkv_status key_scale_launch(const lrkv_dims& dm, float eps, int n_new, const void* k_s, const void* z_k,

@@ -765,11 +765,7 @@ lrkv_status rope_axes_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, AxesA
   const float scale = d.scale > 0.f ? d.scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
   P.scale_log2 = scale * kLog2e;
   P.bf16 = 1; P.esz = 2; P.T = kRT; P.stream = 1;
-  {
-    const char* v = std::getenv("LRKV_WAIT_LIMIT_CYCLES");
-    const long long x = (v && *v) ? std::atoll(v) : 0;
-    P.wait_limit = x > 0 ? x : kWaitLimitCycles;
-  }
+  P.wait_limit = wait_limit_cycles();
   P.mt = P.H / kRHeads;
   P.grid = std::max(1, num_sms / P.mt);
   P.ngw = 1;

@@ -107,6 +107,7 @@ struct PromptParams {
   float* partial;            // [nhg][B][max_len]
   uint32_t* cta_status;      // [grid]
   int grid;
+  long long wait_limit;      // bound of the roles' waits (SM cycles)
 };
 
 struct PromptMaps {
@@ -310,10 +311,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   constexpr int KB = ONE ? 2 : 1;  // k_s buffers in TMEM
   extern __shared__ __align__(16) unsigned char pw_raw[];
   __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready[KB], kfree[KB], kfull, zready[kPwZ], zfree[kPwZ],
-      accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL];
+      accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL], mdone[2];
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad;
-  __shared__ int s_use[kPwA], s_k, s_q, s_acc[kPwAcc];  // boxes and tiles issued, half units committed
+  __shared__ int s_use[kPwA], s_k, s_q;  // boxes and tiles issued
   __shared__ __align__(16) float s_lse[kPwL][kPwCols];  // read four columns at a time
   __shared__ float s_part[2][4][2][kPwHalf];
   unsigned char* smem = pw_raw + ((1024u - (smem_u32(pw_raw) & 1023u)) & 1023u);
@@ -331,8 +332,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     for (int i = 0; i < kPwL; ++i) { mbar_init(&lfull[i], 1); mbar_init(&lempty[i], kPwEpi); }
     for (int i = 0; i < KB; ++i) { mbar_init(&kready[i], 4); mbar_init(&kfree[i], 2); }
     mbar_init(&kfull, 1);
+    mbar_init(&mdone[0], 1);
+    mbar_init(&mdone[1], 1);
     for (int i = 0; i < kPwA; ++i) s_use[i] = 0;
-    s_fail = s_bad = s_k = s_q = s_acc[0] = s_acc[1] = 0;
+    s_fail = s_bad = s_k = s_q = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, kPwTmem);
@@ -368,6 +371,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     }
   };
 
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, P.wait_limit); };
   if (warp == 0) {
     if (ONE && lane == 0) {
       // ---- the heads' latents one after another, both halves of each --------------
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           for (int m = 0; m < 2; ++m) {
             if (m >= w.halves) break;
             const int s = m * (kPwA / 2) + zi[m] % (kPwA / 2), u = zi[m] / (kPwA / 2);  // slot, use of it
-            live = live && (u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u));
+            live = live && (u < 1 || wait(&aempty[s], static_cast<uint32_t>(u - 1) & 1u));
             if (!live) {
               *fail = 1;
               break;
@@ -398,7 +402,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const int nk = w.halves * NB, nz = P.r > 0 ? w.halves * P.hg : 0;
         for (int i = 0; i < nk + nz; ++i) {
           const int s = ai % kPwA, u = ai / kPwA;  // slot, use of it
-          live = u < 1 || mbar_wait_bounded(&aempty[s], static_cast<uint32_t>(u - 1) & 1u);
+          // let go by its readers and, since readers that gave up let go too, landed: a
+          // second copy must never join a phase that is still pending
+          const uint32_t last = static_cast<uint32_t>(u - 1) & 1u;
+          live = u < 1 || (wait(&aempty[s], last) && wait(&afull[s], last));
           if (!live) {
             *fail = 1;
             break;
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         for (int hs = w.h0; hs < w.h0 + P.hg && live; hs += P.hpt)
           for (int qt = w.qt0; qt < P.nqt; ++qt, ++qi) {
             const int s = qi % kPwQ;
-            live = qi < kPwQ || mbar_wait_bounded(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u);
+            live = qi < kPwQ || wait(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u);
             if (!live) {
               *fail = 1;
               break;
@@ -447,14 +454,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       bool ok = true;
       Walk w;
       for (bool more = w.first(P); more && ok && !*fail; more = w.next(P)) {
-        ok = mbar_wait_bounded(&kready[w.n % KB], static_cast<uint32_t>(w.n / KB) & 1u);
+        ok = wait(&kready[w.n % KB], static_cast<uint32_t>(w.n / KB) & 1u);
         const uint32_t ka = tmem + kColK + (w.n % KB) * 128 + m * (NB * 32);
         const bool on = m < w.halves;
         for (int hs = 0; hs < P.hg && ok; hs += P.hpt) {
           for (int qt = w.qt0; qt < P.nqt && ok; ++qt, ++qi) {
             const int s = qi % kPwQ;
-            ok = mbar_wait_bounded(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u) &&
-                 (!on || x < 1 || mbar_wait_bounded(&acce[m], static_cast<uint32_t>(x - 1) & 1u));
+            ok = wait(&qfull[s], static_cast<uint32_t>(qi / kPwQ) & 1u) &&
+                 (!on || x < 1 || wait(&acce[m], static_cast<uint32_t>(x - 1) & 1u));
             if (!ok) break;
             if (on) {
               tc_fence_after();
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 const uint32_t at = acc + i * P.wt;
                 if (ONE) {
                   const int sl = z % (kPwA / 2), bar = m * (kPwA / 2) + sl;
-                  ok = mbar_wait_bounded(&afull[bar], static_cast<uint32_t>(z / (kPwA / 2)) & 1u);
+                  ok = wait(&afull[bar], static_cast<uint32_t>(z / (kPwA / 2)) & 1u);
                   if (!ok) break;
                   const uint64_t ad = a0 + static_cast<uint32_t>(sl * (kPwBox / 16));
 #pragma unroll
@@ -483,7 +490,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 } else {
                   const int sl = m * (kPwZ / 2) + z % (kPwZ / 2);
                   if (qt == w.qt0) {
-                    ok = mbar_wait_bounded(&zready[sl], static_cast<uint32_t>(z / (kPwZ / 2)) & 1u);
+                    ok = wait(&zready[sl], static_cast<uint32_t>(z / (kPwZ / 2)) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                   }
@@ -499,7 +506,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               }
               if (!ok) break;
               tc_commit(&accf[m]);
-              s_acc[m] = ++x;
+              ++x;
             }
             tc_commit(&qempty[s]);
           }
@@ -507,6 +514,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         }
         if (ok) tc_commit(&kfree[w.n % KB]);
       }
+      tc_commit(&mdone[m]);  // every MMA issued, also by a pass that gave up within a tile
       if (!ok) *fail = 1;
     }
   } else if (warp == 3) {
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       for (int hs = w.h0; hs < w.h0 + P.hg && ok; hs += P.hpt)
         for (int qt = w.qt0; qt < P.nqt; ++qt, ++u) {
           const int s = u % kPwL;
-          ok = ok && !*fail && (u < kPwL || mbar_wait_bounded(&lempty[s], static_cast<uint32_t>(u / kPwL - 1) & 1u));
+          ok = ok && !*fail && (u < kPwL || wait(&lempty[s], static_cast<uint32_t>(u / kPwL - 1) & 1u));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) {
             *fail = 1;
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     };
     auto move = [&](uint32_t col) {
       const int s = ai % kPwA;
-      ok = ok && !*fail && mbar_wait_bounded(&afull[s], static_cast<uint32_t>(ai / kPwA) & 1u);
+      ok = ok && !*fail && wait(&afull[s], static_cast<uint32_t>(ai / kPwA) & 1u);
       ok = __all_sync(0xffffffffu, ok);  // the warp moves together
       if (ok)
         to_tmem(s_aring + s * kPwBox, col);
@@ -580,10 +588,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             s_k = ai + 1;
           }
           if (i == 0) {
-            ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
+            ok = ok && (w.n < KB || wait(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
             tc_fence_after();
           }
-          ok = ok && !*fail && mbar_wait_bounded(&kfull, static_cast<uint32_t>(ai) & 1u);
+          ok = ok && !*fail && wait(&kfull, static_cast<uint32_t>(ai) & 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (ok)
             to_tmem(s_kbox, kColK + buf * 128 + i * 32);
@@ -591,7 +599,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             *fail = 1;
         }
       } else {
-        ok = ok && (w.n < KB || mbar_wait_bounded(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
+        ok = ok && (w.n < KB || wait(&kfree[buf], static_cast<uint32_t>(w.n / KB - 1) & 1u));
         tc_fence_after();
         for (int i = 0; i < w.halves * NB; ++i) move(kColK + i * 32);
       }
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (lane == 0) mbar_arrive_cta(&kready[buf]);
       for (int i = 0; !ONE && P.r > 0 && i < w.halves * P.hg; ++i) {
         const int m = i % w.halves, z = m ? z1++ : z0++, sl = m * (kPwZ / 2) + z % (kPwZ / 2);
-        ok = ok && (z < kPwZ / 2 || mbar_wait_bounded(&zfree[sl], static_cast<uint32_t>(z / (kPwZ / 2) - 1) & 1u));
+        ok = ok && (z < kPwZ / 2 || wait(&zfree[sl], static_cast<uint32_t>(z / (kPwZ / 2) - 1) & 1u));
         tc_fence_after();
         move(kColZ + sl * 32);
         tc_fence_before();
@@ -622,12 +630,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       for (int hs = w.h0; hs < w.h0 + P.hg; hs += P.hpt)
         for (int qt = w.qt0; qt < P.nqt; ++qt, ++u) {
           const float* lse = s_lse[u % kPwL] + 32 * part;
-          ok = ok && !*fail && mbar_wait_bounded(&lfull[u % kPwL], static_cast<uint32_t>(u / kPwL) & 1u);
+          ok = ok && !*fail && wait(&lfull[u % kPwL], static_cast<uint32_t>(u / kPwL) & 1u);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             if (m >= w.halves) break;
             const int row = w.kt * kPwKeys + m * kPwHalf + key;
-            ok = ok && !*fail && mbar_wait_bounded(&accf[m], static_cast<uint32_t>(x[m]) & 1u);
+            ok = ok && !*fail && wait(&accf[m], static_cast<uint32_t>(x[m]) & 1u);
             ok = __all_sync(0xffffffffu, ok);
             uint32_t v[32];
             if (!ok) {
@@ -684,8 +692,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     if (s_k > 0) done = mbar_wait_bounded(&kfull, static_cast<uint32_t>(s_k - 1) & 1u) && done;
     for (int i = max(0, s_q - kPwQ); i < s_q; ++i)
       done = mbar_wait_bounded(&qfull[i % kPwQ], static_cast<uint32_t>(i / kPwQ) & 1u) && done;
-    for (int i = 0; i < kPwAcc; ++i)
-      if (s_acc[i] > 0) done = mbar_wait_bounded(&accf[i], static_cast<uint32_t>(s_acc[i] - 1) & 1u) && done;
+    for (int i = 0; i < 2; ++i) done = mbar_wait_bounded(&mdone[i], 0u) && done;
     P.cta_status[blockIdx.x] = (s_fail || !done ? kDevTimeout : 0u) | (s_bad ? kDevBounds : 0u);
   }
   tc_fence_before();
@@ -835,6 +842,7 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
   P.p = reinterpret_cast<__nv_bfloat16*>(base + l.p);
   P.partial = reinterpret_cast<float*>(base + l.partial);
   P.cta_status = reinterpret_cast<uint32_t*>(base + l.status);
+  P.wait_limit = wait_limit_cycles();
   P.scale_log2 = (dims->scale > 0.f ? dims->scale : 1.f / std::sqrt(static_cast<float>(P.dh))) * dec::kLog2e;
   P.block_table = block_table;
   P.page_shift = shift;

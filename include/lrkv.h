@@ -42,12 +42,14 @@
  *    failure returns LRKV_ERR_CUDA.  Problems only the device can see (a
  *    seq_lens entry outside [0, max_len], a bounded wait that ran out) never
  *    trap: the kernels clamp, finish, and record the status in the workspace,
- *    readable with lrkv_read_device_status().  A wait of the bf16 decode scan
- *    for its copies gives up after LRKV_WAIT_LIMIT_CYCLES SM cycles (an
- *    environment variable read at each call; default 2e9, about 1 s); the
- *    scan then skips the work that depended on it, still waits at the full
- *    bound for every copy it issued, and records LRKV_ERR_TIMEOUT.  Set the
- *    variable only to exercise that path.
+ *    readable with lrkv_read_device_status().  A wait of the kernels that
+ *    keep copies or MMAs in flight (the bf16 decode scan, the RoPE and
+ *    comparison decodes, lrkv_prefill_weights) gives up after
+ *    LRKV_WAIT_LIMIT_CYCLES SM cycles (an environment variable read at each
+ *    call; default 2e9, about 1 s); the kernel then skips the work that
+ *    depended on it, still waits at the full bound for all that it issued,
+ *    and records LRKV_ERR_TIMEOUT: the call's outputs are then not to be used.
+ *    Set the variable only to exercise that path.
  *  * Planning.  Launch grids and workspace sizes follow the current device's
  *    SM count, or LRKV_SM_COUNT when that environment variable holds a
  *    positive number (read at each call: workspace sizes without a device;
