@@ -90,6 +90,7 @@ struct EvictParams {
   int H, axes;
   float* key_scale;        // [B][H][max_len] or NULL
   int32_t* positions;      // [B][max_len][axes] or NULL
+  long long wait_limit;    // bound of a moving warp's waits for its copies (SM cycles)
 };
 
 // Order-preserving image of a weight: larger weight, larger integer, -0 as
@@ -513,6 +514,15 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) lrkv_evict_move_kernel(con
   const int2* dst = P.dst + static_cast<size_t>(b) * P.cap;
   unsigned char* slot = s_rows + static_cast<size_t>(warp) * P.slot;
   uint32_t phase = 0;
+  // (the hardware suspends a waiting thread for longer than a row's copy takes: a
+  // shorter bound is polled)
+  auto landed = [&](uint32_t parity) {
+    if (P.wait_limit >= kWaitLimitCycles) return mbar_wait_bounded(&full[warp], parity, P.wait_limit);
+    const long long t0 = clock64();
+    while (!mbar_test(&full[warp], parity))
+      if (clock64() - t0 > P.wait_limit) return false;
+    return true;
+  };
   bool ok = true;
   const int stride = gridDim.x * warps;
   int k = blockIdx.x * warps + warp;
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) lrkv_evict_move_kernel(con
         if (lane == 6 && P.kept) P.kept[static_cast<size_t>(b) * P.budget + d] = f;
       }
       if (!paged_in) break;
-      ok = mbar_wait_bounded(&full[warp], phase & 1u);
+      ok = landed(phase & 1u);
       ok = __all_sync(0xffffffffu, ok);
       ++phase;
       if (ok && lane == 0) {
@@ -718,6 +728,7 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
   P.base[2] = static_cast<unsigned char*>(z_k); P.base[3] = static_cast<unsigned char*>(z_v);
   P.H = dims->heads; P.axes = axes;
   P.key_scale = key_scale; P.positions = positions;
+  P.wait_limit = wait_limit_cycles();
   const int sms = device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
 

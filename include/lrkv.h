@@ -44,7 +44,7 @@
  *    trap: the kernels clamp, finish, and record the status in the workspace,
  *    readable with lrkv_read_device_status().  A wait of the kernels that
  *    keep copies or MMAs in flight (the bf16 decode scan, the RoPE and
- *    comparison decodes, lrkv_prefill_weights) gives up after
+ *    comparison decodes, lrkv_prefill_weights, lrkv_evict) gives up after
  *    LRKV_WAIT_LIMIT_CYCLES SM cycles (an environment variable read at each
  *    call; default 2e9, about 1 s); the kernel then skips the work that
  *    depended on it, still waits at the full bound for all that it issued,
@@ -530,7 +530,9 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
  * 2^31 - 2^16 (for lrkv_prefill_weights too); 1 <= budget <= max_len;
  * sink, recent >= 0 and sink + recent <= budget; axes 1 .. 4 with positions, 0
  * without.  z_k, z_v may be NULL when rank == 0.  Workspace:
- * lrkv_evict_workspace_size() bytes, its status word set afresh.
+ * lrkv_evict_workspace_size() bytes, its status word set afresh.  The call
+ * works in place: after LRKV_ERR_TIMEOUT some rows have moved and others have
+ * not, and the sequences have to be built anew.
  */
 lrkv_status lrkv_evict_workspace_size(int batch, int max_len, int budget, size_t* bytes);
 lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, const float* weights,

@@ -89,3 +89,23 @@ def test_prefill_weights(heads, head_dim, rank, q_len, window, monkeypatch):
                                     ws=ws)[:1]
 
     _give_up_and_recover(run, ws, monkeypatch)
+
+
+@pytest.mark.parametrize("heads, head_dim, rank, dtype", [(32, 128, 48, "bf16"), (64, 128, 64, "f32")])
+def test_evict(heads, head_dim, rank, dtype, monkeypatch):
+    """Rows of one part and of two; every run on a fresh copy of the cache."""
+    L, budget = (32768, 16000) if dtype == "bf16" else (6000, 3000)
+    case = T.cuda(inputs.random_decode_case(seed=5, batch=2, heads=heads, head_dim=head_dim, rank=rank, max_len=L,
+                                            dtype=dtype, lens=[L, L - 1000]))
+    case["weights"] = torch.rand((2, L), generator=torch.Generator().manual_seed(1)).cuda()
+    names = ("k_s", "v_s", "z_k", "z_v", "weights", "seq_lens")
+    ws = lrkv.evict_workspace(2, L, budget)
+    flush = torch.empty(512 << 20, dtype=torch.uint8, device="cuda")
+
+    def run():
+        state = [case[k].clone() for k in names]
+        flush.fill_(1)
+        lrkv.evict(*state, budget, sink=2, recent=10, ws=ws)
+        return state
+
+    _give_up_and_recover(run, ws, monkeypatch)
