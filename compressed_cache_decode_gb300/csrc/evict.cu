@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   __shared__ int s_hist[3][kEvBins];            // one table per level: no level waits to clear another's
   __shared__ int s_sum[kEvBins / 2];            // this CTA's share of a level's cluster-wide counts
   __shared__ int s_warp[kEvWarps];
-  __shared__ int s_cta[4];                      // this CTA's max age + 1, held rows, equal rows, holes
+  __shared__ int s_cta[4];                      // this CTA's largest age, held rows, equal rows, holes
   __shared__ int s_cta2;                        // ... moved rows
   __shared__ int s_bin, s_above, s_bad;
   __shared__ int s_all[5][kEvMaxCluster];
@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
   uint32_t threshold = kKeyOut;    // smallest kept key
   bool among_held = false;         // more held rows than n: they compete among themselves
   const bool all = L <= n;         // nothing goes
-  int newest = L;                  // tokens seen: one past the largest age
+  int newest = L - 1;              // the largest age (one past it need not fit 32 bits)
   auto key = [&](float x, int a) -> uint32_t {  // of weight x and age a
     const uint32_t k = weight_key(x);
-    const bool hd = a < P.sink || a >= newest - P.recent;
+    const bool hd = a < P.sink || a > newest - P.recent;
     return among_held ? (hd ? k : kKeyOut) : (hd ? kKeyHeld : k);
   };
   // Keys of rows t, t + 32, ... (kKeyOut past whi; some row of the warp must be
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) lrkv_evict_select_kernel(const 
       for (int t = wlo + lane; t < whi; t += 32 * kEvUnroll) {
 #pragma unroll
         for (int u = 0; u < kEvUnroll; ++u)
-          m = max(m, age[min(t + 32 * u, whi - 1)] + 1);
+          m = max(m, age[min(t + 32 * u, whi - 1)]);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
