@@ -311,10 +311,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   constexpr int KB = ONE ? 2 : 1;  // k_s buffers in TMEM
   extern __shared__ __align__(16) unsigned char pw_raw[];
   __shared__ uint64_t afull[kPwA], aempty[kPwA], qfull[kPwQ], qempty[kPwQ], kready[KB], kfree[KB], kfull, zready[kPwZ], zfree[kPwZ],
-      accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL], mdone[2];
+      accf[kPwAcc], acce[kPwAcc], lfull[kPwL], lempty[kPwL], qland, mdone[2];
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad;
-  __shared__ int s_use[kPwA], s_k, s_q;  // boxes and tiles issued
+  __shared__ int s_use[kPwA], s_k, s_q[kPwQ], s_land;  // uses of the boxes and tiles begun
   __shared__ __align__(16) float s_lse[kPwL][kPwCols];  // read four columns at a time
   __shared__ float s_part[2][4][2][kPwHalf];
   unsigned char* smem = pw_raw + ((1024u - (smem_u32(pw_raw) & 1023u)) & 1023u);
@@ -332,10 +332,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     for (int i = 0; i < kPwL; ++i) { mbar_init(&lfull[i], 1); mbar_init(&lempty[i], kPwEpi); }
     for (int i = 0; i < KB; ++i) { mbar_init(&kready[i], 4); mbar_init(&kfree[i], 2); }
     mbar_init(&kfull, 1);
+    mbar_init(&qland, 1);
     mbar_init(&mdone[0], 1);
     mbar_init(&mdone[1], 1);
     for (int i = 0; i < kPwA; ++i) s_use[i] = 0;
-    s_fail = s_bad = s_k = s_q = 0;
+    s_fail = s_bad = s_k = s_q[0] = s_q[1] = s_land = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, kPwTmem);
@@ -419,26 +420,72 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
     }
   } else if (warp == 2) {
-    if (lane == 0) {
-      // ---- query tiles -----------------------------------------------------------
-      int qi = 0;
-      bool live = true;
-      Walk w;
-      for (bool more = w.first(P); more && live && !*fail; more = w.next(P))
-        for (int hs = w.h0; hs < w.h0 + P.hg && live; hs += P.hpt)
-          for (int qt = w.qt0; qt < P.nqt; ++qt, ++qi) {
-            const int s = qi % kPwQ;
-            live = qi < kPwQ || wait(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u);
-            if (!live) {
-              *fail = 1;
-              break;
-            }
-            unsigned char* st = s_qring + s * kStage;
-            mbar_arrive_expect_tx(&qfull[s], static_cast<uint32_t>(ncols) * 128u * (NB + (P.r > 0 ? 2 : 0)));
-            tma_load_5d(st, &maps.q, 0, P.q_len - P.window + qt * P.wt, hs, 0, w.b, &qfull[s]);
-            if (P.r > 0) tma_load_5d(st + NB * kPwBox, &maps.p, 0, qt * P.wt, hs, 0, w.b, &qfull[s]);
-            s_q = qi + 1;
-          }
+    // ---- query tiles.  A query with log-sum-exp -inf gives nothing and may hold
+    // anything (padding): its rows of a tile become zeros before the MMAs read it, so
+    // that its scores are numbers.  Such a tile's copy lands on a barrier of its own. ----
+    Walk w;
+    bool more = w.first(P);
+    int hs = w.h0, qt = w.qt0;
+    float next[kPwCols / 32];  // log-sum-exps of the tile (w, hs, qt), under way a tile ahead
+    auto load_next = [&]() {
+#pragma unroll
+      for (int k = 0; k < kPwCols / 32; ++k) {
+        const int col = lane + 32 * k, i = qt * P.wt + (col & (P.wt - 1)), h = hs + (col >> P.wt_log);
+        next[k] = col < ncols && i < P.window
+                      ? P.lse[(static_cast<size_t>(w.b) * P.H + h) * P.q_len + P.q_len - P.window + i]
+                      : 0.f;
+      }
+    };
+    if (more) load_next();
+    int ql = 0;
+    bool live = true;
+    for (int qi = 0; more; ++qi) {
+      const int s = qi % kPwQ, b = w.b, h0 = hs, t0 = qt * P.wt;
+      unsigned blank[kPwCols / 32], any = 0u;
+#pragma unroll
+      for (int k = 0; k < kPwCols / 32; ++k) any |= blank[k] = __ballot_sync(0xffffffffu, next[k] == -INFINITY);
+      if (++qt == P.nqt) {
+        if ((hs += P.hpt) == w.h0 + P.hg) {
+          more = w.next(P);
+          hs = w.h0;
+        }
+        qt = w.qt0;
+      }
+      if (more) load_next();
+      live = !*fail && (qi < kPwQ || wait(&qempty[s], static_cast<uint32_t>(qi / kPwQ - 1) & 1u));
+      live = __all_sync(0xffffffffu, live);
+      if (!live) {
+        *fail = 1;
+        break;
+      }
+      unsigned char* st = s_qring + s * kStage;
+      if (lane == 0) {
+        uint64_t* full = any ? &qland : &qfull[s];
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>(ncols) * 128u * (NB + (P.r > 0 ? 2 : 0)));
+        tma_load_5d(st, &maps.q, 0, P.q_len - P.window + t0, h0, 0, b, full);
+        if (P.r > 0) tma_load_5d(st + NB * kPwBox, &maps.p, 0, t0, h0, 0, b, full);
+        if (any) s_land = ql + 1;
+      }
+      if (any) {
+        live = wait(&qland, static_cast<uint32_t>(ql++) & 1u);
+        live = __all_sync(0xffffffffu, live);
+        if (!live) {
+          *fail = 1;
+          break;
+        }
+        const int box = lane >> 3;  // 8 lanes a row of a box: NB of the queries, two of the absorbed parts
+        unsigned char* at =
+            st + (lane & 7) * 16 + (box < NB ? box * ncols * 128 : NB * kPwBox + (box - NB) * ncols * 128);
+#pragma unroll
+        for (int k = 0; k < kPwCols / 32; ++k)
+          for (unsigned bits = blank[k]; bits; bits &= bits - 1u)
+            if (box < NB || (P.r > 0 && box < NB + 2))
+              *reinterpret_cast<uint4*>(at + (32 * k + __ffs(bits) - 1) * 128) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&qfull[s]);
+      }
+      if (lane == 0) s_q[s] = qi / kPwQ + 1;
     }
   } else if (warp == 1 || warp == 24) {
     if (lane == 0) {
@@ -690,8 +737,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     for (int i = 0; i < kPwA; ++i)
       if (s_use[i] > 0) done = mbar_wait_bounded(&afull[i], static_cast<uint32_t>(s_use[i] - 1) & 1u) && done;
     if (s_k > 0) done = mbar_wait_bounded(&kfull, static_cast<uint32_t>(s_k - 1) & 1u) && done;
-    for (int i = max(0, s_q - kPwQ); i < s_q; ++i)
-      done = mbar_wait_bounded(&qfull[i % kPwQ], static_cast<uint32_t>(i / kPwQ) & 1u) && done;
+    for (int i = 0; i < kPwQ; ++i)
+      if (s_q[i] > 0) done = mbar_wait_bounded(&qfull[i], static_cast<uint32_t>(s_q[i] - 1) & 1u) && done;
+    if (s_land > 0) done = mbar_wait_bounded(&qland, static_cast<uint32_t>(s_land - 1) & 1u) && done;
     for (int i = 0; i < 2; ++i) done = mbar_wait_bounded(&mdone[i], 0u) && done;
     P.cta_status[blockIdx.x] = (s_fail || !done ? kDevTimeout : 0u) | (s_bad ? kDevBounds : 0u);
   }

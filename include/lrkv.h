@@ -476,7 +476,7 @@ lrkv_status lrkv_decode_rope(const lrkv_dims* dims, const void* q_rot, const voi
  * from q [batch][q_len][heads][head_dim], the keys' half of the cache and the
  * lse [batch][heads][q_len] that lrkv_prefill (lrkv_prefill_normed with
  * key_scale, lrkv_prefill_paged with block_table) wrote; a query with lse -inf
- * gives nothing.  Query i sits at row seq_lens[b] - q_len + i and sees the rows
+ * gives nothing, whatever it holds (padding).  Query i sits at row seq_lens[b] - q_len + i and sees the rows
  * up to its own; the prompt's q_len rows are the call's new tokens, so call it
  * once per chunk.  seq_lens[b] outside [q_len, max_len] is clamped and sets
  * LRKV_ERR_DEVICE_BOUNDS.  1 <= window <= q_len (else LRKV_ERR_INVALID_ARG),

@@ -48,3 +48,34 @@ def test_evict_up_to_the_largest_age(L, budget, sink, recent):
         want = O.evict_reference(weights[b].numpy(), n, budget, sink, recent, order[b].numpy())
         assert kept[b].tolist() == want.tolist()
         assert int((order[b, want] > LAST - recent).sum()) == recent
+
+
+@pytest.mark.parametrize("heads, q_len, window", [(8, 40, 32), (8, 40, 17), (3, 40, 5), (4, 300, 300), (5, 290, 130)])
+@pytest.mark.parametrize("rank", [16, 0])
+def test_prefill_weights_of_queries_that_are_padding(heads, q_len, window, rank):
+    """A query with lse -inf gives nothing, whatever it holds: the weights of the
+    others are those of a call on zeros in its place."""
+    B, dh, L, lens = 2, 64, 700, [700, 430]
+    case = inputs.random_prefill_case(seed=heads + window, batch=B, q_len=q_len, heads=heads, head_dim=dh, rank=rank,
+                                      max_len=L, lens=lens)
+    gen = torch.Generator().manual_seed(window)
+    lse = torch.rand((B, heads, q_len), generator=gen) + 6
+    pad = torch.rand((B, q_len), generator=gen) < 0.3
+    pad[:, -1] = True
+    lse[pad[:, None, :].expand(B, heads, q_len)] = -math.inf
+    case["q"][pad] = 0
+    d = T.cuda(case)
+
+    def run(q):
+        w, ws = lrkv.prefill_weights(q, d["k_s"], d["z_k"], d["b_k"], lse.cuda(), d["seq_lens"], None, window=window,
+                                     decay=0.0)
+        torch.cuda.synchronize()
+        assert lrkv.lrkv_read_device_status(ws) == lrkv.LRKV_OK
+        return w
+
+    want = run(d["q"])
+    assert torch.isfinite(want).all() and float(want.max()) > 0
+    for fill in (math.nan, math.inf):
+        q = d["q"].clone()
+        q[pad.cuda()] = fill
+        assert torch.equal(run(q), want)

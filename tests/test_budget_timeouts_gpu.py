@@ -6,6 +6,8 @@ somewhere: at one cycle at its first waits, at larger bounds in the middle of it
 work, with some warps gone on and others not.  It must end, wait at the full
 bound for every copy and MMA that it issued, and say so in its status word; the
 next call on the same workspace is whole."""
+import math
+
 import pytest
 import torch
 
@@ -70,18 +72,21 @@ def test_decode_rope_axes(heads, head_dim, rank, monkeypatch):
     _give_up_and_recover(run, ws, monkeypatch)
 
 
+@pytest.mark.parametrize("padded", [False, True])
 @pytest.mark.parametrize("heads, head_dim, rank, q_len, window", [
     (32, 128, 48, 32, 32),      # a window of one tile
     (16, 64, 64, 40, 7),
     (32, 128, 48, 300, 300),    # of several
     (16, 64, 64, 200, 130),
 ])
-def test_prefill_weights(heads, head_dim, rank, q_len, window, monkeypatch):
+def test_prefill_weights(heads, head_dim, rank, q_len, window, padded, monkeypatch):
     d = T.cuda(inputs.random_prefill_case(seed=2, batch=2, q_len=q_len, heads=heads, head_dim=head_dim, rank=rank,
                                           max_len=32768, lens=[32768, 20000]))
     dims = lrkv.make_dims(2, heads, head_dim, rank, 32768, torch.bfloat16)
     ws = lrkv.prefill_weights_workspace(dims, window)
     lse = torch.full((2, heads, q_len), 8.0, device="cuda")
+    if padded:
+        lse[..., ::3] = -math.inf
 
     def run():
         w = torch.zeros((2, 32768), device="cuda")
