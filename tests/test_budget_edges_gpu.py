@@ -79,3 +79,65 @@ def test_prefill_weights_of_queries_that_are_padding(heads, q_len, window, rank)
         q = d["q"].clone()
         q[pad.cuda()] = fill
         assert torch.equal(run(q), want)
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_a_budget_kept_where_rows_are_within_their_errors(seed):
+    """Steps of decode_weighted and evict followed on the host by the device's own
+    choice: every dropped row weighs no more than every kept one that is not held,
+    within the errors of their weights (equal keys make many rows that near), and
+    what is kept is whole."""
+    B, H, dh, r, L, budget, sink, recent, steps, decay = 2, 8, 64, 16, 80, 48, 2, 6, 12, 0.9
+    gen = torch.Generator().manual_seed(seed)
+    case = inputs.random_decode_case(seed=seed, batch=B, heads=H, head_dim=dh, rank=r, max_len=L, dtype="bf16",
+                                     lens=[budget] * B)
+    for k in ("k_s", "z_k"):                                  # three keys for all rows: ties up to the arithmetic
+        case[k][:] = case[k][:, torch.arange(L) % 3]
+    d = T.cuda(case)
+    host = {k: case[k].clone() for k in ("k_s", "v_s", "z_k", "z_v")}
+    w = np.zeros((B, L))
+    error = np.zeros((B, L))
+    number = np.tile(np.arange(L), (B, 1))                    # the row's token
+    order = torch.arange(L, dtype=torch.int32).repeat(B, 1).cuda()
+    weights, lens = torch.zeros((B, L), device="cuda"), d["seq_lens"]
+    for step in range(steps):
+        n = budget + 1
+        new = {k: torch.randn((B,) + tuple(host[k].shape[2:]), generator=gen).bfloat16() for k in ("v_s", "z_v")}
+        new.update({k: host[k][:, step % 3].clone() for k in ("k_s", "z_k")})
+        q = torch.randn((B, H, dh), generator=gen).bfloat16()
+        for k in host:
+            host[k][:, budget] = new[k]
+            d[k][:, budget] = new[k].cuda()
+        number[:, budget] = L + step
+        order[:, budget] = L + step
+        lens.fill_(n)
+        kept = torch.empty((B, budget), dtype=torch.int32, device="cuda")
+        lrkv.decode_weighted(q.cuda(), d["k_s"], d["v_s"], d["z_k"], d["z_v"], d["b_k"], d["b_v"], lens, weights,
+                             decay=decay)
+        got = T.f64(weights)
+        lrkv.evict(d["k_s"], d["v_s"], d["z_k"], d["z_v"], weights, lens, budget, sink=sink, recent=recent,
+                   order=order, kept=kept)
+        torch.cuda.synchronize()
+        c = dict(q=q, b_k=case["b_k"], b_v=case["b_v"], seq_lens=torch.tensor([n] * B), **host)
+        fresh = O.decode_weights_reference(*[c[k] for k in T.NAMES])[2]
+        for b in range(B):
+            w[b, :n] = O.accumulate_weights(fresh[b], w[b], decay, n, 1)
+            error[b, :budget] *= decay
+            error[b, budget] = 0
+            # (the sum over the heads, the decay as fp32 and its product)
+            error[b, :n] += sum(T.decode_bounds(c, b, h, 1 / math.sqrt(dh))[2] for h in range(H))
+            error[b, :n] += (H + 4) * T.U * w[b, :n]
+            assert np.all(np.abs(got[b, :n] - w[b, :n]) <= error[b, :n])
+            source = kept[b].cpu().numpy()
+            stays = np.zeros(n, bool)
+            stays[source] = True
+            assert len(set(source.tolist())) == budget
+            held = (number[b, :n] < sink) | (number[b, :n] >= number[b, :n].max() + 1 - recent)
+            assert np.all(stays[held])
+            top, bottom = w[b, :n] + error[b, :n], w[b, :n] - error[b, :n]
+            assert bottom[~stays].max() <= top[stays & ~held].min()
+            w[b, :budget], error[b, :budget], number[b, :budget] = w[b, source], error[b, source], number[b, source]
+            assert order[b, :budget].tolist() == number[b, :budget].tolist()
+            for k in host:
+                host[k][b, :budget] = host[k][b, source].clone()
+                assert torch.equal(d[k][b, :budget].cpu(), host[k][b, :budget]), k
