@@ -13,12 +13,17 @@
 // owns one key (one TMEM lane), adds up its row in a register, and neither
 // atomics nor exchanges between threads are needed.  p = q B_h^K enters as bf16
 // high + low parts (lrkv_prefill_absorb_kernel), two MMAs over the same
-// latents, as the prefill's own scores do.
+// latents, as the prefill's own scores do: up to 2^-16 of |p| |z| off.  A third
+// part, as the decode's weights take, is a query tile of 80 KB for 64, and the ring
+// of two would leave no room for the keys' boxes.
 //
 // What bounds it: the rate at which one SM takes the MMAs.  For all the queries
 // of 2 x 4K prompts (32 heads, d_h 128, rank 64: 108.6 us of tensor work at the
-// rate of a large bf16 product, p's two parts counted) the call takes 258 us:
-// 33 for p, 217 for the scores.  What was tried, at that shape:
+// rate of a large bf16 product, p's two parts counted) the call takes 260 us:
+// 33 for p, 217 for the scores, an N = 128 instruction every 75 cycles of an SM
+// (64 of tensor work) but for the 20% of the time that a half waits for its
+// accumulator to be read back and the 8% for queries and k_s.  What was tried, at
+// that shape:
 //   - both operands in shared memory: an N = 128 instruction reads 8 KB for 64
 //     cycles of work and took ~95.  So the keys, the same for every query of the
 //     item (k_s) or of the head (z_k,h), are the A operand from TMEM: 548 -> 312 us.
@@ -35,15 +40,18 @@
 // A window of one tile (ONE) uses each latent box once: it stays in shared memory
 // as the A operand, and its TMEM takes a second k_s buffer, so the next item's
 // keys are moved during this one.  4 x 16K keys of 32 heads, rank 64, window 32
-// (277 MB, 41.5 us at the copy rate): 115 us with the boxes moved, 82 us so.  There
-// the N = 32 products of one head each bound it; four issuing threads, each with
-// half of a tile's heads, took 106 us where two took 95.  For the long windows the
+// (277 MB, 41.5 us at the copy rate): 115 us with the boxes moved, 84 us so.  There
+// the issuing threads wait for latents a fifth of the time and for k_s 8%; in the
+// rest an SM takes an instruction (N = 32, one head) every 80 cycles, for 16 of
+// tensor work and 40 of operand reads.  Four issuing threads, each with half of a
+// tile's heads, took 106 us where two took 95.  For the long windows the
 // boxes moved to TMEM are better: read from shared memory for each of a head's
 // tiles, even with the TMEM they free as a third accumulator, 233 us for 217.
 //
 // Persistent: one CTA per SM walks the items, those with the most queries (the
 // first keys) first and dealt in a snake; the rings run on across items.
-// Warp 0 copies the keys' boxes (TMA), warp 2 the query tiles; warps 4-7 move
+// Warp 0 copies the keys' boxes (TMA), warp 2 the query tiles (and blanks the
+// queries that give nothing: 1 us of the 84); warps 4-7 move
 // keys to TMEM; one thread of warp 1 and one of warp 24 issue the MMAs of a half
 // each; warp 3 lays down the log-sum-exps; warps 8-23 read the accumulators back.
 // Each item leaves one partial sum per key; the last kernel adds the head groups'

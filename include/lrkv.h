@@ -50,6 +50,16 @@
  *    depended on it, still waits at the full bound for all that it issued,
  *    and records LRKV_ERR_TIMEOUT: the call's outputs are then not to be used.
  *    Set the variable only to exercise that path.
+ *  * Order on the stream.  The calls' kernels use programmatic dependent
+ *    launch.  A decode (lrkv_decode and its forms, the weighted, RoPE and
+ *    comparison decodes) reads its inputs before it waits for the launch
+ *    before it: they must be complete when that launch lets its dependents
+ *    start.  A kernel that does not do so explicitly lets them start when it
+ *    ends; so do all calls here that write a decode's input, but for
+ *    lrkv_decode_step, whose new rows are sure to be seen by its own decode
+ *    and by calls that wait (the next lrkv_decode_step, lrkv_append,
+ *    lrkv_evict, lrkv_prefill_weights).  A kernel of the caller's that signals
+ *    early must not write q, positions, lengths, tables or rows afterwards.
  *  * Planning.  Launch grids and workspace sizes follow the current device's
  *    SM count, or LRKV_SM_COUNT when that environment variable holds a
  *    positive number (read at each call: workspace sizes without a device;
@@ -135,9 +145,8 @@ lrkv_status lrkv_decode_workspace_size(const lrkv_dims* dims, size_t* bytes);
  * ceil(heads/16) * head_dim / 8 <= 32; dtype F32 with rank <= 64,
  * head_dim <= 8 * (lanes per head); batch <= 4096.  Others return
  * LRKV_ERR_UNSUPPORTED.
- * The call's kernels use programmatic dependent launch: its inputs must be
- * complete when the launch before it on the stream lets its dependents start
- * (a kernel that does not do so explicitly lets them start when it ends).
+ * Its inputs must be complete when the launch before it on the stream lets its
+ * dependents start ("Order on the stream" above).
  */
 lrkv_status lrkv_decode(const lrkv_dims* dims, const void* q, const void* k_s, const void* v_s,
                         const void* z_k, const void* z_v, const void* b_k, const void* b_v,
@@ -480,10 +489,13 @@ lrkv_status lrkv_decode_rope(const lrkv_dims* dims, const void* q_rot, const voi
  * up to its own; the prompt's q_len rows are the call's new tokens, so call it
  * once per chunk.  seq_lens[b] outside [q_len, max_len] is clamped and sets
  * LRKV_ERR_DEVICE_BOUNDS.  1 <= window <= q_len (else LRKV_ERR_INVALID_ARG),
- * q_len <= max_len.  Supported: dtype BF16, head_dim 64 or 128, rank a
- * multiple of 8 up to 64, heads <= 256; page_size a power of two >= 16.
- * z_k and b_k may be NULL when rank == 0.  Workspace:
- * lrkv_prefill_weights_workspace_size() bytes; its status word is set afresh.
+ * q_len <= max_len.  q B^K enters the scores as two bf16 parts (the decode's
+ * as three): a score is off by up to 2^-16 of sum |q B^K| |z_k| more than
+ * fp32 arithmetic makes it, a weight by that much of itself.  Supported:
+ * dtype BF16, head_dim 64 or 128, rank a multiple of 8 up to 64, heads <=
+ * 256; page_size a power of two >= 16. z_k and b_k may be NULL when rank ==
+ * 0.  Workspace: lrkv_prefill_weights_workspace_size() bytes; its status
+ * word is set afresh.
  */
 lrkv_status lrkv_decode_weighted_workspace_size(const lrkv_dims* dims, size_t* bytes);
 lrkv_status lrkv_decode_weighted(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
@@ -563,8 +575,10 @@ lrkv_status lrkv_evict(const lrkv_dims* dims, int budget, int sink, int recent, 
  * seq_lens[b] are not read), so that rows may have been moved or evicted, and
  * with the accumulation of lrkv_decode_weighted when weights_out is not NULL
  * (then lse must not be NULL either).  out is held to fp32 accuracy.
- * Supported: the shapes of lrkv_decode_rope.  Workspace:
- * lrkv_decode_rope_axes_workspace_size() bytes.
+ * Supported: the shapes of lrkv_decode_rope, which are fewer than lrkv_evict
+ * moves: contiguous bf16 caches without key scales.  Workspace:
+ * lrkv_decode_rope_axes_workspace_size() bytes (the scores of the accumulation
+ * among them, also for a call without it).
  */
 lrkv_status lrkv_rope_rotate(const lrkv_dims* dims, int n, const void* x, const int32_t* positions, int axes,
                              const int* sections, const float* cos_sin, int max_pos, void* out, void* ws,
