@@ -1,0 +1,885 @@
+// decode8.cu — one decode step over the factored cache in 8 bits
+// (lrkv_decode8): every element is an e4m3 number times the scale of its block
+// of 16 rows and head.
+//
+//   score_{h,j} = (ks_j (q_h . k8_j) + kz_{j,h} (p_h . z8_{j,h})) scale,  p_h = q_h B_h^K
+//   o_h = sum_j a_{h,j} vs_j v8_j + (sum_j a_{h,j} vz_{j,h} z8_{j,h}) (B_h^V)^T
+//
+// The cache's bytes bound it, so they go from memory to the tensor cores as
+// they are: TMA lays 128 rows x 128 columns boxes down, tcgen05.mma (kind
+// f8f6f4) takes them as its A operand, K-major (rows as M) for the scores,
+// MN-major (columns as M, rows as K) for the values.  What multiplies them is
+// fp32 (p, the probabilities) or bf16 (q), and is split into e4m3 parts, each
+// the rounding of what the ones before left, times 16: four significant bits a
+// part, six parts for fp32, four for q.  The parts are columns of the B
+// operand; a product of 128 x N x 32 costs the same 46 cycles for every N up
+// to 48, so the parts of eight heads cost what one column would.  The part
+// sums come back from TMEM and are added in fp32.  A tile's products start
+// from zero, so that the tensor core's truncation (2^-21 of the sum of the
+// magnitudes at worst) does not grow with the length; the sums over the tiles
+// are in registers.
+//
+// Heads go in groups of eight, a CTA each; the latents of a group are a block
+// diagonal operand (zero columns for the other heads).  The shared rows are read
+// by every group; all but the first find them in L2.
+//
+// Grid (range CTAs, groups).  15 warps: 0-7 the softmax (a thread per row, four
+// heads each), 8-11 the value sums (a thread per column), 12 the copies, 13
+// the MMAs, 14 the operands of each sequence, which
+// lrkv_decode8_operands_kernel has laid out before.  The keys of tile i + 1 are
+// multiplied while the softmax works on tile i.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "cache8.h"
+#include "decode_common.cuh"
+#include "decode_plan.h"
+#include "host_cache.h"
+#include "lrkv.h"
+#include "ptx.cuh"
+#include "tmap.h"
+#include "trace.h"
+
+namespace lrkv {
+
+using namespace dec;
+
+namespace {
+
+constexpr int k8Rows = 128;        // rows of a tile
+constexpr int k8Unit = 32;         // rows of a unit: the split's step, one K step of the value products
+constexpr int k8Units = k8Rows / k8Unit;
+constexpr int k8Heads = 8;         // heads of a CTA
+constexpr int k8QParts = 4, k8Parts = 6;
+constexpr int k8NQ = k8Heads * k8QParts, k8N = k8Heads * k8Parts;  // columns of the operands
+constexpr int k8Box = 16384;       // 128 rows x 128 columns
+constexpr int k8MaxSlots = 14;
+constexpr int k8Softmax = 8, k8Values = 4;
+constexpr int k8Threads = 32 * (k8Softmax + k8Values + 3);
+constexpr int k8MaxD = 2, k8MaxZ = 4;  // 128-column chunks of a shared row, of a group's latents
+// TMEM columns: two score buffers, then the value products
+constexpr uint32_t k8S = 0, k8SWidth = k8NQ + k8N, k8Os = 2 * k8SWidth, k8Oz = k8Os + k8MaxD * k8N, k8Cols = 512;
+static_assert(k8Oz + k8MaxZ * k8N <= k8Cols, "more TMEM than there is");
+
+struct Args8 {
+  int groups, nd, nz;   // head groups; chunks of a shared row and of a group's latents
+  int img_bytes;        // operands of a (sequence, group): q parts | p parts | 16 factors
+  int img_pad;          // the same in shared memory, on a 1 KB boundary
+  int slots, box_rows;  // ring depth; rows of a copy (32, or 16 where a page holds no more)
+  int off_img, off_p, off_ring;
+  int blocks;           // scale blocks of a sequence (contiguous) or page
+  unsigned char* images;
+  lrkv_cache8 cache;
+};
+
+__device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                     uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// e4m3 A and B, fp32 D, M = 128; a_mn: A is MN-major.
+__host__ __device__ constexpr uint32_t idesc8(int N, int a_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* v) {
+  static_assert(N == 16 || N == 8 || N == 4 || N == 2, "");
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(t));
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(t));
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(t));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(t));
+}
+// Sum of N part sums, each worth a 16th of the one before.
+template <int N>
+__device__ __forceinline__ float join(const uint32_t* v) {
+  float s = __uint_as_float(v[N - 1]);
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) s = fmaf(s, 0.0625f, __uint_as_float(v[i]));
+  return s;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void bar_named(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Waits for a phase unless the CTA has given up, and gives up itself at the bound.
+__device__ __forceinline__ bool wait8(uint64_t* bar, uint32_t parity, volatile int* fail, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*fail) return false;
+    if (clock64() - t0 > limit) {
+      *fail = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same by a whole warp.
+__device__ __forceinline__ bool wait8_warp(uint64_t* bar, uint32_t parity, volatile int* fail, long long limit) {
+  const bool ok = wait8(bar, parity, fail, limit);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+}  // namespace
+
+// ============================================================== the operands
+// One CTA per (head, sequence): p = q B^K in fp32, then q and p as e4m3 parts
+// in the layout of the MMA's B operand (K-major, 128-byte swizzle): row
+// (head, part), a byte per column, zeros in the columns of the other heads.
+// Both are brought to a largest magnitude in [128, 256) first; the factors
+// undo that and hold the scale (log2 domain).
+__global__ void __launch_bounds__(128) lrkv_decode8_operands_kernel(const __grid_constant__ DecodePlan P,
+                                                                    const __grid_constant__ Args8 A) {
+  __shared__ float s_q[256], s_part[4][64];
+  __shared__ uint32_t s_max[2];
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x, b = blockIdx.y, hl = h & 7, d = P.dh, r = P.r;
+  const bool there = h < P.H;
+  if (tid < 2) s_max[tid] = 0u;
+  __syncthreads();
+  uint32_t top = 0u;
+  for (int k = tid; k < d; k += 128) {
+    const float q = there ? __bfloat162float(
+                                static_cast<const __nv_bfloat16*>(P.q)[(static_cast<size_t>(b) * P.H + h) * d + k])
+                          : 0.f;
+    s_q[k] = q;
+    top = max(top, __float_as_uint(q) & 0x7fffffffu);
+  }
+  atomicMax(&s_max[0], top);
+  __syncthreads();
+  if (r > 0) {
+    // lanes hold two columns each, warps every fourth row of B_h
+    float a0 = 0.f, a1 = 0.f;
+    if (there && 2 * lane < r) {
+      const uint32_t* bk = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(P.b_k) +
+                                                             static_cast<size_t>(h) * d * r) + lane;
+#pragma unroll 16
+      for (int k = warp; k < d; k += 4) {
+        const uint32_t w = __ldg(bk + k * (r / 2));
+        a0 = fmaf(s_q[k], bf_lo(w), a0);
+        a1 = fmaf(s_q[k], bf_hi(w), a1);
+      }
+    }
+    s_part[warp][2 * lane] = a0;
+    s_part[warp][2 * lane + 1] = a1;
+    __syncthreads();
+    if (tid < 64) {
+      const float p = tid < r ? (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]) : 0.f;
+      s_part[0][tid] = p;
+      atomicMax(&s_max[1], __float_as_uint(p) & 0x7fffffffu);
+    }
+    __syncthreads();
+  }
+  float up[2], down[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = max(static_cast<int>(s_max[i] >> 23) - 127, -100);
+    up[i] = pow2(7 - e);
+    // (infinities and NaN make the scores NaN)
+    down[i] = e == 128 ? __uint_as_float(0x7fffffffu) : pow2(e - 7) * P.scale_log2;
+    if (e == 128) up[i] = 0.f;
+  }
+  pdl_wait();  // the launch before may still read the workspace
+  unsigned char* img = A.images + (static_cast<size_t>(b) * A.groups + (h >> 3)) * A.img_bytes;
+  for (int j = 0; j < A.nd; ++j) {
+    float x = 128 * j + tid < d ? s_q[128 * j + tid] * up[0] : 0.f;
+#pragma unroll
+    for (int i = 0; i < k8QParts; ++i) {
+      const int n = hl * k8QParts + i;
+      const uint32_t v = e4m3x2(x, 0.f);
+      img[n * 128 + (tid ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
+      x = (x - from_e4m3x2(v).x) * 16.f;
+    }
+    img += k8NQ * 128;
+  }
+  for (int j = 0; j < A.nz; ++j) {
+    const int c = 128 * j + tid - hl * r;  // this head's latent column
+    float x = c >= 0 && c < r ? s_part[0][c] * up[1] : 0.f;
+#pragma unroll
+    for (int i = 0; i < k8Parts; ++i) {
+      const int n = hl * k8Parts + i;
+      const uint32_t v = e4m3x2(x, 0.f);
+      img[n * 128 + (tid ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
+      x = (x - from_e4m3x2(v).x) * 16.f;
+    }
+    img += k8N * 128;
+  }
+  if (tid < 2) reinterpret_cast<float*>(img)[8 * tid + hl] = there ? down[tid] : 0.f;
+}
+
+// ================================================================== the scan
+__global__ void __launch_bounds__(k8Threads, 1)
+    lrkv_decode8_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_zk,
+                        const __grid_constant__ CUtensorMap tm_zv, const __grid_constant__ Args8 A) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  // full/empty: ring slots; ifull/iempty: operands; sfull/sempty: scores; pfull: probabilities; pv: their
+  // products done (and the probabilities' buffer free); oempty: products read; mdone: every MMA done
+  __shared__ uint64_t full[k8MaxSlots], empty[k8MaxSlots], ifull[2], iempty[2], sfull[2], sempty[2], pfull, pv, oempty,
+      mdone;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_fail, s_bad, s_copies, s_images;
+  __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
+  __shared__ float s_fac[2][20];                      // [tile parity]: alpha[8], latent scale[8], shared scale
+  __shared__ float s_sum[2][4][4];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  volatile int* fail = &s_fail;
+
+  pdl_trigger();  // the merge may launch: it waits for this grid before it reads
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = P.B, H = P.H, r = P.r, group = blockIdx.y, h0 = group * k8Heads;
+  const int heads = min(k8Heads, H - h0);
+  const int nd = A.nd, nz = (heads * r + 127) / 128;
+  int* pre = reinterpret_cast<int*>(smem);
+
+  // ---- barriers, TMEM, sequence starts in units of 32 rows -----------------------------
+  if (tid == 0) {
+    for (int i = 0; i < k8MaxSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ifull[i], 1);
+      mbar_init(&iempty[i], 1 + k8Softmax);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sempty[i], k8Softmax);
+    }
+    mbar_init(&pfull, k8Softmax);
+    mbar_init(&pv, 1);
+    mbar_init(&oempty, k8Values);
+    mbar_init(&mdone, 1);
+    s_fail = s_bad = s_copies = s_images = 0;
+    fence_barrier_init();
+  }
+  if (warp == 13) tmem_alloc(&tmem_base, k8Cols);
+  int bad = 0;
+  for (int b = tid; b < B; b += k8Threads) {
+    int L = P.seq_lens[b];
+    if (L < 0 || L > P.max_len) {
+      bad = 1;
+      L = min(max(L, 0), P.max_len);
+    }
+    pre[b + 1] = (L + k8Unit - 1) / k8Unit;
+  }
+  if (tid == 0) pre[0] = 0;
+  bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    int carry = 0;
+    for (int base = 1; base <= B; base += 32) {
+      const int i = base + lane;
+      int v = (i <= B) ? pre[i] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (i <= B) pre[i] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const int N = pre[B];
+  const int G = max(1, min(static_cast<int>(gridDim.x), (N + P.min_tokens - 1) / max(P.min_tokens, 1)));
+  const int c = blockIdx.x;
+  const bool work = N > 0 && c < G;
+  const int g0 = work ? static_cast<int>(static_cast<long long>(c) * N / G) : 0;
+  const int g1 = work ? static_cast<int>(static_cast<long long>(c + 1) * N / G) : 0;
+  auto rows_of = [&](int b) { return min(max(__ldg(P.seq_lens + b), 0), P.max_len); };
+
+  TileWalk w;
+  if (!work) {
+    // nothing to do
+  } else if (warp < k8Softmax) {
+    // ---- softmax: row 32 quad + lane of a tile, heads 4 half .. + 3 of the group ----------
+    const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, hb = h0 + 4 * half;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    unsigned char* ps = smem + A.off_p + half * (4 * k8Parts * 128);
+    unsigned char* pz = ps + k8N * 128;
+    const bool vec = H % 4 == 0;
+    float m[4], l[4], fq[4], fz[4];
+    int cur_b = -1, L = 0, i = 0, piece = -1;
+    // scales of this thread's row: shared key and value, latents' keys and values
+    float nks = 0.f, nvs = 0.f, nkz[4], nvz[4];
+    auto load_scales = [&](const TileWalk& t) {
+      const int row_b = k8Unit * t.t0 + row;
+      nks = nvs = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) nkz[k] = nvz[k] = 0.f;
+      if (row_b >= min(rows_of(t.b), k8Unit * t.t_end)) return;
+      size_t blk = static_cast<size_t>(t.b) * A.blocks + row_b / kBlock8;
+      if (P.block_table) {
+        const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (row_b >> P.page_shift));
+        if (page < 0 || page >= P.num_pages) return;
+        blk = static_cast<size_t>(page) * A.blocks + (row_b & ((1 << P.page_shift) - 1)) / kBlock8;
+      }
+      nks = __ldg(A.cache.k_s_scale + blk);
+      nvs = __ldg(A.cache.v_s_scale + blk);
+      if (r == 0) return;
+      const float* kz = A.cache.z_k_scale + blk * H + hb;
+      const float* vz = A.cache.z_v_scale + blk * H + hb;
+      if (vec && hb < H) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(kz)), e = __ldg(reinterpret_cast<const float4*>(vz));
+        nkz[0] = a.x; nkz[1] = a.y; nkz[2] = a.z; nkz[3] = a.w;
+        nvz[0] = e.x; nvz[1] = e.y; nvz[2] = e.z; nvz[3] = e.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (hb + k < H) {
+            nkz[k] = __ldg(kz + k);
+            nvz[k] = __ldg(vz + k);
+          }
+      }
+    };
+    bool more = walk_first(w, pre, B, g0, g1);
+    if (more) load_scales(w);
+    pdl_wait();  // the launch before may still read the workspace
+    for (; more; ++i) {
+      TileWalk nx = w;
+      const bool nmore = walk_next(nx, pre, B, g1, k8Units);
+      const bool last = !nmore || nx.b != w.b;
+      if (w.b != cur_b) {
+        cur_b = w.b;
+        ++piece;
+        L = rows_of(w.b);
+        wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
+        const float* f = reinterpret_cast<const float*>(smem + A.off_img + (piece & 1) * A.img_pad + A.img_bytes - 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          fq[k] = f[4 * half + k];
+          fz[k] = f[8 + 4 * half + k];
+          m[k] = -INFINITY;
+          l[k] = 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&iempty[piece & 1]);
+      }
+      const int units = min(k8Units, w.t_end - w.t0);
+      const int rows = min(k8Unit * units, L - k8Unit * w.t0);
+      float ks = nks, vs = nvs, kz[4], vz[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) { kz[k] = nkz[k]; vz[k] = nvz[k]; }
+      if (nmore) load_scales(nx);
+
+      // the scores
+      uint32_t dq[16], dz[24];
+      wait8_warp(&sfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+      tc_fence_after();
+      const uint32_t sb = at + k8S + (i & 1) * k8SWidth;
+      tmem_ld<16>(sb + 16 * half, dq);
+      if (r > 0) {
+        tmem_ld<16>(sb + k8NQ + 24 * half, dz);
+        tmem_ld<8>(sb + k8NQ + 24 * half + 16, dz + 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 24; ++k) dz[k] = 0u;
+      }
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&sempty[i & 1]);
+      float s[4], top[4], tz[4], ts = warp_max(row < rows ? vs : 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = join<4>(dq + 4 * k) * (fq[k] * ks), y = join<6>(dz + 6 * k) * (fz[k] * kz[k]);
+        s[k] = row < rows ? x + y : -INFINITY;
+        top[k] = warp_max(s[k]);
+        tz[k] = warp_max(row < rows ? vz[k] : 0.f);
+      }
+      // maxima over the tile
+      float(*red)[12] = s_red[i & 1][half];
+      if (lane == 0) {
+        *reinterpret_cast<float4*>(&red[quad][0]) = make_float4(top[0], top[1], top[2], top[3]);
+        *reinterpret_cast<float4*>(&red[quad][4]) = make_float4(tz[0], tz[1], tz[2], tz[3]);
+        red[quad][8] = ts;
+      }
+      bar_named(1 + half, 128);
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const float4 a = *reinterpret_cast<const float4*>(&red[o][0]), e = *reinterpret_cast<const float4*>(&red[o][4]);
+        top[0] = fmaxf(top[0], a.x); top[1] = fmaxf(top[1], a.y); top[2] = fmaxf(top[2], a.z); top[3] = fmaxf(top[3], a.w);
+        tz[0] = fmaxf(tz[0], e.x); tz[1] = fmaxf(tz[1], e.y); tz[2] = fmaxf(tz[2], e.z); tz[3] = fmaxf(tz[3], e.w);
+        ts = fmaxf(ts, red[o][8]);
+      }
+      // one online softmax per head; the probabilities times the block's share of the tile's largest value
+      // scale, brought to 256 at most
+      float xs[4], xz[4], alpha[4];
+      const float us = ts > 0.f ? 256.f * (vs / ts) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float mx = fmaxf(m[k], top[k]);
+        alpha[k] = m[k] == -INFINITY ? 0.f : exp2f(m[k] - mx);
+        m[k] = mx;
+        const float p = row < rows ? exp2f(s[k] - mx) : 0.f;
+        l[k] = fmaf(l[k], alpha[k], p);
+        xs[k] = p * us;
+        xz[k] = tz[k] > 0.f ? p * (256.f * (vz[k] / tz[k])) : 0.f;
+        if (row >= rows) xs[k] = xz[k] = 0.f;
+      }
+      // into the operand of the value products, once the ones before are done with it
+      if (i > 0) wait8_warp(&pv, static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit);
+      if (quad == 0 && lane == 0) {
+        float* fac = s_fac[i & 1];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          fac[4 * half + k] = alpha[k];
+          fac[8 + 4 * half + k] = tz[k] * (1.f / 256.f);
+        }
+        if (half == 0) fac[16] = ts * (1.f / 256.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+#pragma unroll
+        for (int t = 0; t < k8Parts; ++t) {
+          const int n0 = k * k8Parts + t, n1 = n0 + k8Parts;  // rows of the two heads (of this half's 24)
+          const uint32_t o0 = n0 * 128 + (row ^ ((n0 & 7) << 4)), o1 = n1 * 128 + (row ^ ((n1 & 7) << 4));
+          const uint32_t a = e4m3x2(xs[k], xs[k + 1]);
+          const float2 fa = from_e4m3x2(a);
+          ps[o0] = static_cast<unsigned char>(a);
+          ps[o1] = static_cast<unsigned char>(a >> 8);
+          xs[k] = (xs[k] - fa.x) * 16.f;
+          xs[k + 1] = (xs[k + 1] - fa.y) * 16.f;
+          if (r > 0) {
+            const uint32_t e = e4m3x2(xz[k], xz[k + 1]);
+            const float2 fe = from_e4m3x2(e);
+            pz[o0] = static_cast<unsigned char>(e);
+            pz[o1] = static_cast<unsigned char>(e >> 8);
+            xz[k] = (xz[k] - fe.x) * 16.f;
+            xz[k + 1] = (xz[k + 1] - fe.y) * 16.f;
+          }
+        }
+      }
+      // value rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
+      if (rows < k8Unit * units) {
+        int idx = (nd + nz) * (2 * i + (nmore ? 2 : 1));  // the tile's first value copy
+        for (int j = 0; j < nd + nz; ++j, ++idx) {
+          const int slot = idx % A.slots;
+          const bool landed =
+              wait8_warp(&full[slot], static_cast<uint32_t>(idx / A.slots) & 1u, fail, P.wait_limit);
+          if (landed && tid < 8 * (k8Unit * units - rows))
+            *reinterpret_cast<uint4*>(smem + A.off_ring + slot * k8Box + rows * 128 + tid * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&pfull);
+      if (last) {  // the piece's maxima and denominators
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+          if (lane == 0) s_sum[half][quad][k] = l[k];
+        }
+        bar_named(1 + half, 128);
+        if (quad == 0 && lane < 4 && hb + lane < H) {
+          float* pml = P.part_ml + (static_cast<size_t>(w.b + c) * H + hb + lane) * 2;
+          pml[0] = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
+          pml[1] = (s_sum[half][0][lane] + s_sum[half][1][lane]) + (s_sum[half][2][lane] + s_sum[half][3][lane]);
+        }
+        bar_named(1 + half, 128);
+      }
+      w = nx;
+      more = nmore;
+    }
+  } else if (warp < k8Softmax + k8Values) {
+    // ---- value sums: column 32 quad + lane of every chunk ------------------------------
+    const int quad = warp & 3, col = 32 * quad + lane, d = P.dh;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    float os[k8MaxD][k8Heads], oz[k8MaxZ];
+    int head[k8MaxZ], lo[k8MaxZ], hi[k8MaxZ];  // this column's head; the warp's first and last
+#pragma unroll
+    for (int j = 0; j < k8MaxZ; ++j) {
+      head[j] = lo[j] = -1;
+      hi[j] = -2;
+      if (j < nz) {
+        head[j] = (128 * j + col) / r;
+        lo[j] = (128 * j + 32 * quad) / r;
+        hi[j] = min((128 * j + 32 * quad + 31) / r, heads - 1);
+      }
+    }
+    pdl_wait();  // the launch before may still read the workspace
+    int i = 0, cur_b = -1;
+    for (bool more = walk_first(w, pre, B, g0, g1); more; ++i) {
+      TileWalk nx = w;
+      const bool nmore = walk_next(nx, pre, B, g1, k8Units);
+      const bool last = !nmore || nx.b != w.b;
+      if (w.b != cur_b) {
+        cur_b = w.b;
+#pragma unroll
+        for (int j = 0; j < k8MaxD; ++j)
+#pragma unroll
+          for (int k = 0; k < k8Heads; ++k) os[j][k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < k8MaxZ; ++j) oz[j] = 0.f;
+      }
+      wait8_warp(&pv, static_cast<uint32_t>(i) & 1u, fail, P.wait_limit);
+      tc_fence_after();
+      const float* fac = s_fac[i & 1];
+      const float us = fac[16];
+#pragma unroll
+      for (int j = 0; j < k8MaxD; ++j) {
+        if (j >= nd) break;
+        uint32_t v[k8N];
+        tmem_ld<16>(at + k8Os + j * k8N, v);
+        tmem_ld<16>(at + k8Os + j * k8N + 16, v + 16);
+        tmem_ld<16>(at + k8Os + j * k8N + 32, v + 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < k8Heads; ++k) os[j][k] = fmaf(os[j][k], fac[k], join<k8Parts>(v + k8Parts * k) * us);
+      }
+#pragma unroll
+      for (int j = 0; j < k8MaxZ; ++j) {
+        for (int k = lo[j]; k <= hi[j]; ++k) {  // (the same for the whole warp)
+          uint32_t v[k8Parts];
+          tmem_ld<4>(at + k8Oz + j * k8N + k * k8Parts, v);
+          tmem_ld<2>(at + k8Oz + j * k8N + k * k8Parts + 4, v + 4);
+          tmem_wait_ld();
+          const float x = fmaf(oz[j], fac[k], join<k8Parts>(v) * fac[8 + k]);
+          if (k == head[j]) oz[j] = x;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&oempty);
+      if (last) {
+        float* out = P.part_acc + (static_cast<size_t>(w.b + c) * H + h0) * (d + r);
+#pragma unroll
+        for (int j = 0; j < k8MaxD; ++j) {
+          if (j < nd && 128 * j + col < d) {
+#pragma unroll
+            for (int k = 0; k < k8Heads; ++k)
+              if (k < heads) out[static_cast<size_t>(k) * (d + r) + 128 * j + col] = os[j][k];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < k8MaxZ; ++j)
+          if (j < nz && head[j] < heads)
+            out[static_cast<size_t>(head[j]) * (d + r) + d + 128 * j + col - head[j] * r] = oz[j];
+      }
+      w = nx;
+      more = nmore;
+    }
+  } else if (warp == 12) {
+    // ---- copies, in the order the MMAs take them: keys of tile 0, then keys of tile i + 1
+    // and values of tile i; a lane per box of box_rows rows.  A slot is let go by the MMAs that
+    // read it, so its last copy has landed ---------------------------------------------------
+    int idx = 0;
+    auto copy = [&](const TileWalk& t, bool values) -> bool {
+      const int units = min(k8Units, t.t_end - t.t0), boxes = units * k8Unit / A.box_rows;
+      const int at = k8Unit * t.t0 + lane * A.box_rows;  // this lane's first row
+      int y = at, z = t.b;
+      if (P.block_table && lane < boxes) {
+        y = at & ((1 << P.page_shift) - 1);
+        z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
+        if (at < rows_of(t.b)) {
+          const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (at >> P.page_shift));
+          if (page >= 0 && page < P.num_pages) z = page; else s_bad = 1;
+        }
+      }
+      for (int j = 0; j < nd + nz; ++j, ++idx) {
+        const int slot = idx % A.slots;
+        if (idx >= A.slots && !wait8_warp(&empty[slot], static_cast<uint32_t>(idx / A.slots - 1) & 1u, fail, P.wait_limit))
+          return false;
+        if (__any_sync(0xffffffffu, *fail)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[slot], units * k8Unit * 128);
+          s_copies = idx + 1;
+        }
+        __syncwarp();
+        if (lane < boxes) {
+          unsigned char* dst = smem + A.off_ring + slot * k8Box + lane * A.box_rows * 128;
+          if (j < nd) tma_load_3d(dst, values ? &tm_v : &tm_k, 128 * j, y, z, &full[slot]);
+          else tma_load_3d(dst, values ? &tm_zv : &tm_zk, h0 * r + 128 * (j - nd), y, z, &full[slot]);
+        }
+      }
+      return true;
+    };
+    TileWalk kw;
+    bool km = walk_first(kw, pre, B, g0, g1);
+    w = kw;
+    bool ok = copy(kw, false);
+    for (bool more = true; more && ok; more = walk_next(w, pre, B, g1, k8Units)) {
+      km = km && walk_next(kw, pre, B, g1, k8Units);
+      if (km) ok = copy(kw, false);
+      ok = ok && copy(w, true);
+    }
+  } else if (warp == 13) {
+    if (lane == 0) {
+      // ---- MMAs ------------------------------------------------------------------------
+      int idx = 0, ki = 0, vi = 0, piece = -1, cur_b = -1;
+      const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
+      const uint64_t img = smem_desc(smem_u32(smem + A.off_img), 16, 1024, 2);
+      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), 16, 1024, 2);
+      auto slot_full = [&](int& slot) {
+        slot = idx % A.slots;
+        return wait8(&full[slot], static_cast<uint32_t>(idx / A.slots) & 1u, fail, P.wait_limit) && !*fail;
+      };
+      // scores of a tile: q against the shared rows, p against the latents
+      auto scores = [&](const TileWalk& t, bool last) -> bool {
+        if (t.b != cur_b) {
+          cur_b = t.b;
+          ++piece;
+          if (!wait8(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit)) return false;
+        }
+        const int a = ki & 1;
+        if (ki >= 2 && !wait8(&sempty[a], static_cast<uint32_t>((ki >> 1) - 1) & 1u, fail, P.wait_limit)) return false;
+        const uint32_t sd = tmem + k8S + a * k8SWidth;
+        uint64_t bd = img + static_cast<uint32_t>((piece & 1) * (A.img_pad / 16));
+        for (int j = 0; j < nd + nz; ++j, ++idx) {
+          int slot;
+          if (!slot_full(slot)) return false;
+          tc_fence_after();
+          const bool z = j >= nd;
+          const int left = z ? heads * r - 128 * (j - nd) : P.dh - 128 * j;
+          const uint64_t ad = ring + static_cast<uint32_t>(slot * (k8Box / 16));
+          for (int kk = 0; kk < 4 && 32 * kk < left; ++kk)
+            mma8(sd + (z ? k8NQ : 0), ad + kk * 2, bd + kk * 2, z ? idesc8(k8N, 0) : idesc8(k8NQ, 0),
+                 (z ? j > nd : j > 0) || kk > 0 ? 1u : 0u);
+          tc_commit(&empty[slot]);
+          bd += (z ? k8N : k8NQ) * 8;
+        }
+        tc_commit(&sfull[a]);
+        if (last) tc_commit(&iempty[piece & 1]);
+        ++ki;
+        return true;
+      };
+      // values of a tile: columns x rows of the box against the probabilities
+      auto values = [&](const TileWalk& t) -> bool {
+        const int units = min(k8Units, t.t_end - t.t0);
+        if (!wait8(&pfull, static_cast<uint32_t>(vi) & 1u, fail, P.wait_limit)) return false;
+        if (vi > 0 && !wait8(&oempty, static_cast<uint32_t>(vi - 1) & 1u, fail, P.wait_limit)) return false;
+        for (int j = 0; j < nd + nz; ++j, ++idx) {
+          int slot;
+          if (!slot_full(slot)) return false;
+          tc_fence_after();
+          const bool z = j >= nd;
+          const uint32_t od = tmem + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N);
+          const uint64_t ad = ring + static_cast<uint32_t>(slot * (k8Box / 16));
+          const uint64_t bd = pd + (z ? k8N * 8 : 0);
+          for (int kk = 0; kk < units; ++kk) mma8(od, ad + kk * 256, bd + kk * 2, idesc8(k8N, 1), kk > 0 ? 1u : 0u);
+          tc_commit(&empty[slot]);
+        }
+        tc_commit(&pv);
+        ++vi;
+        return true;
+      };
+      TileWalk kw, nx;
+      bool km = walk_first(kw, pre, B, g0, g1);
+      w = kw;
+      auto next_scores = [&]() -> bool {  // of kw, which then moves on
+        nx = kw;
+        const bool nm = walk_next(nx, pre, B, g1, k8Units);
+        const bool ok = scores(kw, !nm || nx.b != kw.b);
+        kw = nx;
+        km = nm;
+        return ok;
+      };
+      bool ok = next_scores();
+      for (bool more = true; more && ok; more = walk_next(w, pre, B, g1, k8Units)) {
+        if (km) ok = next_scores();
+        ok = ok && values(w);
+      }
+      tc_commit(&mdone);  // every MMA issued, also by a pass that gave up
+    }
+  } else if (lane == 0) {
+    // ---- the operands of each piece, two buffers ------------------------------------------
+    pdl_wait();
+    int piece = 0, cur_b = -1;
+    for (bool more = walk_first(w, pre, B, g0, g1); more && !*fail; more = walk_next(w, pre, B, g1, k8Units)) {
+      if (w.b == cur_b) continue;
+      cur_b = w.b;
+      if (piece >= 2 &&
+          !wait8(&iempty[piece & 1], static_cast<uint32_t>((piece >> 1) - 1) & 1u, fail, P.wait_limit))
+        break;
+      mbar_arrive_expect_tx(&ifull[piece & 1], A.img_bytes);
+      tma_load_1d(smem + A.off_img + (piece & 1) * A.img_pad,
+                  A.images + (static_cast<size_t>(w.b) * A.groups + group) * A.img_bytes, A.img_bytes,
+                  &ifull[piece & 1]);
+      s_images = ++piece;
+    }
+  }
+
+  // ---- every copy and MMA this CTA issued is complete before it exits ----
+  __syncthreads();
+  if (tid == 0) {
+    bool done = true;
+    for (int i = max(0, s_copies - A.slots); i < s_copies; ++i)
+      done = mbar_wait_bounded(&full[i % A.slots], static_cast<uint32_t>(i / A.slots) & 1u) && done;
+    for (int i = max(0, s_images - 2); i < s_images; ++i)
+      done = mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u) && done;
+    if (work) done = mbar_wait_bounded(&mdone, 0u) && done;
+    if (!done) *fail = 1;
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      P.meta[0] = N;
+      P.meta[1] = G;
+    }
+    P.cta_status[blockIdx.y * gridDim.x + blockIdx.x] = (bad || s_bad ? kDevBounds : 0u) | (*fail ? kDevTimeout : 0u);
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    pdl_wait();
+    for (int b = tid; b <= B; b += k8Threads) P.prefix[b] = pre[b];
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 13) tmem_dealloc(tmem, k8Cols);
+}
+
+// ======================================================================= host
+namespace {
+
+lrkv_status decode8_check(const lrkv_dims* d) {
+  const lrkv_status st = cache8_check_dims(d);
+  if (st != LRKV_OK) return st;
+  return d->dtype == LRKV_BF16 ? LRKV_OK : LRKV_ERR_UNSUPPORTED;
+}
+
+lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& A, size_t* image_off, size_t* bytes) {
+  std::memset(&P, 0, sizeof(P));
+  std::memset(&A, 0, sizeof(A));
+  P.B = d.batch; P.H = d.heads; P.dh = d.head_dim; P.r = d.rank; P.max_len = d.max_len;
+  const float scale = d.scale > 0.f ? d.scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
+  P.scale_log2 = scale * kLog2e;
+  P.bf16 = 1; P.esz = 2; P.ngw = 1;
+  P.wait_limit = wait_limit_cycles();
+  A.groups = (P.H + k8Heads - 1) / k8Heads;
+  A.nd = (P.dh + 127) / 128;
+  A.nz = (std::min(P.H, k8Heads) * P.r + 127) / 128;
+  P.mt = A.groups;
+  P.grid = std::max(1, num_sms / A.groups);
+  P.min_tokens = 2;  // units of 32 rows a CTA gets at least
+  A.img_bytes = A.nd * k8NQ * 128 + A.nz * k8N * 128 + 128;
+  A.img_pad = round_up(A.img_bytes, 1024);
+  int off = round_up((P.B + 1) * 4, 1024);
+  A.off_img = off; off += 2 * A.img_pad;
+  A.off_p = off; off += 2 * k8N * 128;
+  A.off_ring = off;
+  const int budget = 224 * 1024;  // (3 KB of the 227 for the static part and the alignment)
+  A.slots = std::min(k8MaxSlots, (budget - off) / k8Box);
+  // (a tile's value copies are all in the ring while its last rows are cleared)
+  if (A.slots < A.nd + A.nz + 1) return LRKV_ERR_UNSUPPORTED;
+  P.smem_bytes = off + A.slots * k8Box + 1024;
+  P.wide_merge = 1;
+  const long long pairs = static_cast<long long>(P.B) * P.H;
+  P.wide_warps = pairs <= 64 ? 16 : 8;
+  P.combine_ctas = static_cast<int>(std::min<long long>(pairs, 4ll * num_sms));
+  *image_off = (decode_workspace_bytes(P) + 255) / 256 * 256;
+  *bytes = *image_off + static_cast<size_t>(P.B) * A.groups * A.img_bytes;
+  return LRKV_OK;
+}
+
+// Rows of `width` bytes, box of 128 bytes x `box` rows with the 128-byte swizzle.
+bool map8(CUtensorMap* map, const void* base, int width, int rows, int lead, int box) {
+  return make_tmap_3d_u8(map, base, width, rows, lead, 128, box);
+}
+
+}  // namespace
+
+}  // namespace lrkv
+
+extern "C" {
+
+lrkv_status lrkv_decode8_workspace_size(const lrkv_dims* dims, size_t* bytes) {
+  if (!bytes) return LRKV_ERR_INVALID_ARG;
+  const lrkv_status st = lrkv::decode8_check(dims);
+  if (st != LRKV_OK) return st;
+  const int sms = lrkv::device_sm_count();
+  if (sms < 1) return LRKV_ERR_CUDA;
+  lrkv::DecodePlan P;
+  lrkv::Args8 A;
+  size_t off = 0;
+  return lrkv::decode8_plan(*dims, sms, P, A, &off, bytes);
+}
+
+lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
+                         const int32_t* block_table, const lrkv_cache8* cache, const void* b_k, const void* b_v,
+                         const int32_t* seq_lens, float* out, float* lse, void* ws, size_t ws_bytes,
+                         lrkv_stream_t stream) {
+  LRKV_TRACE_CALL("lrkv_decode8");
+  lrkv_status st = lrkv::decode8_check(dims);
+  if (st != LRKV_OK) return st;
+  if ((st = lrkv::cache8_check(dims, cache)) != LRKV_OK) return st;
+  if (!q || !seq_lens || !out || (dims->rank > 0 && (!b_k || !b_v))) return LRKV_ERR_INVALID_ARG;
+  if (!lrkv::cache8_a16(q) || reinterpret_cast<uintptr_t>(b_k) % 4 != 0 || reinterpret_cast<uintptr_t>(b_v) % 2 != 0)
+    return LRKV_ERR_INVALID_ARG;
+  if ((st = lrkv::cache8_check_paging(dims, page_size, num_pages, block_table)) != LRKV_OK) return st;
+  if (!ws) return LRKV_ERR_WORKSPACE;
+  if (!lrkv::cache8_a16(ws)) return LRKV_ERR_INVALID_ARG;
+  const int sms = lrkv::device_sm_count();
+  if (sms < 1) return LRKV_ERR_CUDA;
+  lrkv::DecodePlan P;
+  lrkv::Args8 A;
+  size_t image_off = 0, need = 0;
+  if ((st = lrkv::decode8_plan(*dims, sms, P, A, &image_off, &need)) != LRKV_OK) return st;
+  if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
+  lrkv::decode_bind_workspace(P, ws);
+  A.images = static_cast<unsigned char*>(ws) + image_off;
+  A.cache = *cache;
+  P.q = q; P.b_k = b_k; P.b_v = b_v;
+  P.seq_lens = seq_lens; P.out = out; P.lse = lse;
+  int rows = P.max_len, lead = P.B;
+  if (block_table) {
+    P.block_table = block_table;
+    P.max_blocks = P.max_len / page_size;
+    P.num_pages = num_pages;
+    while ((1 << P.page_shift) < page_size) ++P.page_shift;
+    rows = page_size;
+    lead = num_pages;
+  }
+  A.blocks = (rows + lrkv::kBlock8 - 1) / lrkv::kBlock8;
+  A.box_rows = block_table && page_size < lrkv::k8Unit ? page_size : lrkv::k8Unit;
+
+  CUtensorMap tm_k, tm_v, tm_zk, tm_zv;
+  std::memset(&tm_zk, 0, sizeof(tm_zk));
+  std::memset(&tm_zv, 0, sizeof(tm_zv));
+  if (!lrkv::map8(&tm_k, cache->k_s, P.dh, rows, lead, A.box_rows) ||
+      !lrkv::map8(&tm_v, cache->v_s, P.dh, rows, lead, A.box_rows) ||
+      (P.r > 0 && (!lrkv::map8(&tm_zk, cache->z_k, P.H * P.r, rows, lead, A.box_rows) ||
+                   !lrkv::map8(&tm_zv, cache->z_v, P.H * P.r, rows, lead, A.box_rows))))
+    return LRKV_ERR_CUDA;
+  const void* kern = reinterpret_cast<const void*>(lrkv::lrkv_decode8_kernel);
+  if (lrkv::ensure_kernel_smem(kern, P.smem_bytes, true) != cudaSuccess) return LRKV_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(A.groups * lrkv::k8Heads, P.B);
+  cfg.blockDim = dim3(128);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_operands_kernel, P, A) != cudaSuccess) return LRKV_ERR_CUDA;
+  cfg.gridDim = dim3(P.grid, P.mt);
+  cfg.blockDim = dim3(lrkv::k8Threads);
+  cfg.dynamicSmemBytes = P.smem_bytes;
+  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_kernel, P, tm_k, tm_v, tm_zk, tm_zv, A) != cudaSuccess)
+    return LRKV_ERR_CUDA;
+  return lrkv::decode_merge_launch(P, stream, true);
+}
+
+}  // extern "C"

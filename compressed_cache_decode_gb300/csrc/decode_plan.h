@@ -21,6 +21,7 @@ constexpr int kStreamConsumers = 8;  // consumer warps of the streaming kernel
 // Bits of the device status word (first 4 bytes of a workspace).
 constexpr uint32_t kDevTimeout = 1u;  // a bounded wait ran out
 constexpr uint32_t kDevBounds = 2u;   // a length or position was clamped
+constexpr uint32_t kDevNoPages = 4u;  // too few free pages
 
 struct DecodePlan {
   // problem

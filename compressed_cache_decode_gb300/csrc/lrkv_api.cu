@@ -53,6 +53,7 @@ const char* lrkv_status_string(lrkv_status s) {
     case LRKV_ERR_CUDA: return "LRKV_ERR_CUDA";
     case LRKV_ERR_TIMEOUT: return "LRKV_ERR_TIMEOUT";
     case LRKV_ERR_DEVICE_BOUNDS: return "LRKV_ERR_DEVICE_BOUNDS";
+    case LRKV_ERR_NO_PAGES: return "LRKV_ERR_NO_PAGES";
   }
   return "LRKV_ERR_UNKNOWN";
 }
@@ -347,6 +348,7 @@ lrkv_status lrkv_read_device_status(const void* ws, lrkv_stream_t stream, lrkv_s
   if (cudaMemcpyAsync(&word, ws, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess) return LRKV_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return LRKV_ERR_CUDA;
   *out_status = (word & lrkv::kDevTimeout) ? LRKV_ERR_TIMEOUT
+                : (word & lrkv::kDevNoPages) ? LRKV_ERR_NO_PAGES
                 : (word & lrkv::kDevBounds) ? LRKV_ERR_DEVICE_BOUNDS
                                                : LRKV_OK;
   return LRKV_OK;

@@ -31,6 +31,12 @@ bool make_tmap_4d_bf16_swizzled(CUtensorMap* map, const void* base, const uint64
 bool make_tmap_5d_bf16_swizzled(CUtensorMap* map, const void* base, const uint64_t dims[5],
                                 const uint64_t strides_bytes[4], const uint32_t box[5]);
 
+// Encode a 3-D tiled tensor map for a row-major [d2][d1][d0] tensor of bytes
+// (d0 a multiple of 16) with box {b0, b1, 1}, b0 <= 128, and the 128-byte
+// swizzle; box elements outside the extents are filled with zeros.
+bool make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
+                     uint32_t b1);
+
 // Encode a 2-D tiled tensor map for a row-major [d1][d0] fp32 tensor with box
 // {b0, b1} (b0 may exceed d0: the excess is filled with zeros) and no swizzle.
 bool make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint32_t b0, uint32_t b1);

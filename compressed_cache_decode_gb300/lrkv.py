@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -23,6 +23,7 @@ LRKV_ERR_WORKSPACE = 3
 LRKV_ERR_CUDA = 4
 LRKV_ERR_TIMEOUT = 5
 LRKV_ERR_DEVICE_BOUNDS = 6
+LRKV_ERR_NO_PAGES = 7
 
 LRKV_F32 = 0
 LRKV_BF16 = 1
@@ -60,6 +61,13 @@ EXPORTED = (
     "lrkv_rope_rotate",
     "lrkv_decode_rope_axes_workspace_size",
     "lrkv_decode_rope_axes",
+    "lrkv_quantize",
+    "lrkv_decode8_workspace_size",
+    "lrkv_decode8",
+    "lrkv_pages_workspace_size",
+    "lrkv_pages_fork",
+    "lrkv_pages_extend",
+    "lrkv_pages_compact",
     "lrkv_dense_decode_workspace_size",
     "lrkv_dense_decode",
     "lrkv_mla_decode_workspace_size",
@@ -88,6 +96,15 @@ class lrkv_dense_dims(ctypes.Structure):
 class lrkv_mla_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("latent_dim", ctypes.c_int), ("max_len", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class lrkv_cache8(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("k_s", "v_s", "z_k", "z_v", "k_s_scale", "v_s_scale",
+                                                     "z_k_scale", "z_v_scale")]
+
+
+class lrkv_pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int), ("bytes", ctypes.c_int)]
 
 
 class LRKVError(RuntimeError):
@@ -187,6 +204,22 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lrkv_decode_rope_axes.restype = ctypes.c_int
     lib.lrkv_decode_rope_axes.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, ci, i32p, ci, ip, i32p, cf, vp,
                                           vp, vp, vp, vp, sz, vp]
+    c8p, plp = ctypes.POINTER(lrkv_cache8), ctypes.POINTER(lrkv_pool)
+    lib.lrkv_quantize.restype = ctypes.c_int
+    lib.lrkv_quantize.argtypes = [dims_p, ci, vp, vp, vp, vp, i32p, i32p, ci, ci, i32p, c8p, vp, sz, vp]
+    lib.lrkv_decode8_workspace_size.restype = ctypes.c_int
+    lib.lrkv_decode8_workspace_size.argtypes = [dims_p, szp]
+    lib.lrkv_decode8.restype = ctypes.c_int
+    lib.lrkv_decode8.argtypes = [dims_p, vp, ci, ci, i32p, c8p, vp, vp, i32p, vp, vp, vp, sz, vp]
+    lib.lrkv_pages_workspace_size.restype = ctypes.c_int
+    lib.lrkv_pages_workspace_size.argtypes = [ci, ci, ci, szp]
+    lib.lrkv_pages_fork.restype = ctypes.c_int
+    lib.lrkv_pages_fork.argtypes = [ci, ci, ci, ci, i32p, i32p, i32p, i32p, i32p, i32p, i32p, i32p, vp, sz, vp]
+    lib.lrkv_pages_extend.restype = ctypes.c_int
+    lib.lrkv_pages_extend.argtypes = [ci, ci, ci, ci, i32p, i32p, i32p, i32p, i32p, i32p, i32p, i32p, plp, ci, vp,
+                                      sz, vp]
+    lib.lrkv_pages_compact.restype = ctypes.c_int
+    lib.lrkv_pages_compact.argtypes = [ci, ci, ci, ci, i32p, i32p, i32p, i32p, i32p, i32p, i32p, plp, ci, vp, sz, vp]
     ddp, mdp = ctypes.POINTER(lrkv_dense_dims), ctypes.POINTER(lrkv_mla_dims)
     lib.lrkv_dense_decode_workspace_size.restype = ctypes.c_int
     lib.lrkv_dense_decode_workspace_size.argtypes = [ddp, ctypes.POINTER(sz)]
@@ -941,6 +974,213 @@ def decode_rope_axes(q_rot, k_s, v_s, z_k, z_v, b_k, b_v, cos_sin, positions, se
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_decode_rope_axes")
     return out, lse, weights_out, ws
+
+
+# ------------------------------------------------ the cache in 8 bits --
+
+BLOCK8 = 16  # rows that share a scale
+_E4M3 = torch.float8_e4m3fn
+
+
+class Cache8(NamedTuple):
+    """A factored cache in 8 bits: k_s, v_s [lead, rows, d_h] and z_k, z_v [lead,
+    rows, H, r] (float8_e4m3fn) with the scales of their blocks of BLOCK8 rows,
+    [lead, ceil(rows / BLOCK8)] and [lead, ceil(rows / BLOCK8), H] fp32; lead x
+    rows is batch x max_len, or pages x page_size of a paged cache.  Rank 0: the
+    z tensors are None."""
+    k_s: torch.Tensor
+    v_s: torch.Tensor
+    z_k: Optional[torch.Tensor]
+    z_v: Optional[torch.Tensor]
+    k_s_scale: torch.Tensor
+    v_s_scale: torch.Tensor
+    z_k_scale: Optional[torch.Tensor]
+    z_v_scale: Optional[torch.Tensor]
+
+    def pools(self):
+        """The tensors, for the pages_* calls (of a paged cache)."""
+        return [t for t in self if t is not None]
+
+
+def empty_cache8(lead: int, rows: int, heads: int, head_dim: int, rank: int, device="cuda") -> Cache8:
+    """An 8-bit cache whose rows hold nothing yet."""
+    blocks = -(-rows // BLOCK8)
+
+    def some(*shape, dtype=_E4M3):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    z, zs = ((lead, rows, heads, rank), (lead, blocks, heads)) if rank else (None, None)
+    return Cache8(some(lead, rows, head_dim), some(lead, rows, head_dim), some(*z) if z else None,
+                  some(*z) if z else None, some(lead, blocks, dtype=_F32), some(lead, blocks, dtype=_F32),
+                  some(*zs, dtype=_F32) if z else None, some(*zs, dtype=_F32) if z else None)
+
+
+def _cache8_specs(cache: Cache8, lead: Tuple[int, int], H: int, dh: int, r: int):
+    """The shape checks of a cache's tensors, and whether its z tensors agree with r."""
+    blocks = (lead[0], -(-lead[1] // BLOCK8))
+    z = lead + (H, r)
+    if (cache.z_k is None) != (r == 0) or any((t is None) != (r == 0)
+                                              for t in (cache.z_v, cache.z_k_scale, cache.z_v_scale)):
+        raise ValueError("the z tensors of an 8-bit cache are given together, and only for a rank above 0")
+    return (("cache.k_s", cache.k_s, _E4M3, lead + (dh,)), ("cache.v_s", cache.v_s, _E4M3, lead + (dh,)),
+            ("cache.z_k", cache.z_k, _E4M3, z), ("cache.z_v", cache.z_v, _E4M3, z),
+            ("cache.k_s_scale", cache.k_s_scale, _F32, blocks), ("cache.v_s_scale", cache.v_s_scale, _F32, blocks),
+            ("cache.z_k_scale", cache.z_k_scale, _F32, blocks + (H,)),
+            ("cache.z_v_scale", cache.z_v_scale, _F32, blocks + (H,)))
+
+
+def _cache8_ref(cache: Cache8):
+    return ctypes.byref(lrkv_cache8(*[_ptr(t) for t in cache]))
+
+
+def quantize(k_s, v_s, z_k, z_v, start_pos, cache: Cache8, new_lens=None, block_table=None, ws=None, stream=None):
+    """Stores rows k_s, v_s [B, n, d_h], z_k, z_v [B, n, H, r] (bf16 or fp32; as
+    append() writes them into a cache of n rows) in an 8-bit cache at rows
+    start_pos[b] + t; new_lens [B] int32: only so many of the n rows.  A status
+    word is kept only in a `ws` of 16 zeroed bytes."""
+    B, n, dh = k_s.shape
+    H, r = (z_k.shape[2], z_k.shape[3]) if z_k is not None else (1, 0)
+    max_len, page_size, num_pages, lead = _cache_rows(cache.k_s, block_table, B)
+    dims = make_dims(B, H, dh, r, max_len, k_s.dtype)
+    dt, dev = k_s.dtype, k_s.get_device()
+    _check(dev, ("k_s", k_s, dt, (B, n, dh)), ("v_s", v_s, dt, (B, n, dh)), ("z_k", z_k, dt, (B, n, H, r)),
+           ("z_v", z_v, dt, (B, n, H, r)), ("start_pos", start_pos, _I32, (B,)), ("new_lens", new_lens, _I32, (B,)),
+           ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
+           ("ws", ws, _U8, ws.shape if ws is not None else None), *_cache8_specs(cache, lead, H, dh, r))
+    with _On(k_s):
+        st = int(load().lrkv_quantize(
+            ctypes.byref(dims), n, _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(start_pos), _ptr(new_lens),
+            page_size, num_pages, _ptr(block_table), _cache8_ref(cache), _ptr(ws), 0 if ws is None else ws.numel(),
+            _stream_on(stream, dev)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_quantize")
+
+
+def decode8_workspace(dims: lrkv_dims, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_decode8_workspace_size", ctypes.byref(dims)), dtype=torch.uint8, device=device)
+
+
+def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float = 0.0, out=None, lse=None, ws=None,
+            stream=None):
+    """decode over an 8-bit cache (paged with block_table).  Returns (out, lse, ws)."""
+    B, H, dh = q.shape
+    r = cache.z_k.shape[-1] if cache.z_k is not None else 0
+    max_len, page_size, num_pages, lead = _cache_rows(cache.k_s, block_table, B)
+    dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
+    dt, dev, basis = q.dtype, q.get_device(), (H, dh, r)
+    _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k, dt, basis), ("b_v", b_v, dt, basis),
+           ("seq_lens", seq_lens, _I32, (B,)), ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
+           ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)), *_cache8_specs(cache, lead, H, dh, r))
+    with _On(q, stream) as on:
+        if out is None:
+            out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
+        if lse is None:
+            lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = on.own(decode8_workspace(dims, q.device))
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
+        st = int(load().lrkv_decode8(
+            ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), _cache8_ref(cache),
+            _ptr(b_k) if r else None, _ptr(b_v) if r else None, _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws),
+            ws.numel(), _stream_on(stream, dev)))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_decode8")
+    return out, lse, ws
+
+
+# ---------------------------------------------------- pages of a cache --
+
+def pages_workspace(batch: int, max_blocks: int, num_pages: int, device="cuda") -> torch.Tensor:
+    return torch.empty(_size_of("lrkv_pages_workspace_size", int(batch), int(max_blocks), int(num_pages)),
+                       dtype=torch.uint8, device=device)
+
+
+def _pools(pools, page_size: int, num_pages: int, device: int):
+    """The C array of pools [num_pages, pieces, ...]: a piece for every page_size / pieces rows."""
+    got = (lrkv_pool * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        if t.dim() < 2 or t.shape[0] != num_pages or t.shape[1] < 1 or page_size % t.shape[1]:
+            raise ValueError(f"pool {i} must have {num_pages} pages and a piece for every so many of a page's "
+                             f"{page_size} rows, not shape {tuple(t.shape)}")
+        if not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"pool {i} must be contiguous, on the call's device")
+        got[i] = lrkv_pool(t.data_ptr(), page_size // t.shape[1], t.stride(1) * t.element_size())
+    return got
+
+
+def _pages_call(name: str, block_table, seq_lens, refs, page_size: int, outs, more, ws, stream, call):
+    """Checks, workspace and status of a pages_* call; call(dims, on) makes it."""
+    B, blocks = block_table.shape
+    pages, dev = refs.shape[0], block_table.get_device()
+    _check(dev, ("block_table", block_table, _I32, (B, blocks)), ("seq_lens", seq_lens, _I32, (B,)),
+           ("refs", refs, _I32, (pages,)), ("table_out", outs[0], _I32, (B, blocks)),
+           ("lens_out", outs[1], _I32, (B,)), ("refs_out", outs[2], _I32, (pages,)),
+           *[(n, t, _I32, (s,)) for n, t, s in more])
+    with _On(block_table, stream) as on:
+        if ws is None:
+            ws = on.own(pages_workspace(B, blocks, pages, block_table.device))
+        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
+        st = int(call(B, blocks, int(page_size), pages, ws, _stream_on(stream, dev)))
+    if st != LRKV_OK:
+        raise LRKVError(st, name)
+    return ws
+
+
+def pages_fork(block_table, seq_lens, refs, page_size: int, parent=None, keep=None, table_out=None, lens_out=None,
+               refs_out=None, ws=None, stream=None):
+    """Sequence b becomes the first keep[b] rows of sequence parent[b] (None:
+    all; itself), on the same pages: forks, reorders, cuts back (keep below its
+    length), frees (keep 0 or parent -1).  Updates block_table [B, max_blocks],
+    seq_lens [B] and refs [num_pages] (int32) in place unless given outputs.
+    Returns (table_out, lens_out, refs_out, ws)."""
+    B = block_table.shape[0]
+    outs = (block_table if table_out is None else table_out, seq_lens if lens_out is None else lens_out,
+            refs if refs_out is None else refs_out)
+    ws = _pages_call(
+        "lrkv_pages_fork", block_table, seq_lens, refs, page_size, outs,
+        (("parent", parent, B), ("keep", keep, B)), ws, stream,
+        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_fork(
+            b, blocks, size, pages, _ptr(parent), _ptr(keep), _ptr(block_table), _ptr(seq_lens), _ptr(refs),
+            *map(_ptr, outs), _ptr(ws), ws.numel(), s))
+    return (*outs, ws)
+
+
+def pages_extend(pools, block_table, seq_lens, refs, page_size: int, new_lens, table_out=None, lens_out=None,
+                 refs_out=None, missing=None, ws=None, stream=None):
+    """Room for rows [seq_lens[b], new_lens[b]) of every sequence: free pages, and
+    copies of begun pages that others use too, in all `pools` (tensors
+    [num_pages, pieces, ...]).  All or nothing: missing [1] int32 receives the
+    number of pages that lack.  Updates block_table, seq_lens and refs in place
+    unless given outputs.  Returns (table_out, lens_out, refs_out, ws)."""
+    B, dev = block_table.shape[0], block_table.get_device()
+    outs = (block_table if table_out is None else table_out, seq_lens if lens_out is None else lens_out,
+            refs if refs_out is None else refs_out)
+    array = _pools(pools, int(page_size), refs.shape[0], dev)
+    ws = _pages_call(
+        "lrkv_pages_extend", block_table, seq_lens, refs, page_size, outs,
+        (("new_lens", new_lens, B), ("missing", missing, 1)), ws, stream,
+        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_extend(
+            b, blocks, size, pages, _ptr(new_lens), _ptr(block_table), _ptr(seq_lens), _ptr(refs), *map(_ptr, outs),
+            _ptr(missing), array, len(pools), _ptr(ws), ws.numel(), s))
+    return (*outs, ws)
+
+
+def pages_compact(pools, block_table, seq_lens, refs, page_size: int, table_out=None, refs_out=None, moved=None,
+                  live=None, ws=None, stream=None):
+    """Moves the pages in use (refs > 0) to the front of all `pools`.  Updates
+    block_table and refs in place unless given outputs; moved [num_pages] int32
+    receives every page's new number, -1 for free ones, live [1] int32 how many
+    are in use.  Returns (table_out, refs_out, ws)."""
+    dev = block_table.get_device()
+    outs = (block_table if table_out is None else table_out, None, refs if refs_out is None else refs_out)
+    array = _pools(pools, int(page_size), refs.shape[0], dev)
+    ws = _pages_call(
+        "lrkv_pages_compact", block_table, seq_lens, refs, page_size, outs,
+        (("moved", moved, refs.shape[0]), ("live", live, 1)), ws, stream,
+        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_compact(
+            b, blocks, size, pages, _ptr(block_table), _ptr(seq_lens), _ptr(refs), _ptr(outs[0]), _ptr(outs[2]),
+            _ptr(moved), _ptr(live), array, len(pools), _ptr(ws), ws.numel(), s))
+    return outs[0], outs[2], ws
 
 
 # ------------------------------------------------- comparison decodes --

@@ -88,7 +88,8 @@ typedef enum {
   LRKV_ERR_WORKSPACE = 3,     /* workspace missing or smaller than required          */
   LRKV_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed         */
   LRKV_ERR_TIMEOUT = 5,       /* device: a bounded wait ran out (reported, not trapped) */
-  LRKV_ERR_DEVICE_BOUNDS = 6  /* device: a length, position or page out of range; clamped or skipped */
+  LRKV_ERR_DEVICE_BOUNDS = 6, /* device: a length, position or page out of range; clamped or skipped */
+  LRKV_ERR_NO_PAGES = 7       /* device: fewer free pages than lrkv_pages_extend needs; nothing done */
 } lrkv_status;
 
 typedef enum { LRKV_F32 = 0, LRKV_BF16 = 1 } lrkv_dtype;
@@ -592,6 +593,152 @@ lrkv_status lrkv_decode_rope_axes(const lrkv_dims* dims, const void* q_rot, cons
                                   lrkv_stream_t stream);
 
 /*
+ * The factored cache in 8 bits.  Every element of k_s, v_s, z_k, z_v is an
+ * e4m3 number (sign, 4 bits of exponent, 3 of mantissa, largest 448, no
+ * infinity; one byte) times the scale of its block: LRKV_BLOCK8 consecutive
+ * rows of a sequence share one fp32 scale per tensor and head (the shared rows
+ * count as one head),
+ *   value = scale[block][head] * e4m3,
+ * so a token costs half of what it costs in bf16, and 8 (1 + heads) / 16 bytes
+ * of scales.  The pages have no counterpart.  Layouts, contiguous (rows =
+ * max_len, lead = batch) or pools of pages (rows = page_size, lead =
+ * num_pages; block_table as in lrkv_decode_paged), with
+ * blocks = ceil(rows / LRKV_BLOCK8):
+ *   k_s, v_s              [lead][rows][head_dim]     e4m3
+ *   z_k, z_v              [lead][rows][heads][rank]  e4m3 (NULL when rank == 0)
+ *   k_s_scale, v_s_scale  [lead][blocks]             fp32
+ *   z_k_scale, z_v_scale  [lead][blocks][heads]      fp32 (NULL when rank == 0)
+ * The eight pointers are 16-byte aligned.
+ */
+#define LRKV_BLOCK8 16
+
+typedef struct {
+  void *k_s, *v_s, *z_k, *z_v;
+  float *k_s_scale, *v_s_scale, *z_k_scale, *z_v_scale;
+} lrkv_cache8;
+
+/*
+ * lrkv_quantize stores n_new rows of every sequence in an 8-bit cache, at rows
+ * start_pos[b] + t: the rows of a prompt, or the one of a decode step.
+ *   k_s, v_s [batch][n_new][head_dim], z_k, z_v [batch][n_new][heads][rank]
+ *            dtype rows, as lrkv_append writes them into a cache of n_new rows
+ *   start_pos [batch] int32; new_lens [batch] int32 or NULL: sequence b brings
+ *            new_lens[b] <= n_new rows only (a padded batch; NULL: n_new each)
+ * For each block of rows, tensor and head that gets rows: with `need` the
+ * smallest power of two, 2^-126 at least, for which the largest finite
+ * magnitude of the new rows is at most 448 need,
+ *   scale = max(need, the block's scale if rows before start_pos[b] lie in it)
+ * (a power of two keeps what a larger scale leaves of a number's bits, and no
+ * finer scale makes an e4m3 number more exact).  New elements are x / scale
+ * rounded to nearest even; magnitudes past 448 scale (infinities) become 448
+ * scale and NaN stays NaN.  Where the scale has grown the earlier rows of the
+ * block are rounded to it anew; a power of two only takes bits off numbers
+ * that become small.  Rows at or past start_pos[b] + n are left as they were,
+ * and so are blocks without a new row.  Only the block of start_pos[b] is read.
+ * start_pos[b] + t outside [0, max_len), new_lens[b] outside [0, n_new] or a
+ * page outside the pool: those rows are skipped, LRKV_ERR_DEVICE_BOUNDS.  Blocks
+ * that are written must belong to one sequence only.  ws: NULL, or 16 bytes
+ * whose status word the call ORs its bits into (the caller clears it).
+ * dims->dtype (BF16 or F32) is that of the rows.  Supported: head_dim a
+ * multiple of 16 up to 256, rank even up to 64, heads rank a multiple of 16,
+ * heads <= 256; page_size a power of two >= 16; block_table NULL: contiguous.
+ *
+ * lrkv_decode8 is lrkv_decode over an 8-bit cache (block_table NULL:
+ * contiguous).  The cache's numbers enter the products as they are; q, q B^K
+ * and the probabilities are split so that no product loses fp32 accuracy, and
+ * out is held to it.  Scales: any finite positive numbers.  Rows at or past
+ * seq_lens[b] and the scales of blocks past them may hold anything; a NaN in a
+ * visible row may make any output of its sequence NaN.  Supported: dtype BF16
+ * (of q and the bases), and the shapes of lrkv_quantize.  Workspace:
+ * lrkv_decode8_workspace_size() bytes; errors as in lrkv_decode_paged.
+ */
+lrkv_status lrkv_quantize(const lrkv_dims* dims, int n_new, const void* k_s, const void* v_s, const void* z_k,
+                          const void* z_v, const int32_t* start_pos, const int32_t* new_lens, int page_size,
+                          int num_pages, const int32_t* block_table, const lrkv_cache8* cache, void* ws,
+                          size_t ws_bytes, lrkv_stream_t stream);
+lrkv_status lrkv_decode8_workspace_size(const lrkv_dims* dims, size_t* bytes);
+lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
+                         const int32_t* block_table, const lrkv_cache8* cache, const void* b_k, const void* b_v,
+                         const int32_t* seq_lens, float* out, float* lse, void* ws, size_t ws_bytes,
+                         lrkv_stream_t stream);
+
+/*
+ * The pages of a paged cache, managed on the device: which page holds which
+ * rows is decided by kernels on the call's stream, from arrays in device
+ * memory, so that a serving step of forks, appends and decodes can be captured
+ * whole.  The pages have no counterpart of it.
+ *
+ *   block_table [batch][max_blocks], seq_lens [batch] int32: as in
+ *       lrkv_decode_paged.  Entry j of sequence b is in use when
+ *       j < ceil(seq_lens[b] / page_size).
+ *   refs [num_pages] int32: how many entries in use name the page, and whatever
+ *       the caller adds to hold a page that no sequence names (a prompt kept
+ *       for later).  A page is free when refs is 0 (or less).
+ * Each call reads these and writes table_out, lens_out, refs_out, which may be
+ * the same arrays (else they do not overlap).  All numbering is fixed: the lowest free pages, in the
+ * order of the sequences.  page_size: a power of two >= 16.  Lengths outside
+ * [0, max_blocks page_size] are clamped; these, and an entry in use that names no
+ * page of the pool, set LRKV_ERR_DEVICE_BOUNDS (such an entry stays as it is).
+ * ws: lrkv_pages_workspace_size() bytes, its status word set afresh.
+ * num_pages and batch * max_blocks at most 2^30, batch <= 4096.
+ *
+ * lrkv_pages_fork: sequence b becomes the first keep[b] rows of sequence
+ * parent[b] as it was before the call, on the same pages: beams that go on
+ * from other beams, samples of one prompt; keep[b] below its own length cuts
+ * b back (after lrkv_evict: keep = new_lens), 0 frees it.  parent NULL: each
+ * its own; -1: empty.  keep NULL: all rows; keep[b] past the parent's length
+ * means all.  refs gains the entries in use after the call and loses those
+ * before.  Entries not in use become -1.  Other values of parent, or a
+ * negative keep, empty the sequence (LRKV_ERR_DEVICE_BOUNDS).
+ *
+ * lrkv_pages_extend: room for the rows [seq_lens[b], new_lens[b]) of every
+ * sequence (new_lens[b] <= seq_lens[b]: none), before they are appended.
+ * Blocks without a page take free ones.  A page that the new rows begin inside
+ * of and that others use too (refs > 1) is copied first: the rows before
+ * seq_lens[b] of every pool go to a free page, and b leaves the shared one; of
+ * sequences that would be its only users and all write, the last one keeps it.
+ * Pages are taken in the order of the sequences, the copy's page first.  All or
+ * nothing: when the free pages do not suffice, tables, lengths, refs and
+ * pools stay as they were and *missing is the number of pages that lack
+ * (LRKV_ERR_NO_PAGES in the status word), else 0.  lens_out = new_lens, refs 1
+ * for each page taken.
+ *
+ * lrkv_pages_compact: the n pages in use (refs > 0) move to pages [0, n): the
+ * k-th used page at or past n goes whole into the k-th free page below it, in
+ * every pool; the tables' entries in use follow.  moved [num_pages] or NULL:
+ * the new number of every page, -1 for free ones (for pages held outside the
+ * tables).  *live = n.  refs_out moves with the pages.
+ *
+ * Pools: the arrays that the pages consist of, host array of n_pools (0 .. 16)
+ * entries: page p of a pool is page_size / rows pieces of `bytes` bytes from
+ * data + p * (page_size / rows) * bytes on, one piece for every `rows` rows (1: a row of a
+ * cache tensor; LRKV_BLOCK8: the scales of a block of an 8-bit cache).  data and
+ * bytes are multiples of 4; rows divides page_size; all pools have num_pages
+ * pages.  Pools do not overlap.
+ */
+typedef struct {
+  void* data;
+  int rows;
+  int bytes;
+} lrkv_pool;
+
+#define LRKV_MAX_POOLS 16
+
+lrkv_status lrkv_pages_workspace_size(int batch, int max_blocks, int num_pages, size_t* bytes);
+lrkv_status lrkv_pages_fork(int batch, int max_blocks, int page_size, int num_pages, const int32_t* parent,
+                            const int32_t* keep, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* refs, int32_t* table_out, int32_t* lens_out, int32_t* refs_out, void* ws,
+                            size_t ws_bytes, lrkv_stream_t stream);
+lrkv_status lrkv_pages_extend(int batch, int max_blocks, int page_size, int num_pages, const int32_t* new_lens,
+                              const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs,
+                              int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* missing,
+                              const lrkv_pool* pools, int n_pools, void* ws, size_t ws_bytes, lrkv_stream_t stream);
+lrkv_status lrkv_pages_compact(int batch, int max_blocks, int page_size, int num_pages, const int32_t* block_table,
+                               const int32_t* seq_lens, const int32_t* refs, int32_t* table_out, int32_t* refs_out,
+                               int32_t* moved, int32_t* live, const lrkv_pool* pools, int n_pools, void* ws,
+                               size_t ws_bytes, lrkv_stream_t stream);
+
+/*
  * Comparison decodes on the same box ("Low-Rank Key Value Attention | What a
  * shared cache can preserve", §4 "Weight count and the two decode regimes"
  * and §5: a fair serving comparison runs optimized GQA, dense MHA and
@@ -653,7 +800,8 @@ lrkv_status lrkv_mla_decode(const lrkv_mla_dims* dims, const void* q, const void
 
 /*
  * Read the device status word that the kernels of the last call(s) using
- * `ws` recorded (LRKV_OK, LRKV_ERR_TIMEOUT or LRKV_ERR_DEVICE_BOUNDS).
+ * `ws` recorded (LRKV_OK, LRKV_ERR_TIMEOUT, LRKV_ERR_NO_PAGES or
+ * LRKV_ERR_DEVICE_BOUNDS).
  * Synchronises `stream`.  Each lrkv_decode/lrkv_prefill call sets the word
  * afresh: a decode writes the bits its kernels recorded (no clearing needed
  * before a call), a prefill clears it when it starts.
