@@ -23,9 +23,9 @@
 // diagonal operand (zero columns for the other heads).  The shared rows are read
 // by every group; all but the first find them in L2.
 //
-// Grid (range CTAs, groups).  15 warps: 0-7 the softmax (a thread per row, four
+// Grid (range CTAs, groups).  16 warps: 0-7 the softmax (a thread per row, four
 // heads each), 8-11 the value sums (a thread per column), 12 the copies, 13
-// the MMAs, 14 the operands of each sequence, which
+// the score MMAs, 14 the value MMAs, 15 the operands of each sequence, which
 // lrkv_decode8_operands_kernel has laid out before.  The keys of tile i + 1 are
 // multiplied while the softmax works on tile i.
 #include <cuda.h>
@@ -50,26 +50,31 @@ using namespace dec;
 
 namespace {
 
-constexpr int k8Rows = 128;        // rows of a tile
-constexpr int k8Unit = 32;         // rows of a unit: the split's step, one K step of the value products
-constexpr int k8Units = k8Rows / k8Unit;
+constexpr int k8Rows = 128;        // rows of a tile, the step of the split
+constexpr int k8Step = 32;         // rows of a K step of the value products
 constexpr int k8Heads = 8;         // heads of a CTA
 constexpr int k8QParts = 4, k8Parts = 6;
 constexpr int k8NQ = k8Heads * k8QParts, k8N = k8Heads * k8Parts;  // columns of the operands
 constexpr int k8Box = 16384;       // 128 rows x 128 columns
 constexpr int k8MaxSlots = 14;
 constexpr int k8Softmax = 8, k8Values = 4;
-constexpr int k8Threads = 32 * (k8Softmax + k8Values + 3);
+constexpr int k8Threads = 32 * (k8Softmax + k8Values + 4);
 constexpr int k8MaxD = 2, k8MaxZ = 4;  // 128-column chunks of a shared row, of a group's latents
 // TMEM columns: two score buffers, then the value products
 constexpr uint32_t k8S = 0, k8SWidth = k8NQ + k8N, k8Os = 2 * k8SWidth, k8Oz = k8Os + k8MaxD * k8N, k8Cols = 512;
 static_assert(k8Oz + k8MaxZ * k8N <= k8Cols, "more TMEM than there is");
 
+// Maps of the cache's tensors: k_s, v_s, z_k, z_v with boxes of Args8::box rows, then of tail_box rows.
+struct Maps8 {
+  CUtensorMap map[8];
+};
+
 struct Args8 {
   int groups, nd, nz;   // head groups; chunks of a shared row and of a group's latents
   int img_bytes;        // operands of a (sequence, group): q parts | p parts | 16 factors
   int img_pad;          // the same in shared memory, on a 1 KB boundary
-  int slots, box_rows;  // ring depth; rows of a copy (32, or 16 where a page holds no more)
+  int slots;            // ring depth
+  int box, tail_box;    // rows of a copy: of a full tile (128, or a page's), of a sequence's last one (32, or a page's)
   int off_img, off_p, off_ring;
   int blocks;           // scale blocks of a sequence (contiguous) or page
   unsigned char* images;
@@ -141,6 +146,30 @@ __device__ __forceinline__ bool wait8(uint64_t* bar, uint32_t parity, volatile i
 __device__ __forceinline__ bool wait8_warp(uint64_t* bar, uint32_t parity, volatile int* fail, long long limit) {
   const bool ok = wait8(bar, parity, fail, limit);
   return __all_sync(0xffffffffu, ok);
+}
+// A place in the ring: a slot, and the phase of its barriers.
+struct Place8 {
+  int slot = 0;
+  uint32_t phase = 0u;
+  __device__ __forceinline__ void move(int n, int slots) {  // n <= slots
+    slot += n;
+    if (slot >= slots) {
+      slot -= slots;
+      phase ^= 1u;
+    }
+  }
+};
+// `steps` (1 .. 4) MMAs of K = 32 along a box and an operand.
+__device__ __forceinline__ void mma8_box(uint32_t d, uint64_t a, int a_step, uint64_t b, uint32_t idesc, int steps,
+                                         bool fresh) {
+  mma8(d, a, b, idesc, fresh ? 0u : 1u);
+  if (steps == 4) {
+    mma8(d, a + a_step, b + 2, idesc, 1u);
+    mma8(d, a + 2 * a_step, b + 4, idesc, 1u);
+    mma8(d, a + 3 * a_step, b + 6, idesc, 1u);
+  } else {
+    for (int k = 1; k < steps; ++k) mma8(d, a + k * a_step, b + 2 * k, idesc, 1u);
+  }
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
@@ -234,18 +263,17 @@ __global__ void __launch_bounds__(128) lrkv_decode8_operands_kernel(const __grid
 
 // ================================================================== the scan
 __global__ void __launch_bounds__(k8Threads, 1)
-    lrkv_decode8_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_zk,
-                        const __grid_constant__ CUtensorMap tm_zv, const __grid_constant__ Args8 A) {
+    lrkv_decode8_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ Maps8 M,
+                        const __grid_constant__ Args8 A) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   // full/empty: ring slots; ifull/iempty: operands; sfull/sempty: scores; pfull: probabilities; pv: their
-  // products done (and the probabilities' buffer free); oempty: products read; mdone: every MMA done
-  __shared__ uint64_t full[k8MaxSlots], empty[k8MaxSlots], ifull[2], iempty[2], sfull[2], sempty[2], pfull, pv, oempty,
-      mdone;
+  // products done (and the probabilities' buffer free); oempty: a chunk's products read; mdone: every MMA done
+  __shared__ uint64_t full[k8MaxSlots], empty[k8MaxSlots], ifull[2], iempty[2], sfull[2], sempty[2], pfull[2], pv[2],
+      oempty[k8MaxD + k8MaxZ], mdone;
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad, s_copies, s_images;
   __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
-  __shared__ float s_fac[2][20];                      // [tile parity]: alpha[8], latent scale[8], shared scale
+  __shared__ float s_fac[4][20];                      // [tile % 4]: alpha[8], latent scale[8], shared scale
   __shared__ float s_sum[2][4][4];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   volatile int* fail = &s_fail;
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
   const int nd = A.nd, nz = (heads * r + 127) / 128;
   int* pre = reinterpret_cast<int*>(smem);
 
-  // ---- barriers, TMEM, sequence starts in units of 32 rows -----------------------------
+  // ---- barriers, TMEM, sequence starts in tiles -----------------------------
   if (tid == 0) {
     for (int i = 0; i < k8MaxSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
@@ -265,11 +293,11 @@ __global__ void __launch_bounds__(k8Threads, 1)
       mbar_init(&iempty[i], 1 + k8Softmax);
       mbar_init(&sfull[i], 1);
       mbar_init(&sempty[i], k8Softmax);
+      mbar_init(&pfull[i], k8Softmax);
+      mbar_init(&pv[i], 1);
     }
-    mbar_init(&pfull, k8Softmax);
-    mbar_init(&pv, 1);
-    mbar_init(&oempty, k8Values);
-    mbar_init(&mdone, 1);
+    for (int i = 0; i < k8MaxD + k8MaxZ; ++i) mbar_init(&oempty[i], k8Values);
+    mbar_init(&mdone, 2);
     s_fail = s_bad = s_copies = s_images = 0;
     fence_barrier_init();
   }
@@ -281,7 +309,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
       bad = 1;
       L = min(max(L, 0), P.max_len);
     }
-    pre[b + 1] = (L + k8Unit - 1) / k8Unit;
+    pre[b + 1] = L / k8Rows + (L % k8Rows != 0);
   }
   if (tid == 0) pre[0] = 0;
   bad = __syncthreads_or(bad);
@@ -318,19 +346,17 @@ __global__ void __launch_bounds__(k8Threads, 1)
     // ---- softmax: row 32 quad + lane of a tile, heads 4 half .. + 3 of the group ----------
     const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, hb = h0 + 4 * half;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    unsigned char* ps = smem + A.off_p + half * (4 * k8Parts * 128);
-    unsigned char* pz = ps + k8N * 128;
     const bool vec = H % 4 == 0;
     float m[4], l[4], fq[4], fz[4];
     int cur_b = -1, L = 0, i = 0, piece = -1;
     // scales of this thread's row: shared key and value, latents' keys and values
     float nks = 0.f, nvs = 0.f, nkz[4], nvz[4];
     auto load_scales = [&](const TileWalk& t) {
-      const int row_b = k8Unit * t.t0 + row;
+      const int row_b = k8Rows * t.t0 + row;
       nks = nvs = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) nkz[k] = nvz[k] = 0.f;
-      if (row_b >= min(rows_of(t.b), k8Unit * t.t_end)) return;
+      if (row_b >= rows_of(t.b)) return;
       size_t blk = static_cast<size_t>(t.b) * A.blocks + row_b / kBlock8;
       if (P.block_table) {
         const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (row_b >> P.page_shift));
@@ -360,7 +386,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     pdl_wait();  // the launch before may still read the workspace
     for (; more; ++i) {
       TileWalk nx = w;
-      const bool nmore = walk_next(nx, pre, B, g1, k8Units);
+      const bool nmore = walk_next(nx, pre, B, g1, 1);
       const bool last = !nmore || nx.b != w.b;
       if (w.b != cur_b) {
         cur_b = w.b;
@@ -378,8 +404,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&iempty[piece & 1]);
       }
-      const int units = min(k8Units, w.t_end - w.t0);
-      const int rows = min(k8Unit * units, L - k8Unit * w.t0);
+      const int rows = min(k8Rows, L - k8Rows * w.t0), padded = round_up(rows, k8Step);
       float ks = nks, vs = nvs, kz[4], vz[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) { kz[k] = nkz[k]; vz[k] = nvz[k]; }
@@ -441,9 +466,11 @@ __global__ void __launch_bounds__(k8Threads, 1)
         if (row >= rows) xs[k] = xz[k] = 0.f;
       }
       // into the operand of the value products, once the ones before are done with it
-      if (i > 0) wait8_warp(&pv, static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit);
+      if (i > 1) wait8_warp(&pv[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit);
+      unsigned char* ps = smem + A.off_p + (i & 1) * (2 * k8N * 128) + half * (4 * k8Parts * 128);
+      unsigned char* pz = ps + k8N * 128;
       if (quad == 0 && lane == 0) {
-        float* fac = s_fac[i & 1];
+        float* fac = s_fac[i & 3];  // (tile i - 4 is read: the products of i - 2 waited for those of i - 3 to be)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           fac[4 * half + k] = alpha[k];
@@ -474,19 +501,19 @@ __global__ void __launch_bounds__(k8Threads, 1)
         }
       }
       // value rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
-      if (rows < k8Unit * units) {
+      if (rows < padded) {
         int idx = (nd + nz) * (2 * i + (nmore ? 2 : 1));  // the tile's first value copy
         for (int j = 0; j < nd + nz; ++j, ++idx) {
           const int slot = idx % A.slots;
           const bool landed =
               wait8_warp(&full[slot], static_cast<uint32_t>(idx / A.slots) & 1u, fail, P.wait_limit);
-          if (landed && tid < 8 * (k8Unit * units - rows))
+          if (landed && tid < 8 * (padded - rows))
             *reinterpret_cast<uint4*>(smem + A.off_ring + slot * k8Box + rows * 128 + tid * 16) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&pfull);
+      if (lane == 0) mbar_arrive_cta(&pfull[i & 1]);
       if (last) {  // the piece's maxima and denominators
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -521,11 +548,16 @@ __global__ void __launch_bounds__(k8Threads, 1)
         hi[j] = min((128 * j + 32 * quad + 31) / r, heads - 1);
       }
     }
+    auto let_go = [&](int chunk) {  // a chunk's products are read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&oempty[chunk]);
+    };
     pdl_wait();  // the launch before may still read the workspace
     int i = 0, cur_b = -1;
     for (bool more = walk_first(w, pre, B, g0, g1); more; ++i) {
       TileWalk nx = w;
-      const bool nmore = walk_next(nx, pre, B, g1, k8Units);
+      const bool nmore = walk_next(nx, pre, B, g1, 1);
       const bool last = !nmore || nx.b != w.b;
       if (w.b != cur_b) {
         cur_b = w.b;
@@ -536,9 +568,9 @@ __global__ void __launch_bounds__(k8Threads, 1)
 #pragma unroll
         for (int j = 0; j < k8MaxZ; ++j) oz[j] = 0.f;
       }
-      wait8_warp(&pv, static_cast<uint32_t>(i) & 1u, fail, P.wait_limit);
+      wait8_warp(&pv[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
       tc_fence_after();
-      const float* fac = s_fac[i & 1];
+      const float* fac = s_fac[i & 3];
       const float us = fac[16];
 #pragma unroll
       for (int j = 0; j < k8MaxD; ++j) {
@@ -548,6 +580,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         tmem_ld<16>(at + k8Os + j * k8N + 16, v + 16);
         tmem_ld<16>(at + k8Os + j * k8N + 32, v + 32);
         tmem_wait_ld();
+        let_go(j);
 #pragma unroll
         for (int k = 0; k < k8Heads; ++k) os[j][k] = fmaf(os[j][k], fac[k], join<k8Parts>(v + k8Parts * k) * us);
       }
@@ -561,10 +594,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
           const float x = fmaf(oz[j], fac[k], join<k8Parts>(v) * fac[8 + k]);
           if (k == head[j]) oz[j] = x;
         }
+        if (j < nz) let_go(nd + j);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&oempty);
       if (last) {
         float* out = P.part_acc + (static_cast<size_t>(w.b + c) * H + h0) * (d + r);
 #pragma unroll
@@ -585,131 +616,142 @@ __global__ void __launch_bounds__(k8Threads, 1)
     }
   } else if (warp == 12) {
     // ---- copies, in the order the MMAs take them: keys of tile 0, then keys of tile i + 1
-    // and values of tile i; a lane per box of box_rows rows.  A slot is let go by the MMAs that
-    // read it, so its last copy has landed ---------------------------------------------------
-    int idx = 0;
-    auto copy = [&](const TileWalk& t, bool values) -> bool {
-      const int units = min(k8Units, t.t_end - t.t0), boxes = units * k8Unit / A.box_rows;
-      const int at = k8Unit * t.t0 + lane * A.box_rows;  // this lane's first row
-      int y = at, z = t.b;
-      if (P.block_table && lane < boxes) {
-        y = at & ((1 << P.page_shift) - 1);
-        z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
-        if (at < rows_of(t.b)) {
+    // and values of tile i; a lane per box.  A slot is let go by the MMAs that read it, so its
+    // last copy has landed -----------------------------------------------------------------
+    int idx = 0, L = 0, cur_b = -1;
+    Place8 at8;
+    struct Where {
+      int padded, y, z;  // rows copied; this lane's box
+    };
+    auto where = [&](const TileWalk& t) -> Where {
+      if (t.b != cur_b) {
+        cur_b = t.b;
+        L = rows_of(t.b);
+      }
+      const int padded = round_up(min(k8Rows, L - k8Rows * t.t0), k8Step);
+      const int at = k8Rows * t.t0 + lane * (padded < k8Rows ? A.tail_box : A.box);  // this lane's first row
+      Where o = {padded, at, t.b};
+      if (P.block_table && at < k8Rows * t.t0 + padded) {
+        o.y = at & ((1 << P.page_shift) - 1);
+        o.z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
+        if (at < L) {
           const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (at >> P.page_shift));
-          if (page >= 0 && page < P.num_pages) z = page; else s_bad = 1;
+          if (page >= 0 && page < P.num_pages) o.z = page; else s_bad = 1;
         }
       }
-      for (int j = 0; j < nd + nz; ++j, ++idx) {
-        const int slot = idx % A.slots;
-        if (idx >= A.slots && !wait8_warp(&empty[slot], static_cast<uint32_t>(idx / A.slots - 1) & 1u, fail, P.wait_limit))
-          return false;
-        if (__any_sync(0xffffffffu, *fail)) return false;
+      return o;
+    };
+    auto copy = [&](const Where& o, bool values) -> bool {
+      const bool tail = o.padded < k8Rows;
+      const int box = tail ? A.tail_box : A.box, boxes = o.padded / box;
+      const CUtensorMap* map = &M.map[(tail ? 4 : 0) + (values ? 1 : 0)];
+      int x = 0;
+      for (int j = 0; j < nd + nz; ++j, ++idx, x += 128, at8.move(1, A.slots)) {
+        if (j == nd) {
+          x = h0 * r;
+          map += 2;
+        }
+        uint64_t* bar = &full[at8.slot];
+        if (idx >= A.slots && !wait8_warp(&empty[at8.slot], at8.phase ^ 1u, fail, P.wait_limit)) return false;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[slot], units * k8Unit * 128);
+          mbar_arrive_expect_tx(bar, o.padded * 128);
           s_copies = idx + 1;
         }
         __syncwarp();
-        if (lane < boxes) {
-          unsigned char* dst = smem + A.off_ring + slot * k8Box + lane * A.box_rows * 128;
-          if (j < nd) tma_load_3d(dst, values ? &tm_v : &tm_k, 128 * j, y, z, &full[slot]);
-          else tma_load_3d(dst, values ? &tm_zv : &tm_zk, h0 * r + 128 * (j - nd), y, z, &full[slot]);
-        }
+        if (lane < boxes)
+          tma_load_3d(smem + A.off_ring + at8.slot * k8Box + lane * box * 128, map, x, o.y, o.z, bar);
       }
       return true;
     };
     TileWalk kw;
-    bool km = walk_first(kw, pre, B, g0, g1);
-    w = kw;
-    bool ok = copy(kw, false);
-    for (bool more = true; more && ok; more = walk_next(w, pre, B, g1, k8Units)) {
-      km = km && walk_next(kw, pre, B, g1, k8Units);
-      if (km) ok = copy(kw, false);
-      ok = ok && copy(w, true);
+    bool more = walk_first(kw, pre, B, g0, g1);
+    Where key = where(kw), value = key;
+    bool ok = copy(key, false);
+    while (more && ok) {
+      more = walk_next(kw, pre, B, g1, 1);
+      if (more) {
+        key = where(kw);
+        ok = copy(key, false);
+      }
+      ok = ok && copy(value, true);
+      value = key;
     }
   } else if (warp == 13) {
     if (lane == 0) {
-      // ---- MMAs ------------------------------------------------------------------------
-      int idx = 0, ki = 0, vi = 0, piece = -1, cur_b = -1;
+      // ---- scores of a tile: q against the shared rows, p against the latents ---------------
       const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
       const uint64_t img = smem_desc(smem_u32(smem + A.off_img), 16, 1024, 2);
-      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), 16, 1024, 2);
-      auto slot_full = [&](int& slot) {
-        slot = idx % A.slots;
-        return wait8(&full[slot], static_cast<uint32_t>(idx / A.slots) & 1u, fail, P.wait_limit) && !*fail;
-      };
-      // scores of a tile: q against the shared rows, p against the latents
-      auto scores = [&](const TileWalk& t, bool last) -> bool {
-        if (t.b != cur_b) {
-          cur_b = t.b;
+      Place8 at8;
+      int i = 0, piece = -1, cur_b = -1;
+      bool ok = true;
+      for (bool more = walk_first(w, pre, B, g0, g1); more && ok; ++i) {
+        TileWalk nx = w;
+        const bool nmore = walk_next(nx, pre, B, g1, 1);
+        if (w.b != cur_b) {
+          cur_b = w.b;
           ++piece;
-          if (!wait8(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit)) return false;
+          ok = wait8(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
         }
-        const int a = ki & 1;
-        if (ki >= 2 && !wait8(&sempty[a], static_cast<uint32_t>((ki >> 1) - 1) & 1u, fail, P.wait_limit)) return false;
+        const int a = i & 1;
+        ok = ok && (i < 2 || wait8(&sempty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit));
         const uint32_t sd = tmem + k8S + a * k8SWidth;
         uint64_t bd = img + static_cast<uint32_t>((piece & 1) * (A.img_pad / 16));
-        for (int j = 0; j < nd + nz; ++j, ++idx) {
-          int slot;
-          if (!slot_full(slot)) return false;
+        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots)) {
+          ok = wait8(&full[at8.slot], at8.phase, fail, P.wait_limit);
+          if (!ok) break;
           tc_fence_after();
           const bool z = j >= nd;
           const int left = z ? heads * r - 128 * (j - nd) : P.dh - 128 * j;
-          const uint64_t ad = ring + static_cast<uint32_t>(slot * (k8Box / 16));
-          for (int kk = 0; kk < 4 && 32 * kk < left; ++kk)
-            mma8(sd + (z ? k8NQ : 0), ad + kk * 2, bd + kk * 2, z ? idesc8(k8N, 0) : idesc8(k8NQ, 0),
-                 (z ? j > nd : j > 0) || kk > 0 ? 1u : 0u);
-          tc_commit(&empty[slot]);
+          mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd,
+                   z ? idesc8(k8N, 0) : idesc8(k8NQ, 0), min(4, (left + 31) >> 5), z ? j == nd : j == 0);
+          tc_commit(&empty[at8.slot]);
           bd += (z ? k8N : k8NQ) * 8;
         }
-        tc_commit(&sfull[a]);
-        if (last) tc_commit(&iempty[piece & 1]);
-        ++ki;
-        return true;
-      };
-      // values of a tile: columns x rows of the box against the probabilities
-      auto values = [&](const TileWalk& t) -> bool {
-        const int units = min(k8Units, t.t_end - t.t0);
-        if (!wait8(&pfull, static_cast<uint32_t>(vi) & 1u, fail, P.wait_limit)) return false;
-        if (vi > 0 && !wait8(&oempty, static_cast<uint32_t>(vi - 1) & 1u, fail, P.wait_limit)) return false;
-        for (int j = 0; j < nd + nz; ++j, ++idx) {
-          int slot;
-          if (!slot_full(slot)) return false;
+        if (i > 0) at8.move(nd + nz, A.slots);  // (the values of the tile before)
+        if (ok) {
+          tc_commit(&sfull[a]);
+          if (!nmore || nx.b != w.b) tc_commit(&iempty[piece & 1]);
+        }
+        w = nx;
+        more = nmore;
+      }
+      tc_commit(&mdone);  // every MMA of this thread, also of a pass that gave up
+    }
+  } else if (warp == 14) {
+    if (lane == 0) {
+      // ---- values of a tile: columns x rows of the boxes against the probabilities ----------
+      const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
+      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), 16, 1024, 2);
+      Place8 at8;
+      at8.move(nd + nz, A.slots);  // (the keys of tile 0)
+      int i = 0;
+      bool ok = true;
+      for (bool more = walk_first(w, pre, B, g0, g1); more && ok; ++i) {
+        const int steps = (min(k8Rows, rows_of(w.b) - k8Rows * w.t0) + k8Step - 1) / k8Step;
+        more = walk_next(w, pre, B, g1, 1);
+        if (more) at8.move(nd + nz, A.slots);  // (the keys of the next tile)
+        ok = wait8(&pfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots)) {
+          ok = wait8(&full[at8.slot], at8.phase, fail, P.wait_limit) &&
+               (i == 0 || wait8(&oempty[j], static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit));
+          if (!ok) break;
           tc_fence_after();
           const bool z = j >= nd;
-          const uint32_t od = tmem + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N);
-          const uint64_t ad = ring + static_cast<uint32_t>(slot * (k8Box / 16));
-          const uint64_t bd = pd + (z ? k8N * 8 : 0);
-          for (int kk = 0; kk < units; ++kk) mma8(od, ad + kk * 256, bd + kk * 2, idesc8(k8N, 1), kk > 0 ? 1u : 0u);
-          tc_commit(&empty[slot]);
+          mma8_box(tmem + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N),
+                   ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 256,
+                   pd + ((i & 1) * 2 + (z ? 1 : 0)) * (k8N * 8), idesc8(k8N, 1),
+                   steps, true);
+          tc_commit(&empty[at8.slot]);
         }
-        tc_commit(&pv);
-        ++vi;
-        return true;
-      };
-      TileWalk kw, nx;
-      bool km = walk_first(kw, pre, B, g0, g1);
-      w = kw;
-      auto next_scores = [&]() -> bool {  // of kw, which then moves on
-        nx = kw;
-        const bool nm = walk_next(nx, pre, B, g1, k8Units);
-        const bool ok = scores(kw, !nm || nx.b != kw.b);
-        kw = nx;
-        km = nm;
-        return ok;
-      };
-      bool ok = next_scores();
-      for (bool more = true; more && ok; more = walk_next(w, pre, B, g1, k8Units)) {
-        if (km) ok = next_scores();
-        ok = ok && values(w);
+        if (ok) tc_commit(&pv[i & 1]);
       }
-      tc_commit(&mdone);  // every MMA issued, also by a pass that gave up
+      tc_commit(&mdone);
     }
   } else if (lane == 0) {
     // ---- the operands of each piece, two buffers ------------------------------------------
     pdl_wait();
     int piece = 0, cur_b = -1;
-    for (bool more = walk_first(w, pre, B, g0, g1); more && !*fail; more = walk_next(w, pre, B, g1, k8Units)) {
+    for (bool more = walk_first(w, pre, B, g0, g1); more && !*fail; more = walk_next(w, pre, B, g1, 1)) {
       if (w.b == cur_b) continue;
       cur_b = w.b;
       if (piece >= 2 &&
@@ -772,12 +814,12 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& 
   A.nz = (std::min(P.H, k8Heads) * P.r + 127) / 128;
   P.mt = A.groups;
   P.grid = std::max(1, num_sms / A.groups);
-  P.min_tokens = 2;  // units of 32 rows a CTA gets at least
+  P.min_tokens = 1;  // tiles a CTA gets at least
   A.img_bytes = A.nd * k8NQ * 128 + A.nz * k8N * 128 + 128;
   A.img_pad = round_up(A.img_bytes, 1024);
   int off = round_up((P.B + 1) * 4, 1024);
   A.off_img = off; off += 2 * A.img_pad;
-  A.off_p = off; off += 2 * k8N * 128;
+  A.off_p = off; off += 4 * k8N * 128;
   A.off_ring = off;
   const int budget = 224 * 1024;  // (3 KB of the 227 for the static part and the alignment)
   A.slots = std::min(k8MaxSlots, (budget - off) / k8Box);
@@ -791,11 +833,6 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& 
   *image_off = (decode_workspace_bytes(P) + 255) / 256 * 256;
   *bytes = *image_off + static_cast<size_t>(P.B) * A.groups * A.img_bytes;
   return LRKV_OK;
-}
-
-// Rows of `width` bytes, box of 128 bytes x `box` rows with the 128-byte swizzle.
-bool map8(CUtensorMap* map, const void* base, int width, int rows, int lead, int box) {
-  return make_tmap_3d_u8(map, base, width, rows, lead, 128, box);
 }
 
 }  // namespace
@@ -852,16 +889,17 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
     lead = num_pages;
   }
   A.blocks = (rows + lrkv::kBlock8 - 1) / lrkv::kBlock8;
-  A.box_rows = block_table && page_size < lrkv::k8Unit ? page_size : lrkv::k8Unit;
-
-  CUtensorMap tm_k, tm_v, tm_zk, tm_zv;
-  std::memset(&tm_zk, 0, sizeof(tm_zk));
-  std::memset(&tm_zv, 0, sizeof(tm_zv));
-  if (!lrkv::map8(&tm_k, cache->k_s, P.dh, rows, lead, A.box_rows) ||
-      !lrkv::map8(&tm_v, cache->v_s, P.dh, rows, lead, A.box_rows) ||
-      (P.r > 0 && (!lrkv::map8(&tm_zk, cache->z_k, P.H * P.r, rows, lead, A.box_rows) ||
-                   !lrkv::map8(&tm_zv, cache->z_v, P.H * P.r, rows, lead, A.box_rows))))
-    return LRKV_ERR_CUDA;
+  A.box = block_table ? std::min(page_size, lrkv::k8Rows) : lrkv::k8Rows;
+  A.tail_box = std::min(A.box, lrkv::k8Step);
+  lrkv::Maps8 M;
+  std::memset(&M, 0, sizeof(M));
+  const void* const held[4] = {cache->k_s, cache->v_s, cache->z_k, cache->z_v};
+  for (int i = 0; i < 8; ++i)
+    if ((i & 2) == 0 || P.r > 0) {
+      const int width = (i & 2) == 0 ? P.dh : P.H * P.r;
+      if (!lrkv::make_tmap_3d_u8(&M.map[i], held[i & 3], width, rows, lead, 128, i < 4 ? A.box : A.tail_box))
+        return LRKV_ERR_CUDA;
+    }
   const void* kern = reinterpret_cast<const void*>(lrkv::lrkv_decode8_kernel);
   if (lrkv::ensure_kernel_smem(kern, P.smem_bytes, true) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[1];
@@ -877,7 +915,7 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
   cfg.gridDim = dim3(P.grid, P.mt);
   cfg.blockDim = dim3(lrkv::k8Threads);
   cfg.dynamicSmemBytes = P.smem_bytes;
-  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_kernel, P, tm_k, tm_v, tm_zk, tm_zv, A) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_kernel, P, M, A) != cudaSuccess)
     return LRKV_ERR_CUDA;
   return lrkv::decode_merge_launch(P, stream, true);
 }
