@@ -89,9 +89,10 @@ __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t 
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// e4m3 A and B, fp32 D, M = 128; a_mn: A is MN-major.
-__host__ __device__ constexpr uint32_t idesc8(int N, int a_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// e4m3 A and B, fp32 D, M = 128; mn: A and B are MN-major.
+__host__ __device__ constexpr uint32_t idesc8(int N, int mn) {
+  return (1u << 4) | (static_cast<uint32_t>(mn) << 15) | (static_cast<uint32_t>(mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* v) {
@@ -121,6 +122,22 @@ __device__ __forceinline__ float join(const uint32_t* v) {
   for (int i = N - 2; i >= 0; --i) s = fmaf(s, 0.0625f, __uint_as_float(v[i]));
   return s;
 }
+// The probabilities' operand, MN-major without swizzle: 16 columns of a row are 16 bytes, 8 rows a core matrix,
+// the three groups of 16 columns follow each other, then the next 8 rows.  A thread writes four heads of a row:
+// parts 0-3 of the first (second) four heads are group 0 (1), parts 4-5 of all the last group.
+constexpr int k8PGroup = 128, k8PRows = 3 * k8PGroup, k8PBytes = k8Rows / 8 * k8PRows;
+// The six part sums of head k of four, of which `v` holds the first 16 columns and `w` the last 8.
+__device__ __forceinline__ float join_values(const uint32_t* v, const uint32_t* w, int k) {
+  float s = fmaf(__uint_as_float(w[4 + k]), 0.0625f, __uint_as_float(w[k]));
+#pragma unroll
+  for (int i = 3; i >= 0; --i) s = fmaf(s, 0.0625f, __uint_as_float(v[4 * i + k]));
+  return s;
+}
+// 2^-e of a positive x in [2^e, 2^(e + 1)) (0: 2^127), and 2^e (0: 0).
+__device__ __forceinline__ float down_to_one(float x) {
+  return __uint_as_float(0x7f000000u - (__float_as_uint(x) & 0x7f800000u));
+}
+__device__ __forceinline__ float power_in(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -160,15 +177,15 @@ struct Place8 {
   }
 };
 // `steps` (1 .. 4) MMAs of K = 32 along a box and an operand.
-__device__ __forceinline__ void mma8_box(uint32_t d, uint64_t a, int a_step, uint64_t b, uint32_t idesc, int steps,
-                                         bool fresh) {
+__device__ __forceinline__ void mma8_box(uint32_t d, uint64_t a, int a_step, uint64_t b, int b_step, uint32_t idesc,
+                                         int steps, bool fresh) {
   mma8(d, a, b, idesc, fresh ? 0u : 1u);
   if (steps == 4) {
-    mma8(d, a + a_step, b + 2, idesc, 1u);
-    mma8(d, a + 2 * a_step, b + 4, idesc, 1u);
-    mma8(d, a + 3 * a_step, b + 6, idesc, 1u);
+    mma8(d, a + a_step, b + b_step, idesc, 1u);
+    mma8(d, a + 2 * a_step, b + 2 * b_step, idesc, 1u);
+    mma8(d, a + 3 * a_step, b + 3 * b_step, idesc, 1u);
   } else {
-    for (int k = 1; k < steps; ++k) mma8(d, a + k * a_step, b + 2 * k, idesc, 1u);
+    for (int k = 1; k < steps; ++k) mma8(d, a + k * a_step, b + k * b_step, idesc, 1u);
   }
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
@@ -450,10 +467,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
         tz[0] = fmaxf(tz[0], e.x); tz[1] = fmaxf(tz[1], e.y); tz[2] = fmaxf(tz[2], e.z); tz[3] = fmaxf(tz[3], e.w);
         ts = fmaxf(ts, red[o][8]);
       }
-      // one online softmax per head; the probabilities times the block's share of the tile's largest value
-      // scale, brought to 256 at most
+      // one online softmax per head; the probabilities times their block's value scale, over the power of two in
+      // the tile's largest: less than 2, brought to 256
       float xs[4], xz[4], alpha[4];
-      const float us = ts > 0.f ? 256.f * (vs / ts) : 0.f;
+      const float us = vs * down_to_one(ts) * 128.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float mx = fmaxf(m[k], top[k]);
@@ -462,44 +479,40 @@ __global__ void __launch_bounds__(k8Threads, 1)
         const float p = row < rows ? exp2f(s[k] - mx) : 0.f;
         l[k] = fmaf(l[k], alpha[k], p);
         xs[k] = p * us;
-        xz[k] = tz[k] > 0.f ? p * (256.f * (vz[k] / tz[k])) : 0.f;
+        xz[k] = p * (vz[k] * down_to_one(tz[k]) * 128.f);
         if (row >= rows) xs[k] = xz[k] = 0.f;
       }
       // into the operand of the value products, once the ones before are done with it
       if (i > 1) wait8_warp(&pv[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit);
-      unsigned char* ps = smem + A.off_p + (i & 1) * (2 * k8N * 128) + half * (4 * k8Parts * 128);
-      unsigned char* pz = ps + k8N * 128;
+      unsigned char* ps = smem + A.off_p + (i & 1) * (2 * k8PBytes) + (row >> 3) * k8PRows + (row & 7) * 16;
       if (quad == 0 && lane == 0) {
         float* fac = s_fac[i & 3];  // (tile i - 4 is read: the products of i - 2 waited for those of i - 3 to be)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           fac[4 * half + k] = alpha[k];
-          fac[8 + 4 * half + k] = tz[k] * (1.f / 256.f);
+          fac[8 + 4 * half + k] = power_in(tz[k]) * (1.f / 128.f);
         }
-        if (half == 0) fac[16] = ts * (1.f / 256.f);
+        if (half == 0) fac[16] = power_in(ts) * (1.f / 128.f);
       }
-#pragma unroll
-      for (int k = 0; k < 4; k += 2) {
+      auto put = [&](float* x, unsigned char* p) {
+        uint32_t v[k8Parts];
 #pragma unroll
         for (int t = 0; t < k8Parts; ++t) {
-          const int n0 = k * k8Parts + t, n1 = n0 + k8Parts;  // rows of the two heads (of this half's 24)
-          const uint32_t o0 = n0 * 128 + (row ^ ((n0 & 7) << 4)), o1 = n1 * 128 + (row ^ ((n1 & 7) << 4));
-          const uint32_t a = e4m3x2(xs[k], xs[k + 1]);
-          const float2 fa = from_e4m3x2(a);
-          ps[o0] = static_cast<unsigned char>(a);
-          ps[o1] = static_cast<unsigned char>(a >> 8);
-          xs[k] = (xs[k] - fa.x) * 16.f;
-          xs[k + 1] = (xs[k + 1] - fa.y) * 16.f;
-          if (r > 0) {
-            const uint32_t e = e4m3x2(xz[k], xz[k + 1]);
-            const float2 fe = from_e4m3x2(e);
-            pz[o0] = static_cast<unsigned char>(e);
-            pz[o1] = static_cast<unsigned char>(e >> 8);
-            xz[k] = (xz[k] - fe.x) * 16.f;
-            xz[k + 1] = (xz[k + 1] - fe.y) * 16.f;
+          const uint32_t lo = e4m3x2(x[0], x[1]), hi = e4m3x2(x[2], x[3]);
+          v[t] = lo | hi << 16;
+          if (t + 1 < k8Parts) {
+            const float2 a = from_e4m3x2(lo), e = from_e4m3x2(hi);
+            x[0] = (x[0] - a.x) * 16.f;
+            x[1] = (x[1] - a.y) * 16.f;
+            x[2] = (x[2] - e.x) * 16.f;
+            x[3] = (x[3] - e.y) * 16.f;
           }
         }
-      }
+        *reinterpret_cast<uint4*>(p + half * k8PGroup) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint2*>(p + 2 * k8PGroup + 8 * half) = make_uint2(v[4], v[5]);
+      };
+      put(xs, ps);
+      if (r > 0) put(xz, ps + k8PBytes);
       // value rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
       if (rows < padded) {
         int idx = (nd + nz) * (2 * i + (nmore ? 2 : 1));  // the tile's first value copy
@@ -582,19 +595,26 @@ __global__ void __launch_bounds__(k8Threads, 1)
         tmem_wait_ld();
         let_go(j);
 #pragma unroll
-        for (int k = 0; k < k8Heads; ++k) os[j][k] = fmaf(os[j][k], fac[k], join<k8Parts>(v + k8Parts * k) * us);
+        for (int k = 0; k < k8Heads; ++k)
+          os[j][k] = fmaf(os[j][k], fac[k], join_values(v + 16 * (k >> 2), v + 32 + 8 * (k >> 2), k & 3) * us);
       }
 #pragma unroll
       for (int j = 0; j < k8MaxZ; ++j) {
-        for (int k = lo[j]; k <= hi[j]; ++k) {  // (the same for the whole warp)
-          uint32_t v[k8Parts];
-          tmem_ld<4>(at + k8Oz + j * k8N + k * k8Parts, v);
-          tmem_ld<2>(at + k8Oz + j * k8N + k * k8Parts + 4, v + 4);
+        if (j >= nz) break;
+        for (int q = lo[j] >> 2; q <= hi[j] >> 2; ++q) {  // four heads at a time (the same for the whole warp)
+          uint32_t v[16], u[8];
+          tmem_ld<16>(at + k8Oz + j * k8N + 16 * q, v);
+          tmem_ld<8>(at + k8Oz + j * k8N + 32 + 8 * q, u);
           tmem_wait_ld();
-          const float x = fmaf(oz[j], fac[k], join<k8Parts>(v) * fac[8 + k]);
-          if (k == head[j]) oz[j] = x;
+          float x = join_values(v, u, 0);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) {
+            const float y = join_values(v, u, k);
+            if ((head[j] & 3) == k) x = y;
+          }
+          if (head[j] >> 2 == q) oz[j] = fmaf(oz[j], fac[head[j]], x * fac[8 + head[j]]);
         }
-        if (j < nz) let_go(nd + j);
+        let_go(nd + j);
       }
       if (last) {
         float* out = P.part_acc + (static_cast<size_t>(w.b + c) * H + h0) * (d + r);
@@ -702,7 +722,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
           tc_fence_after();
           const bool z = j >= nd;
           const int left = z ? heads * r - 128 * (j - nd) : P.dh - 128 * j;
-          mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd,
+          mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd, 2,
                    z ? idesc8(k8N, 0) : idesc8(k8NQ, 0), min(4, (left + 31) >> 5), z ? j == nd : j == 0);
           tc_commit(&empty[at8.slot]);
           bd += (z ? k8N : k8NQ) * 8;
@@ -721,7 +741,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     if (lane == 0) {
       // ---- values of a tile: columns x rows of the boxes against the probabilities ----------
       const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
-      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), 16, 1024, 2);
+      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), k8PRows, k8PGroup, 0);
       Place8 at8;
       at8.move(nd + nz, A.slots);  // (the keys of tile 0)
       int i = 0;
@@ -739,8 +759,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
           const bool z = j >= nd;
           mma8_box(tmem + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N),
                    ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 256,
-                   pd + ((i & 1) * 2 + (z ? 1 : 0)) * (k8N * 8), idesc8(k8N, 1),
-                   steps, true);
+                   pd + ((i & 1) * 2 + (z ? 1 : 0)) * (k8PBytes / 16), 4 * k8PRows / 16, idesc8(k8N, 1), steps, true);
           tc_commit(&empty[at8.slot]);
         }
         if (ok) tc_commit(&pv[i & 1]);
@@ -819,7 +838,7 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& 
   A.img_pad = round_up(A.img_bytes, 1024);
   int off = round_up((P.B + 1) * 4, 1024);
   A.off_img = off; off += 2 * A.img_pad;
-  A.off_p = off; off += 4 * k8N * 128;
+  A.off_p = off; off += 4 * k8PBytes;
   A.off_ring = off;
   const int budget = 224 * 1024;  // (3 KB of the 227 for the static part and the alignment)
   A.slots = std::min(k8MaxSlots, (budget - off) / k8Box);
