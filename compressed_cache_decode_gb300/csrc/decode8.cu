@@ -24,10 +24,11 @@
 // by every group; all but the first find them in L2.
 //
 // Grid (range CTAs, groups).  16 warps: 0-7 the softmax (a thread per row, four
-// heads each), 8-11 the value sums (a thread per column), 12 the copies, 13
-// the score MMAs, 14 the value MMAs, 15 the operands of each sequence, which
-// lrkv_decode8_operands_kernel has laid out before.  The keys of tile i + 1 are
-// multiplied while the softmax works on tile i.
+// heads each), 8-11 the value sums (a thread per column), 12 and 15 the copies
+// (keys, with the operands of each sequence, which lrkv_decode8_operands_kernel
+// has laid out before; values), 13 the score MMAs, 14 the value MMAs.  Keys and
+// values have a ring each; the scores of the next tile are formed while the
+// softmax works on this one.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -73,7 +74,7 @@ struct Args8 {
   int groups, nd, nz;   // head groups; chunks of a shared row and of a group's latents
   int img_bytes;        // operands of a (sequence, group): q parts | p parts | 16 factors
   int img_pad;          // the same in shared memory, on a 1 KB boundary
-  int slots;            // ring depth
+  int slots[2];         // ring depths: keys, values
   int box, tail_box;    // rows of a copy: of a full tile (128, or a page's), of a sequence's last one (32, or a page's)
   int off_img, off_p, off_ring;
   int blocks;           // scale blocks of a sequence (contiguous) or page
@@ -188,6 +189,35 @@ __device__ __forceinline__ void mma8_box(uint32_t d, uint64_t a, int a_step, uin
     for (int k = 1; k < steps; ++k) mma8(d, a + k * a_step, b + k * b_step, idesc, 1u);
   }
 }
+// The copying and issuing warps run as whole warps on values that every lane has, so that the operands of their
+// instructions are in uniform registers: with one lane's own values each MMA took three times as long to issue.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
+}
+// The pieces of a CTA's range of tiles [g0, g1): tiles [t0, t0 + n) of sequence b.
+struct Pieces8 {
+  int b, g, t0, n;
+  __device__ __forceinline__ bool first(const int* pre, int B, int g0, int g1) {
+    TileWalk w;
+    if (!walk_first(w, pre, B, g0, g1)) return false;
+    b = uniform(w.b);
+    g = uniform(g0);
+    t0 = uniform(w.t0);
+    n = uniform(w.t_end) - t0;
+    return true;
+  }
+  __device__ __forceinline__ bool next(const int* pre, int B, int g1) {
+    g += n;
+    if (g >= uniform(g1)) return false;
+    do ++b; while (uniform(pre[b + 1]) <= g);  // (empty sequences)
+    t0 = 0;
+    n = uniform(min(pre[b + 1], g1)) - g;
+    return true;
+  }
+};
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 }  // namespace
@@ -288,7 +318,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
   __shared__ uint64_t full[k8MaxSlots], empty[k8MaxSlots], ifull[2], iempty[2], sfull[2], sempty[2], pfull[2], pv[2],
       oempty[k8MaxD + k8MaxZ], mdone;
   __shared__ uint32_t tmem_base;
-  __shared__ int s_fail, s_bad, s_copies, s_images;
+  __shared__ int s_fail, s_bad, s_images, s_copies[2];  // copies issued
   __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
   __shared__ float s_fac[4][20];                      // [tile % 4]: alpha[8], latent scale[8], shared scale
   __shared__ float s_sum[2][4][4];
@@ -296,7 +326,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
   volatile int* fail = &s_fail;
 
   pdl_trigger();  // the merge may launch: it waits for this grid before it reads
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const int B = P.B, H = P.H, r = P.r, group = blockIdx.y, h0 = group * k8Heads;
   const int heads = min(k8Heads, H - h0);
   const int nd = A.nd, nz = (heads * r + 127) / 128;
@@ -315,7 +345,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     }
     for (int i = 0; i < k8MaxD + k8MaxZ; ++i) mbar_init(&oempty[i], k8Values);
     mbar_init(&mdone, 2);
-    s_fail = s_bad = s_copies = s_images = 0;
+    s_fail = s_bad = s_images = s_copies[0] = s_copies[1] = 0;
     fence_barrier_init();
   }
   if (warp == 13) tmem_alloc(&tmem_base, k8Cols);
@@ -421,7 +451,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&iempty[piece & 1]);
       }
-      const int rows = min(k8Rows, L - k8Rows * w.t0), padded = round_up(rows, k8Step);
+      const int rows = min(k8Rows, L - k8Rows * w.t0);
       float ks = nks, vs = nvs, kz[4], vz[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) { kz[k] = nkz[k]; vz[k] = nvz[k]; }
@@ -513,17 +543,6 @@ __global__ void __launch_bounds__(k8Threads, 1)
       };
       put(xs, ps);
       if (r > 0) put(xz, ps + k8PBytes);
-      // value rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
-      if (rows < padded) {
-        int idx = (nd + nz) * (2 * i + (nmore ? 2 : 1));  // the tile's first value copy
-        for (int j = 0; j < nd + nz; ++j, ++idx) {
-          const int slot = idx % A.slots;
-          const bool landed =
-              wait8_warp(&full[slot], static_cast<uint32_t>(idx / A.slots) & 1u, fail, P.wait_limit);
-          if (landed && tid < 8 * (padded - rows))
-            *reinterpret_cast<uint4*>(smem + A.off_ring + slot * k8Box + rows * 128 + tid * 16) = make_uint4(0, 0, 0, 0);
-        }
-      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&pfull[i & 1]);
@@ -634,162 +653,167 @@ __global__ void __launch_bounds__(k8Threads, 1)
       w = nx;
       more = nmore;
     }
-  } else if (warp == 12) {
-    // ---- copies, in the order the MMAs take them: keys of tile 0, then keys of tile i + 1
-    // and values of tile i; a lane per box.  A slot is let go by the MMAs that read it, so its
-    // last copy has landed -----------------------------------------------------------------
-    int idx = 0, L = 0, cur_b = -1;
+  } else if (warp == 12 || warp == 15) {
+    // ---- copies of the keys (warp 12, with each piece's operands) and of the values (15), a
+    // ring each: with one ring for both, a parity could not tell a phase from the one two
+    // before it when one side runs ahead.  A lane per box; a slot is let go by the MMAs that
+    // read it, so its last copy has landed -----------------------------------------------
+    const bool values = warp == 15, leader = elect();
+    const int slots = A.slots[values], s0 = values ? A.slots[0] : 0, nc = nd + nz;
+    int copies = 0, piece = 0;
+    bool ok = true, first = true;
     Place8 at8;
-    struct Where {
-      int padded, y, z;  // rows copied; this lane's box
+    Pieces8 w8 = {};
+    auto operands = [&](int b) {
+      ok = ok && (piece < 2 || wait8_warp(&iempty[piece & 1], static_cast<uint32_t>((piece >> 1) - 1) & 1u, fail,
+                                          P.wait_limit));
+      if (ok && leader) {
+        mbar_arrive_expect_tx(&ifull[piece & 1], A.img_bytes);
+        tma_load_1d(smem + A.off_img + (piece & 1) * A.img_pad,
+                    A.images + (static_cast<size_t>(b) * A.groups + group) * A.img_bytes, A.img_bytes,
+                    &ifull[piece & 1]);
+        s_images = piece + 1;
+      }
+      ++piece;
     };
-    auto where = [&](const TileWalk& t) -> Where {
-      if (t.b != cur_b) {
-        cur_b = t.b;
-        L = rows_of(t.b);
-      }
-      const int padded = round_up(min(k8Rows, L - k8Rows * t.t0), k8Step);
-      const int at = k8Rows * t.t0 + lane * (padded < k8Rows ? A.tail_box : A.box);  // this lane's first row
-      Where o = {padded, at, t.b};
-      if (P.block_table && at < k8Rows * t.t0 + padded) {
-        o.y = at & ((1 << P.page_shift) - 1);
-        o.z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
-        if (at < L) {
-          const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (at >> P.page_shift));
-          if (page >= 0 && page < P.num_pages) o.z = page; else s_bad = 1;
-        }
-      }
-      return o;
+    auto begin = [&] {  // the first operands are the launch before's
+      first = false;
+      pdl_wait();
+      operands(w8.b);
     };
-    auto copy = [&](const Where& o, bool values) -> bool {
-      const bool tail = o.padded < k8Rows;
-      const int box = tail ? A.tail_box : A.box, boxes = o.padded / box;
-      const CUtensorMap* map = &M.map[(tail ? 4 : 0) + (values ? 1 : 0)];
-      int x = 0;
-      for (int j = 0; j < nd + nz; ++j, ++idx, x += 128, at8.move(1, A.slots)) {
-        if (j == nd) {
-          x = h0 * r;
-          map += 2;
+    for (bool more = w8.first(pre, B, g0, g1); more && ok; more = w8.next(pre, B, g1)) {
+      const int L = uniform(rows_of(w8.b));
+      if (!values && !first) operands(w8.b);
+      for (int t = w8.t0; t < w8.t0 + w8.n && ok; ++t) {
+        const int padded = round_up(min(k8Rows, L - k8Rows * t), k8Step);
+        const bool tail = padded < k8Rows;
+        const int box = tail ? A.tail_box : A.box, boxes = padded / box;
+        const int at = k8Rows * t + lane * box;  // this lane's first row
+        int y = at, z = w8.b;
+        if (P.block_table && lane < boxes) {
+          y = at & ((1 << P.page_shift) - 1);
+          z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
+          if (at < L) {
+            const int page = __ldg(P.block_table + static_cast<size_t>(w8.b) * P.max_blocks + (at >> P.page_shift));
+            if (page >= 0 && page < P.num_pages) z = page; else s_bad = 1;
+          }
         }
-        uint64_t* bar = &full[at8.slot];
-        if (idx >= A.slots && !wait8_warp(&empty[at8.slot], at8.phase ^ 1u, fail, P.wait_limit)) return false;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, o.padded * 128);
-          s_copies = idx + 1;
+        const CUtensorMap* map = &M.map[(tail ? 4 : 0) + (values ? 1 : 0)];
+        int x = 0;
+        for (int j = 0; j < nc; ++j, x += 128, at8.move(1, slots)) {
+          if (j == nd) {
+            x = h0 * r;
+            map += 2;
+          }
+          const int slot = s0 + at8.slot;
+          // (with the ring full the first scores are waited for)
+          if (first && !values && copies == slots) begin();
+          if (copies >= slots) ok = ok && wait8_warp(&empty[slot], at8.phase ^ 1u, fail, P.wait_limit);
+          if (!ok) break;
+          ++copies;
+          if (leader) {
+            mbar_arrive_expect_tx(&full[slot], padded * 128);
+            s_copies[values] = copies;
+          }
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_3d(smem + A.off_ring + slot * k8Box + lane * box * 128, map, x, y, z, &full[slot]);
         }
-        __syncwarp();
-        if (lane < boxes)
-          tma_load_3d(smem + A.off_ring + at8.slot * k8Box + lane * box * 128, map, x, o.y, o.z, bar);
+        if (first && !values) begin();
+        first = false;
       }
-      return true;
-    };
-    TileWalk kw;
-    bool more = walk_first(kw, pre, B, g0, g1);
-    Where key = where(kw), value = key;
-    bool ok = copy(key, false);
-    while (more && ok) {
-      more = walk_next(kw, pre, B, g1, 1);
-      if (more) {
-        key = where(kw);
-        ok = copy(key, false);
-      }
-      ok = ok && copy(value, true);
-      value = key;
     }
   } else if (warp == 13) {
-    if (lane == 0) {
-      // ---- scores of a tile: q against the shared rows, p against the latents ---------------
-      const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
-      const uint64_t img = smem_desc(smem_u32(smem + A.off_img), 16, 1024, 2);
-      Place8 at8;
-      int i = 0, piece = -1, cur_b = -1;
-      bool ok = true;
-      for (bool more = walk_first(w, pre, B, g0, g1); more && ok; ++i) {
-        TileWalk nx = w;
-        const bool nmore = walk_next(nx, pre, B, g1, 1);
-        if (w.b != cur_b) {
-          cur_b = w.b;
-          ++piece;
-          ok = wait8(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
-        }
+    // ---- scores of a tile: q against the shared rows, p against the latents -----------------
+    const bool leader = elect();
+    const uint32_t td = uniform(tmem);
+    const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
+    const uint64_t img = smem_desc(smem_u32(smem + A.off_img), 16, 1024, 2);
+    Place8 at8;
+    Pieces8 w8 = {};
+    int i = 0, piece = 0;
+    bool ok = true;
+    for (bool more = w8.first(pre, B, g0, g1); more && ok; more = w8.next(pre, B, g1), ++piece) {
+      ok = wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
+      for (int t = 0; t < w8.n && ok; ++t, ++i) {
         const int a = i & 1;
-        ok = ok && (i < 2 || wait8(&sempty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit));
-        const uint32_t sd = tmem + k8S + a * k8SWidth;
+        ok = i < 2 || wait8_warp(&sempty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit);
+        const uint32_t sd = td + k8S + a * k8SWidth;
         uint64_t bd = img + static_cast<uint32_t>((piece & 1) * (A.img_pad / 16));
-        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots)) {
-          ok = wait8(&full[at8.slot], at8.phase, fail, P.wait_limit);
+        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots[0])) {
+          ok = wait8_warp(&full[at8.slot], at8.phase, fail, P.wait_limit);
           if (!ok) break;
           tc_fence_after();
           const bool z = j >= nd;
           const int left = z ? heads * r - 128 * (j - nd) : P.dh - 128 * j;
-          mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd, 2,
-                   z ? idesc8(k8N, 0) : idesc8(k8NQ, 0), min(4, (left + 31) >> 5), z ? j == nd : j == 0);
-          tc_commit(&empty[at8.slot]);
+          if (leader) {
+            mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd, 2,
+                     z ? idesc8(k8N, 0) : idesc8(k8NQ, 0), min(4, (left + 31) >> 5), z ? j == nd : j == 0);
+            tc_commit(&empty[at8.slot]);
+          }
+          __syncwarp();
           bd += (z ? k8N : k8NQ) * 8;
         }
-        if (i > 0) at8.move(nd + nz, A.slots);  // (the values of the tile before)
-        if (ok) {
+        if (ok && leader) {
           tc_commit(&sfull[a]);
-          if (!nmore || nx.b != w.b) tc_commit(&iempty[piece & 1]);
+          if (t + 1 == w8.n) tc_commit(&iempty[piece & 1]);
         }
-        w = nx;
-        more = nmore;
+        __syncwarp();
       }
-      tc_commit(&mdone);  // every MMA of this thread, also of a pass that gave up
     }
+    if (leader) tc_commit(&mdone);  // every MMA of this warp, also of a pass that gave up
   } else if (warp == 14) {
-    if (lane == 0) {
-      // ---- values of a tile: columns x rows of the boxes against the probabilities ----------
-      const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring), 16, 1024, 2);
-      const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), k8PRows, k8PGroup, 0);
-      Place8 at8;
-      at8.move(nd + nz, A.slots);  // (the keys of tile 0)
-      int i = 0;
-      bool ok = true;
-      for (bool more = walk_first(w, pre, B, g0, g1); more && ok; ++i) {
-        const int steps = (min(k8Rows, rows_of(w.b) - k8Rows * w.t0) + k8Step - 1) / k8Step;
-        more = walk_next(w, pre, B, g1, 1);
-        if (more) at8.move(nd + nz, A.slots);  // (the keys of the next tile)
-        ok = wait8(&pfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
-        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots)) {
-          ok = wait8(&full[at8.slot], at8.phase, fail, P.wait_limit) &&
-               (i == 0 || wait8(&oempty[j], static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit));
+    // ---- values of a tile: columns x rows of the boxes against the probabilities ------------
+    const bool leader = elect();
+    const uint32_t td = uniform(tmem);
+    const uint64_t ring = smem_desc(smem_u32(smem + A.off_ring + A.slots[0] * k8Box), 16, 1024, 2);
+    const uint64_t pd = smem_desc(smem_u32(smem + A.off_p), k8PRows, k8PGroup, 0);
+    Place8 at8;
+    Pieces8 w8 = {};
+    int i = 0;
+    bool ok = true;
+    for (bool more = w8.first(pre, B, g0, g1); more && ok; more = w8.next(pre, B, g1)) {
+      const int L = uniform(rows_of(w8.b));
+      for (int t = w8.t0; t < w8.t0 + w8.n && ok; ++t, ++i) {
+        const int rows = min(k8Rows, L - k8Rows * t), steps = (rows + k8Step - 1) / k8Step;
+        ok = wait8_warp(&pfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+        for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots[1])) {
+          const int slot = A.slots[0] + at8.slot;
+          ok = wait8_warp(&full[slot], at8.phase, fail, P.wait_limit) &&
+               (i == 0 || wait8_warp(&oempty[j], static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit));
           if (!ok) break;
+          if (rows < steps * k8Step) {
+            // rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
+            uint4* past = reinterpret_cast<uint4*>(smem + A.off_ring + slot * k8Box + rows * 128);
+            for (int k = lane; k < 8 * (steps * k8Step - rows); k += 32) past[k] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           tc_fence_after();
           const bool z = j >= nd;
-          mma8_box(tmem + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N),
-                   ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 256,
-                   pd + ((i & 1) * 2 + (z ? 1 : 0)) * (k8PBytes / 16), 4 * k8PRows / 16, idesc8(k8N, 1), steps, true);
-          tc_commit(&empty[at8.slot]);
+          if (leader) {
+            mma8_box(td + (z ? k8Oz + (j - nd) * k8N : k8Os + j * k8N),
+                     ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 256,
+                     pd + ((i & 1) * 2 + (z ? 1 : 0)) * (k8PBytes / 16), 4 * k8PRows / 16, idesc8(k8N, 1), steps,
+                     true);
+            tc_commit(&empty[slot]);
+          }
+          __syncwarp();
         }
-        if (ok) tc_commit(&pv[i & 1]);
+        if (ok && leader) tc_commit(&pv[i & 1]);
+        __syncwarp();
       }
-      tc_commit(&mdone);
     }
-  } else if (lane == 0) {
-    // ---- the operands of each piece, two buffers ------------------------------------------
-    pdl_wait();
-    int piece = 0, cur_b = -1;
-    for (bool more = walk_first(w, pre, B, g0, g1); more && !*fail; more = walk_next(w, pre, B, g1, 1)) {
-      if (w.b == cur_b) continue;
-      cur_b = w.b;
-      if (piece >= 2 &&
-          !wait8(&iempty[piece & 1], static_cast<uint32_t>((piece >> 1) - 1) & 1u, fail, P.wait_limit))
-        break;
-      mbar_arrive_expect_tx(&ifull[piece & 1], A.img_bytes);
-      tma_load_1d(smem + A.off_img + (piece & 1) * A.img_pad,
-                  A.images + (static_cast<size_t>(w.b) * A.groups + group) * A.img_bytes, A.img_bytes,
-                  &ifull[piece & 1]);
-      s_images = ++piece;
-    }
+    if (leader) tc_commit(&mdone);
   }
 
   // ---- every copy and MMA this CTA issued is complete before it exits ----
   __syncthreads();
   if (tid == 0) {
     bool done = true;
-    for (int i = max(0, s_copies - A.slots); i < s_copies; ++i)
-      done = mbar_wait_bounded(&full[i % A.slots], static_cast<uint32_t>(i / A.slots) & 1u) && done;
+    for (int v = 0, s0 = 0; v < 2; s0 += A.slots[v], ++v)
+      for (int i = max(0, s_copies[v] - A.slots[v]); i < s_copies[v]; ++i)
+        done = mbar_wait_bounded(&full[s0 + i % A.slots[v]], static_cast<uint32_t>(i / A.slots[v]) & 1u) && done;
     for (int i = max(0, s_images - 2); i < s_images; ++i)
       done = mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u) && done;
     if (work) done = mbar_wait_bounded(&mdone, 0u) && done;
@@ -841,10 +865,11 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& 
   A.off_p = off; off += 4 * k8PBytes;
   A.off_ring = off;
   const int budget = 224 * 1024;  // (3 KB of the 227 for the static part and the alignment)
-  A.slots = std::min(k8MaxSlots, (budget - off) / k8Box);
-  // (a tile's value copies are all in the ring while its last rows are cleared)
-  if (A.slots < A.nd + A.nz + 1) return LRKV_ERR_UNSUPPORTED;
-  P.smem_bytes = off + A.slots * k8Box + 1024;
+  const int slots = std::min(k8MaxSlots, (budget - off) / k8Box);
+  if (slots < 4) return LRKV_ERR_UNSUPPORTED;
+  A.slots[0] = slots / 2;
+  A.slots[1] = slots - A.slots[0];
+  P.smem_bytes = off + slots * k8Box + 1024;
   P.wide_merge = 1;
   const long long pairs = static_cast<long long>(P.B) * P.H;
   P.wide_warps = pairs <= 64 ? 16 : 8;
