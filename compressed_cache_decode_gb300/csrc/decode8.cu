@@ -71,15 +71,29 @@ struct Maps8 {
 };
 
 struct Args8 {
+  int B, H, dh, r, max_len;
+  float scale_log2;     // scale * log2(e): scores live in the base-2 domain
+  long long wait_limit; // SM cycles a wait may take before it gives up
   int groups, nd, nz;   // head groups; chunks of a shared row and of a group's latents
   int img_bytes;        // operands of a (sequence, group): q parts | p parts | 16 factors
   int img_pad;          // the same in shared memory, on a 1 KB boundary
   int slots[2];         // ring depths: keys, values
   int box, tail_box;    // rows of a copy: of a full tile (128, or a page's), of a sequence's last one (32, or a page's)
-  int off_img, off_p, off_ring;
+  int off_img, off_p, off_ring, smem_bytes;
   int blocks;           // scale blocks of a sequence (contiguous) or page
-  unsigned char* images;
+  int grid;             // range CTAs of a group
+  const int32_t* block_table;  // [B][max_blocks] or NULL (contiguous)
+  int max_blocks, page_shift, num_pages;
+  const void *q, *b_k, *b_v;
+  const int32_t* seq_lens;
+  float *out, *lse;
   lrkv_cache8 cache;
+  // workspace
+  uint32_t* status;
+  int* arrived;           // [B][groups] range CTAs done with a sequence
+  float* part_ml;         // [B + grid][H][2] maxima (log2 domain) and denominators of the pieces
+  float* part_acc;        // [B + grid][H][dh + r] their sums of shared values and latents
+  unsigned char* images;  // [B][groups][img_bytes]
 };
 
 __device__ __forceinline__ void mma8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -228,90 +242,112 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // (head, part), a byte per column, zeros in the columns of the other heads.
 // Both are brought to a largest magnitude in [128, 256) first; the factors
 // undo that and hold the scale (log2 domain).
-__global__ void __launch_bounds__(128) lrkv_decode8_operands_kernel(const __grid_constant__ DecodePlan P,
-                                                                    const __grid_constant__ Args8 A) {
-  __shared__ float s_q[256], s_part[4][64];
-  __shared__ uint32_t s_max[2];
+// Latency is all it costs (B_h^K once per sequence, from L2): the words of B_h^K
+// are under way before q is.
+constexpr int k8OpWarps = 8, k8OpThreads = 32 * k8OpWarps;
+constexpr int k8OpRows = 16;  // rows of B_h^K a warp has in flight
+
+__global__ void __launch_bounds__(k8OpThreads) lrkv_decode8_operands_kernel(const __grid_constant__ Args8 A) {
+  __shared__ float s_q[256], s_part[k8OpWarps][64];
+  __shared__ uint32_t s_max[2][k8OpWarps];
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, b = blockIdx.y, hl = h & 7, d = P.dh, r = P.r;
-  const bool there = h < P.H;
-  if (tid < 2) s_max[tid] = 0u;
-  __syncthreads();
-  uint32_t top = 0u;
-  for (int k = tid; k < d; k += 128) {
-    const float q = there ? __bfloat162float(
-                                static_cast<const __nv_bfloat16*>(P.q)[(static_cast<size_t>(b) * P.H + h) * d + k])
-                          : 0.f;
-    s_q[k] = q;
-    top = max(top, __float_as_uint(q) & 0x7fffffffu);
+  const int h = blockIdx.x, b = blockIdx.y, hl = h & 7, d = A.dh, r = A.r;
+  const bool there = h < A.H;
+  // lanes hold two columns each, warps every eighth row
+  const uint32_t* bk = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(A.b_k) +
+                                                         static_cast<size_t>(h) * d * r) + lane;
+  const bool mine = there && 2 * lane < r;
+  uint32_t word[k8OpRows];
+#pragma unroll
+  for (int i = 0; i < k8OpRows; ++i) {
+    const int k = warp + k8OpWarps * i;
+    word[i] = mine && k < d ? __ldg(bk + k * (r / 2)) : 0u;
   }
-  atomicMax(&s_max[0], top);
+  const float q = there && tid < d ? __bfloat162float(static_cast<const __nv_bfloat16*>(
+                                         A.q)[(static_cast<size_t>(b) * A.H + h) * d + tid])
+                                   : 0.f;
+  s_q[tid] = q;
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(q) & 0x7fffffffu);
+  if (lane == 0) s_max[0][warp] = top;
   __syncthreads();
+  float p = 0.f;  // (threads 0 .. r - 1)
   if (r > 0) {
-    // lanes hold two columns each, warps every fourth row of B_h
     float a0 = 0.f, a1 = 0.f;
-    if (there && 2 * lane < r) {
-      const uint32_t* bk = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(P.b_k) +
-                                                             static_cast<size_t>(h) * d * r) + lane;
-#pragma unroll 16
-      for (int k = warp; k < d; k += 4) {
+#pragma unroll
+    for (int i = 0; i < k8OpRows; ++i) {
+      a0 = fmaf(s_q[warp + k8OpWarps * i], bf_lo(word[i]), a0);
+      a1 = fmaf(s_q[warp + k8OpWarps * i], bf_hi(word[i]), a1);
+    }
+    if (mine)
+      for (int k = warp + k8OpWarps * k8OpRows; k < d; k += k8OpWarps) {
         const uint32_t w = __ldg(bk + k * (r / 2));
         a0 = fmaf(s_q[k], bf_lo(w), a0);
         a1 = fmaf(s_q[k], bf_hi(w), a1);
       }
-    }
     s_part[warp][2 * lane] = a0;
     s_part[warp][2 * lane + 1] = a1;
     __syncthreads();
-    if (tid < 64) {
-      const float p = tid < r ? (s_part[0][tid] + s_part[1][tid]) + (s_part[2][tid] + s_part[3][tid]) : 0.f;
-      s_part[0][tid] = p;
-      atomicMax(&s_max[1], __float_as_uint(p) & 0x7fffffffu);
+    if (tid < r) {
+#pragma unroll
+      for (int i = 0; i < k8OpWarps; ++i) p += s_part[i][tid];
     }
+    top = __reduce_max_sync(0xffffffffu, __float_as_uint(p) & 0x7fffffffu);
+    if (lane == 0) s_max[1][warp] = top;
+    __syncthreads();
+    if (tid < r) s_part[0][tid] = p;
     __syncthreads();
   }
   float up[2], down[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int e = max(static_cast<int>(s_max[i] >> 23) - 127, -100);
+    top = 0u;
+    if (i == 0 || r > 0)
+      for (int k = 0; k < k8OpWarps; ++k) top = max(top, s_max[i][k]);
+    const int e = max(static_cast<int>(top >> 23) - 127, -100);
     up[i] = pow2(7 - e);
     // (infinities and NaN make the scores NaN)
-    down[i] = e == 128 ? __uint_as_float(0x7fffffffu) : pow2(e - 7) * P.scale_log2;
+    down[i] = e == 128 ? __uint_as_float(0x7fffffffu) : pow2(e - 7) * A.scale_log2;
     if (e == 128) up[i] = 0.f;
   }
   pdl_wait();  // the launch before may still read the workspace
+  if (hl == 0 && tid == 0) A.arrived[b * A.groups + (h >> 3)] = 0;
+  if (h == 0 && b == 0 && tid == 0) *A.status = 0u;
+  if (there && A.seq_lens[b] <= 0) {  // nothing to attend
+    if (tid < d) A.out[(static_cast<size_t>(b) * A.H + h) * d + tid] = 0.f;
+    if (tid == 0 && A.lse) A.lse[static_cast<size_t>(b) * A.H + h] = -INFINITY;
+  }
   unsigned char* img = A.images + (static_cast<size_t>(b) * A.groups + (h >> 3)) * A.img_bytes;
-  for (int j = 0; j < A.nd; ++j) {
-    float x = 128 * j + tid < d ? s_q[128 * j + tid] * up[0] : 0.f;
+  const int col = tid & 127;
+  for (int j = tid >> 7; j < A.nd; j += k8OpThreads / 128) {
+    float x = 128 * j + col < d ? s_q[128 * j + col] * up[0] : 0.f;
 #pragma unroll
     for (int i = 0; i < k8QParts; ++i) {
       const int n = hl * k8QParts + i;
       const uint32_t v = e4m3x2(x, 0.f);
-      img[n * 128 + (tid ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
+      img[j * (k8NQ * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
       x = (x - from_e4m3x2(v).x) * 16.f;
     }
-    img += k8NQ * 128;
   }
-  for (int j = 0; j < A.nz; ++j) {
-    const int c = 128 * j + tid - hl * r;  // this head's latent column
+  img += A.nd * (k8NQ * 128);
+  for (int j = tid >> 7; j < A.nz; j += k8OpThreads / 128) {
+    const int c = 128 * j + col - hl * r;  // this head's latent column
     float x = c >= 0 && c < r ? s_part[0][c] * up[1] : 0.f;
 #pragma unroll
     for (int i = 0; i < k8Parts; ++i) {
       const int n = hl * k8Parts + i;
       const uint32_t v = e4m3x2(x, 0.f);
-      img[n * 128 + (tid ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
+      img[j * (k8N * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
       x = (x - from_e4m3x2(v).x) * 16.f;
     }
-    img += k8N * 128;
   }
+  img += A.nz * (k8N * 128);
   if (tid < 2) reinterpret_cast<float*>(img)[8 * tid + hl] = there ? down[tid] : 0.f;
 }
 
 // ================================================================== the scan
 __global__ void __launch_bounds__(k8Threads, 1)
-    lrkv_decode8_kernel(const __grid_constant__ DecodePlan P, const __grid_constant__ Maps8 M,
-                        const __grid_constant__ Args8 A) {
+    lrkv_decode8_kernel(const __grid_constant__ Maps8 M, const __grid_constant__ Args8 A) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   // full/empty: ring slots; ifull/iempty: operands; sfull/sempty: scores; pfull: probabilities; pv: their
   // products done (and the probabilities' buffer free); oempty: a chunk's products read; mdone: every MMA done
@@ -325,9 +361,9 @@ __global__ void __launch_bounds__(k8Threads, 1)
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   volatile int* fail = &s_fail;
 
-  pdl_trigger();  // the merge may launch: it waits for this grid before it reads
+  pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-  const int B = P.B, H = P.H, r = P.r, group = blockIdx.y, h0 = group * k8Heads;
+  const int B = A.B, H = A.H, r = A.r, group = blockIdx.y, h0 = group * k8Heads;
   const int heads = min(k8Heads, H - h0);
   const int nd = A.nd, nz = (heads * r + 127) / 128;
   int* pre = reinterpret_cast<int*>(smem);
@@ -351,10 +387,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
   if (warp == 13) tmem_alloc(&tmem_base, k8Cols);
   int bad = 0;
   for (int b = tid; b < B; b += k8Threads) {
-    int L = P.seq_lens[b];
-    if (L < 0 || L > P.max_len) {
+    int L = A.seq_lens[b];
+    if (L < 0 || L > A.max_len) {
       bad = 1;
-      L = min(max(L, 0), P.max_len);
+      L = min(max(L, 0), A.max_len);
     }
     pre[b + 1] = L / k8Rows + (L % k8Rows != 0);
   }
@@ -379,12 +415,12 @@ __global__ void __launch_bounds__(k8Threads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const int N = pre[B];
-  const int G = max(1, min(static_cast<int>(gridDim.x), (N + P.min_tokens - 1) / max(P.min_tokens, 1)));
+  const int G = max(1, min(static_cast<int>(gridDim.x), N));
   const int c = blockIdx.x;
   const bool work = N > 0 && c < G;
   const int g0 = work ? static_cast<int>(static_cast<long long>(c) * N / G) : 0;
   const int g1 = work ? static_cast<int>(static_cast<long long>(c + 1) * N / G) : 0;
-  auto rows_of = [&](int b) { return min(max(__ldg(P.seq_lens + b), 0), P.max_len); };
+  auto rows_of = [&](int b) { return min(max(__ldg(A.seq_lens + b), 0), A.max_len); };
 
   TileWalk w;
   if (!work) {
@@ -405,10 +441,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
       for (int k = 0; k < 4; ++k) nkz[k] = nvz[k] = 0.f;
       if (row_b >= rows_of(t.b)) return;
       size_t blk = static_cast<size_t>(t.b) * A.blocks + row_b / kBlock8;
-      if (P.block_table) {
-        const int page = __ldg(P.block_table + static_cast<size_t>(t.b) * P.max_blocks + (row_b >> P.page_shift));
-        if (page < 0 || page >= P.num_pages) return;
-        blk = static_cast<size_t>(page) * A.blocks + (row_b & ((1 << P.page_shift) - 1)) / kBlock8;
+      if (A.block_table) {
+        const int page = __ldg(A.block_table + static_cast<size_t>(t.b) * A.max_blocks + (row_b >> A.page_shift));
+        if (page < 0 || page >= A.num_pages) return;
+        blk = static_cast<size_t>(page) * A.blocks + (row_b & ((1 << A.page_shift) - 1)) / kBlock8;
       }
       nks = __ldg(A.cache.k_s_scale + blk);
       nvs = __ldg(A.cache.v_s_scale + blk);
@@ -439,7 +475,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         cur_b = w.b;
         ++piece;
         L = rows_of(w.b);
-        wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
+        wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, A.wait_limit);
         const float* f = reinterpret_cast<const float*>(smem + A.off_img + (piece & 1) * A.img_pad + A.img_bytes - 128);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -459,7 +495,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
 
       // the scores
       uint32_t dq[16], dz[24];
-      wait8_warp(&sfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+      wait8_warp(&sfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, A.wait_limit);
       tc_fence_after();
       const uint32_t sb = at + k8S + (i & 1) * k8SWidth;
       tmem_ld<16>(sb + 16 * half, dq);
@@ -513,7 +549,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         if (row >= rows) xs[k] = xz[k] = 0.f;
       }
       // into the operand of the value products, once the ones before are done with it
-      if (i > 1) wait8_warp(&pv[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit);
+      if (i > 1) wait8_warp(&pv[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, A.wait_limit);
       unsigned char* ps = smem + A.off_p + (i & 1) * (2 * k8PBytes) + (row >> 3) * k8PRows + (row & 7) * 16;
       if (quad == 0 && lane == 0) {
         float* fac = s_fac[i & 3];  // (tile i - 4 is read: the products of i - 2 waited for those of i - 3 to be)
@@ -555,7 +591,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         }
         bar_named(1 + half, 128);
         if (quad == 0 && lane < 4 && hb + lane < H) {
-          float* pml = P.part_ml + (static_cast<size_t>(w.b + c) * H + hb + lane) * 2;
+          float* pml = A.part_ml + (static_cast<size_t>(w.b + c) * H + hb + lane) * 2;
           pml[0] = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
           pml[1] = (s_sum[half][0][lane] + s_sum[half][1][lane]) + (s_sum[half][2][lane] + s_sum[half][3][lane]);
         }
@@ -566,7 +602,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     }
   } else if (warp < k8Softmax + k8Values) {
     // ---- value sums: column 32 quad + lane of every chunk ------------------------------
-    const int quad = warp & 3, col = 32 * quad + lane, d = P.dh;
+    const int quad = warp & 3, col = 32 * quad + lane, d = A.dh;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     float os[k8MaxD][k8Heads], oz[k8MaxZ];
     int head[k8MaxZ], lo[k8MaxZ], hi[k8MaxZ];  // this column's head; the warp's first and last
@@ -600,7 +636,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
 #pragma unroll
         for (int j = 0; j < k8MaxZ; ++j) oz[j] = 0.f;
       }
-      wait8_warp(&pv[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+      wait8_warp(&pv[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, A.wait_limit);
       tc_fence_after();
       const float* fac = s_fac[i & 3];
       const float us = fac[16];
@@ -636,7 +672,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         let_go(nd + j);
       }
       if (last) {
-        float* out = P.part_acc + (static_cast<size_t>(w.b + c) * H + h0) * (d + r);
+        float* out = A.part_acc + (static_cast<size_t>(w.b + c) * H + h0) * (d + r);
 #pragma unroll
         for (int j = 0; j < k8MaxD; ++j) {
           if (j < nd && 128 * j + col < d) {
@@ -666,7 +702,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     Pieces8 w8 = {};
     auto operands = [&](int b) {
       ok = ok && (piece < 2 || wait8_warp(&iempty[piece & 1], static_cast<uint32_t>((piece >> 1) - 1) & 1u, fail,
-                                          P.wait_limit));
+                                          A.wait_limit));
       if (ok && leader) {
         mbar_arrive_expect_tx(&ifull[piece & 1], A.img_bytes);
         tma_load_1d(smem + A.off_img + (piece & 1) * A.img_pad,
@@ -690,12 +726,12 @@ __global__ void __launch_bounds__(k8Threads, 1)
         const int box = tail ? A.tail_box : A.box, boxes = padded / box;
         const int at = k8Rows * t + lane * box;  // this lane's first row
         int y = at, z = w8.b;
-        if (P.block_table && lane < boxes) {
-          y = at & ((1 << P.page_shift) - 1);
-          z = P.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
+        if (A.block_table && lane < boxes) {
+          y = at & ((1 << A.page_shift) - 1);
+          z = A.num_pages;  // rows past the sequence, or whose page is not one of the pool's: zeros
           if (at < L) {
-            const int page = __ldg(P.block_table + static_cast<size_t>(w8.b) * P.max_blocks + (at >> P.page_shift));
-            if (page >= 0 && page < P.num_pages) z = page; else s_bad = 1;
+            const int page = __ldg(A.block_table + static_cast<size_t>(w8.b) * A.max_blocks + (at >> A.page_shift));
+            if (page >= 0 && page < A.num_pages) z = page; else s_bad = 1;
           }
         }
         const CUtensorMap* map = &M.map[(tail ? 4 : 0) + (values ? 1 : 0)];
@@ -708,7 +744,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
           const int slot = s0 + at8.slot;
           // (with the ring full the first scores are waited for)
           if (first && !values && copies == slots) begin();
-          if (copies >= slots) ok = ok && wait8_warp(&empty[slot], at8.phase ^ 1u, fail, P.wait_limit);
+          if (copies >= slots) ok = ok && wait8_warp(&empty[slot], at8.phase ^ 1u, fail, A.wait_limit);
           if (!ok) break;
           ++copies;
           if (leader) {
@@ -734,18 +770,18 @@ __global__ void __launch_bounds__(k8Threads, 1)
     int i = 0, piece = 0;
     bool ok = true;
     for (bool more = w8.first(pre, B, g0, g1); more && ok; more = w8.next(pre, B, g1), ++piece) {
-      ok = wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, P.wait_limit);
+      ok = wait8_warp(&ifull[piece & 1], static_cast<uint32_t>(piece >> 1) & 1u, fail, A.wait_limit);
       for (int t = 0; t < w8.n && ok; ++t, ++i) {
         const int a = i & 1;
-        ok = i < 2 || wait8_warp(&sempty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, P.wait_limit);
+        ok = i < 2 || wait8_warp(&sempty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, A.wait_limit);
         const uint32_t sd = td + k8S + a * k8SWidth;
         uint64_t bd = img + static_cast<uint32_t>((piece & 1) * (A.img_pad / 16));
         for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots[0])) {
-          ok = wait8_warp(&full[at8.slot], at8.phase, fail, P.wait_limit);
+          ok = wait8_warp(&full[at8.slot], at8.phase, fail, A.wait_limit);
           if (!ok) break;
           tc_fence_after();
           const bool z = j >= nd;
-          const int left = z ? heads * r - 128 * (j - nd) : P.dh - 128 * j;
+          const int left = z ? heads * r - 128 * (j - nd) : A.dh - 128 * j;
           if (leader) {
             mma8_box(sd + (z ? k8NQ : 0), ring + static_cast<uint32_t>(at8.slot * (k8Box / 16)), 2, bd, 2,
                      z ? idesc8(k8N, 0) : idesc8(k8NQ, 0), min(4, (left + 31) >> 5), z ? j == nd : j == 0);
@@ -776,11 +812,11 @@ __global__ void __launch_bounds__(k8Threads, 1)
       const int L = uniform(rows_of(w8.b));
       for (int t = w8.t0; t < w8.t0 + w8.n && ok; ++t, ++i) {
         const int rows = min(k8Rows, L - k8Rows * t), steps = (rows + k8Step - 1) / k8Step;
-        ok = wait8_warp(&pfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, P.wait_limit);
+        ok = wait8_warp(&pfull[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, A.wait_limit);
         for (int j = 0; j < nd + nz && ok; ++j, at8.move(1, A.slots[1])) {
           const int slot = A.slots[0] + at8.slot;
-          ok = wait8_warp(&full[slot], at8.phase, fail, P.wait_limit) &&
-               (i == 0 || wait8_warp(&oempty[j], static_cast<uint32_t>(i - 1) & 1u, fail, P.wait_limit));
+          ok = wait8_warp(&full[slot], at8.phase, fail, A.wait_limit) &&
+               (i == 0 || wait8_warp(&oempty[j], static_cast<uint32_t>(i - 1) & 1u, fail, A.wait_limit));
           if (!ok) break;
           if (rows < steps * k8Step) {
             // rows past the sequence (which may hold anything) must not meet their zero probabilities as 0 x NaN
@@ -807,32 +843,175 @@ __global__ void __launch_bounds__(k8Threads, 1)
     if (leader) tc_commit(&mdone);
   }
 
-  // ---- every copy and MMA this CTA issued is complete before it exits ----
+  // ---- every copy and MMA this CTA issued is complete before it goes on (a pass that did not
+  // give up has waited for every copy) -------------------------------------------------------
+  pdl_wait();
+  __threadfence();  // the pieces' results, for the CTA that joins them
   __syncthreads();
   if (tid == 0) {
     bool done = true;
-    for (int v = 0, s0 = 0; v < 2; s0 += A.slots[v], ++v)
-      for (int i = max(0, s_copies[v] - A.slots[v]); i < s_copies[v]; ++i)
-        done = mbar_wait_bounded(&full[s0 + i % A.slots[v]], static_cast<uint32_t>(i / A.slots[v]) & 1u) && done;
-    for (int i = max(0, s_images - 2); i < s_images; ++i)
-      done = mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u) && done;
+    if (*fail) {
+      for (int v = 0, s0 = 0; v < 2; s0 += A.slots[v], ++v)
+        for (int i = max(0, s_copies[v] - A.slots[v]); i < s_copies[v]; ++i)
+          done = mbar_wait_bounded(&full[s0 + i % A.slots[v]], static_cast<uint32_t>(i / A.slots[v]) & 1u) && done;
+      for (int i = max(0, s_images - 2); i < s_images; ++i)
+        done = mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u) && done;
+    }
     if (work) done = mbar_wait_bounded(&mdone, 0u) && done;
     if (!done) *fail = 1;
-    pdl_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      P.meta[0] = N;
-      P.meta[1] = G;
-    }
-    P.cta_status[blockIdx.y * gridDim.x + blockIdx.x] = (bad || s_bad ? kDevBounds : 0u) | (*fail ? kDevTimeout : 0u);
-  }
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    pdl_wait();
-    for (int b = tid; b <= B; b += k8Threads) P.prefix[b] = pre[b];
+    const uint32_t bits = (bad || s_bad ? kDevBounds : 0u) | (*fail ? kDevTimeout : 0u);
+    if (bits) record_status(A.status, bits);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 13) tmem_dealloc(tmem, k8Cols);
+
+  // ---- the sequences of this CTA's range: the last CTA done with one joins its pieces, in
+  // their order, lifts the latents' sum through B_h^V and writes the outputs.  The loads do not
+  // wait for one another: pieces and rows of B_h^V are under way before the weights are known --
+  const int W = A.dh + r, d = A.dh;
+  int* s_c0 = reinterpret_cast<int*>(smem + A.off_img);        // a sequence's first CTA
+  int* s_n = s_c0 + k8Threads;                                 // its pieces, 0: another CTA joins them
+  float* s_w = reinterpret_cast<float*>(s_n + k8Threads);      // [8][pieces] weights, then [8][W] sums
+  auto cta_of = [&](int tile) -> int {  // (N G < 2^32 but for absurd CTA counts)
+    if (static_cast<unsigned long long>(N) * G >> 32) return cta_of_token(tile, N, G);
+    return static_cast<int>(((tile + 1u) * G - 1u) / static_cast<uint32_t>(N));
+  };
+  // the lift reads B_h^V front to back, 8 or 4 columns a thread, and adds a row's parts up
+  const uintptr_t bva = reinterpret_cast<uintptr_t>(A.b_v);
+  const int vec = r % 8 == 0 && bva % 16 == 0 ? 8 : r % 4 == 0 && bva % 8 == 0 ? 4 : 2, parts = r / vec;
+  const int rows_at_once = parts > 0 ? k8Threads / parts : k8Threads;
+  const int part = parts > 0 ? tid % parts : 0, row0 = parts > 0 ? tid / parts : tid;
+  int b0 = B;
+  if (work && walk_first(w, pre, B, g0, g1)) b0 = w.b;
+  for (; b0 < B && pre[b0] < g1; b0 += k8Threads) {
+    {
+      const int b = b0 + tid;
+      int c0 = 0, n = 0;
+      if (b < B && pre[b] < g1 && pre[b + 1] > pre[b]) {
+        c0 = cta_of(pre[b]);
+        n = cta_of(pre[b + 1] - 1) - c0 + 1;
+        if (n > 1 && atomicAdd(&A.arrived[b * A.groups + group], 1) != n - 1) n = 0;
+      }
+      s_c0[tid] = c0;
+      s_n[tid] = n;
+      if (n > 1) __threadfence();
+      __syncthreads();
+    }
+    for (int i0 = 0; i0 < k8Threads && b0 + i0 < B && pre[b0 + i0] < g1; ++i0) {
+      const int b = b0 + i0, c0 = s_c0[i0], n = s_n[i0];
+      if (n == 0) continue;
+      const float* ml = A.part_ml + (static_cast<size_t>(b + c0) * H + h0) * 2;
+      const float* acc = A.part_acc + (static_cast<size_t>(b + c0) * H + h0) * W;
+      const size_t step = static_cast<size_t>(H) * W;
+      float* s_o = s_w + k8Heads * n;
+      // (eight pieces' values of three columns under way at a time, the first ones before the weights)
+      float v[3][8];
+      auto fetch = [&](int e0, int i0) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = e0 + tid + j * k8Threads;
+            v[j][i] = i0 + i < n && e < heads * W ? __ldcg(acc + (i0 + i) * step + e) : 0.f;
+          }
+      };
+      fetch(0, 0);
+      if (warp < heads) {
+        auto piece = [&](int i) {
+          return i < n ? __ldcg(reinterpret_cast<const float2*>(ml + (static_cast<size_t>(i) * H + warp) * 2))
+                       : make_float2(-INFINITY, 0.f);
+        };
+        const float2 own = piece(lane);
+        float m = own.x, l = 0.f;
+        for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, piece(i).x);
+        m = warp_max(m);
+        for (int i = lane; i < n; i += 32) {
+          const float2 x = i == lane ? own : piece(i);
+          const float y = x.x == -INFINITY ? 0.f : exp2f(x.x - m);
+          s_w[warp * n + i] = y;
+          l = fmaf(y, x.y, l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const float inv = 1.f / l;
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) s_w[warp * n + i] *= inv;
+        if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
+      }
+      __syncthreads();
+      for (int e0 = 0; e0 < heads * W; e0 += 3 * k8Threads) {
+        float x[3] = {0.f, 0.f, 0.f};
+        for (int i0 = 0; i0 < n; i0 += 8) {
+          if (e0 > 0 || i0 > 0) fetch(e0, i0);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            const int k = min((e0 + tid + j * k8Threads) / W, heads - 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < n) x[j] = fmaf(s_w[k * n + i0 + i], v[j][i], x[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (e0 + tid + j * k8Threads < heads * W) s_o[e0 + tid + j * k8Threads] = x[j];
+      }
+      __syncthreads();
+      float* s_p = s_o + k8Heads * W;  // [heads d][parts]
+      if (row0 < rows_at_once && parts > 0) {
+        const __nv_bfloat16* bv = static_cast<const __nv_bfloat16*>(A.b_v) + static_cast<size_t>(h0) * d * r + part * vec;
+        for (int t0 = row0; t0 < d; t0 += 2 * rows_at_once)
+          for (int k0 = 0; k0 < heads; k0 += 4) {  // two rows of four heads under way
+            uint4 u[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int t = t0 + i * rows_at_once;
+                const __nv_bfloat16* at = bv + (static_cast<size_t>(k0 + k) * d + t) * r;
+                u[k][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (k0 + k >= heads || t >= d) continue;
+                if (vec == 8) {
+                  u[k][i] = __ldg(reinterpret_cast<const uint4*>(at));
+                } else if (vec == 4) {
+                  const uint2 y = __ldg(reinterpret_cast<const uint2*>(at));
+                  u[k][i].x = y.x;
+                  u[k][i].y = y.y;
+                } else {
+                  u[k][i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
+                }
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k0 + k >= heads) break;
+              float z[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) z[q] = q < vec ? s_o[(k0 + k) * W + d + part * vec + q] : 0.f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint4 y = u[k][i];
+                float x = fmaf(bf_hi(y.x), z[1], bf_lo(y.x) * z[0]);
+                x = fmaf(bf_hi(y.y), z[3], fmaf(bf_lo(y.y), z[2], x));
+                x = fmaf(bf_hi(y.z), z[5], fmaf(bf_lo(y.z), z[4], x));
+                x = fmaf(bf_hi(y.w), z[7], fmaf(bf_lo(y.w), z[6], x));
+                if (t0 + i * rows_at_once < d) s_p[((k0 + k) * d + t0 + i * rows_at_once) * parts + part] = x;
+              }
+            }
+          }
+      }
+      __syncthreads();
+      float* out = A.out + (static_cast<size_t>(b) * H + h0) * d;
+      for (int e = tid; e < heads * d; e += k8Threads) {
+        const int k = e / d;
+        float x = s_o[k * W + e - k * d];
+        for (int i = 0; i < parts; ++i) x += s_p[e * parts + i];
+        out[e] = x;
+      }
+      __syncthreads();  // (the sums are free)
+    }
+    __syncthreads();
+  }
 }
 
 // ======================================================================= host
@@ -844,23 +1023,36 @@ lrkv_status decode8_check(const lrkv_dims* d) {
   return d->dtype == LRKV_BF16 ? LRKV_OK : LRKV_ERR_UNSUPPORTED;
 }
 
-lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& A, size_t* image_off, size_t* bytes) {
-  std::memset(&P, 0, sizeof(P));
+// Carves the workspace up from `ws` on; returns its size.
+size_t decode8_bind(Args8& A, void* ws) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char* p = static_cast<unsigned char*>(ws) + off;
+    off += (bytes + 255) / 256 * 256;
+    return ws ? p : nullptr;
+  };
+  const size_t slots = static_cast<size_t>(A.B + A.grid) * A.H;
+  A.status = reinterpret_cast<uint32_t*>(take(256));
+  A.arrived = reinterpret_cast<int*>(take(sizeof(int) * A.B * A.groups));
+  A.part_ml = reinterpret_cast<float*>(take(sizeof(float) * slots * 2));
+  A.part_acc = reinterpret_cast<float*>(take(sizeof(float) * slots * (A.dh + A.r)));
+  A.images = take(static_cast<size_t>(A.B) * A.groups * A.img_bytes);
+  return off;
+}
+
+lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* bytes) {
   std::memset(&A, 0, sizeof(A));
-  P.B = d.batch; P.H = d.heads; P.dh = d.head_dim; P.r = d.rank; P.max_len = d.max_len;
+  A.B = d.batch; A.H = d.heads; A.dh = d.head_dim; A.r = d.rank; A.max_len = d.max_len;
   const float scale = d.scale > 0.f ? d.scale : 1.f / std::sqrt(static_cast<float>(d.head_dim));
-  P.scale_log2 = scale * kLog2e;
-  P.bf16 = 1; P.esz = 2; P.ngw = 1;
-  P.wait_limit = wait_limit_cycles();
-  A.groups = (P.H + k8Heads - 1) / k8Heads;
-  A.nd = (P.dh + 127) / 128;
-  A.nz = (std::min(P.H, k8Heads) * P.r + 127) / 128;
-  P.mt = A.groups;
-  P.grid = std::max(1, num_sms / A.groups);
-  P.min_tokens = 1;  // tiles a CTA gets at least
+  A.scale_log2 = scale * kLog2e;
+  A.wait_limit = wait_limit_cycles();
+  A.groups = (A.H + k8Heads - 1) / k8Heads;
+  A.nd = (A.dh + 127) / 128;
+  A.nz = (std::min(A.H, k8Heads) * A.r + 127) / 128;
+  A.grid = std::max(1, num_sms / A.groups);
   A.img_bytes = A.nd * k8NQ * 128 + A.nz * k8N * 128 + 128;
   A.img_pad = round_up(A.img_bytes, 1024);
-  int off = round_up((P.B + 1) * 4, 1024);
+  int off = round_up((A.B + 1) * 4, 1024);
   A.off_img = off; off += 2 * A.img_pad;
   A.off_p = off; off += 4 * k8PBytes;
   A.off_ring = off;
@@ -869,13 +1061,11 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, DecodePlan& P, Args8& 
   if (slots < 4) return LRKV_ERR_UNSUPPORTED;
   A.slots[0] = slots / 2;
   A.slots[1] = slots - A.slots[0];
-  P.smem_bytes = off + slots * k8Box + 1024;
-  P.wide_merge = 1;
-  const long long pairs = static_cast<long long>(P.B) * P.H;
-  P.wide_warps = pairs <= 64 ? 16 : 8;
-  P.combine_ctas = static_cast<int>(std::min<long long>(pairs, 4ll * num_sms));
-  *image_off = (decode_workspace_bytes(P) + 255) / 256 * 256;
-  *bytes = *image_off + static_cast<size_t>(P.B) * A.groups * A.img_bytes;
+  A.smem_bytes = off + slots * k8Box + 1024;
+  // the join's weights, sums and products lie over the operands, the probabilities and the ring
+  const long long join = 8ll * k8Threads + 4ll * k8Heads * (A.grid + A.dh + A.r + static_cast<long long>(A.dh) * (A.r / 2));
+  if (join > off + slots * k8Box - A.off_img) return LRKV_ERR_UNSUPPORTED;
+  *bytes = decode8_bind(A, nullptr);
   return LRKV_OK;
 }
 
@@ -891,10 +1081,8 @@ lrkv_status lrkv_decode8_workspace_size(const lrkv_dims* dims, size_t* bytes) {
   if (st != LRKV_OK) return st;
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
-  lrkv::DecodePlan P;
   lrkv::Args8 A;
-  size_t off = 0;
-  return lrkv::decode8_plan(*dims, sms, P, A, &off, bytes);
+  return lrkv::decode8_plan(*dims, sms, A, bytes);
 }
 
 lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, int num_pages,
@@ -906,29 +1094,27 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
   if (st != LRKV_OK) return st;
   if ((st = lrkv::cache8_check(dims, cache)) != LRKV_OK) return st;
   if (!q || !seq_lens || !out || (dims->rank > 0 && (!b_k || !b_v))) return LRKV_ERR_INVALID_ARG;
-  if (!lrkv::cache8_a16(q) || reinterpret_cast<uintptr_t>(b_k) % 4 != 0 || reinterpret_cast<uintptr_t>(b_v) % 2 != 0)
+  if (!lrkv::cache8_a16(q) || reinterpret_cast<uintptr_t>(b_k) % 4 != 0 || reinterpret_cast<uintptr_t>(b_v) % 4 != 0)
     return LRKV_ERR_INVALID_ARG;
   if ((st = lrkv::cache8_check_paging(dims, page_size, num_pages, block_table)) != LRKV_OK) return st;
   if (!ws) return LRKV_ERR_WORKSPACE;
   if (!lrkv::cache8_a16(ws)) return LRKV_ERR_INVALID_ARG;
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
-  lrkv::DecodePlan P;
   lrkv::Args8 A;
-  size_t image_off = 0, need = 0;
-  if ((st = lrkv::decode8_plan(*dims, sms, P, A, &image_off, &need)) != LRKV_OK) return st;
+  size_t need = 0;
+  if ((st = lrkv::decode8_plan(*dims, sms, A, &need)) != LRKV_OK) return st;
   if (ws_bytes < need) return LRKV_ERR_WORKSPACE;
-  lrkv::decode_bind_workspace(P, ws);
-  A.images = static_cast<unsigned char*>(ws) + image_off;
+  lrkv::decode8_bind(A, ws);
   A.cache = *cache;
-  P.q = q; P.b_k = b_k; P.b_v = b_v;
-  P.seq_lens = seq_lens; P.out = out; P.lse = lse;
-  int rows = P.max_len, lead = P.B;
+  A.q = q; A.b_k = b_k; A.b_v = b_v;
+  A.seq_lens = seq_lens; A.out = out; A.lse = lse;
+  int rows = A.max_len, lead = A.B;
   if (block_table) {
-    P.block_table = block_table;
-    P.max_blocks = P.max_len / page_size;
-    P.num_pages = num_pages;
-    while ((1 << P.page_shift) < page_size) ++P.page_shift;
+    A.block_table = block_table;
+    A.max_blocks = A.max_len / page_size;
+    A.num_pages = num_pages;
+    while ((1 << A.page_shift) < page_size) ++A.page_shift;
     rows = page_size;
     lead = num_pages;
   }
@@ -939,29 +1125,27 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
   std::memset(&M, 0, sizeof(M));
   const void* const held[4] = {cache->k_s, cache->v_s, cache->z_k, cache->z_v};
   for (int i = 0; i < 8; ++i)
-    if ((i & 2) == 0 || P.r > 0) {
-      const int width = (i & 2) == 0 ? P.dh : P.H * P.r;
+    if ((i & 2) == 0 || A.r > 0) {
+      const int width = (i & 2) == 0 ? A.dh : A.H * A.r;
       if (!lrkv::make_tmap_3d_u8(&M.map[i], held[i & 3], width, rows, lead, 128, i < 4 ? A.box : A.tail_box))
         return LRKV_ERR_CUDA;
     }
   const void* kern = reinterpret_cast<const void*>(lrkv::lrkv_decode8_kernel);
-  if (lrkv::ensure_kernel_smem(kern, P.smem_bytes, true) != cudaSuccess) return LRKV_ERR_CUDA;
+  if (lrkv::ensure_kernel_smem(kern, A.smem_bytes, true) != cudaSuccess) return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(A.groups * lrkv::k8Heads, P.B);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(A.groups * lrkv::k8Heads, A.B);
+  cfg.blockDim = dim3(lrkv::k8OpThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_operands_kernel, P, A) != cudaSuccess) return LRKV_ERR_CUDA;
-  cfg.gridDim = dim3(P.grid, P.mt);
+  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_operands_kernel, A) != cudaSuccess) return LRKV_ERR_CUDA;
+  cfg.gridDim = dim3(A.grid, A.groups);
   cfg.blockDim = dim3(lrkv::k8Threads);
-  cfg.dynamicSmemBytes = P.smem_bytes;
-  if (cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_kernel, P, M, A) != cudaSuccess)
-    return LRKV_ERR_CUDA;
-  return lrkv::decode_merge_launch(P, stream, true);
+  cfg.dynamicSmemBytes = A.smem_bytes;
+  return cudaLaunchKernelEx(&cfg, lrkv::lrkv_decode8_kernel, M, A) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple, Optional, Tuple
+from typing import Optional, Tuple
 
 import torch
 
@@ -982,24 +982,53 @@ BLOCK8 = 16  # rows that share a scale
 _E4M3 = torch.float8_e4m3fn
 
 
-class Cache8(NamedTuple):
+class Cache8:
     """A factored cache in 8 bits: k_s, v_s [lead, rows, d_h] and z_k, z_v [lead,
     rows, H, r] (float8_e4m3fn) with the scales of their blocks of BLOCK8 rows,
     [lead, ceil(rows / BLOCK8)] and [lead, ceil(rows / BLOCK8), H] fp32; lead x
     rows is batch x max_len, or pages x page_size of a paged cache.  Rank 0: the
-    z tensors are None."""
-    k_s: torch.Tensor
-    v_s: torch.Tensor
-    z_k: Optional[torch.Tensor]
-    z_v: Optional[torch.Tensor]
-    k_s_scale: torch.Tensor
-    v_s_scale: torch.Tensor
-    z_k_scale: Optional[torch.Tensor]
-    z_v_scale: Optional[torch.Tensor]
+    z tensors are None.  The tensors are checked once, here; they stay the
+    cache's as long as it is used."""
+
+    __slots__ = ("k_s", "v_s", "z_k", "z_v", "k_s_scale", "v_s_scale", "z_k_scale", "z_v_scale", "device", "shape",
+                 "ref")
+    NAMES = __slots__[:8]
+
+    def __init__(self, k_s, v_s, z_k, z_v, k_s_scale, v_s_scale, z_k_scale, z_v_scale):
+        given = (k_s, v_s, z_k, z_v, k_s_scale, v_s_scale, z_k_scale, z_v_scale)
+        latents = (z_k, z_v, z_k_scale, z_v_scale)
+        if any((t is None) != (z_k is None) for t in latents):
+            raise ValueError("the z tensors of an 8-bit cache are given together")
+        lead, rows, dh = k_s.shape
+        H, r = (z_k.shape[2], z_k.shape[3]) if z_k is not None else (0, 0)
+        blocks = (lead, -(-rows // BLOCK8))
+        row, z = (lead, rows, dh), (lead, rows, H, r)
+        shapes = (row, row, z, z, blocks, blocks, blocks + (H,), blocks + (H,))
+        self.device = k_s.get_device()
+        _check(self.device, *[("cache." + n, t, _E4M3 if i < 4 else _F32, s)
+                              for i, (n, t, s) in enumerate(zip(self.NAMES, given, shapes))])
+        for n, t in zip(self.NAMES, given):
+            object.__setattr__(self, n, t)
+        self.shape = (lead, rows, H, dh, r)
+        self.ref = ctypes.byref(lrkv_cache8(*[_ptr(t) for t in given]))
 
     def pools(self):
         """The tensors, for the pages_* calls (of a paged cache)."""
-        return [t for t in self if t is not None]
+        return [t for t in (getattr(self, n) for n in self.NAMES) if t is not None]
+
+    def rows(self, block_table, batch: int, heads: int, head_dim: int, rank: int, device: int):
+        """(max_len, page_size, num_pages) of a call with these sizes."""
+        lead, rows, H, dh, r = self.shape
+        if dh != head_dim or r != rank or (r and H != heads):
+            raise ValueError(f"the cache holds {H} heads of rank {r} and width {dh}, the call's are {heads}, {rank}, "
+                             f"{head_dim}")
+        if device != self.device:
+            raise ValueError(f"the cache is on device {self.device}, the call's first tensor on device {device}")
+        if block_table is None:
+            if lead != batch:
+                raise ValueError(f"the cache holds {lead} sequences, the call {batch}")
+            return rows, 0, 0
+        return block_table.shape[1] * rows, rows, lead
 
 
 def empty_cache8(lead: int, rows: int, heads: int, head_dim: int, rank: int, device="cuda") -> Cache8:
@@ -1015,24 +1044,6 @@ def empty_cache8(lead: int, rows: int, heads: int, head_dim: int, rank: int, dev
                   some(*zs, dtype=_F32) if z else None, some(*zs, dtype=_F32) if z else None)
 
 
-def _cache8_specs(cache: Cache8, lead: Tuple[int, int], H: int, dh: int, r: int):
-    """The shape checks of a cache's tensors, and whether its z tensors agree with r."""
-    blocks = (lead[0], -(-lead[1] // BLOCK8))
-    z = lead + (H, r)
-    if (cache.z_k is None) != (r == 0) or any((t is None) != (r == 0)
-                                              for t in (cache.z_v, cache.z_k_scale, cache.z_v_scale)):
-        raise ValueError("the z tensors of an 8-bit cache are given together, and only for a rank above 0")
-    return (("cache.k_s", cache.k_s, _E4M3, lead + (dh,)), ("cache.v_s", cache.v_s, _E4M3, lead + (dh,)),
-            ("cache.z_k", cache.z_k, _E4M3, z), ("cache.z_v", cache.z_v, _E4M3, z),
-            ("cache.k_s_scale", cache.k_s_scale, _F32, blocks), ("cache.v_s_scale", cache.v_s_scale, _F32, blocks),
-            ("cache.z_k_scale", cache.z_k_scale, _F32, blocks + (H,)),
-            ("cache.z_v_scale", cache.z_v_scale, _F32, blocks + (H,)))
-
-
-def _cache8_ref(cache: Cache8):
-    return ctypes.byref(lrkv_cache8(*[_ptr(t) for t in cache]))
-
-
 def quantize(k_s, v_s, z_k, z_v, start_pos, cache: Cache8, new_lens=None, block_table=None, ws=None, stream=None):
     """Stores rows k_s, v_s [B, n, d_h], z_k, z_v [B, n, H, r] (bf16 or fp32; as
     append() writes them into a cache of n rows) in an 8-bit cache at rows
@@ -1040,17 +1051,17 @@ def quantize(k_s, v_s, z_k, z_v, start_pos, cache: Cache8, new_lens=None, block_
     word is kept only in a `ws` of 16 zeroed bytes."""
     B, n, dh = k_s.shape
     H, r = (z_k.shape[2], z_k.shape[3]) if z_k is not None else (1, 0)
-    max_len, page_size, num_pages, lead = _cache_rows(cache.k_s, block_table, B)
-    dims = make_dims(B, H, dh, r, max_len, k_s.dtype)
     dt, dev = k_s.dtype, k_s.get_device()
+    max_len, page_size, num_pages = cache.rows(block_table, B, H, dh, r, dev)
+    dims = make_dims(B, H, dh, r, max_len, dt)
     _check(dev, ("k_s", k_s, dt, (B, n, dh)), ("v_s", v_s, dt, (B, n, dh)), ("z_k", z_k, dt, (B, n, H, r)),
            ("z_v", z_v, dt, (B, n, H, r)), ("start_pos", start_pos, _I32, (B,)), ("new_lens", new_lens, _I32, (B,)),
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
-           ("ws", ws, _U8, ws.shape if ws is not None else None), *_cache8_specs(cache, lead, H, dh, r))
+           ("ws", ws, _U8, ws.shape if ws is not None else None))
     with _On(k_s):
         st = int(load().lrkv_quantize(
             ctypes.byref(dims), n, _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(start_pos), _ptr(new_lens),
-            page_size, num_pages, _ptr(block_table), _cache8_ref(cache), _ptr(ws), 0 if ws is None else ws.numel(),
+            page_size, num_pages, _ptr(block_table), cache.ref, _ptr(ws), 0 if ws is None else ws.numel(),
             _stream_on(stream, dev)))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_quantize")
@@ -1064,13 +1075,13 @@ def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float
             stream=None):
     """decode over an 8-bit cache (paged with block_table).  Returns (out, lse, ws)."""
     B, H, dh = q.shape
-    r = cache.z_k.shape[-1] if cache.z_k is not None else 0
-    max_len, page_size, num_pages, lead = _cache_rows(cache.k_s, block_table, B)
-    dims = make_dims(B, H, dh, r, max_len, q.dtype, scale)
+    r = cache.shape[4]
     dt, dev, basis = q.dtype, q.get_device(), (H, dh, r)
-    _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k, dt, basis), ("b_v", b_v, dt, basis),
+    max_len, page_size, num_pages = cache.rows(block_table, B, H, dh, r, dev)
+    dims = make_dims(B, H, dh, r, max_len, dt, scale)
+    _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k if r else None, dt, basis), ("b_v", b_v if r else None, dt, basis),
            ("seq_lens", seq_lens, _I32, (B,)), ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
-           ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)), *_cache8_specs(cache, lead, H, dh, r))
+           ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
     with _On(q, stream) as on:
         if out is None:
             out = on.own(torch.empty((B, H, dh), dtype=torch.float32, device=q.device))
@@ -1080,7 +1091,7 @@ def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float
             ws = on.own(decode8_workspace(dims, q.device))
         _check(dev, ("ws", ws, _U8, (ws.numel(),)))
         st = int(load().lrkv_decode8(
-            ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), _cache8_ref(cache),
+            ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), cache.ref,
             _ptr(b_k) if r else None, _ptr(b_v) if r else None, _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws),
             ws.numel(), _stream_on(stream, dev)))
     if st != LRKV_OK:
