@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "decode_plan.h"
@@ -51,6 +52,7 @@ struct PagesArgs {
   int* ws_table;  // [B][nb]
   int* ws_a;      // [pages]
   int* ws_b;      // [pages]
+  int* ws_c;      // [pages]
   int4* copies;   // [min(pages, ...)]: from, to, rows
 };
 
@@ -109,14 +111,20 @@ __device__ __forceinline__ int clamp_len(const PagesArgs& A, int len, bool& bad)
 __device__ __forceinline__ int blocks_of(const PagesArgs& A, int len) {
   return (len >> A.shift) + ((len & ((1 << A.shift) - 1)) != 0);
 }
-// The status of the call: the bits of every CTA.
-__device__ __forceinline__ void write_status(cg::cluster_group& cl, const PagesArgs& A, bool bad, uint32_t more,
-                                             int* slot) {
-  const int any = __syncthreads_or(bad);
-  int total;
-  cluster_prefix(cl, any, slot, total);
-  if (cl.block_rank() == 0 && threadIdx.x == 0) *A.status = (total ? kDevBounds : 0u) | more;
-  cl.sync();  // (no CTA leaves while another reads its shared memory)
+// f(sequence, first block, blocks) for pieces of the tables' rows, a warp each.
+constexpr int kPgPiece = 256;
+template <typename F>
+__device__ __forceinline__ void for_rows(cg::cluster_group& cl, const PagesArgs& A, F f) {
+  const int pieces = (A.nb + kPgPiece - 1) / kPgPiece, all = A.B * pieces;
+  for (int u = cl.block_rank() * kPgWarps + (threadIdx.x >> 5); u < all; u += cl.num_blocks() * kPgWarps) {
+    const int b = u / pieces, j = (u - b * pieces) * kPgPiece;
+    f(b, j, min(kPgPiece, A.nb - j));
+  }
+}
+// The status word was cleared before a cluster barrier that every CTA has passed.
+__device__ __forceinline__ void add_status(const PagesArgs& A, bool bad, uint32_t more) {
+  if (__syncthreads_or(bad)) more |= kDevBounds;
+  if (threadIdx.x == 0 && more) atomicOr(A.status, more);
 }
 // A warp's contiguous share of the pages, a multiple of 32.
 __device__ __forceinline__ void page_share(cg::cluster_group& cl, const PagesArgs& A, int& lo, int& hi) {
@@ -131,64 +139,70 @@ __device__ __forceinline__ void page_share(cg::cluster_group& cl, const PagesArg
 
 // ===================================================================== fork
 __global__ void __launch_bounds__(kPgThreads) lrkv_pages_fork_kernel(const __grid_constant__ PagesArgs A) {
-  __shared__ int s_slot;
   cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
   const int at = cl.block_rank() * kPgThreads + threadIdx.x, step = cl.num_blocks() * kPgThreads;
   const bool in_place = A.table_out == A.table;
   bool bad = false;
+  if (at == 0) *A.status = 0u;
   if (A.refs_out != A.refs)
     for (int p = at; p < A.pages; p += step) A.refs_out[p] = A.refs[p];
-  // the new lengths, with the parent in the upper half
-  for (int b = at; b < A.B; b += step) {
-    const int parent = A.parent ? A.parent[b] : b;
+  // the length of sequence b after the call
+  auto length = [&](int b, int& parent) {
+    parent = A.parent ? A.parent[b] : b;
+    const int keep = A.keep ? A.keep[b] : INT_MAX;
     int len = 0;
     if (parent >= 0 && parent < A.B) len = clamp_len(A, A.lens[parent], bad);
     else if (parent != -1) bad = true;
-    if (A.keep) {
-      const int keep = A.keep[b];
-      if (keep < 0) bad = true;
-      len = min(len, max(keep, 0));
-    }
-    A.ws_lens[b] = len;
+    if (keep < 0) bad = true;
+    return min(len, max(keep, 0));
+  };
+  for (int b = at; b < A.B; b += step) {
+    int parent;
+    A.ws_lens[b] = length(b, parent);
   }
   cl.sync();
-  const long long entries = static_cast<long long>(A.B) * A.nb;
-  for (long long e = at; e < entries; e += step) {
-    const int b = static_cast<int>(e / A.nb), j = static_cast<int>(e - static_cast<long long>(b) * A.nb);
-    bool clamped = false;
-    const int used = blocks_of(A, clamp_len(A, A.lens[b], clamped)), want = blocks_of(A, A.ws_lens[b]);
-    bad = bad || clamped;
-    int before = -1, after = -1;
-    if (j < used) {
-      before = A.table[e];
-      if (before < 0 || before >= A.pages) { bad = true; before = -1; }
+  int32_t* to = in_place ? A.ws_table : A.table_out;
+  for_rows(cl, A, [&](int b, int j0, int n) {
+    int parent;
+    const int want = blocks_of(A, length(b, parent)), used = blocks_of(A, clamp_len(A, A.lens[b], bad));
+    const int32_t* mine = A.table + static_cast<long long>(b) * A.nb;
+    const int32_t* from = A.table + static_cast<long long>(max(parent, 0)) * A.nb;
+    int32_t* row = to + static_cast<long long>(b) * A.nb;
+    constexpr int kEach = kPgPiece / 32;
+    int before[kEach], after[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + lane + 32 * i;
+      before[i] = j < j0 + n && j < used ? mine[j] : -1;
+      after[i] = j < j0 + n && j < want ? from[j] : -1;
     }
-    if (j < want) {
-      after = A.table[static_cast<long long>(A.parent ? A.parent[b] : b) * A.nb + j];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + lane + 32 * i;
+      if (j >= j0 + n) continue;
+      row[j] = after[i];
+      const bool was = static_cast<unsigned>(before[i]) < static_cast<unsigned>(A.pages);
+      const bool is = static_cast<unsigned>(after[i]) < static_cast<unsigned>(A.pages);
+      if ((j < used && !was) || (j < want && !is)) bad = true;
+      if (before[i] == after[i]) continue;
+      if (was) atomicSub(&A.refs_out[before[i]], 1);
+      if (is) atomicAdd(&A.refs_out[after[i]], 1);
     }
-    (in_place ? A.ws_table : A.table_out)[e] = after;
-    if (after < 0 || after >= A.pages) {
-      if (j < want) bad = true;
-      after = -1;
-    }
-    if (before != after) {
-      if (before >= 0) atomicSub(&A.refs_out[before], 1);
-      if (after >= 0) atomicAdd(&A.refs_out[after], 1);
-    }
-  }
+  });
   cl.sync();
   if (in_place)
-    for (long long e = at; e < entries; e += step) A.table_out[e] = A.ws_table[e];
+    for (long long e = at; e < static_cast<long long>(A.B) * A.nb; e += step) A.table_out[e] = A.ws_table[e];
   for (int b = at; b < A.B; b += step) A.lens_out[b] = A.ws_lens[b];
-  write_status(cl, A, bad, 0u, &s_slot);
+  add_status(A, bad, 0u);
 }
 
 // =================================================================== extend
-// ws_a, ws_b: of a page that new rows begin inside of, how many sequences do so
-// and the last of them; then ws_a: the k-th free page.
+// ws_a, ws_b: of a shared page that new rows begin inside of, how many sequences
+// do so and the last of them; ws_c: the k-th free page.
 __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __grid_constant__ PagesArgs A) {
   extern __shared__ int s_dyn[];
-  __shared__ int s_warp[kPgWarps], s_free[kPgWarps], s_slots[2];
+  __shared__ int s_warp[kPgWarps], s_free[kPgWarps], s_slot;
   int* s_len = s_dyn;            // [B] lengths
   int* s_new = s_len + A.B;      // [B] lengths after the call
   int* s_page = s_new + A.B;     // [B] the begun page that is copied, or -1
@@ -199,32 +213,57 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
   const int rest = (1 << A.shift) - 1;
   pdl_trigger();  // (the copies wait for this grid)
   bool bad = false;
-  const long long entries = static_cast<long long>(A.B) * A.nb;
-  if (A.table_out != A.table)
-    for (long long e = at; e < entries; e += step) A.table_out[e] = A.table[e];
-  if (A.refs_out != A.refs)
-    for (int p = at; p < A.pages; p += step) A.refs_out[p] = A.refs[p];
-  // 1. lengths; the page that a sequence's new rows begin inside of
+  if (at == 0) *A.status = 0u;
+  // 1. lengths; the page that a sequence's new rows begin inside of, if others use it too (each CTA for itself)
+  int shared = 0;
   for (int b = tid; b < A.B; b += kPgThreads) {
     const int len = clamp_len(A, A.lens[b], bad), to = max(len, clamp_len(A, A.new_lens[b], bad));
     int page = -1;
     if (to > len && (len & rest) != 0) {
       page = A.table[static_cast<long long>(b) * A.nb + (len >> A.shift)];
-      if (page < 0 || page >= A.pages) { bad = true; page = -1; }
-      else { A.ws_a[page] = 0; A.ws_b[page] = -1; }
+      if (page < 0 || page >= A.pages) {
+        bad = true;
+        page = -1;
+      } else if (A.refs[page] > 1) {
+        A.ws_a[page] = 0;
+        A.ws_b[page] = -1;
+        shared = 1;
+      } else {
+        page = -1;
+      }
     }
     s_len[b] = len;
     s_new[b] = to;
     s_page[b] = page;
   }
-  cl.sync();
-  if (cl.block_rank() == 0)
-    for (int b = tid; b < A.B; b += kPgThreads)
-      if (s_page[b] >= 0) {
-        atomicAdd(&A.ws_a[s_page[b]], 1);
-        atomicMax(&A.ws_b[s_page[b]], b);
-      }
-  cl.sync();
+  // meanwhile: the free pages of each warp's share, and copies of what has outputs of its own
+  int lo, hi, mine = 0;
+  page_share(cl, A, lo, hi);
+#pragma unroll 4
+  for (int p = lo + lane; p < hi; p += 32) {
+    const int refs = A.refs[p];
+    mine += refs <= 0;
+    if (A.refs_out != A.refs) A.refs_out[p] = refs;
+  }
+  const long long entries = static_cast<long long>(A.B) * A.nb;
+  if (A.table_out != A.table)
+#pragma unroll 4
+    for (long long e = at; e < entries; e += step) A.table_out[e] = A.table[e];
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) s_free[warp] = mine;
+  shared = __syncthreads_or(shared);  // (the same in every CTA)
+  if (shared) {
+    cl.sync();
+    if (cl.block_rank() == 0)
+      for (int b = tid; b < A.B; b += kPgThreads)
+        if (s_page[b] >= 0) {
+          atomicAdd(&A.ws_a[s_page[b]], 1);
+          atomicMax(&A.ws_b[s_page[b]], b);
+        }
+  }
+  const int incl = warp_scan(lane < kPgWarps ? s_free[lane] : 0);
+  int free_pages;
+  const int before = cluster_prefix(cl, __shfl_sync(0xffffffffu, incl, kPgWarps - 1), &s_slot, free_pages);
   // 2. what every sequence takes (each CTA for itself); the pages copied, in order
   int total = 0, copied = 0;
   for (int b0 = 0; b0 < A.B; b0 += kPgThreads) {
@@ -234,8 +273,8 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
       const int page = s_page[b];
       need = blocks_of(A, s_new[b]) - blocks_of(A, s_len[b]);
       if (page >= 0) {
-        const int refs = A.refs[page];
-        copy = refs > 1 && !(refs == A.ws_a[page] && b == A.ws_b[page]);
+        // (of the users of a page that all write, the last one keeps it)
+        copy = !(A.refs[page] == __ldcg(A.ws_a + page) && b == __ldcg(A.ws_b + page));
         if (!copy) s_page[b] = -1;
       }
       need += copy;
@@ -248,43 +287,32 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
     total += sum;
     copied += sum_copies;
   }
-  // 3. the free pages in order
-  int lo, hi, mine = 0;
-  page_share(cl, A, lo, hi);
-  for (int p = lo + lane; p < hi; p += 32) mine += A.refs[p] <= 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  __syncthreads();
-  if (lane == 0) s_free[warp] = mine;
-  __syncthreads();
-  const int incl = warp_scan(lane < kPgWarps ? s_free[lane] : 0);
-  int free_pages;
-  const int before = cluster_prefix(cl, __shfl_sync(0xffffffffu, incl, kPgWarps - 1), &s_slots[0], free_pages);
+  // 3. the free pages in order, as many as are taken
   int rank = before + __shfl_sync(0xffffffffu, incl, warp) - s_free[warp];
   for (int p0 = lo; p0 < hi && rank < total; p0 += 32) {
     const bool is = p0 + lane < hi && A.refs[p0 + lane] <= 0;
     const unsigned m = __ballot_sync(0xffffffffu, is);
     const int k = rank + __popc(m & ((1u << lane) - 1u));
-    if (is && k < total) A.ws_a[k] = p0 + lane;
+    if (is && k < total) A.ws_c[k] = p0 + lane;
     rank += __popc(m);
   }
   cl.sync();
   // 4. hand them out, if there are enough
   const bool enough = total <= free_pages;
   if (enough) {
-    for (int k = at; k < total; k += step) A.refs_out[A.ws_a[k]] = 1;
+    for (int k = at; k < total; k += step) A.refs_out[__ldcg(A.ws_c + k)] = 1;
     for (int b = cl.block_rank() * kPgWarps + warp; b < A.B; b += cl.num_blocks() * kPgWarps) {
       const int copy = s_page[b] >= 0, have = blocks_of(A, s_len[b]), want = blocks_of(A, s_new[b]);
       int32_t* row = A.table_out + static_cast<long long>(b) * A.nb;
       if (copy && lane == 0) {
-        row[s_len[b] >> A.shift] = A.ws_a[s_first[b]];
+        row[s_len[b] >> A.shift] = __ldcg(A.ws_c + s_first[b]);
         atomicSub(&A.refs_out[s_page[b]], 1);
       }
-      for (int j = have + lane; j < want; j += 32) row[j] = A.ws_a[s_first[b] + copy + j - have];
+      for (int j = have + lane; j < want; j += 32) row[j] = __ldcg(A.ws_c + s_first[b] + copy + j - have);
       if (lane == 0) A.lens_out[b] = s_new[b];
     }
     if (cl.block_rank() == 0)
-      for (int k = tid; k < copied; k += kPgThreads) A.copies[k].y = A.ws_a[A.copies[k].y];
+      for (int k = tid; k < copied; k += kPgThreads) A.copies[k].y = __ldcg(A.ws_c + A.copies[k].y);
   } else {
     for (int b = at; b < A.B; b += step) A.lens_out[b] = A.lens[b];
   }
@@ -292,90 +320,98 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
     *A.count = enough ? copied : 0;
     if (A.missing) *A.missing = enough ? 0 : total - free_pages;
   }
-  write_status(cl, A, bad, enough ? 0u : kDevNoPages, &s_slots[1]);
+  add_status(A, bad, enough ? 0u : kDevNoPages);
 }
 
 // ================================================================== compact
-// ws_a: the k-th free page below the end, then every page's new number in ws_b.
+// ws_a: the k-th free page below the end; ws_b: every page's new number; ws_c:
+// the k-th used page.
 __global__ void __launch_bounds__(kPgThreads) lrkv_pages_compact_kernel(const __grid_constant__ PagesArgs A) {
-  __shared__ int s_live[kPgWarps], s_hole[kPgWarps], s_slots[4];
+  __shared__ int s_live[kPgWarps], s_slot;
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = cl.block_rank() * kPgThreads + tid, step = cl.num_blocks() * kPgThreads;
   pdl_trigger();  // (the copies wait for this grid)
   bool bad = false;
-  // 1. how many pages are in use
+  if (at == 0) *A.status = 0u;
+  // 1. how many pages are in use: they go to the pages before that number
   int lo, hi, mine = 0;
   page_share(cl, A, lo, hi);
+#pragma unroll 4
   for (int p = lo + lane; p < hi; p += 32) mine += A.refs[p] > 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) s_live[warp] = mine;
   __syncthreads();
-  int incl = warp_scan(lane < kPgWarps ? s_live[lane] : 0), live;
-  const int live_before = cluster_prefix(cl, __shfl_sync(0xffffffffu, incl, kPgWarps - 1), &s_slots[0], live);
-  // used pages before this warp's share; a page p before the end has p - that many free ones before it
-  int used = live_before + __shfl_sync(0xffffffffu, incl, warp) - s_live[warp];
-  // 2. used pages before the end, in all: how many at or past it move
-  int low = 0;
-  for (int p = lo + lane; p < min(hi, live); p += 32) low += A.refs[p] > 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) low += __shfl_xor_sync(0xffffffffu, low, o);
-  if (lane == 0) s_hole[warp] = low;
-  __syncthreads();
-  incl = warp_scan(lane < kPgWarps ? s_hole[lane] : 0);
-  int low_all;
-  cluster_prefix(cl, __shfl_sync(0xffffffffu, incl, kPgWarps - 1), &s_slots[1], low_all);
-  const int moves = live - low_all;
-  // 3. the k-th free page before the end, the k-th used one past it
+  const int incl = warp_scan(lane < kPgWarps ? s_live[lane] : 0);
+  int live;
+  const int before = cluster_prefix(cl, __shfl_sync(0xffffffffu, incl, kPgWarps - 1), &s_slot, live);
+  // 2. numbers of the used pages and of the free ones before the end: a page p there has p less the used ones
+  // before it.  (*count: used pages before the end, for the moment)
+  int used = before + __shfl_sync(0xffffffffu, incl, warp) - s_live[warp];
   for (int p0 = lo; p0 < hi; p0 += 32) {
     const int p = p0 + lane;
     const bool is = p < hi && A.refs[p] > 0;
     const unsigned m = __ballot_sync(0xffffffffu, is);
-    const int before = used + __popc(m & ((1u << lane) - 1u));
+    const int rank = used + __popc(m & ((1u << lane) - 1u));
     if (p < hi) {
-      if (p < live) {
-        if (!is) A.ws_a[p - before] = p;
-        A.ws_b[p] = is ? p : -1;
-      } else if (is) {
-        A.copies[before - low_all].x = p;
-      } else {
-        A.ws_b[p] = -1;
-      }
+      if (is) A.ws_c[rank] = p;
+      else if (p < live) A.ws_a[p - rank] = p;
+      A.ws_b[p] = is && p < live ? p : -1;
+      if (p == live) *A.count = rank;
     }
     used += __popc(m);
   }
+  if (at == 0 && live == A.pages) *A.count = live;
   cl.sync();
+  const int low = __ldcg(A.count), moves = live - low;
+  // 3. the k-th used page past the end into the k-th free one before it, with its references
   for (int k = at; k < moves; k += step) {
-    const int from = A.copies[k].x, to = A.ws_a[k];
+    const int from = __ldcg(A.ws_c + low + k), to = __ldcg(A.ws_a + k);
     A.copies[k] = make_int4(from, to, 1 << A.shift, 0);
     A.ws_b[from] = to;
+    A.refs_out[to] = A.refs[from];
   }
-  cl.sync();
-  // 4. references (each page's own before the end; a moved page's go with it), tables
-  for (int k = at; k < moves; k += step) A.refs_out[A.copies[k].y] = A.refs[A.copies[k].x];
   if (A.refs_out != A.refs)
-    for (int p = at; p < live; p += step)
-      if (A.ws_b[p] == p) A.refs_out[p] = A.refs[p];
-  if (A.moved)
-    for (int p = at; p < A.pages; p += step) A.moved[p] = A.ws_b[p];
-  const long long entries = static_cast<long long>(A.B) * A.nb;
-  for (long long e = at; e < entries; e += step) {
-    const int b = static_cast<int>(e / A.nb), j = static_cast<int>(e - static_cast<long long>(b) * A.nb);
-    int page = A.table[e];
-    if (j < blocks_of(A, clamp_len(A, A.lens[b], bad))) {
-      const int to = page >= 0 && page < A.pages ? A.ws_b[page] : -1;
-      if (to < 0) bad = true; else page = to;
+    for (int k = at; k < low; k += step) {
+      const int p = __ldcg(A.ws_c + k);
+      A.refs_out[p] = A.refs[p];
     }
-    A.table_out[e] = page;
-  }
-  cl.sync();  // every moved page's references are read
+  cl.sync();
+  // 4. nothing lies past the end any more; tables
   for (int p = live + at; p < A.pages; p += step) A.refs_out[p] = 0;
+  if (A.moved)
+    for (int p = at; p < A.pages; p += step) A.moved[p] = __ldcg(A.ws_b + p);
+  for_rows(cl, A, [&](int b, int j0, int n) {
+    const int in_use = blocks_of(A, clamp_len(A, A.lens[b], bad));
+    const int32_t* from = A.table + static_cast<long long>(b) * A.nb;
+    int32_t* row = A.table_out + static_cast<long long>(b) * A.nb;
+    constexpr int kEach = kPgPiece / 32;
+    int page[kEach], to[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + lane + 32 * i;
+      page[i] = j < j0 + n ? from[j] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + lane + 32 * i;
+      to[i] = j < j0 + n && j < in_use && static_cast<unsigned>(page[i]) < static_cast<unsigned>(A.pages)
+                  ? __ldcg(A.ws_b + page[i])
+                  : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + lane + 32 * i;
+      if (j >= j0 + n) continue;
+      if (j < in_use && to[i] < 0) bad = true;
+      row[j] = to[i] >= 0 ? to[i] : page[i];
+    }
+  });
   if (at == 0) {
     *A.count = moves;
     if (A.live) *A.live = live;
   }
-  write_status(cl, A, bad, 0u, &s_slots[2]);
+  add_status(A, bad, 0u);
 }
 
 // =================================================================== copies
@@ -432,9 +468,9 @@ lrkv_status pages_check(int batch, int max_blocks, int page_size, int num_pages)
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// status, count | ws_lens | ws_table | ws_a | ws_b | copies
+// status, count | ws_lens | ws_table | ws_a | ws_b | ws_c | copies
 size_t pages_bytes(int B, int nb, int pages) {
-  return 256 + up(4ull * B) + up(4ull * B * nb) + 2 * up(4ull * pages) +
+  return 256 + up(4ull * B) + up(4ull * B * nb) + 3 * up(4ull * pages) +
          up(sizeof(int4) * static_cast<size_t>(std::max(B, pages)));
 }
 
@@ -450,6 +486,8 @@ void pages_bind(PagesArgs& A, void* ws) {
   A.ws_a = reinterpret_cast<int*>(p);
   p += up(4ull * A.pages);
   A.ws_b = reinterpret_cast<int*>(p);
+  p += up(4ull * A.pages);
+  A.ws_c = reinterpret_cast<int*>(p);
   p += up(4ull * A.pages);
   A.copies = reinterpret_cast<int4*>(p);
 }
@@ -473,12 +511,13 @@ lrkv_status pages_args(PagesArgs& A, int batch, int max_blocks, int page_size, i
   return LRKV_OK;
 }
 
-// One CTA for small tables: the cluster's barriers cost more than its other CTAs save.
+// One CTA for the smallest tables, where its barriers are the cheapest.  (One against eight CTAs: 6.1 and 4.6 us for
+// 64 x 64 blocks, 59 and 12.4 us for 512 x 512.)
 template <typename K>
 lrkv_status pages_launch(K kern, const PagesArgs& A, size_t smem, cudaStream_t stream) {
   const long long work = static_cast<long long>(A.B) * A.nb + A.pages;
   int n = 1;
-  while (n < kPgMaxCluster && work > 8192ll * n) n *= 2;
+  while (n < kPgMaxCluster && work > 1024ll * n) n *= 2;
   if (smem > 48 * 1024 && ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
     return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[1];

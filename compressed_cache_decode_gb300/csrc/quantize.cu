@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "cache8.h"
 #include "decode_plan.h"
@@ -28,7 +29,10 @@ namespace lrkv {
 
 namespace {
 
-constexpr int kQzThreads = 512;
+constexpr int kQzThreads = 512;  // at most
+// Registers a thread: three CTAs of 224 threads an SM (32 heads of rank 48) keep more rows under way than two, and
+// four leave a thread too few for its 16 rows (96: 95 us, 80: 81, 72: 92 for 8 prompts of 4-8K rows).
+constexpr int kQzRegs = 80;
 
 struct QuantizeArgs {
   int n_new, max_len, H, d, r;
@@ -43,9 +47,14 @@ struct QuantizeArgs {
   uint32_t* status;                // or NULL
 };
 
-// V elements of a row, and the same as e4m3.
+// V elements of a row.  peak(): the largest bits of a magnitude, of any kind, or 0x7f800000 and up where one is
+// not finite; finite(): of the finite ones.
 template <typename T, int V>
 struct Vec;
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
 template <int V>
 struct Vec<__nv_bfloat16, V> {
   uint32_t w[V / 2];
@@ -61,6 +70,23 @@ struct Vec<__nv_bfloat16, V> {
     }
   }
   __device__ __forceinline__ float get(int i) const { return i & 1 ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]); }
+  // two magnitudes at a time: the bits of bf16 are ordered as integers
+  __device__ __forceinline__ void peak(uint32_t& m) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  }
+  static __device__ __forceinline__ uint32_t peak_of(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  // times a power of two: exact, but for what e4m3 has no bits for
+  __device__ __forceinline__ void scaled(float inv, float* y) const {
+    const __nv_bfloat162 by = __float2bfloat162_rn(inv);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), by);
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&p);
+      y[2 * i] = bf_lo(u);
+      y[2 * i + 1] = bf_hi(u);
+    }
+  }
 };
 template <int V>
 struct Vec<float, V> {
@@ -75,6 +101,15 @@ struct Vec<float, V> {
     }
   }
   __device__ __forceinline__ float get(int i) const { return f[i]; }
+  __device__ __forceinline__ void peak(uint32_t& m) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t peak_of(uint32_t m) { return m; }
+  __device__ __forceinline__ void scaled(float inv, float* y) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = f[i] * inv;
+  }
 };
 template <int V>
 __device__ __forceinline__ void store8(unsigned char* p, const float* x) {
@@ -99,7 +134,7 @@ __device__ __forceinline__ float scale_for(uint32_t amax) {
 
 // grid (blocks a sequence's rows can touch, sequences, halves x slabs of heads)
 template <typename T, int V>
-__global__ void __launch_bounds__(kQzThreads) lrkv_quantize_kernel(const __grid_constant__ QuantizeArgs A) {
+__global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant__ QuantizeArgs A) {
   extern __shared__ uint32_t s_amax[];  // the shared row, then the slab's heads
   const int b = blockIdx.y, tid = threadIdx.x, half = blockIdx.z & 1, slab = blockIdx.z >> 1;
   const long long start = A.start_pos[b];
@@ -150,15 +185,19 @@ __global__ void __launch_bounds__(kQzThreads) lrkv_quantize_kernel(const __grid_
   const size_t at = latent ? blk * A.H + h0 + head : blk;
   const float before = mine && lo > 0 ? scale[at] : 0.f;
   if (mine) {
+    uint32_t m = 0u;
 #pragma unroll
     for (int i = 0; i < kBlock8; ++i)
-      if (i >= lo && i < hi) {
+      if (i >= lo && i < hi) x[i].peak(m);
+    top = Vec<T, V>::peak_of(m);
+    if (top >= 0x7f800000u) {  // infinities and NaN do not count
+      top = 0u;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const uint32_t u = __float_as_uint(x[i].get(k)) & 0x7fffffffu;
-          if (u < 0x7f800000u) top = max(top, u);  // (infinities and NaN do not count)
-        }
-      }
+      for (int i = 0; i < kBlock8; ++i)
+        if (i >= lo && i < hi)
+#pragma unroll
+          for (int k = 0; k < V; ++k) top = max(top, finite_bits(x[i].get(k)));
+    }
   }
   __syncthreads();
   if (mine && top) atomicMax(&s_amax[item], top);
@@ -167,17 +206,24 @@ __global__ void __launch_bounds__(kQzThreads) lrkv_quantize_kernel(const __grid_
   const float s = fmaxf(before, scale_for(s_amax[item]));
   if (owner) scale[at] = s;
   unsigned char* dst = A.cache[which] + row0 * width + col;
-  // x / s; the same as x * (1 / s) where s is a power of two
-  const bool power = (__float_as_uint(s) & 0x7fffffu) == 0u;
   const float inv = 1.f / s;
+  const auto put = [&](auto divide) {
 #pragma unroll
-  for (int i = 0; i < kBlock8; ++i)
-    if (i >= lo && i < hi) {
-      float y[V];
+    for (int i = 0; i < kBlock8; ++i)
+      if (i >= lo && i < hi) {
+        float y[V];
+        if (decltype(divide)::value) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = power ? x[i].get(k) * inv : x[i].get(k) / s;
-      store8<V>(dst + static_cast<size_t>(i) * width, y);
-    }
+          for (int k = 0; k < V; ++k) y[k] = x[i].get(k) / s;
+        } else {
+          x[i].scaled(inv, y);
+        }
+        store8<V>(dst + static_cast<size_t>(i) * width, y);
+      }
+  };
+  // x / s is x * (1 / s) where s is a power of two, as all scales but a caller's own are
+  if ((__float_as_uint(s) & 0x7fffffu) == 0u) put(std::false_type{});
+  else put(std::true_type{});
   if (lo > 0 && s > before) {  // the earlier rows, to the larger scale
     const float ratio = before / s;
     for (int i = 0; i < lo; ++i) {

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -101,10 +102,6 @@ class lrkv_mla_dims(ctypes.Structure):
 class lrkv_cache8(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("k_s", "v_s", "z_k", "z_v", "k_s_scale", "v_s_scale",
                                                      "z_k_scale", "z_v_scale")]
-
-
-class lrkv_pool(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int), ("bytes", ctypes.c_int)]
 
 
 class LRKVError(RuntimeError):
@@ -204,7 +201,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lrkv_decode_rope_axes.restype = ctypes.c_int
     lib.lrkv_decode_rope_axes.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, ci, i32p, ci, ip, i32p, cf, vp,
                                           vp, vp, vp, vp, sz, vp]
-    c8p, plp = ctypes.POINTER(lrkv_cache8), ctypes.POINTER(lrkv_pool)
+    c8p, plp = ctypes.POINTER(lrkv_cache8), ctypes.c_char_p  # (an array of lrkv_pool, packed)
     lib.lrkv_quantize.restype = ctypes.c_int
     lib.lrkv_quantize.argtypes = [dims_p, ci, vp, vp, vp, vp, i32p, i32p, ci, ci, i32p, c8p, vp, sz, vp]
     lib.lrkv_decode8_workspace_size.restype = ctypes.c_int
@@ -1106,17 +1103,18 @@ def pages_workspace(batch: int, max_blocks: int, num_pages: int, device="cuda") 
                        dtype=torch.uint8, device=device)
 
 
-def _pools(pools, page_size: int, num_pages: int, device: int):
+def _pools(pools, page_size: int, num_pages: int, device: int) -> bytes:
     """The C array of pools [num_pages, pieces, ...]: a piece for every page_size / pieces rows."""
-    got = (lrkv_pool * max(1, len(pools)))()
+    flat = []
     for i, t in enumerate(pools):
-        if t.dim() < 2 or t.shape[0] != num_pages or t.shape[1] < 1 or page_size % t.shape[1]:
+        shape = t.shape
+        if len(shape) < 2 or shape[0] != num_pages or shape[1] < 1 or page_size % shape[1]:
             raise ValueError(f"pool {i} must have {num_pages} pages and a piece for every so many of a page's "
-                             f"{page_size} rows, not shape {tuple(t.shape)}")
+                             f"{page_size} rows, not shape {tuple(shape)}")
         if not t.is_contiguous() or t.get_device() != device:
             raise ValueError(f"pool {i} must be contiguous, on the call's device")
-        got[i] = lrkv_pool(t.data_ptr(), page_size // t.shape[1], t.stride(1) * t.element_size())
-    return got
+        flat += (t.data_ptr(), page_size // shape[1], t.stride(1) * t.element_size())
+    return struct.pack("Pii" * len(pools), *flat)
 
 
 def _pages_call(name: str, block_table, seq_lens, refs, page_size: int, outs, more, ws, stream, call):
