@@ -161,11 +161,13 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ void bar_named(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// Waits for a phase unless the CTA has given up, and gives up itself at the bound.
+// Waits for a phase unless the CTA has given up, and gives up itself at the bound.  (A try may last as long as the
+// hardware likes, a few microseconds: bounds below that are polled.)
 __device__ __forceinline__ bool wait8(uint64_t* bar, uint32_t parity, volatile int* fail, long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return limit > 100000 ? mbar_try_wait(bar, parity) : mbar_test(bar, parity); };
+  if (done()) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!done()) {
     if (*fail) return false;
     if (clock64() - t0 > limit) {
       *fail = 1;
@@ -958,57 +960,56 @@ __global__ void __launch_bounds__(k8Threads, 1)
           if (e0 + tid + j * k8Threads < heads * W) s_o[e0 + tid + j * k8Threads] = x[j];
       }
       __syncthreads();
-      float* s_p = s_o + k8Heads * W;  // [heads d][parts]
-      if (row0 < rows_at_once && parts > 0) {
-        const __nv_bfloat16* bv = static_cast<const __nv_bfloat16*>(A.b_v) + static_cast<size_t>(h0) * d * r + part * vec;
-        for (int t0 = row0; t0 < d; t0 += 2 * rows_at_once)
-          for (int k0 = 0; k0 < heads; k0 += 4) {  // two rows of four heads under way
-            uint4 u[4][2];
+      float* s_p = s_o + k8Heads * W;  // [4 d][parts]
+      float* out = A.out + (static_cast<size_t>(b) * H + h0) * d;
+      const __nv_bfloat16* bv = static_cast<const __nv_bfloat16*>(A.b_v) + static_cast<size_t>(h0) * d * r + part * vec;
+      for (int k0 = 0; k0 < heads; k0 += 4) {
+        for (int t0 = row0; row0 < rows_at_once && parts > 0 && t0 < d; t0 += 2 * rows_at_once) {
+          uint4 u[4][2];  // two rows of four heads under way
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int t = t0 + i * rows_at_once;
-                const __nv_bfloat16* at = bv + (static_cast<size_t>(k0 + k) * d + t) * r;
-                u[k][i] = make_uint4(0u, 0u, 0u, 0u);
-                if (k0 + k >= heads || t >= d) continue;
-                if (vec == 8) {
-                  u[k][i] = __ldg(reinterpret_cast<const uint4*>(at));
-                } else if (vec == 4) {
-                  const uint2 y = __ldg(reinterpret_cast<const uint2*>(at));
-                  u[k][i].x = y.x;
-                  u[k][i].y = y.y;
-                } else {
-                  u[k][i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
-                }
-              }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k0 + k >= heads) break;
-              float z[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) z[q] = q < vec ? s_o[(k0 + k) * W + d + part * vec + q] : 0.f;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint4 y = u[k][i];
-                float x = fmaf(bf_hi(y.x), z[1], bf_lo(y.x) * z[0]);
-                x = fmaf(bf_hi(y.y), z[3], fmaf(bf_lo(y.y), z[2], x));
-                x = fmaf(bf_hi(y.z), z[5], fmaf(bf_lo(y.z), z[4], x));
-                x = fmaf(bf_hi(y.w), z[7], fmaf(bf_lo(y.w), z[6], x));
-                if (t0 + i * rows_at_once < d) s_p[((k0 + k) * d + t0 + i * rows_at_once) * parts + part] = x;
+            for (int i = 0; i < 2; ++i) {
+              const int t = t0 + i * rows_at_once;
+              const __nv_bfloat16* at = bv + (static_cast<size_t>(k0 + k) * d + t) * r;
+              u[k][i] = make_uint4(0u, 0u, 0u, 0u);
+              if (k0 + k >= heads || t >= d) continue;
+              if (vec == 8) {
+                u[k][i] = __ldg(reinterpret_cast<const uint4*>(at));
+              } else if (vec == 4) {
+                const uint2 y = __ldg(reinterpret_cast<const uint2*>(at));
+                u[k][i].x = y.x;
+                u[k][i].y = y.y;
+              } else {
+                u[k][i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
               }
             }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k0 + k >= heads) break;
+            float z[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) z[q] = q < vec ? s_o[(k0 + k) * W + d + part * vec + q] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 y = u[k][i];
+              float x = fmaf(bf_hi(y.x), z[1], bf_lo(y.x) * z[0]);
+              x = fmaf(bf_hi(y.y), z[3], fmaf(bf_lo(y.y), z[2], x));
+              x = fmaf(bf_hi(y.z), z[5], fmaf(bf_lo(y.z), z[4], x));
+              x = fmaf(bf_hi(y.w), z[7], fmaf(bf_lo(y.w), z[6], x));
+              if (t0 + i * rows_at_once < d) s_p[(k * d + t0 + i * rows_at_once) * parts + part] = x;
+            }
           }
+        }
+        __syncthreads();
+        for (int e = tid; e < min(4, heads - k0) * d; e += k8Threads) {
+          const int k = e / d;
+          float x = s_o[(k0 + k) * W + e - k * d];
+          for (int i = 0; i < parts; ++i) x += s_p[e * parts + i];
+          out[k0 * d + e] = x;
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      float* out = A.out + (static_cast<size_t>(b) * H + h0) * d;
-      for (int e = tid; e < heads * d; e += k8Threads) {
-        const int k = e / d;
-        float x = s_o[k * W + e - k * d];
-        for (int i = 0; i < parts; ++i) x += s_p[e * parts + i];
-        out[e] = x;
-      }
-      __syncthreads();  // (the sums are free)
     }
     __syncthreads();
   }
@@ -1049,7 +1050,7 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* byte
   A.groups = (A.H + k8Heads - 1) / k8Heads;
   A.nd = (A.dh + 127) / 128;
   A.nz = (std::min(A.H, k8Heads) * A.r + 127) / 128;
-  A.grid = std::max(1, num_sms / A.groups);
+  A.grid = std::min(std::max(1, num_sms / A.groups), 1024);  // (the join keeps a weight per piece in shared memory)
   A.img_bytes = A.nd * k8NQ * 128 + A.nz * k8N * 128 + 128;
   A.img_pad = round_up(A.img_bytes, 1024);
   int off = round_up((A.B + 1) * 4, 1024);
@@ -1063,7 +1064,7 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* byte
   A.slots[1] = slots - A.slots[0];
   A.smem_bytes = off + slots * k8Box + 1024;
   // the join's weights, sums and products lie over the operands, the probabilities and the ring
-  const long long join = 8ll * k8Threads + 4ll * k8Heads * (A.grid + A.dh + A.r + static_cast<long long>(A.dh) * (A.r / 2));
+  const long long join = 8ll * k8Threads + 4ll * k8Heads * (A.grid + A.dh + A.r) + 16ll * A.dh * (A.r / 2);
   if (join > off + slots * k8Box - A.off_img) return LRKV_ERR_UNSUPPORTED;
   *bytes = decode8_bind(A, nullptr);
   return LRKV_OK;

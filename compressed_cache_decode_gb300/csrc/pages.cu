@@ -45,6 +45,7 @@ struct PagesArgs {
   const int32_t* new_lens;             // extend
   int32_t* missing;                    // extend, or NULL
   int32_t *moved, *live;               // compact, or NULL
+  int copies_follow;                   // 1: the next launch is lrkv_pages_copy_kernel
   // workspace: the status word, how many pages to copy, and arrays
   uint32_t* status;
   int* count;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = cl.block_rank() * kPgThreads + tid, step = cl.num_blocks() * kPgThreads;
   const int rest = (1 << A.shift) - 1;
-  pdl_trigger();  // (the copies wait for this grid)
+  if (A.copies_follow) pdl_trigger();  // (they wait for this grid; any other launch starts when it has ended)
   bool bad = false;
   if (at == 0) *A.status = 0u;
   // 1. lengths; the page that a sequence's new rows begin inside of, if others use it too (each CTA for itself)
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_compact_kernel(const __
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = cl.block_rank() * kPgThreads + tid, step = cl.num_blocks() * kPgThreads;
-  pdl_trigger();  // (the copies wait for this grid)
+  if (A.copies_follow) pdl_trigger();  // (they wait for this grid; any other launch starts when it has ended)
   bool bad = false;
   if (at == 0) *A.status = 0u;
   // 1. how many pages are in use: they go to the pages before that number
@@ -534,7 +535,7 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kern, A) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
 }
 
-lrkv_status copy_args(CopyArgs& C, const PagesArgs& A, const lrkv_pool* pools, int n) {
+lrkv_status copy_args(CopyArgs& C, PagesArgs& A, const lrkv_pool* pools, int n) {
   if (n < 0 || n > LRKV_MAX_POOLS || (n > 0 && !pools)) return LRKV_ERR_INVALID_ARG;
   C = CopyArgs{};
   C.n = n;
@@ -555,6 +556,7 @@ lrkv_status copy_args(CopyArgs& C, const PagesArgs& A, const lrkv_pool* pools, i
     if (segments > (1 << 30)) return LRKV_ERR_UNSUPPORTED;
   }
   C.segments = static_cast<int>(segments);
+  A.copies_follow = n > 0;
   C.count = A.count;
   C.copies = A.copies;
   return LRKV_OK;

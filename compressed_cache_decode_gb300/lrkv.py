@@ -1108,12 +1108,13 @@ def _pools(pools, page_size: int, num_pages: int, device: int) -> bytes:
     flat = []
     for i, t in enumerate(pools):
         shape = t.shape
-        if len(shape) < 2 or shape[0] != num_pages or shape[1] < 1 or page_size % shape[1]:
+        pieces = shape[1] if len(shape) > 1 and shape[0] == num_pages else 0
+        if pieces < 1 or page_size % pieces:
             raise ValueError(f"pool {i} must have {num_pages} pages and a piece for every so many of a page's "
                              f"{page_size} rows, not shape {tuple(shape)}")
         if not t.is_contiguous() or t.get_device() != device:
             raise ValueError(f"pool {i} must be contiguous, on the call's device")
-        flat += (t.data_ptr(), page_size // shape[1], t.stride(1) * t.element_size())
+        flat += (t.data_ptr(), page_size // pieces, t.nbytes // (num_pages * pieces))
     return struct.pack("Pii" * len(pools), *flat)
 
 

@@ -689,3 +689,144 @@ def evict_reference(weights, length: int, budget: int, sink: int = 0, recent: in
     source = [j if j in keep else None for j in range(n)]
     movers = iter(sorted(j for j in keep if j >= n))
     return np.array([next(movers) if j is None else j for j in source], dtype=np.int64)
+
+
+# ------------------------------------------------------------------ 8 bits --
+# The factored cache in 8 bits and the pages of a paged cache.  The pages have
+# no counterpart; the readings are those of include/lrkv.h.
+
+BLOCK8 = 16
+
+
+def e4m3_round(x) -> np.ndarray:
+    """The e4m3 number nearest to each x, ties to even, magnitudes past 448 to
+    448 (infinities too), NaN to NaN."""
+    x = _f64(x)
+    out = np.empty_like(x)
+    with np.errstate(invalid="ignore"):
+        mag = np.minimum(np.abs(x), 448.0)
+        e = np.frexp(np.maximum(mag, 2.0 ** -6))[1] - 1       # 2^e <= mag < 2^(e+1), the smallest normal 2^-6
+        step = np.ldexp(1.0, e - 3)
+        out[...] = np.sign(x) * np.rint(mag / step) * step
+    out[np.isnan(x)] = np.nan
+    return out
+
+
+def scale_for(amax: float) -> float:
+    """The smallest power of two s, 2^-126 at least, with amax <= 448 s."""
+    s = 2.0 ** -126
+    while amax > 448.0 * s:
+        s *= 2.0
+    return s
+
+
+def quantize_reference(values, scales, rows, start: int, n: int):
+    """(values, scales) of a sequence's 8-bit tensor after rows [n_new, heads,
+    width] are stored at start .. start + n - 1: values [max_len, heads, width]
+    (the e4m3 numbers), scales [blocks, heads] before the call."""
+    values, scales, rows = _f64(values).copy(), _f64(scales).copy(), _f64(rows)
+    end = start + n
+    for block in range(start // BLOCK8, -(-end // BLOCK8) if n > 0 else 0):
+        first = block * BLOCK8
+        lo, hi = max(start, first), min(end, first + BLOCK8)
+        for h in range(values.shape[1]):
+            new = rows[lo - start:hi - start, h]
+            finite = np.abs(new[np.isfinite(new)])
+            s = scale_for(float(finite.max()) if finite.size else 0.0)
+            if lo > first:
+                old = float(scales[block, h])
+                if old > s:
+                    s = old
+                elif s > old:
+                    values[first:lo, h] = e4m3_round(values[first:lo, h] * (old / s))
+            values[lo:hi, h] = e4m3_round(new / s)
+            scales[block, h] = s
+    return values, scales
+
+
+def cache8_rows(values, scales) -> np.ndarray:
+    """What the 8-bit tensor of a sequence stands for: values [rows, heads, width]
+    times the scale of each row's block."""
+    return _f64(values) * np.repeat(_f64(scales), BLOCK8, axis=0)[: len(values)][:, :, None]
+
+
+# ------------------------------------------------------------------- pages --
+
+def _used(length: int, page_size: int) -> int:
+    return -(-int(length) // page_size)
+
+
+def pages_fork_reference(table, lens, refs, page_size: int, parent, keep):
+    """(table, lens, refs) after sequence b became the first keep[b] rows of
+    parent[b]: one entry after another, on what was there before."""
+    table, lens, refs = np.array(table), np.array(lens), np.array(refs)
+    new_table, new_lens, new_refs = np.full_like(table, -1), np.zeros_like(lens), refs.copy()
+    for b in range(len(lens)):
+        for j in range(_used(lens[b], page_size)):
+            if 0 <= table[b, j] < len(refs):
+                new_refs[table[b, j]] -= 1
+    for b in range(len(lens)):
+        p = b if parent is None else int(parent[b])
+        if not 0 <= p < len(lens):
+            continue
+        new_lens[b] = lens[p] if keep is None else min(lens[p], max(0, int(keep[b])))
+        for j in range(_used(new_lens[b], page_size)):
+            new_table[b, j] = table[p, j]
+            if 0 <= table[p, j] < len(refs):
+                new_refs[table[p, j]] += 1
+    return new_table, new_lens, new_refs
+
+
+def pages_extend_reference(table, lens, refs, page_size: int, new_lens):
+    """(table, lens, refs, copies, missing): copies lists (from, to, rows)."""
+    table, lens, refs = np.array(table), np.array(lens), np.array(refs)
+    out_table, out_lens, out_refs = table.copy(), lens.copy(), refs.copy()
+    free = [p for p in range(len(refs)) if refs[p] <= 0]
+    writers = {}
+    for b, length in enumerate(lens):
+        if new_lens[b] > length and length % page_size:
+            writers.setdefault(int(table[b, length // page_size]), []).append(b)
+    taken, copies = 0, []
+
+    def take():
+        nonlocal taken
+        taken += 1
+        return free[taken - 1] if taken <= len(free) else -1
+
+    for b, length in enumerate(lens):
+        length, to = int(length), max(int(lens[b]), int(new_lens[b]))
+        if to > length and length % page_size:
+            j = length // page_size
+            p = int(table[b, j])
+            if 0 <= p < len(refs) and refs[p] > 1 and not (refs[p] == len(writers[p]) and writers[p][-1] == b):
+                out_table[b, j] = take()
+                copies.append((p, int(out_table[b, j]), length % page_size))
+                out_refs[p] -= 1
+        for j in range(_used(length, page_size), _used(to, page_size)):
+            out_table[b, j] = take()
+        out_lens[b] = to
+    if taken > len(free):
+        return table, lens, refs, [], taken - len(free)
+    out_refs[free[:taken]] = 1
+    return out_table, out_lens, out_refs, copies, 0
+
+
+def pages_compact_reference(table, lens, refs, page_size: int):
+    """(table, refs, moved, live, copies)."""
+    table, lens, refs = np.array(table), np.array(lens), np.array(refs)
+    live = int((refs > 0).sum())
+    holes = iter([p for p in range(live) if refs[p] <= 0])
+    moved, copies = np.full_like(refs, -1), []
+    for p in range(len(refs)):
+        if refs[p] > 0:
+            moved[p] = p if p < live else next(holes)
+            if moved[p] != p:
+                copies.append((p, int(moved[p])))
+    out_refs = np.zeros_like(refs)
+    out_refs[moved[refs > 0]] = refs[refs > 0]
+    out_table = table.copy()
+    for b, length in enumerate(lens):
+        for j in range(_used(length, page_size)):
+            if 0 <= table[b, j] < len(refs) and moved[table[b, j]] >= 0:
+                out_table[b, j] = moved[table[b, j]]
+    return out_table, out_refs, moved, live, copies
