@@ -82,6 +82,8 @@ struct Args8 {
   int off_img, off_p, off_ring, smem_bytes;
   int blocks;           // scale blocks of a sequence (contiguous) or page
   int grid;             // range CTAs of a group
+  // the join: columns of b_v a copy takes (its alignment), heads lifted at once (shared memory), bytes of a row there
+  int vec, lift, pitch;
   const int32_t* block_table;  // [B][max_blocks] or NULL (contiguous)
   int max_blocks, page_shift, num_pages;
   const void *q, *b_k, *b_v;
@@ -352,11 +354,13 @@ __global__ void __launch_bounds__(k8Threads, 1)
     lrkv_decode8_kernel(const __grid_constant__ Maps8 M, const __grid_constant__ Args8 A) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   // full/empty: ring slots; ifull/iempty: operands; sfull/sempty: scores; pfull: probabilities; pv: their
-  // products done (and the probabilities' buffer free); oempty: a chunk's products read; mdone: every MMA done
+  // products done (and the probabilities' buffer free); oempty: a chunk's products read; mdone: every MMA done;
+  // mlfirst: the first piece's maxima and denominators written
   __shared__ uint64_t full[k8MaxSlots], empty[k8MaxSlots], ifull[2], iempty[2], sfull[2], sempty[2], pfull[2], pv[2],
-      oempty[k8MaxD + k8MaxZ], mdone;
+      oempty[k8MaxD + k8MaxZ], mdone, mlfirst;
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad, s_images, s_copies[2];  // copies issued
+  __shared__ int s_first[2], s_last[3];  // a shared sequence's first CTA and pieces (0: another CTA joins them)
   __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
   __shared__ float s_fac[4][20];                      // [tile % 4]: alpha[8], latent scale[8], shared scale
   __shared__ float s_sum[2][4][4];
@@ -383,7 +387,9 @@ __global__ void __launch_bounds__(k8Threads, 1)
     }
     for (int i = 0; i < k8MaxD + k8MaxZ; ++i) mbar_init(&oempty[i], k8Values);
     mbar_init(&mdone, 2);
+    mbar_init(&mlfirst, 2);
     s_fail = s_bad = s_images = s_copies[0] = s_copies[1] = 0;
+    s_first[1] = s_last[2] = 0;
     fence_barrier_init();
   }
   if (warp == 13) tmem_alloc(&tmem_base, k8Cols);
@@ -422,6 +428,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
   const bool work = N > 0 && c < G;
   const int g0 = work ? static_cast<int>(static_cast<long long>(c) * N / G) : 0;
   const int g1 = work ? static_cast<int>(static_cast<long long>(c + 1) * N / G) : 0;
+  auto cta_of = [&](int tile) -> int {  // (N G < 2^32 but for absurd CTA counts)
+    if (static_cast<unsigned long long>(N) * G >> 32) return cta_of_token(tile, N, G);
+    return static_cast<int>(((tile + 1u) * G - 1u) / static_cast<uint32_t>(N));
+  };
   auto rows_of = [&](int b) { return min(max(__ldg(A.seq_lens + b), 0), A.max_len); };
 
   TileWalk w;
@@ -596,7 +606,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
           float* pml = A.part_ml + (static_cast<size_t>(w.b + c) * H + hb + lane) * 2;
           pml[0] = lane == 0 ? m[0] : lane == 1 ? m[1] : lane == 2 ? m[2] : m[3];
           pml[1] = (s_sum[half][0][lane] + s_sum[half][1][lane]) + (s_sum[half][2][lane] + s_sum[half][3][lane]);
+          if (piece == 0) __threadfence();
         }
+        __syncwarp();
+        if (piece == 0 && quad == 0 && lane == 0) mbar_arrive_cta(&mlfirst);
         bar_named(1 + half, 128);
       }
       w = nx;
@@ -687,6 +700,19 @@ __global__ void __launch_bounds__(k8Threads, 1)
         for (int j = 0; j < k8MaxZ; ++j)
           if (j < nz && head[j] < heads)
             out[static_cast<size_t>(head[j]) * (d + r) + d + 128 * j + col - head[j] * r] = oz[j];
+        if (nmore && pre[w.b] < g0) {  // the first of several: this CTA is done with it
+          __threadfence();
+          bar_named(5, 32 * k8Values);
+          if (warp == k8Softmax && lane == 0) {
+            wait8(&mlfirst, 0u, fail, A.wait_limit);
+            __threadfence();
+            const int c0 = cta_of(pre[w.b]), n = c - c0 + 1;
+            s_first[0] = c0;
+            s_first[1] = atomicAdd(&A.arrived[w.b * A.groups + group], 1) == n - 1 ? n : 0;
+            __threadfence();
+          }
+          __syncwarp();
+        }
       }
       w = nx;
       more = nmore;
@@ -845,173 +871,183 @@ __global__ void __launch_bounds__(k8Threads, 1)
     if (leader) tc_commit(&mdone);
   }
 
-  // ---- every copy and MMA this CTA issued is complete before it goes on (a pass that did not
-  // give up has waited for every copy) -------------------------------------------------------
+  // ---- the end.  A sequence's pieces are joined by the last CTA done with one of them: in their
+  // order, with the latents' sum lifted through B_h^V.  A CTA has said so already of its first
+  // sequence if that one ends inside its range (above), says so now of its last one, and joins
+  // alone what lies between.  The group's B_h^V, the same for all of them, is on its way to shared
+  // memory before it is known who joins ------------------------------------------------------
   pdl_wait();
-  __threadfence();  // the pieces' results, for the CTA that joins them
-  __syncthreads();
-  if (tid == 0) {
-    bool done = true;
-    if (*fail) {
-      for (int v = 0, s0 = 0; v < 2; s0 += A.slots[v], ++v)
-        for (int i = max(0, s_copies[v] - A.slots[v]); i < s_copies[v]; ++i)
-          done = mbar_wait_bounded(&full[s0 + i % A.slots[v]], static_cast<uint32_t>(i / A.slots[v]) & 1u) && done;
-      for (int i = max(0, s_images - 2); i < s_images; ++i)
-        done = mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u) && done;
-    }
-    if (work) done = mbar_wait_bounded(&mdone, 0u) && done;
-    if (!done) *fail = 1;
-    const uint32_t bits = (bad || s_bad ? kDevBounds : 0u) | (*fail ? kDevTimeout : 0u);
-    if (bits) record_status(A.status, bits);
-  }
+  if (warp < k8Softmax + k8Values) __threadfence();  // the last piece's results, for the CTA that joins it
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 13) tmem_dealloc(tmem, k8Cols);
-
-  // ---- the sequences of this CTA's range: the last CTA done with one joins its pieces, in
-  // their order, lifts the latents' sum through B_h^V and writes the outputs.  The loads do not
-  // wait for one another: pieces and rows of B_h^V are under way before the weights are known --
   const int W = A.dh + r, d = A.dh;
-  int* s_c0 = reinterpret_cast<int*>(smem + A.off_img);        // a sequence's first CTA
-  int* s_n = s_c0 + k8Threads;                                 // its pieces, 0: another CTA joins them
-  float* s_w = reinterpret_cast<float*>(s_n + k8Threads);      // [8][pieces] weights, then [8][W] sums
-  auto cta_of = [&](int tile) -> int {  // (N G < 2^32 but for absurd CTA counts)
-    if (static_cast<unsigned long long>(N) * G >> 32) return cta_of_token(tile, N, G);
-    return static_cast<int>(((tile + 1u) * G - 1u) / static_cast<uint32_t>(N));
-  };
-  // the lift reads B_h^V front to back, 8 or 4 columns a thread, and adds a row's parts up
-  const uintptr_t bva = reinterpret_cast<uintptr_t>(A.b_v);
-  const int vec = r % 8 == 0 && bva % 16 == 0 ? 8 : r % 4 == 0 && bva % 8 == 0 ? 4 : 2, parts = r / vec;
-  const int rows_at_once = parts > 0 ? k8Threads / parts : k8Threads;
-  const int part = parts > 0 ? tid % parts : 0, row0 = parts > 0 ? tid / parts : tid;
-  int b0 = B;
-  if (work && walk_first(w, pre, B, g0, g1)) b0 = w.b;
-  for (; b0 < B && pre[b0] < g1; b0 += k8Threads) {
-    {
-      const int b = b0 + tid;
-      int c0 = 0, n = 0;
-      if (b < B && pre[b] < g1 && pre[b + 1] > pre[b]) {
-        c0 = cta_of(pre[b]);
-        n = cta_of(pre[b + 1] - 1) - c0 + 1;
-        if (n > 1 && atomicAdd(&A.arrived[b * A.groups + group], 1) != n - 1) n = 0;
-      }
-      s_c0[tid] = c0;
-      s_n[tid] = n;
-      if (n > 1) __threadfence();
-      __syncthreads();
+  // [lift][d] rows of B_h^V, over the operands, the probabilities and the ring: a row every odd number of 16 bytes,
+  // so that the threads of a warp, a row each, read different banks
+  unsigned char* s_b = smem + A.off_img;
+  const int pitch = A.pitch, vec = A.vec, parts = r / vec;  // columns of a copy, copies of a row
+  auto fetch_b = [&](int k0) {  // (all warps but warp 1, which finds out meanwhile who joins)
+    const int t = tid - (warp > 1 ? 32 : 0), threads = k8Threads - 32;
+    if (warp == 1 || parts == 0) return;
+    const int rows = threads / parts, part = t % parts;  // (r <= 64: at least 15 rows at once)
+    int row = t / parts;
+    if (row >= rows) return;
+    const __nv_bfloat16* src =
+        static_cast<const __nv_bfloat16*>(A.b_v) + (static_cast<size_t>(h0 + k0) * d + row) * r + part * vec;
+    uint32_t dst = smem_u32(s_b) + static_cast<uint32_t>(row * pitch + part * vec * 2);
+    for (; row < min(A.lift, heads - k0) * d; row += rows, src += rows * r, dst += rows * pitch) {
+      if (vec == 8)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      else if (vec == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
     }
-    for (int i0 = 0; i0 < k8Threads && b0 + i0 < B && pre[b0 + i0] < g1; ++i0) {
-      const int b = b0 + i0, c0 = s_c0[i0], n = s_n[i0];
-      if (n == 0) continue;
-      const float* ml = A.part_ml + (static_cast<size_t>(b + c0) * H + h0) * 2;
-      const float* acc = A.part_acc + (static_cast<size_t>(b + c0) * H + h0) * W;
-      const size_t step = static_cast<size_t>(H) * W;
-      float* s_o = s_w + k8Heads * n;
-      // (eight pieces' values of three columns under way at a time, the first ones before the weights)
-      float v[3][8];
-      auto fetch = [&](int e0, int i0) {
+  };
+  // (a pass that did not give up has waited for every copy and every product)
+  const bool gave_up = *fail;
+  if (work && !gave_up) fetch_b(0);
+  if (warp == 13) {
+    if (work && !mbar_wait_bounded(&mdone, 0u) && lane == 0) record_status(A.status, kDevTimeout);
+    __syncwarp();
+    tmem_dealloc(tmem, k8Cols);
+  } else if (tid == 0) {
+    if (gave_up) {
+      for (int v = 0, s0 = 0; v < 2; s0 += A.slots[v], ++v)
+        for (int i = max(0, s_copies[v] - A.slots[v]); i < s_copies[v]; ++i)
+          mbar_wait_bounded(&full[s0 + i % A.slots[v]], static_cast<uint32_t>(i / A.slots[v]) & 1u);
+      for (int i = max(0, s_images - 2); i < s_images; ++i)
+        mbar_wait_bounded(&ifull[i & 1], static_cast<uint32_t>(i >> 1) & 1u);
+    }
+    const uint32_t bits = (bad || s_bad ? kDevBounds : 0u) | (gave_up ? kDevTimeout : 0u);
+    if (bits) record_status(A.status, bits);
+  } else if (tid == 32 && work) {
+    TileWalk e;
+    walk_first(e, pre, B, g1 - 1, g1);
+    const int c0 = pre[e.b] < g0 ? cta_of(pre[e.b]) : c, c1 = pre[e.b + 1] > g1 ? cta_of(pre[e.b + 1] - 1) : c;
+    int n = c1 - c0 + 1;
+    if (n > 1 && atomicAdd(&A.arrived[e.b * A.groups + group], 1) != n - 1) n = 0;
+    __threadfence();
+    s_last[0] = e.b;
+    s_last[1] = c0;
+    s_last[2] = n;
+  }
+  __syncthreads();
+  if (!work || gave_up) return;
+  float* s_w = reinterpret_cast<float*>(s_b + A.lift * d * pitch);  // [8][pieces] weights, then [8][W] sums
+  walk_first(w, pre, B, g0, g1);
+  const int b_first = w.b, b_last = s_last[0];
+  const size_t step = static_cast<size_t>(H) * W;
+  struct Joined {  // a sequence to join, and what its first eight pieces hold
+    int b, c0, n;
+    float2 ml;
+    float v[3][8];
+  } x;
+  auto fetch = [&](Joined& x, int e0, int i0) {
+    const float* acc = A.part_acc + (static_cast<size_t>(x.b + x.c0) * H + h0) * W;
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
+    for (int j = 0; j < 3; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = e0 + tid + j * k8Threads;
-            v[j][i] = i0 + i < n && e < heads * W ? __ldcg(acc + (i0 + i) * step + e) : 0.f;
-          }
-      };
-      fetch(0, 0);
-      if (warp < heads) {
-        auto piece = [&](int i) {
-          return i < n ? __ldcg(reinterpret_cast<const float2*>(ml + (static_cast<size_t>(i) * H + warp) * 2))
-                       : make_float2(-INFINITY, 0.f);
-        };
-        const float2 own = piece(lane);
-        float m = own.x, l = 0.f;
-        for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, piece(i).x);
-        m = warp_max(m);
-        for (int i = lane; i < n; i += 32) {
-          const float2 x = i == lane ? own : piece(i);
-          const float y = x.x == -INFINITY ? 0.f : exp2f(x.x - m);
-          s_w[warp * n + i] = y;
-          l = fmaf(y, x.y, l);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const float inv = 1.f / l;
-        __syncwarp();
-        for (int i = lane; i < n; i += 32) s_w[warp * n + i] *= inv;
-        if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
+      for (int i = 0; i < 8; ++i) {
+        const int e = e0 + tid + j * k8Threads;
+        x.v[j][i] = i0 + i < x.n && e < heads * W ? __ldcg(acc + (i0 + i) * step + e) : 0.f;
       }
-      __syncthreads();
-      for (int e0 = 0; e0 < heads * W; e0 += 3 * k8Threads) {
-        float x[3] = {0.f, 0.f, 0.f};
-        for (int i0 = 0; i0 < n; i0 += 8) {
-          if (e0 > 0 || i0 > 0) fetch(e0, i0);
-#pragma unroll
-          for (int j = 0; j < 3; ++j) {
-            const int k = min((e0 + tid + j * k8Threads) / W, heads - 1);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i0 + i < n) x[j] = fmaf(s_w[k * n + i0 + i], v[j][i], x[j]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (e0 + tid + j * k8Threads < heads * W) s_o[e0 + tid + j * k8Threads] = x[j];
+  };
+  auto piece = [&](const Joined& x, int i) {  // its maximum and denominator for head `warp`
+    return i < x.n && warp < heads
+               ? __ldcg(reinterpret_cast<const float2*>(A.part_ml) + static_cast<size_t>(x.b + x.c0 + i) * H + h0 + warp)
+               : make_float2(-INFINITY, 0.f);
+  };
+  auto find = [&](Joined& x) {  // the first one to join from x.b on
+    for (; x.b <= b_last; ++x.b) {
+      x.n = pre[x.b + 1] > pre[x.b] ? 1 : 0;
+      x.c0 = c;
+      if (x.b == b_last) {
+        x.n = s_last[2];
+        x.c0 = s_last[1];
+      } else if (x.b == b_first && pre[x.b] < g0) {
+        x.n = s_first[1];
+        x.c0 = s_first[0];
       }
-      __syncthreads();
-      float* s_p = s_o + k8Heads * W;  // [4 d][parts]
-      float* out = A.out + (static_cast<size_t>(b) * H + h0) * d;
-      const __nv_bfloat16* bv = static_cast<const __nv_bfloat16*>(A.b_v) + static_cast<size_t>(h0) * d * r + part * vec;
-      for (int k0 = 0; k0 < heads; k0 += 4) {
-        for (int t0 = row0; row0 < rows_at_once && parts > 0 && t0 < d; t0 += 2 * rows_at_once) {
-          uint4 u[4][2];  // two rows of four heads under way
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int t = t0 + i * rows_at_once;
-              const __nv_bfloat16* at = bv + (static_cast<size_t>(k0 + k) * d + t) * r;
-              u[k][i] = make_uint4(0u, 0u, 0u, 0u);
-              if (k0 + k >= heads || t >= d) continue;
-              if (vec == 8) {
-                u[k][i] = __ldg(reinterpret_cast<const uint4*>(at));
-              } else if (vec == 4) {
-                const uint2 y = __ldg(reinterpret_cast<const uint2*>(at));
-                u[k][i].x = y.x;
-                u[k][i].y = y.y;
-              } else {
-                u[k][i].x = __ldg(reinterpret_cast<const uint32_t*>(at));
-              }
-            }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k0 + k >= heads) break;
-            float z[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) z[q] = q < vec ? s_o[(k0 + k) * W + d + part * vec + q] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 y = u[k][i];
-              float x = fmaf(bf_hi(y.x), z[1], bf_lo(y.x) * z[0]);
-              x = fmaf(bf_hi(y.y), z[3], fmaf(bf_lo(y.y), z[2], x));
-              x = fmaf(bf_hi(y.z), z[5], fmaf(bf_lo(y.z), z[4], x));
-              x = fmaf(bf_hi(y.w), z[7], fmaf(bf_lo(y.w), z[6], x));
-              if (t0 + i * rows_at_once < d) s_p[(k * d + t0 + i * rows_at_once) * parts + part] = x;
-            }
-          }
-        }
-        __syncthreads();
-        for (int e = tid; e < min(4, heads - k0) * d; e += k8Threads) {
-          const int k = e / d;
-          float x = s_o[(k0 + k) * W + e - k * d];
-          for (int i = 0; i < parts; ++i) x += s_p[e * parts + i];
-          out[k0 * d + e] = x;
-        }
-        __syncthreads();
+      if (x.n == 0) continue;
+      x.ml = piece(x, lane);
+      fetch(x, 0, 0);
+      return true;
+    }
+    return false;
+  };
+  x.b = b_first;
+  bool have_b = true;
+  for (bool any = find(x); any;) {
+    const int b = x.b, n = x.n;
+    float* s_o = s_w + k8Heads * n;
+    if (warp < heads) {
+      float m = x.ml.x, l = 0.f;
+      for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, piece(x, i).x);
+      m = warp_max(m);
+      for (int i = lane; i < n; i += 32) {
+        const float2 own = i == lane ? x.ml : piece(x, i);
+        const float y = own.x == -INFINITY ? 0.f : exp2f(own.x - m);
+        s_w[warp * n + i] = y;
+        l = fmaf(y, own.y, l);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      const float inv = 1.f / l;
+      __syncwarp();
+      for (int i = lane; i < n; i += 32) s_w[warp * n + i] *= inv;
+      if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
     }
     __syncthreads();
+    for (int e0 = 0; e0 < heads * W; e0 += 3 * k8Threads) {
+      float y[3] = {0.f, 0.f, 0.f};
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        if (e0 > 0 || i0 > 0) fetch(x, e0, i0);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          const int k = min((e0 + tid + j * k8Threads) / W, heads - 1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + i < n) y[j] = fmaf(s_w[k * n + i0 + i], x.v[j][i], y[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (e0 + tid + j * k8Threads < heads * W) s_o[e0 + tid + j * k8Threads] = y[j];
+    }
+    ++x.b;
+    any = find(x);  // the next one's loads are under way during this one's lift
+    float* out = A.out + (static_cast<size_t>(b) * H + h0) * d;
+    for (int k0 = 0; k0 < heads; k0 += A.lift) {
+      if (!have_b) fetch_b(k0);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      for (int e = tid; e < min(A.lift, heads - k0) * d; e += k8Threads) {
+        const int k = k0 + e / d;
+        const float* z = s_o + k * W + d;
+        const unsigned char* row = s_b + e * pitch;
+        float y = 0.f, y1 = 0.f;
+        if (vec == 8) {
+#pragma unroll 2
+          for (int i = 0; i < r; i += 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(row + 2 * i);
+            const float4 za = *reinterpret_cast<const float4*>(z + i), zb = *reinterpret_cast<const float4*>(z + i + 4);
+            y = fmaf(bf_hi(a.x), za.y, fmaf(bf_lo(a.x), za.x, y));
+            y1 = fmaf(bf_hi(a.y), za.w, fmaf(bf_lo(a.y), za.z, y1));
+            y = fmaf(bf_hi(a.z), zb.y, fmaf(bf_lo(a.z), zb.x, y));
+            y1 = fmaf(bf_hi(a.w), zb.w, fmaf(bf_lo(a.w), zb.z, y1));
+          }
+        } else {
+          for (int i = 0; i < r; i += 2) {
+            const uint32_t a = *reinterpret_cast<const uint32_t*>(row + 2 * i);
+            y = fmaf(bf_hi(a), z[i + 1], fmaf(bf_lo(a), z[i], y));
+          }
+        }
+        out[k0 * d + e] = s_o[k * W + e - (k - k0) * d] + (y + y1);
+      }
+      have_b = A.lift >= heads;  // (it stays for the next sequence)
+      __syncthreads();
+    }
   }
 }
 
@@ -1041,6 +1077,11 @@ size_t decode8_bind(Args8& A, void* ws) {
   return off;
 }
 
+// Shared memory of the join: B_h^V of `lift` heads, weights of the pieces, sums.
+long long decode8_lift_bytes(const Args8& A, int lift) {
+  return 1ll * lift * A.dh * A.pitch + 4ll * k8Heads * (A.grid + A.dh + A.r);
+}
+
 lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* bytes) {
   std::memset(&A, 0, sizeof(A));
   A.B = d.batch; A.H = d.heads; A.dh = d.head_dim; A.r = d.rank; A.max_len = d.max_len;
@@ -1063,9 +1104,10 @@ lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* byte
   A.slots[0] = slots / 2;
   A.slots[1] = slots - A.slots[0];
   A.smem_bytes = off + slots * k8Box + 1024;
-  // the join's weights, sums and products lie over the operands, the probabilities and the ring
-  const long long join = 8ll * k8Threads + 4ll * k8Heads * (A.grid + A.dh + A.r) + 16ll * A.dh * (A.r / 2);
-  if (join > off + slots * k8Box - A.off_img) return LRKV_ERR_UNSUPPORTED;
+  A.pitch = (round_up(2 * A.r, 16) / 16 | 1) * 16;
+  const long long room = off + slots * k8Box - A.off_img;
+  for (A.lift = k8Heads; A.lift > 1 && decode8_lift_bytes(A, A.lift) > room;) A.lift /= 2;
+  if (decode8_lift_bytes(A, A.lift) > room) return LRKV_ERR_UNSUPPORTED;
   *bytes = decode8_bind(A, nullptr);
   return LRKV_OK;
 }
@@ -1122,6 +1164,8 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
   A.blocks = (rows + lrkv::kBlock8 - 1) / lrkv::kBlock8;
   A.box = block_table ? std::min(page_size, lrkv::k8Rows) : lrkv::k8Rows;
   A.tail_box = std::min(A.box, lrkv::k8Step);
+  const uintptr_t bv = reinterpret_cast<uintptr_t>(b_v);
+  A.vec = A.r % 8 == 0 && bv % 16 == 0 ? 8 : A.r % 4 == 0 && bv % 8 == 0 ? 4 : 2;
   lrkv::Maps8 M;
   std::memset(&M, 0, sizeof(M));
   const void* const held[4] = {cache->k_s, cache->v_s, cache->z_k, cache->z_v};
