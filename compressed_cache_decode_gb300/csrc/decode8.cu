@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
       oempty[k8MaxD + k8MaxZ], mdone, mlfirst;
   __shared__ uint32_t tmem_base;
   __shared__ int s_fail, s_bad, s_images, s_copies[2];  // copies issued
-  __shared__ int s_first[2], s_last[3];  // a shared sequence's first CTA and pieces (0: another CTA joins them)
+  // the first sequence's first CTA, pieces (0: another CTA joins them) and number; the last one's
+  __shared__ int s_first[3], s_last[3];
   __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
   __shared__ float s_fac[4][20];                      // [tile % 4]: alpha[8], latent scale[8], shared scale
   __shared__ float s_sum[2][4][4];
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
     mbar_init(&mdone, 2);
     mbar_init(&mlfirst, 2);
     s_fail = s_bad = s_images = s_copies[0] = s_copies[1] = 0;
-    s_first[1] = s_last[2] = 0;
+    s_first[1] = s_last[1] = 0;
     fence_barrier_init();
   }
   if (warp == 13) tmem_alloc(&tmem_base, k8Cols);
@@ -877,6 +878,17 @@ __global__ void __launch_bounds__(k8Threads, 1)
   // alone what lies between.  The group's B_h^V, the same for all of them, is on its way to shared
   // memory before it is known who joins ------------------------------------------------------
   pdl_wait();
+  int last_n = 0;
+  if (tid == 32 && work) {
+    TileWalk e;
+    walk_first(e, pre, B, g0, g1);
+    s_first[2] = e.b;
+    walk_first(e, pre, B, g1 - 1, g1);
+    const int c0 = pre[e.b] < g0 ? cta_of(pre[e.b]) : c, c1 = pre[e.b + 1] > g1 ? cta_of(pre[e.b + 1] - 1) : c;
+    last_n = c1 - c0 + 1;
+    s_last[2] = e.b;
+    s_last[0] = c0;
+  }
   if (warp < k8Softmax + k8Values) __threadfence();  // the last piece's results, for the CTA that joins it
   tc_fence_before();
   __syncthreads();
@@ -922,35 +934,30 @@ __global__ void __launch_bounds__(k8Threads, 1)
     const uint32_t bits = (bad || s_bad ? kDevBounds : 0u) | (gave_up ? kDevTimeout : 0u);
     if (bits) record_status(A.status, bits);
   } else if (tid == 32 && work) {
-    TileWalk e;
-    walk_first(e, pre, B, g1 - 1, g1);
-    const int c0 = pre[e.b] < g0 ? cta_of(pre[e.b]) : c, c1 = pre[e.b + 1] > g1 ? cta_of(pre[e.b + 1] - 1) : c;
-    int n = c1 - c0 + 1;
-    if (n > 1 && atomicAdd(&A.arrived[e.b * A.groups + group], 1) != n - 1) n = 0;
+    int n = last_n;
+    if (n > 1 && atomicAdd(&A.arrived[s_last[2] * A.groups + group], 1) != n - 1) n = 0;
     __threadfence();
-    s_last[0] = e.b;
-    s_last[1] = c0;
-    s_last[2] = n;
+    s_last[1] = n;
   }
   __syncthreads();
   if (!work || gave_up) return;
   float* s_w = reinterpret_cast<float*>(s_b + A.lift * d * pitch);  // [8][pieces] weights, then [8][W] sums
-  walk_first(w, pre, B, g0, g1);
-  const int b_first = w.b, b_last = s_last[0];
+  const int b_first = s_first[2], b_last = s_last[2];
   const size_t step = static_cast<size_t>(H) * W;
-  struct Joined {  // a sequence to join, and what its first eight pieces hold
+  constexpr int kCols = 2, kDeep = 10;  // pairs of columns a thread sums at once, pieces it has under way
+  struct Joined {  // a sequence to join, and what its first pieces hold
     int b, c0, n;
-    float2 ml;
-    float v[3][8];
+    float2 ml, v[kCols][kDeep];
   } x;
   auto fetch = [&](Joined& x, int e0, int i0) {
     const float* acc = A.part_acc + (static_cast<size_t>(x.b + x.c0) * H + h0) * W;
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
+    for (int j = 0; j < kCols; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = e0 + tid + j * k8Threads;
-        x.v[j][i] = i0 + i < x.n && e < heads * W ? __ldcg(acc + (i0 + i) * step + e) : 0.f;
+      for (int i = 0; i < kDeep; ++i) {
+        const int e = 2 * (e0 + tid + j * k8Threads);
+        x.v[j][i] = i0 + i < x.n && e < heads * W ? __ldcg(reinterpret_cast<const float2*>(acc + (i0 + i) * step + e))
+                                                  : make_float2(0.f, 0.f);
       }
   };
   auto piece = [&](const Joined& x, int i) {  // its maximum and denominator for head `warp`
@@ -963,8 +970,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
       x.n = pre[x.b + 1] > pre[x.b] ? 1 : 0;
       x.c0 = c;
       if (x.b == b_last) {
-        x.n = s_last[2];
-        x.c0 = s_last[1];
+        x.n = s_last[1];
+        x.c0 = s_last[0];
       } else if (x.b == b_first && pre[x.b] < g0) {
         x.n = s_first[1];
         x.c0 = s_first[0];
@@ -999,21 +1006,26 @@ __global__ void __launch_bounds__(k8Threads, 1)
       if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
     }
     __syncthreads();
-    for (int e0 = 0; e0 < heads * W; e0 += 3 * k8Threads) {
-      float y[3] = {0.f, 0.f, 0.f};
-      for (int i0 = 0; i0 < n; i0 += 8) {
+    for (int e0 = 0; 2 * e0 < heads * W; e0 += kCols * k8Threads) {  // (W is even: a pair is of one head)
+      float2 y[kCols] = {};
+      for (int i0 = 0; i0 < n; i0 += kDeep) {
         if (e0 > 0 || i0 > 0) fetch(x, e0, i0);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const int k = min((e0 + tid + j * k8Threads) / W, heads - 1);
+        for (int j = 0; j < kCols; ++j) {
+          const int k = min(2 * (e0 + tid + j * k8Threads) / W, heads - 1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i0 + i < n) y[j] = fmaf(s_w[k * n + i0 + i], x.v[j][i], y[j]);
+          for (int i = 0; i < kDeep; ++i)
+            if (i0 + i < n) {
+              y[j].x = fmaf(s_w[k * n + i0 + i], x.v[j][i].x, y[j].x);
+              y[j].y = fmaf(s_w[k * n + i0 + i], x.v[j][i].y, y[j].y);
+            }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 3; ++j)
-        if (e0 + tid + j * k8Threads < heads * W) s_o[e0 + tid + j * k8Threads] = y[j];
+      for (int j = 0; j < kCols; ++j) {
+        const int e = 2 * (e0 + tid + j * k8Threads);
+        if (e < heads * W) *reinterpret_cast<float2*>(s_o + e) = y[j];
+      }
     }
     ++x.b;
     any = find(x);  // the next one's loads are under way during this one's lift
