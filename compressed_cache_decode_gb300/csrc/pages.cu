@@ -13,6 +13,13 @@
 // The pages that a plan copies are then moved by lrkv_pages_copy_kernel, bound by
 // memory: a warp per 2 KB segment of a page of a pool.  It reads how many
 // there are from the workspace, so the host never waits.
+//
+// Measured on GB300, back-to-back calls of a graph: a fork of 64 x 64 blocks 4.6 us,
+// of 512 x 512 blocks 12 us; room for one more row of 256 sequences, four to a
+// prompt, whose begun pages are copied (39 MB of an 8-bit cache), 17 us, of which
+// the copies' bytes are 6; a compaction that moves 1,067 pages of 426 KB (909 MB
+// read and written) 147 us, 0.93 of a measured copy's rate.  The plans are bound
+// by latency: each pass waits for the loads of the one before.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -13,6 +13,11 @@
 // A block that was begun before (a decode step, or a prompt that goes on) keeps
 // its scale unless the new rows need a larger one; then its earlier rows are
 // rounded anew in place.
+//
+// Measured on GB300, back-to-back calls: 8 prompts of 4-8K rows, bf16, 32 heads
+// of rank 48, d_h 128: 81 us, 6.4 TB/s read and written (0.96 of a measured
+// copy's 6.7); 32 decode steps, rank 56, in pages: 3.6 us, a launch's latency
+// (a caller's own 10 us a call are the bound there).
 #include <cuda_bf16.h>
 
 #include <algorithm>

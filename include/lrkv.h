@@ -43,7 +43,7 @@
  *    seq_lens entry outside [0, max_len], a bounded wait that ran out) never
  *    trap: the kernels clamp, finish, and record the status in the workspace,
  *    readable with lrkv_read_device_status().  A wait of the kernels that
- *    keep copies or MMAs in flight (the bf16 decode scan, the RoPE and
+ *    keep copies or MMAs in flight (the bf16 decode scan, the RoPE, 8-bit and
  *    comparison decodes, lrkv_prefill_weights, lrkv_evict) gives up after
  *    LRKV_WAIT_LIMIT_CYCLES SM cycles (an environment variable read at each
  *    call; default 2e9, about 1 s); the kernel then skips the work that
@@ -51,8 +51,8 @@
  *    and records LRKV_ERR_TIMEOUT: the call's outputs are then not to be used.
  *    Set the variable only to exercise that path.
  *  * Order on the stream.  The calls' kernels use programmatic dependent
- *    launch.  A decode (lrkv_decode and its forms, the weighted, RoPE and
- *    comparison decodes) reads its inputs before it waits for the launch
+ *    launch.  A decode (lrkv_decode and its forms, the weighted, RoPE, 8-bit
+ *    and comparison decodes) reads its inputs before it waits for the launch
  *    before it: they must be complete when that launch lets its dependents
  *    start.  A kernel that does not do so explicitly lets them start when it
  *    ends; so do all calls here that write a decode's input, but for
@@ -649,8 +649,9 @@ typedef struct {
  * out is held to it.  Scales: any finite positive numbers.  Rows at or past
  * seq_lens[b] and the scales of blocks past them may hold anything; a NaN in a
  * visible row may make any output of its sequence NaN.  Supported: dtype BF16
- * (of q and the bases), and the shapes of lrkv_quantize.  Workspace:
- * lrkv_decode8_workspace_size() bytes; errors as in lrkv_decode_paged.
+ * (of q and the bases), and the shapes of lrkv_quantize; b_k and b_v 4-byte
+ * aligned, faster at 16 bytes.  Workspace: lrkv_decode8_workspace_size()
+ * bytes; errors as in lrkv_decode_paged.
  */
 lrkv_status lrkv_quantize(const lrkv_dims* dims, int n_new, const void* k_s, const void* v_s, const void* z_k,
                           const void* z_v, const int32_t* start_pos, const int32_t* new_lens, int page_size,
@@ -675,12 +676,12 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
  *       the caller adds to hold a page that no sequence names (a prompt kept
  *       for later).  A page is free when refs is 0 (or less).
  * Each call reads these and writes table_out, lens_out, refs_out, which may be
- * the same arrays (else they do not overlap).  All numbering is fixed: the lowest free pages, in the
- * order of the sequences.  page_size: a power of two >= 16.  Lengths outside
- * [0, max_blocks page_size] are clamped; these, and an entry in use that names no
- * page of the pool, set LRKV_ERR_DEVICE_BOUNDS (such an entry stays as it is).
- * ws: lrkv_pages_workspace_size() bytes, its status word set afresh.
- * num_pages and batch * max_blocks at most 2^30, batch <= 4096.
+ * the same arrays (else they do not overlap).  All numbering is fixed: the
+ * lowest free pages, in the order of the sequences.  page_size: a power of two
+ * >= 16.  Lengths outside [0, max_blocks page_size] are clamped; these, and an
+ * entry in use that names no page of the pool, set LRKV_ERR_DEVICE_BOUNDS (such
+ * an entry stays as it is).  ws: lrkv_pages_workspace_size() bytes, its status
+ * word set afresh.  num_pages and batch * max_blocks at most 2^30, batch <= 4096.
  *
  * lrkv_pages_fork: sequence b becomes the first keep[b] rows of sequence
  * parent[b] as it was before the call, on the same pages: beams that go on
@@ -711,9 +712,9 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
  *
  * Pools: the arrays that the pages consist of, host array of n_pools (0 .. 16)
  * entries: page p of a pool is page_size / rows pieces of `bytes` bytes from
- * data + p * (page_size / rows) * bytes on, one piece for every `rows` rows (1: a row of a
- * cache tensor; LRKV_BLOCK8: the scales of a block of an 8-bit cache).  data and
- * bytes are multiples of 4; rows divides page_size; all pools have num_pages
+ * data + p * (page_size / rows) * bytes on, one piece for every `rows` rows (1:
+ * a row of a cache tensor; LRKV_BLOCK8: the scales of a block of an 8-bit
+ * cache).  data and bytes are multiples of 4; rows divides page_size; all pools have num_pages
  * pages.  Pools do not overlap.
  */
 typedef struct {
