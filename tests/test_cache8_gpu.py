@@ -68,6 +68,26 @@ def test_decode8_of_any_split(sms, monkeypatch):
     case.check(out, lse, pairs={(b, b % 8) for b in range(B)})
 
 
+@pytest.mark.parametrize("sms, shape, offset", [
+    (2, (9, 12, 256, 64, 330, [(150 * b) % 331 for b in range(9)]), 0),   # a CTA joins many sequences, heads in slices
+    (2, (9, 12, 256, 64, 330, [(150 * b) % 331 for b in range(9)]), 2),   # bases read 4 bytes at a time
+    (6, (7, 16, 64, 28, 700, [(333 * b) % 701 for b in range(7)]), 4),    # 8 bytes at a time; some joined, some shared
+    (400, (2, 8, 64, 32, 9000, [9000, 700]), 0),                          # more pieces than a warp has lanes
+    (152, (4096, 8, 16, 2, 16, [b % 17 for b in range(4096)]), 0),        # the largest batch
+])
+def test_decode8_joins(sms, shape, offset, monkeypatch):
+    B, H, dh, r, L, lens = shape
+    case = C.Case(B, H, dh, r, L, lens, seed=sms)
+    q, cache, b_k, b_v, n, _ = case.cuda()
+    flat = torch.empty(offset + b_v.numel(), dtype=torch.bfloat16, device="cuda")
+    flat[offset:] = b_v.view(-1)
+    monkeypatch.setenv("LRKV_SM_COUNT", str(sms))
+    out, lse, ws = lrkv.decode8(q, cache, b_k, flat[offset:].view(b_v.shape), n)
+    torch.cuda.synchronize()
+    assert lrkv.lrkv_read_device_status(ws) == lrkv.LRKV_OK
+    case.check(out, lse, pairs={(b, b % H) for b in range(0, B, max(1, B // 200))})
+
+
 def test_decode8_over_a_long_cache():
     """More than 2^32 bytes of latents: offsets past 32 bits (the shared rows and most latents are zero)."""
     B, H, dh, r, L = 2, 32, 64, 64, 1 << 20
