@@ -1056,10 +1056,10 @@ def quantize(k_s, v_s, z_k, z_v, start_pos, cache: Cache8, new_lens=None, block_
            ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
            ("ws", ws, _U8, ws.shape if ws is not None else None))
     with _On(k_s):
-        st = int(load().lrkv_quantize(
-            ctypes.byref(dims), n, _ptr(k_s), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(start_pos), _ptr(new_lens),
-            page_size, num_pages, _ptr(block_table), cache.ref, _ptr(ws), 0 if ws is None else ws.numel(),
-            _stream_on(stream, dev)))
+        st = load().lrkv_quantize(
+            ctypes.byref(dims), n, k_s.data_ptr(), _ptr(v_s), _ptr(z_k), _ptr(z_v), _ptr(start_pos),
+            _ptr(new_lens), page_size, num_pages, _ptr(block_table), cache.ref, _ptr(ws),
+            0 if ws is None else ws.numel(), _stream_on(stream, dev))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_quantize")
 
@@ -1086,11 +1086,12 @@ def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float
             lse = on.own(torch.empty((B, H), dtype=torch.float32, device=q.device))
         if ws is None:
             ws = on.own(decode8_workspace(dims, q.device))
-        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
-        st = int(load().lrkv_decode8(
-            ctypes.byref(dims), _ptr(q), page_size, num_pages, _ptr(block_table), cache.ref,
-            _ptr(b_k) if r else None, _ptr(b_v) if r else None, _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws),
-            ws.numel(), _stream_on(stream, dev)))
+        size = ws.numel()
+        _check(dev, ("ws", ws, _U8, (size,)))
+        st = load().lrkv_decode8(
+            ctypes.byref(dims), q.data_ptr(), page_size, num_pages, _ptr(block_table), cache.ref,
+            _ptr(b_k) if r else None, _ptr(b_v) if r else None, _ptr(seq_lens), out.data_ptr(),
+            lse.data_ptr(), ws.data_ptr(), size, _stream_on(stream, dev))
     if st != LRKV_OK:
         raise LRKVError(st, "lrkv_decode8")
     return out, lse, ws
@@ -1106,34 +1107,26 @@ def pages_workspace(batch: int, max_blocks: int, num_pages: int, device="cuda") 
 def _pools(pools, page_size: int, num_pages: int, device: int) -> bytes:
     """The C array of pools [num_pages, pieces, ...]: a piece for every page_size / pieces rows."""
     flat = []
-    for i, t in enumerate(pools):
+    for t in pools:
         shape = t.shape
-        pieces = shape[1] if len(shape) > 1 and shape[0] == num_pages else 0
-        if pieces < 1 or page_size % pieces:
-            raise ValueError(f"pool {i} must have {num_pages} pages and a piece for every so many of a page's "
-                             f"{page_size} rows, not shape {tuple(shape)}")
-        if not t.is_contiguous() or t.get_device() != device:
-            raise ValueError(f"pool {i} must be contiguous, on the call's device")
+        if (len(shape) < 2 or shape[0] != num_pages or (pieces := shape[1]) < 1 or page_size % pieces
+                or not t.is_contiguous() or t.get_device() != device):
+            if len(shape) < 2 or shape[0] != num_pages or shape[1] < 1 or page_size % shape[1]:
+                raise ValueError(f"a pool must have {num_pages} pages and a piece for every so many of a page's "
+                                 f"{page_size} rows, not shape {tuple(shape)}")
+            raise ValueError(f"a pool of shape {tuple(shape)} must be contiguous, on the call's device")
         flat += (t.data_ptr(), page_size // pieces, t.nbytes // (num_pages * pieces))
     return struct.pack("Pii" * len(pools), *flat)
 
 
-def _pages_call(name: str, block_table, seq_lens, refs, page_size: int, outs, more, ws, stream, call):
-    """Checks, workspace and status of a pages_* call; call(dims, on) makes it."""
-    B, blocks = block_table.shape
+def _pages_arrays(block_table, seq_lens, refs, table_out, lens_out, refs_out, more):
+    """Checks of a pages_* call's arrays (outputs that are the inputs: None); (B, blocks, pages, device)."""
+    B, blocks = table = block_table.shape
     pages, dev = refs.shape[0], block_table.get_device()
-    _check(dev, ("block_table", block_table, _I32, (B, blocks)), ("seq_lens", seq_lens, _I32, (B,)),
-           ("refs", refs, _I32, (pages,)), ("table_out", outs[0], _I32, (B, blocks)),
-           ("lens_out", outs[1], _I32, (B,)), ("refs_out", outs[2], _I32, (pages,)),
-           *[(n, t, _I32, (s,)) for n, t, s in more])
-    with _On(block_table, stream) as on:
-        if ws is None:
-            ws = on.own(pages_workspace(B, blocks, pages, block_table.device))
-        _check(dev, ("ws", ws, _U8, (ws.numel(),)))
-        st = int(call(B, blocks, int(page_size), pages, ws, _stream_on(stream, dev)))
-    if st != LRKV_OK:
-        raise LRKVError(st, name)
-    return ws
+    _check(dev, ("block_table", block_table, _I32, table), ("seq_lens", seq_lens, _I32, (B,)),
+           ("refs", refs, _I32, (pages,)), ("table_out", table_out, _I32, table), ("lens_out", lens_out, _I32, (B,)),
+           ("refs_out", refs_out, _I32, (pages,)), *more)
+    return B, blocks, pages, dev
 
 
 def pages_fork(block_table, seq_lens, refs, page_size: int, parent=None, keep=None, table_out=None, lens_out=None,
@@ -1144,15 +1137,23 @@ def pages_fork(block_table, seq_lens, refs, page_size: int, parent=None, keep=No
     seq_lens [B] and refs [num_pages] (int32) in place unless given outputs.
     Returns (table_out, lens_out, refs_out, ws)."""
     B = block_table.shape[0]
-    outs = (block_table if table_out is None else table_out, seq_lens if lens_out is None else lens_out,
-            refs if refs_out is None else refs_out)
-    ws = _pages_call(
-        "lrkv_pages_fork", block_table, seq_lens, refs, page_size, outs,
-        (("parent", parent, B), ("keep", keep, B)), ws, stream,
-        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_fork(
-            b, blocks, size, pages, _ptr(parent), _ptr(keep), _ptr(block_table), _ptr(seq_lens), _ptr(refs),
-            *map(_ptr, outs), _ptr(ws), ws.numel(), s))
-    return (*outs, ws)
+    B, blocks, pages, dev = _pages_arrays(block_table, seq_lens, refs, table_out, lens_out, refs_out,
+                                          (("parent", parent, _I32, (B,)), ("keep", keep, _I32, (B,))))
+    table_out = block_table if table_out is None else table_out
+    lens_out = seq_lens if lens_out is None else lens_out
+    refs_out = refs if refs_out is None else refs_out
+    with _On(block_table, stream) as on:
+        if ws is None:
+            ws = on.own(pages_workspace(B, blocks, pages, block_table.device))
+        size = ws.numel()
+        _check(dev, ("ws", ws, _U8, (size,)))
+        st = load().lrkv_pages_fork(
+            B, blocks, int(page_size), pages, _ptr(parent), _ptr(keep), block_table.data_ptr(), _ptr(seq_lens),
+            refs.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(), size,
+            _stream_on(stream, dev))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_pages_fork")
+    return table_out, lens_out, refs_out, ws
 
 
 def pages_extend(pools, block_table, seq_lens, refs, page_size: int, new_lens, table_out=None, lens_out=None,
@@ -1162,17 +1163,26 @@ def pages_extend(pools, block_table, seq_lens, refs, page_size: int, new_lens, t
     [num_pages, pieces, ...]).  All or nothing: missing [1] int32 receives the
     number of pages that lack.  Updates block_table, seq_lens and refs in place
     unless given outputs.  Returns (table_out, lens_out, refs_out, ws)."""
-    B, dev = block_table.shape[0], block_table.get_device()
-    outs = (block_table if table_out is None else table_out, seq_lens if lens_out is None else lens_out,
-            refs if refs_out is None else refs_out)
-    array = _pools(pools, int(page_size), refs.shape[0], dev)
-    ws = _pages_call(
-        "lrkv_pages_extend", block_table, seq_lens, refs, page_size, outs,
-        (("new_lens", new_lens, B), ("missing", missing, 1)), ws, stream,
-        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_extend(
-            b, blocks, size, pages, _ptr(new_lens), _ptr(block_table), _ptr(seq_lens), _ptr(refs), *map(_ptr, outs),
-            _ptr(missing), array, len(pools), _ptr(ws), ws.numel(), s))
-    return (*outs, ws)
+    B, blocks, pages, dev = _pages_arrays(
+        block_table, seq_lens, refs, table_out, lens_out, refs_out,
+        (("new_lens", new_lens, _I32, (block_table.shape[0],)), ("missing", missing, _I32, (1,))))
+    table_out = block_table if table_out is None else table_out
+    lens_out = seq_lens if lens_out is None else lens_out
+    refs_out = refs if refs_out is None else refs_out
+    page_size = int(page_size)
+    array = _pools(pools, page_size, pages, dev)
+    with _On(block_table, stream) as on:
+        if ws is None:
+            ws = on.own(pages_workspace(B, blocks, pages, block_table.device))
+        size = ws.numel()
+        _check(dev, ("ws", ws, _U8, (size,)))
+        st = load().lrkv_pages_extend(
+            B, blocks, page_size, pages, _ptr(new_lens), block_table.data_ptr(), _ptr(seq_lens), refs.data_ptr(),
+            table_out.data_ptr(), lens_out.data_ptr(), refs_out.data_ptr(), _ptr(missing), array, len(pools),
+            ws.data_ptr(), size, _stream_on(stream, dev))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_pages_extend")
+    return table_out, lens_out, refs_out, ws
 
 
 def pages_compact(pools, block_table, seq_lens, refs, page_size: int, table_out=None, refs_out=None, moved=None,
@@ -1181,16 +1191,25 @@ def pages_compact(pools, block_table, seq_lens, refs, page_size: int, table_out=
     block_table and refs in place unless given outputs; moved [num_pages] int32
     receives every page's new number, -1 for free ones, live [1] int32 how many
     are in use.  Returns (table_out, refs_out, ws)."""
-    dev = block_table.get_device()
-    outs = (block_table if table_out is None else table_out, None, refs if refs_out is None else refs_out)
-    array = _pools(pools, int(page_size), refs.shape[0], dev)
-    ws = _pages_call(
-        "lrkv_pages_compact", block_table, seq_lens, refs, page_size, outs,
-        (("moved", moved, refs.shape[0]), ("live", live, 1)), ws, stream,
-        lambda b, blocks, size, pages, ws, s: load().lrkv_pages_compact(
-            b, blocks, size, pages, _ptr(block_table), _ptr(seq_lens), _ptr(refs), _ptr(outs[0]), _ptr(outs[2]),
-            _ptr(moved), _ptr(live), array, len(pools), _ptr(ws), ws.numel(), s))
-    return outs[0], outs[2], ws
+    pages = refs.shape[0]
+    B, blocks, pages, dev = _pages_arrays(block_table, seq_lens, refs, table_out, None, refs_out,
+                                          (("moved", moved, _I32, (pages,)), ("live", live, _I32, (1,))))
+    table_out = block_table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    page_size = int(page_size)
+    array = _pools(pools, page_size, pages, dev)
+    with _On(block_table, stream) as on:
+        if ws is None:
+            ws = on.own(pages_workspace(B, blocks, pages, block_table.device))
+        size = ws.numel()
+        _check(dev, ("ws", ws, _U8, (size,)))
+        st = load().lrkv_pages_compact(
+            B, blocks, page_size, pages, block_table.data_ptr(), _ptr(seq_lens), refs.data_ptr(),
+            table_out.data_ptr(), refs_out.data_ptr(), _ptr(moved), _ptr(live), array, len(pools), ws.data_ptr(),
+            size, _stream_on(stream, dev))
+    if st != LRKV_OK:
+        raise LRKVError(st, "lrkv_pages_compact")
+    return table_out, refs_out, ws
 
 
 # ------------------------------------------------- comparison decodes --
