@@ -267,6 +267,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // Latency is all it costs (B_h^K once per sequence, from L2): the words of B_h^K
 // are under way before q is.
 constexpr int k8OpWarps = 8, k8OpThreads = 32 * k8OpWarps;
+static_assert(k8MaxD * 128 <= k8OpThreads && k8MaxZ * 128 <= 2 * k8OpThreads, "a thread's columns");
 constexpr int k8OpRows = 16;  // rows of B_h^K a warp has in flight
 
 __global__ void __launch_bounds__(k8OpThreads) lrkv_decode8_operands_kernel(const __grid_constant__ Args8 A) {
@@ -332,39 +333,51 @@ __global__ void __launch_bounds__(k8OpThreads) lrkv_decode8_operands_kernel(cons
     down[i] = e == 128 ? __uint_as_float(0x7fffffffu) : pow2(e - 7) * A.scale_log2;
     if (e == 128) up[i] = 0.f;
   }
-  pdl_wait();  // the launch before may still read the workspace
-  if (hl == 0 && tid == 0) A.arrived[b * A.groups + (h >> 3)] = 0;
-  if (h == 0 && b == 0 && tid == 0) *A.status = 0u;
-  if (there && A.seq_lens[b] <= 0) {  // nothing to attend
-    if (tid < d) A.out[(static_cast<size_t>(b) * A.H + h) * d + tid] = 0.f;
-    if (tid == 0 && A.lse) A.lse[static_cast<size_t>(b) * A.H + h] = -INFINITY;
+  // the parts of this thread's columns: chunk tid / 128 of q, chunks tid / 128 and 2 further of p
+  const int col = tid & 127, j0 = tid >> 7;
+  uint32_t qv[k8QParts], zv[2][k8Parts];
+  auto split = [](float x, auto& v) {
+#pragma unroll
+    for (uint32_t& y : v) {
+      y = e4m3x2(x, 0.f);
+      x = (x - from_e4m3x2(y).x) * 16.f;
+    }
+  };
+  split(128 * j0 + col < d ? s_q[128 * j0 + col] * up[0] : 0.f, qv);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = 128 * (j0 + 2 * k) + col - hl * r;  // this head's latent column
+    split(c >= 0 && c < r ? s_part[0][c] * up[1] : 0.f, zv[k]);
   }
+  const bool empty = there && __ldg(A.seq_lens + b) <= 0;
+  pdl_wait();  // the launch before may still read the workspace
   unsigned char* img = A.images + (static_cast<size_t>(b) * A.groups + (h >> 3)) * A.img_bytes;
-  const int col = tid & 127;
-  for (int j = tid >> 7; j < A.nd; j += k8OpThreads / 128) {
-    float x = 128 * j + col < d ? s_q[128 * j + col] * up[0] : 0.f;
+  if (j0 < A.nd) {
 #pragma unroll
     for (int i = 0; i < k8QParts; ++i) {
       const int n = hl * k8QParts + i;
-      const uint32_t v = e4m3x2(x, 0.f);
-      img[j * (k8NQ * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
-      x = (x - from_e4m3x2(v).x) * 16.f;
+      img[j0 * (k8NQ * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(qv[i]);
     }
   }
   img += A.nd * (k8NQ * 128);
-  for (int j = tid >> 7; j < A.nz; j += k8OpThreads / 128) {
-    const int c = 128 * j + col - hl * r;  // this head's latent column
-    float x = c >= 0 && c < r ? s_part[0][c] * up[1] : 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int j = j0 + 2 * k;
+    if (j >= A.nz) continue;
 #pragma unroll
     for (int i = 0; i < k8Parts; ++i) {
       const int n = hl * k8Parts + i;
-      const uint32_t v = e4m3x2(x, 0.f);
-      img[j * (k8N * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(v);
-      x = (x - from_e4m3x2(v).x) * 16.f;
+      img[j * (k8N * 128) + n * 128 + (col ^ ((n & 7) << 4))] = static_cast<unsigned char>(zv[k][i]);
     }
   }
   img += A.nz * (k8N * 128);
   if (tid < 2) reinterpret_cast<float*>(img)[8 * tid + hl] = there ? down[tid] : 0.f;
+  if (hl == 0 && tid == 0) A.arrived[b * A.groups + (h >> 3)] = 0;
+  if (h == 0 && b == 0 && tid == 0) *A.status = 0u;
+  if (empty) {  // nothing to attend
+    if (tid < d) A.out[(static_cast<size_t>(b) * A.H + h) * d + tid] = 0.f;
+    if (tid == 0 && A.lse) A.lse[static_cast<size_t>(b) * A.H + h] = -INFINITY;
+  }
 }
 
 // ================================================================== the scan
@@ -979,9 +992,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
       }
   };
   auto piece = [&](const Joined& x, int i) {  // its maximum and denominator for head `warp`
-    return i < x.n && warp < heads
-               ? __ldcg(reinterpret_cast<const float2*>(A.part_ml) + static_cast<size_t>(x.b + x.c0 + i) * H + h0 + warp)
-               : make_float2(-INFINITY, 0.f);
+    const float2* ml = reinterpret_cast<const float2*>(A.part_ml) + static_cast<size_t>(x.b + x.c0) * H + h0 + warp;
+    return i < x.n && warp < heads ? __ldcg(ml + static_cast<size_t>(i) * H) : make_float2(-INFINITY, 0.f);
   };
   auto find = [&](Joined& x) {  // the first one to join from x.b on
     for (; x.b <= b_last; ++x.b) {

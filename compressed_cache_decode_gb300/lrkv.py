@@ -1076,8 +1076,8 @@ def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float
     dt, dev, basis = q.dtype, q.get_device(), (H, dh, r)
     max_len, page_size, num_pages = cache.rows(block_table, B, H, dh, r, dev)
     dims = make_dims(B, H, dh, r, max_len, dt, scale)
-    _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k if r else None, dt, basis), ("b_v", b_v if r else None, dt, basis),
-           ("seq_lens", seq_lens, _I32, (B,)), ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
+    _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k if r else None, dt, basis),
+           ("b_v", b_v if r else None, dt, basis), ("seq_lens", seq_lens, _I32, (B,)), ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
            ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
     with _On(q, stream) as on:
         if out is None:
@@ -1109,9 +1109,9 @@ def _pools(pools, page_size: int, num_pages: int, device: int) -> bytes:
     flat = []
     for t in pools:
         shape = t.shape
-        if (len(shape) < 2 or shape[0] != num_pages or (pieces := shape[1]) < 1 or page_size % pieces
+        if (len(shape) < 2 or not shape[0] == num_pages > 0 or (pieces := shape[1]) < 1 or page_size % pieces
                 or not t.is_contiguous() or t.get_device() != device):
-            if len(shape) < 2 or shape[0] != num_pages or shape[1] < 1 or page_size % shape[1]:
+            if len(shape) < 2 or not shape[0] == num_pages > 0 or shape[1] < 1 or page_size % shape[1]:
                 raise ValueError(f"a pool must have {num_pages} pages and a piece for every so many of a page's "
                                  f"{page_size} rows, not shape {tuple(shape)}")
             raise ValueError(f"a pool of shape {tuple(shape)} must be contiguous, on the call's device")
@@ -1136,9 +1136,9 @@ def pages_fork(block_table, seq_lens, refs, page_size: int, parent=None, keep=No
     length), frees (keep 0 or parent -1).  Updates block_table [B, max_blocks],
     seq_lens [B] and refs [num_pages] (int32) in place unless given outputs.
     Returns (table_out, lens_out, refs_out, ws)."""
-    B = block_table.shape[0]
+    each = (block_table.shape[0],)
     B, blocks, pages, dev = _pages_arrays(block_table, seq_lens, refs, table_out, lens_out, refs_out,
-                                          (("parent", parent, _I32, (B,)), ("keep", keep, _I32, (B,))))
+                                          (("parent", parent, _I32, each), ("keep", keep, _I32, each)))
     table_out = block_table if table_out is None else table_out
     lens_out = seq_lens if lens_out is None else lens_out
     refs_out = refs if refs_out is None else refs_out
