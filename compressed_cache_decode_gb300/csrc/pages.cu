@@ -15,7 +15,7 @@
 // there are from the workspace, so the host never waits.
 //
 // Measured on GB300, back-to-back calls of a graph: a fork of 64 x 64 blocks 4.6 us,
-// of 512 x 512 blocks 12 us; room for one more row of 256 sequences, four to a
+// of 512 x 512 blocks 9 us; room for one more row of 256 sequences, four to a
 // prompt, whose begun pages are copied (39 MB of an 8-bit cache), 17 us, of which
 // the copies' bytes are 6; a compaction that moves 1,067 pages of 426 KB (909 MB
 // read and written) 147 us, 0.93 of a measured copy's rate.  The plans are bound
@@ -26,6 +26,8 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <map>
+#include <mutex>
 
 #include "decode_plan.h"
 #include "host_cache.h"
@@ -40,7 +42,7 @@ namespace lrkv {
 namespace {
 
 constexpr int kPgThreads = 1024, kPgWarps = kPgThreads / 32;
-constexpr int kPgMaxCluster = 8;
+constexpr int kPgMaxCluster = 8, kPgForkCluster = 16;  // CTAs of a plan; of a fork, where the device allows it
 constexpr int kPgSegment = 2048;       // bytes of a page that a warp moves at a time
 constexpr int kPgCopyThreads = 256;
 
@@ -519,13 +521,43 @@ lrkv_status pages_args(PagesArgs& A, int batch, int max_blocks, int page_size, i
   return LRKV_OK;
 }
 
-// One CTA for the smallest tables, where its barriers are the cheapest.  (One against eight CTAs: 6.1 and 4.6 us for
-// 64 x 64 blocks, 59 and 12.4 us for 512 x 512.)
+// Whether a cluster of kPgForkCluster CTAs of a fork (more than the portable 8: the kernel's opt-in is set here) can
+// run on the current device.
+bool fork_cluster_fits() {
+  static std::mutex mu;
+  static std::map<int, bool> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = known.find(dev);
+  if (it != known.end()) return it->second;
+  const void* kern = reinterpret_cast<const void*>(&lrkv_pages_fork_kernel);
+  int n = 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPgForkCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPgForkCluster);
+  cfg.blockDim = dim3(kPgThreads);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool fits = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n >= 1;
+  if (!fits) cudaGetLastError();  // (eight are used then)
+  known[dev] = fits;
+  return fits;
+}
+
+// One CTA for the smallest tables, where its barriers are the cheapest.  (One against eight CTAs: 6.1 and 4.6 us for a
+// fork of 64 x 64 blocks, 59 and 12.4 us for 512 x 512.)  Sixteen for a fork, whose passes share the table out (12.1
+// and 9.1 us for 512 x 512 with prompts in common, 7.1 and 6.7 for 128 x 128, 94 and 52 for 2048 x 512); not for the
+// others, whose passes over the sequences every CTA makes for itself (16.9 and 18.2 us for 256 more rows).
 template <typename K>
-lrkv_status pages_launch(K kern, const PagesArgs& A, size_t smem, cudaStream_t stream) {
+lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cudaStream_t stream) {
   const long long work = static_cast<long long>(A.B) * A.nb + A.pages;
   int n = 1;
-  while (n < kPgMaxCluster && work > 1024ll * n) n *= 2;
+  while (n < most && work > 1024ll * n) n *= 2;
   if (smem > 48 * 1024 && ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
     return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[1];
@@ -610,7 +642,9 @@ lrkv_status lrkv_pages_fork(int batch, int max_blocks, int page_size, int num_pa
   A.lens_out = lens_out;
   A.parent = parent;
   A.keep = keep;
-  return lrkv::pages_launch(lrkv::lrkv_pages_fork_kernel, A, 0, static_cast<cudaStream_t>(stream));
+  return lrkv::pages_launch(lrkv::lrkv_pages_fork_kernel, A,
+                            lrkv::fork_cluster_fits() ? lrkv::kPgForkCluster : lrkv::kPgMaxCluster, 0,
+                            static_cast<cudaStream_t>(stream));
 }
 
 lrkv_status lrkv_pages_extend(int batch, int max_blocks, int page_size, int num_pages, const int32_t* new_lens,
@@ -630,8 +664,9 @@ lrkv_status lrkv_pages_extend(int batch, int max_blocks, int page_size, int num_
   if ((st = lrkv::copy_args(C, A, pools, n_pools)) != LRKV_OK) return st;
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
-  if ((st = lrkv::pages_launch(lrkv::lrkv_pages_extend_kernel, A, 4 * sizeof(int) * static_cast<size_t>(batch),
-                               static_cast<cudaStream_t>(stream))) != LRKV_OK)
+  if ((st = lrkv::pages_launch(lrkv::lrkv_pages_extend_kernel, A, lrkv::kPgMaxCluster,
+                               4 * sizeof(int) * static_cast<size_t>(batch), static_cast<cudaStream_t>(stream))) !=
+      LRKV_OK)
     return st;
   return lrkv::copy_launch(C, sms, static_cast<cudaStream_t>(stream));
 }
@@ -651,7 +686,8 @@ lrkv_status lrkv_pages_compact(int batch, int max_blocks, int page_size, int num
   if ((st = lrkv::copy_args(C, A, pools, n_pools)) != LRKV_OK) return st;
   const int sms = lrkv::device_sm_count();
   if (sms < 1) return LRKV_ERR_CUDA;
-  if ((st = lrkv::pages_launch(lrkv::lrkv_pages_compact_kernel, A, 0, static_cast<cudaStream_t>(stream))) != LRKV_OK)
+  if ((st = lrkv::pages_launch(lrkv::lrkv_pages_compact_kernel, A, lrkv::kPgMaxCluster, 0,
+                               static_cast<cudaStream_t>(stream))) != LRKV_OK)
     return st;
   return lrkv::copy_launch(C, sms, static_cast<cudaStream_t>(stream));
 }
