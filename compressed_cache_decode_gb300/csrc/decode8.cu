@@ -1019,20 +1019,21 @@ __global__ void __launch_bounds__(k8Threads, 1)
     const int b = x.b, n = x.n;
     float* s_o = s_w + k8Heads * n;
     if (warp < heads) {
-      float m = x.ml.x, l = 0.f;
+      float m = x.ml.x;
       for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, piece(x, i).x);
       m = warp_max(m);
-      for (int i = lane; i < n; i += 32) {
-        const float2 own = i == lane ? x.ml : piece(x, i);
-        const float y = own.x == -INFINITY ? 0.f : exp2f(own.x - m);
-        s_w[warp * n + i] = y;
-        l = fmaf(y, own.y, l);
+      auto weight = [&](float of) { return of == -INFINITY ? 0.f : exp2f(of - m); };
+      const float own = weight(x.ml.x);
+      float l = own * x.ml.y;
+      for (int i = lane + 32; i < n; i += 32) {
+        const float2 ml = piece(x, i);
+        l = fmaf(weight(ml.x), ml.y, l);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       const float inv = 1.f / l;
-      __syncwarp();
-      for (int i = lane; i < n; i += 32) s_w[warp * n + i] *= inv;
+      if (lane < n) s_w[warp * n + lane] = own * inv;
+      for (int i = lane + 32; i < n; i += 32) s_w[warp * n + i] = weight(piece(x, i).x) * inv;
       if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
     }
     __syncthreads();
