@@ -381,6 +381,8 @@ __global__ void __launch_bounds__(k8OpThreads) lrkv_decode8_operands_kernel(cons
 }
 
 // ================================================================== the scan
+// (112 registers a thread at most: the next call's operand CTAs then fit beside a scan CTA.  With 115, 8 x 4096 rows
+// took 18.6 us a call for 16.5.)
 __global__ void __launch_bounds__(k8Threads, 1)
     lrkv_decode8_kernel(const __grid_constant__ Maps8 M, const __grid_constant__ Args8 A) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -972,7 +974,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
   }
   __syncthreads();
   if (!work || gave_up) return;
-  float* s_w = reinterpret_cast<float*>(s_b + A.lift * d * pitch);  // [8][pieces] weights, then [8][W] sums
+  const int pad = round_up(W, 4);
+  float* s_w = reinterpret_cast<float*>(s_b + A.lift * d * pitch);  // [8][pieces] weights, then [8][pad] sums
   const int b_first = s_first[2], b_last = s_last[2];
   const size_t step = static_cast<size_t>(H) * W;
   constexpr int kCols = 2, kDeep = 10;  // pairs of columns a thread sums at once, pieces it has under way
@@ -1036,26 +1039,27 @@ __global__ void __launch_bounds__(k8Threads, 1)
       for (int i = lane + 32; i < n; i += 32) s_w[warp * n + i] = weight(piece(x, i).x) * inv;
       if (lane == 0 && A.lse) A.lse[static_cast<size_t>(b) * H + h0 + warp] = (m + log2f(l)) * kLn2;
     }
-    __syncthreads();
     for (int e0 = 0; 2 * e0 < heads * W; e0 += kCols * k8Threads) {  // (W is even: a pair is of one head)
+      int k[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) k[j] = min(2 * (e0 + tid + j * k8Threads) / W, heads - 1);
+      if (e0 == 0) __syncthreads();  // (the weights)
       float2 y[kCols] = {};
       for (int i0 = 0; i0 < n; i0 += kDeep) {
         if (e0 > 0 || i0 > 0) fetch(x, e0, i0);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          const int k = min(2 * (e0 + tid + j * k8Threads) / W, heads - 1);
+        for (int j = 0; j < kCols; ++j)
 #pragma unroll
           for (int i = 0; i < kDeep; ++i)
             if (i0 + i < n) {
-              y[j].x = fmaf(s_w[k * n + i0 + i], x.v[j][i].x, y[j].x);
-              y[j].y = fmaf(s_w[k * n + i0 + i], x.v[j][i].y, y[j].y);
+              y[j].x = fmaf(s_w[k[j] * n + i0 + i], x.v[j][i].x, y[j].x);
+              y[j].y = fmaf(s_w[k[j] * n + i0 + i], x.v[j][i].y, y[j].y);
             }
-        }
       }
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
         const int e = 2 * (e0 + tid + j * k8Threads);
-        if (e < heads * W) *reinterpret_cast<float2*>(s_o + e) = y[j];
+        if (e < heads * W) *reinterpret_cast<float2*>(s_o + k[j] * (pad - W) + e) = y[j];
       }
     }
     ++x.b;
@@ -1067,26 +1071,25 @@ __global__ void __launch_bounds__(k8Threads, 1)
       __syncthreads();
       for (int e = tid; e < min(A.lift, heads - k0) * d; e += k8Threads) {
         const int k = k0 + e / d;
-        const float* z = s_o + k * W + d;
+        const float* o = s_o + k * pad;
         const unsigned char* row = s_b + e * pitch;
-        float y = 0.f, y1 = 0.f;
-        if (vec == 8) {
-#pragma unroll 2
-          for (int i = 0; i < r; i += 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(row + 2 * i);
-            const float4 za = *reinterpret_cast<const float4*>(z + i), zb = *reinterpret_cast<const float4*>(z + i + 4);
-            y = fmaf(bf_hi(a.x), za.y, fmaf(bf_lo(a.x), za.x, y));
-            y1 = fmaf(bf_hi(a.y), za.w, fmaf(bf_lo(a.y), za.z, y1));
-            y = fmaf(bf_hi(a.z), zb.y, fmaf(bf_lo(a.z), zb.x, y));
-            y1 = fmaf(bf_hi(a.w), zb.w, fmaf(bf_lo(a.w), zb.z, y1));
-          }
-        } else {
-          for (int i = 0; i < r; i += 2) {
-            const uint32_t a = *reinterpret_cast<const uint32_t*>(row + 2 * i);
-            y = fmaf(bf_hi(a), z[i + 1], fmaf(bf_lo(a), z[i], y));
-          }
+        float y[4] = {o[e - (k - k0) * d], 0.f, 0.f, 0.f};
+        int i = 0;
+#pragma unroll 1
+        for (; i + 8 <= r; i += 8) {
+          const uint4 a = *reinterpret_cast<const uint4*>(row + 2 * i);
+          const float4 z = *reinterpret_cast<const float4*>(o + d + i);
+          const float4 zz = *reinterpret_cast<const float4*>(o + d + i + 4);
+          y[0] = fmaf(bf_hi(a.x), z.y, fmaf(bf_lo(a.x), z.x, y[0]));
+          y[1] = fmaf(bf_hi(a.y), z.w, fmaf(bf_lo(a.y), z.z, y[1]));
+          y[2] = fmaf(bf_hi(a.z), zz.y, fmaf(bf_lo(a.z), zz.x, y[2]));
+          y[3] = fmaf(bf_hi(a.w), zz.w, fmaf(bf_lo(a.w), zz.z, y[3]));
         }
-        out[k0 * d + e] = s_o[k * W + e - (k - k0) * d] + (y + y1);
+        for (; i < r; i += 2) {
+          const uint32_t a = *reinterpret_cast<const uint32_t*>(row + 2 * i);
+          y[1] = fmaf(bf_hi(a), o[d + i + 1], fmaf(bf_lo(a), o[d + i], y[1]));
+        }
+        out[k0 * d + e] = (y[0] + y[1]) + (y[2] + y[3]);
       }
       have_b = A.lift >= heads;  // (it stays for the next sequence)
       __syncthreads();
@@ -1122,7 +1125,7 @@ size_t decode8_bind(Args8& A, void* ws) {
 
 // Shared memory of the join: B_h^V of `lift` heads, weights of the pieces, sums.
 long long decode8_lift_bytes(const Args8& A, int lift) {
-  return 1ll * lift * A.dh * A.pitch + 4ll * k8Heads * (A.grid + A.dh + A.r);
+  return 1ll * lift * A.dh * A.pitch + 4ll * k8Heads * (A.grid + round_up(A.dh + A.r, 4));
 }
 
 lrkv_status decode8_plan(const lrkv_dims& d, int num_sms, Args8& A, size_t* bytes) {
