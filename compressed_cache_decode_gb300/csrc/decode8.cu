@@ -37,16 +37,17 @@
 // scan a call took 21 us of the host's time instead of 13.)
 //
 // Measured on GB300, back-to-back calls of a graph, scales read along with the
-// cache: 4 x 65,536 rows of 32 heads, rank 48, d_h 128: 135 us, 6.5 TB/s (0.97 of
-// a measured copy's 6.7); 32 x 1-8K rows in pages of 256, rank 56: 101 us, 5.5 TB/s;
-// 8 x 4096 rows, 16 heads, rank 28, d_h 64: 17 us, 2 TB/s; one sequence of 517 rows:
-// 11 us.  The long scans are bound by memory; what the others take beside it is
-// latency: 3-4 us until the first operands are there, 2 us per call from the last
-// product to knowing who joins, 3 us for a join.
+// cache: 4 x 65,536 rows of 32 heads, rank 48, d_h 128: 135-138 us, 6.4-6.5 TB/s
+// (0.95-0.97 of a measured copy's 6.7); 32 x 1-8K rows in pages of 256, rank 56:
+// 101-102 us, 5.5 TB/s; 8 x 4096 rows, 16 heads, rank 28, d_h 64: 16.5 us, 2 TB/s;
+// one sequence of 517 rows: 10.2 us.  The long scans are bound by memory; what the
+// others take beside it is latency: 3-4 us until the first operands are there, 2 us
+// from the last product to knowing who joins, 2-3 us for a join.
 //
 // Slower, and not taken: latents marked evict-first in L2 (4 x 65,536 rows: 154 us for 145 then), operands formed by
 // each CTA of the scan, which then need not wait for the launch before (28 us for 19 on 8 x 4096 rows: the CTAs drift
-// apart and no longer find the shared rows in L2).
+// apart and no longer find the shared rows in L2), B_h^V fetched in part or whole only once it is known who joins
+// (10.5 us for 10.2, 137.7 for 137.5).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
