@@ -576,8 +576,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
         const float4 a = *reinterpret_cast<const float4*>(&red[o][0]), e = *reinterpret_cast<const float4*>(&red[o][4]);
-        top[0] = fmaxf(top[0], a.x); top[1] = fmaxf(top[1], a.y); top[2] = fmaxf(top[2], a.z); top[3] = fmaxf(top[3], a.w);
-        tz[0] = fmaxf(tz[0], e.x); tz[1] = fmaxf(tz[1], e.y); tz[2] = fmaxf(tz[2], e.z); tz[3] = fmaxf(tz[3], e.w);
+        top[0] = fmaxf(top[0], a.x); top[1] = fmaxf(top[1], a.y);
+        top[2] = fmaxf(top[2], a.z); top[3] = fmaxf(top[3], a.w);
+        tz[0] = fmaxf(tz[0], e.x); tz[1] = fmaxf(tz[1], e.y);
+        tz[2] = fmaxf(tz[2], e.z); tz[3] = fmaxf(tz[3], e.w);
         ts = fmaxf(ts, red[o][8]);
       }
       // one online softmax per head; the probabilities times their block's value scale, over the power of two in
