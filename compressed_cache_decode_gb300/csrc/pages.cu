@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_fork_kernel(const __gri
   const int at = cl.block_rank() * kPgThreads + threadIdx.x, step = cl.num_blocks() * kPgThreads;
   const bool in_place = A.table_out == A.table;
   bool bad = false;
+  pdl_wait();  // the launch before
   if (at == 0) *A.status = 0u;
   if (A.refs_out != A.refs)
     for (int p = at; p < A.pages; p += step) A.refs_out[p] = A.refs[p];
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_extend_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = cl.block_rank() * kPgThreads + tid, step = cl.num_blocks() * kPgThreads;
   const int rest = (1 << A.shift) - 1;
+  pdl_wait();  // the launch before
   if (A.copies_follow) pdl_trigger();  // (they wait for this grid; any other launch starts when it has ended)
   bool bad = false;
   if (at == 0) *A.status = 0u;
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(kPgThreads) lrkv_pages_compact_kernel(const __
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = cl.block_rank() * kPgThreads + tid, step = cl.num_blocks() * kPgThreads;
+  pdl_wait();  // the launch before
   if (A.copies_follow) pdl_trigger();  // (they wait for this grid; any other launch starts when it has ended)
   bool bad = false;
   if (at == 0) *A.status = 0u;
@@ -560,17 +563,19 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cuda
   while (n < most && work > 1024ll * n) n *= 2;
   if (smem > 48 * 1024 && ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
     return LRKV_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(n);
   cfg.blockDim = dim3(kPgThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, A) == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
 }
 
