@@ -567,6 +567,7 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cuda
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  // (launched ahead of the end of the launch before, for which it waits: back to back 19.3 -> 17.4 us for 256 more rows)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
