@@ -561,13 +561,14 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cuda
   const long long work = static_cast<long long>(A.B) * A.nb + A.pages;
   int n = 1;
   while (n < most && work > 1024ll * n) n *= 2;
-  if (smem > 48 * 1024 && ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
+  if (smem > 48 * 1024 &&
+      ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
     return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  // (launched ahead of the end of the launch before, for which it waits: back to back 19.3 -> 17.4 us for 256 more rows)
+  // (launched ahead of the end of the launch before, for which it waits: 19.3 -> 17.4 us for 256 more rows)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
