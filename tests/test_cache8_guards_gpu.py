@@ -124,6 +124,65 @@ def test_a_captured_step_replayed_on_other_contents():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_write_what_a_decode_still_reads(captured):
+    """A decode, then rows quantized over its cache, its lengths cut to nothing, its pages moved: none of them waits
+    on the host, each waits for the decode."""
+    B, H, dh, r, L, page = 4, 16, 128, 48, 8192, 256
+    lens = (8192, 8000, 5000, 8192)
+    case = C.Case(B, H, dh, r, L, lens, seed=11)
+    q, cache, b_k, b_v, n, table = case.cuda(page, seed=3, garbage=False)
+    pages = cache.k_s.shape[0]
+    refs = torch.zeros(pages, dtype=torch.int32)
+    for b, k in enumerate(lens):
+        refs[table[b, :-(-k // page)].cpu().long()] += 1
+    refs = refs.cuda()
+    dims = lrkv.make_dims(B, H, dh, r, L, torch.bfloat16)
+    ws, pws = lrkv.decode8_workspace(dims), lrkv.pages_workspace(B, L // page, pages)
+    rows = [torch.zeros(B, 64, *((H, r) if z else (dh,)), dtype=torch.bfloat16, device="cuda") for z in (0, 0, 1, 1)]
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    outs = [torch.empty(B, H, dh, device="cuda") for _ in range(4)]
+    first, other = (torch.empty(B, H, device="cuda") for _ in range(2))
+
+    def decode(o):
+        lrkv.decode8(q, cache, b_k, b_v, n, block_table=table, out=o, lse=first if o is outs[0] else other, ws=ws)
+
+    def run():
+        decode(outs[0])
+        lrkv.pages_compact(cache.pools(), table, n, refs, page, ws=pws)
+        decode(outs[1])
+        lrkv.quantize(*rows, zero, cache, block_table=table)   # the first rows to zeros
+        decode(outs[2])
+        lrkv.pages_fork(table, n, refs, page, keep=zero, ws=pws)
+        decode(outs[3])
+
+    state = [*cache.pools(), table, n, refs]
+    saved = [t.clone() for t in state]
+
+    def restore():
+        for t, x in zip(state, saved):
+            t.view(torch.uint8).copy_(x.view(torch.uint8))
+
+    run()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    case.check(want[0], first, pairs={(b, 3 * b) for b in range(B)})
+    assert torch.equal(want[0], want[1]) and not torch.equal(want[1], want[2]) and not want[3].any()
+    restore()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        run = g.replay
+    for _ in range(5):
+        restore()
+        for o in outs:
+            o.fill_(7)
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 @pytest.mark.parametrize("heads, head_dim, rank, page", [(32, 128, 48, 0), (16, 64, 28, 0), (8, 256, 64, 64)])
 def test_waits_that_run_out(heads, head_dim, rank, page, monkeypatch):
     B, L = 2, 32768
