@@ -36,7 +36,8 @@ inline int device_sm_count() {
 
 // Raises `func`'s dynamic shared-memory limit to at least `bytes` on the
 // current device (a no-op when an earlier call set as much) and, with
-// `max_shared_carveout`, asks for the largest shared-memory carveout.
+// `max_shared_carveout`, asks for the largest shared-memory carveout.  The 48 KB
+// that need no raising are those of the dynamic and the static part together.
 inline cudaError_t ensure_kernel_smem(const void* func, int bytes, bool max_shared_carveout = false) {
   static std::mutex mu;
   static std::map<std::tuple<int, const void*>, int> set_bytes;
@@ -47,8 +48,10 @@ inline cudaError_t ensure_kernel_smem(const void* func, int bytes, bool max_shar
   auto key = std::make_tuple(dev, func);
   auto it = set_bytes.find(key);
   if (it != set_bytes.end() && it->second >= bytes) return cudaSuccess;
-  if (bytes > 48 * 1024 && (e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) !=
-                               cudaSuccess)
+  cudaFuncAttributes attr;
+  if ((e = cudaFuncGetAttributes(&attr, func)) != cudaSuccess) return e;
+  if (bytes + attr.sharedSizeBytes > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     return e;
   if (max_shared_carveout &&
       (e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,

@@ -561,7 +561,7 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cuda
   const long long work = static_cast<long long>(A.B) * A.nb + A.pages;
   int n = 1;
   while (n < most && work > 1024ll * n) n *= 2;
-  if (smem > 48 * 1024 &&
+  if (smem > 32 * 1024 &&  // (with the static part it may pass 48 KB)
       ensure_kernel_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)) != cudaSuccess)
     return LRKV_ERR_CUDA;
   cudaLaunchAttribute attr[2];
