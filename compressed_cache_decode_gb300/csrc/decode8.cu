@@ -37,10 +37,10 @@
 // scan a call took 21 us of the host's time instead of 13.)
 //
 // Measured on GB300, back-to-back calls of a graph, scales read along with the
-// cache: 4 x 65,536 rows of 32 heads, rank 48, d_h 128: 135-138 us, 6.4-6.5 TB/s
+// cache: 4 x 65,536 rows of 32 heads, rank 48, d_h 128: 135-139 us, 6.3-6.5 TB/s
 // (0.95-0.97 of a measured copy's 6.7); 32 x 1-8K rows in pages of 256, rank 56:
-// 101-102 us, 5.5 TB/s; 8 x 4096 rows, 16 heads, rank 28, d_h 64: 16.5 us, 2 TB/s;
-// one sequence of 517 rows: 10.2 us.  The long scans are bound by memory; what the
+// 101-103 us, 5.5 TB/s; 8 x 4096 rows, 16 heads, rank 28, d_h 64: 17.2 us, 2 TB/s;
+// one sequence of 517 rows: 10.4 us.  The long scans are bound by memory; what the
 // others take beside it is latency: 3-4 us until the first operands are there, 2 us
 // from the last product to knowing who joins, 2-3 us for a join.
 //
@@ -169,14 +169,33 @@ __device__ __forceinline__ float join_values(const uint32_t* v, const uint32_t* 
   for (int i = 3; i >= 0; --i) s = fmaf(s, 0.0625f, __uint_as_float(v[4 * i + k]));
   return s;
 }
-// 2^-e of a positive x in [2^e, 2^(e + 1)) (0: 2^127), and 2^e (0: 0).
+// 2^-e of x in [2^e, 2^(e + 1)) (0: 2^127), and 2^e (0: 0), of numbers far from the ends of fp32's range.
 __device__ __forceinline__ float down_to_one(float x) {
   return __uint_as_float(0x7f000000u - (__float_as_uint(x) & 0x7f800000u));
 }
 __device__ __forceinline__ float power_in(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
+// m in [1, 2) and a whole number e with x = m 2^e, of any positive finite x (subnormal ones too); 0: m = 0, e = -191.
+// Through a power of two that makes x normal and 2^-e representable.
+__device__ __forceinline__ float split_scale(float x, float& e) {
+  const bool small = x < 1.f;
+  const float y = x * (small ? 0x1p64f : 0x1p-64f);
+  const uint32_t u = __float_as_uint(y);
+  e = __uint_as_float(0x4b000000u | u >> 23) - (small ? 0x1p23f + 191.f : 0x1p23f + 63.f);  // (2^23 + the field, exact)
+  return y * __uint_as_float(0x7f000000u - (u & 0x7f800000u));
+}
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ void bar_named(int id, int threads) {
@@ -396,8 +415,10 @@ __global__ void __launch_bounds__(k8Threads, 1)
   __shared__ int s_fail, s_bad, s_images, s_copies[2];  // copies issued
   // the first sequence's first CTA, pieces (0: another CTA joins them) and number; the last one's
   __shared__ int s_first[3], s_last[3];
-  __shared__ __align__(16) float s_red[2][2][4][12];  // [tile parity][half][warp]: maxima of 4 scores, 4 + 1 scales
-  __shared__ float s_fac[4][20];                      // [tile % 4]: alpha[8], latent scale[8], shared scale
+  // [tile parity][half][warp]: maxima of 4 scores, largest and smallest value scale of the shared rows, of the latents;
+  // [half][warp]: maxima of 4 + 4 products
+  __shared__ __align__(16) float s_red[2][2][4][8], s_top[2][4][8];
+  __shared__ float s_fac[4][24];                      // [tile % 4]: alpha[8], the products' powers: latents[8], shared[8]
   __shared__ float s_sum[2][4][4];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   volatile int* fail = &s_fail;
@@ -535,9 +556,19 @@ __global__ void __launch_bounds__(k8Threads, 1)
         if (lane == 0) mbar_arrive_cta(&iempty[piece & 1]);
       }
       const int rows = min(k8Rows, L - k8Rows * w.t0);
-      float ks = nks, vs = nvs, kz[4], vz[4];
+      float ks = nks, vs = nvs, kz[4], vz[4], zmax = 0.f, zmin = INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) { kz[k] = nkz[k]; vz[k] = nvz[k]; }
+      for (int k = 0; k < 4; ++k) {
+        kz[k] = nkz[k];
+        vz[k] = nvz[k];
+        if (row < rows && r > 0 && hb + k < H) {
+          zmax = fmaxf(zmax, vz[k]);
+          zmin = fminf(zmin, vz[k]);
+        }
+      }
+      zmax = warp_max(zmax);
+      zmin = warp_min(zmin);
+      float smax = warp_max(row < rows ? vs : 0.f), smin = warp_min(row < rows ? vs : INFINITY);
       if (nmore) load_scales(nx);
 
       // the scores
@@ -557,20 +588,18 @@ __global__ void __launch_bounds__(k8Threads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&sempty[i & 1]);
-      float s[4], top[4], tz[4], ts = warp_max(row < rows ? vs : 0.f);
+      float s[4], top[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float x = join<4>(dq + 4 * k) * (fq[k] * ks), y = join<6>(dz + 6 * k) * (fz[k] * kz[k]);
         s[k] = row < rows ? x + y : -INFINITY;
         top[k] = warp_max(s[k]);
-        tz[k] = warp_max(row < rows ? vz[k] : 0.f);
       }
       // maxima over the tile
-      float(*red)[12] = s_red[i & 1][half];
+      float(*red)[8] = s_red[i & 1][half];
       if (lane == 0) {
         *reinterpret_cast<float4*>(&red[quad][0]) = make_float4(top[0], top[1], top[2], top[3]);
-        *reinterpret_cast<float4*>(&red[quad][4]) = make_float4(tz[0], tz[1], tz[2], tz[3]);
-        red[quad][8] = ts;
+        *reinterpret_cast<float4*>(&red[quad][4]) = make_float4(smax, smin, zmax, zmin);
       }
       bar_named(1 + half, 128);
 #pragma unroll
@@ -578,36 +607,83 @@ __global__ void __launch_bounds__(k8Threads, 1)
         const float4 a = *reinterpret_cast<const float4*>(&red[o][0]), e = *reinterpret_cast<const float4*>(&red[o][4]);
         top[0] = fmaxf(top[0], a.x); top[1] = fmaxf(top[1], a.y);
         top[2] = fmaxf(top[2], a.z); top[3] = fmaxf(top[3], a.w);
-        tz[0] = fmaxf(tz[0], e.x); tz[1] = fmaxf(tz[1], e.y);
-        tz[2] = fmaxf(tz[2], e.z); tz[3] = fmaxf(tz[3], e.w);
-        ts = fmaxf(ts, red[o][8]);
+        smax = fmaxf(smax, e.x); smin = fminf(smin, e.y);
+        zmax = fmaxf(zmax, e.z); zmin = fminf(zmin, e.w);
       }
-      // one online softmax per head; the probabilities times their block's value scale, over the power of two in
-      // the tile's largest: less than 2, brought to 256
-      float xs[4], xz[4], alpha[4];
-      const float us = vs * down_to_one(ts) * 128.f;
+      // one online softmax per head: maxima and sums against those of the tiles before, probabilities against the tile's
+      float xs[4], xz[4], ps[4], pz[4], alpha[4], beta[4], below = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float mx = fmaxf(m[k], top[k]);
+        top[k] = fmaxf(top[k], -0x1.fffffep127f);  // (a tile of scores that are -inf: no weight)
+        const float mx = fmaxf(m[k], top[k]), p = row < rows ? exp2f(s[k] - top[k]) : 0.f;
         alpha[k] = m[k] == -INFINITY ? 0.f : exp2f(m[k] - mx);
+        beta[k] = exp2f(top[k] - mx);
+        below = fminf(below, top[k] - mx);
         m[k] = mx;
-        const float p = row < rows ? exp2f(s[k] - mx) : 0.f;
-        l[k] = fmaf(l[k], alpha[k], p);
-        xs[k] = p * us;
-        xz[k] = p * (vz[k] * down_to_one(tz[k]) * 128.f);
-        if (row >= rows) xs[k] = xz[k] = 0.f;
+        l[k] = fmaf(l[k], alpha[k], p * beta[k]);
+        xs[k] = xz[k] = p;
       }
+      // The probabilities times their block's value scale, over powers of two (of the shared values, of the latents)
+      // that bring the tile's largest product of a head to between 2 and 256.  Scales within 2^6 of one another: over
+      // the power in the largest scale.
+      if (smax <= 64.f * smin && zmax <= 64.f * zmin && fmaxf(smax, zmax) < 0x1p100f && fminf(smin, zmin) > 0x1p-100f &&
+          below > -64.f) {
+        const float us = vs * (down_to_one(smax) * 128.f), uz = down_to_one(zmax) * 128.f;
+        const float fs = power_in(smax) * (1.f / 128.f), fz = power_in(zmax) * (1.f / 128.f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          xs[k] *= us;
+          xz[k] *= vz[k] * uz;
+          ps[k] = fs * beta[k];
+          pz[k] = fz * beta[k];
+        }
+      } else {
+        // Any scales, as m 2^e: over a power of two 2^E next to the largest 2^(x + e), x = log2 of the probability, found
+        // in a turn of its own.  The probability, which may be too small for a number, does not enter by itself.  (E
+        // from -119 on: a 2^-30th of 2^-126 is no number any more.  All tiles this way: 19.5 us for 8 x 4096 rows, 16
+        // heads, rank 28, d_h 64, for 17.2; with the turn taken along with that of the scores: 17.7.)
+        float es, ez[4];
+        const float ms = split_scale(vs, es) * 128.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          vz[k] = split_scale(vz[k], ez[k]) * 128.f;
+          s[k] -= m[k];
+          ps[k] = warp_max(s[k] + es);
+          pz[k] = warp_max(s[k] + ez[k]);
+        }
+        if (lane == 0) {
+          *reinterpret_cast<float4*>(&s_top[half][quad][0]) = make_float4(ps[0], ps[1], ps[2], ps[3]);
+          *reinterpret_cast<float4*>(&s_top[half][quad][4]) = make_float4(pz[0], pz[1], pz[2], pz[3]);
+        }
+        bar_named(1 + half, 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ps[k] = pz[k] = -119.f;
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {  // (NaN is left out)
+            ps[k] = fmaxf(ps[k], ceilf(s_top[half][o][k]));
+            pz[k] = fmaxf(pz[k], ceilf(s_top[half][o][4 + k]));
+          }
+          xs[k] = ms * exp2_ftz(s[k] + (es - ps[k]));
+          xz[k] = vz[k] * exp2_ftz(s[k] + (ez[k] - pz[k]));
+          ps[k] = pow2(static_cast<int>(ps[k]) - 7);
+          pz[k] = pow2(static_cast<int>(pz[k]) - 7);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (row >= rows) xs[k] = xz[k] = 0.f;
       // into the operand of the value products, once the ones before are done with it
       if (i > 1) wait8_warp(&pv[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, fail, A.wait_limit);
-      unsigned char* ps = smem + A.off_p + (i & 1) * (2 * k8PBytes) + (row >> 3) * k8PRows + (row & 7) * 16;
+      unsigned char* to = smem + A.off_p + (i & 1) * (2 * k8PBytes) + (row >> 3) * k8PRows + (row & 7) * 16;
       if (quad == 0 && lane == 0) {
         float* fac = s_fac[i & 3];  // (tile i - 4 is read: the products of i - 2 waited for those of i - 3 to be)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           fac[4 * half + k] = alpha[k];
-          fac[8 + 4 * half + k] = power_in(tz[k]) * (1.f / 128.f);
+          fac[8 + 4 * half + k] = pz[k];
+          fac[16 + 4 * half + k] = ps[k];
         }
-        if (half == 0) fac[16] = power_in(ts) * (1.f / 128.f);
       }
       auto put = [&](float* x, unsigned char* p) {
         uint32_t v[k8Parts];
@@ -626,8 +702,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
         *reinterpret_cast<uint4*>(p + half * k8PGroup) = make_uint4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<uint2*>(p + 2 * k8PGroup + 8 * half) = make_uint2(v[4], v[5]);
       };
-      put(xs, ps);
-      if (r > 0) put(xz, ps + k8PBytes);
+      put(xs, to);
+      if (r > 0) put(xz, to + k8PBytes);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&pfull[i & 1]);
@@ -691,7 +767,6 @@ __global__ void __launch_bounds__(k8Threads, 1)
       wait8_warp(&pv[i & 1], static_cast<uint32_t>(i >> 1) & 1u, fail, A.wait_limit);
       tc_fence_after();
       const float* fac = s_fac[i & 3];
-      const float us = fac[16];
 #pragma unroll
       for (int j = 0; j < k8MaxD; ++j) {
         if (j >= nd) break;
@@ -703,7 +778,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         let_go(j);
 #pragma unroll
         for (int k = 0; k < k8Heads; ++k)
-          os[j][k] = fmaf(os[j][k], fac[k], join_values(v + 16 * (k >> 2), v + 32 + 8 * (k >> 2), k & 3) * us);
+          os[j][k] = fmaf(os[j][k], fac[k], join_values(v + 16 * (k >> 2), v + 32 + 8 * (k >> 2), k & 3) * fac[16 + k]);
       }
 #pragma unroll
       for (int j = 0; j < k8MaxZ; ++j) {

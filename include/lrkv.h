@@ -644,9 +644,13 @@ typedef struct {
  * heads <= 256; page_size a power of two >= 16; block_table NULL: contiguous.
  *
  * lrkv_decode8 is lrkv_decode over an 8-bit cache (block_table NULL:
- * contiguous).  The cache's numbers enter the products as they are; q, q B^K
- * and the probabilities are split so that no product loses fp32 accuracy, and
- * out is held to it.  Scales: any finite positive numbers.  Rows at or past
+ * contiguous).  The cache's numbers enter the products as they are; what
+ * multiplies them is split into e4m3 parts that hold 24 bits, but that what is
+ * small beside the largest of its kind is off by up to 2^-29 (q of a head),
+ * 2^-37 (q B^K of a head) and 2^-30 (probability times value scale, of 128 rows
+ * that begin at a multiple of 128) of that largest one.  Scales: any finite
+ * positive numbers; where a score, the largest q or q B^K times a key scale or
+ * a sum of values leaves fp32's range, so do outputs.  Rows at or past
  * seq_lens[b] and the scales of blocks past them may hold anything; a NaN in a
  * visible row may make any output of its sequence NaN.  Supported: dtype BF16
  * (of q and the bases), and the shapes of lrkv_quantize; b_k and b_v 4-byte
