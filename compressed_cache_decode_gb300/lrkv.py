@@ -984,11 +984,12 @@ class Cache8:
     rows, H, r] (float8_e4m3fn) with the scales of their blocks of BLOCK8 rows,
     [lead, ceil(rows / BLOCK8)] and [lead, ceil(rows / BLOCK8), H] fp32; lead x
     rows is batch x max_len, or pages x page_size of a paged cache.  Rank 0: the
-    z tensors are None.  The tensors are checked once, here; they stay the
-    cache's as long as it is used."""
+    z tensors are None.  The tensors are checked once, here: another tensor needs
+    another Cache8, attributes cannot be set, and a tensor's own memory is not to
+    be exchanged (set_, .data) while the cache is used."""
 
     __slots__ = ("k_s", "v_s", "z_k", "z_v", "k_s_scale", "v_s_scale", "z_k_scale", "z_v_scale", "device", "shape",
-                 "ref")
+                 "ref", "at", "held")
     NAMES = __slots__[:8]
 
     def __init__(self, k_s, v_s, z_k, z_v, k_s_scale, v_s_scale, z_k_scale, z_v_scale):
@@ -1001,17 +1002,28 @@ class Cache8:
         blocks = (lead, -(-rows // BLOCK8))
         row, z = (lead, rows, dh), (lead, rows, H, r)
         shapes = (row, row, z, z, blocks, blocks, blocks + (H,), blocks + (H,))
-        self.device = k_s.get_device()
-        _check(self.device, *[("cache." + n, t, _E4M3 if i < 4 else _F32, s)
-                              for i, (n, t, s) in enumerate(zip(self.NAMES, given, shapes))])
-        for n, t in zip(self.NAMES, given):
-            object.__setattr__(self, n, t)
-        self.shape = (lead, rows, H, dh, r)
-        self.ref = ctypes.byref(lrkv_cache8(*[_ptr(t) for t in given]))
+        device = k_s.get_device()
+        _check(device, *[("cache." + n, t, _E4M3 if i < 4 else _F32, s)
+                         for i, (n, t, s) in enumerate(zip(self.NAMES, given, shapes))])
+        at = tuple(_ptr(t) for t in given)
+        # (the storages: the memory that `ref` names lasts as long as this does)
+        values = given + (device, (lead, rows, H, dh, r), ctypes.byref(lrkv_cache8(*at)), at,
+                          [t.untyped_storage() for t in given if t is not None])
+        for n, v in zip(self.__slots__, values):
+            object.__setattr__(self, n, v)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"the {name} of a Cache8 stays what it was made with: make another Cache8")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
 
     def pools(self):
         """The tensors, for the pages_* calls (of a paged cache)."""
-        return [t for t in (getattr(self, n) for n in self.NAMES) if t is not None]
+        given = [getattr(self, n) for n in self.NAMES]
+        if tuple(_ptr(t) for t in given) != self.at:
+            raise ValueError("a tensor of the cache no longer has the memory that the cache was made with")
+        return [t for t in given if t is not None]
 
     def rows(self, block_table, batch: int, heads: int, head_dim: int, rank: int, device: int):
         """(max_len, page_size, num_pages) of a call with these sizes."""
