@@ -128,6 +128,13 @@ __device__ __forceinline__ void store8(unsigned char* p, const float* x) {
   }
 }
 
+// y, the fp32 number nearest to y + rest, moved by its last bit towards it where that makes the bit 1: never a tie of
+// fewer bits then, so that a second rounding gives what one of y + rest would.
+__device__ __forceinline__ float sticky(float y, float rest) {
+  const uint32_t u = __float_as_uint(y);
+  if ((u & 1u) != 0u || y == 0.f || !(rest != 0.f) || !(fabsf(rest) <= 3e38f)) return y;
+  return __uint_as_float((rest > 0.f) == (y > 0.f) ? u + 1u : u - 1u);
+}
 // The smallest power of two s, 2^-126 at least, with amax <= 448 s = 1.75 * 2^8 s (bits of amax, finite).
 __device__ __forceinline__ float scale_for(uint32_t amax) {
   const int e = static_cast<int>(amax >> 23) - 127;  // amax = 1.m * 2^e
@@ -219,8 +226,13 @@ __global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant_
       if (i >= lo && i < hi) {
         float y[V];
         if (decltype(divide)::value) {
+          // (in a range where what the quotient leaves is a number)
+          const float up = s < 0x1p-60f ? 0x1p64f : 1.f, d = s * up;
 #pragma unroll
-          for (int k = 0; k < V; ++k) y[k] = x[i].get(k) / s;
+          for (int k = 0; k < V; ++k) {
+            const float f = x[i].get(k) * up, p = f / d;
+            y[k] = sticky(p, fmaf(-p, d, f));
+          }
         } else {
           x[i].scaled(inv, y);
         }
@@ -231,7 +243,7 @@ __global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant_
   if ((__float_as_uint(s) & 0x7fffffu) == 0u) put(std::false_type{});
   else put(std::true_type{});
   if (lo > 0 && s > before) {  // the earlier rows, to the larger scale
-    const float ratio = before / s;
+    const float ratio = before / s;  // (exact: s is a power of two)
     for (int i = 0; i < lo; ++i) {
       unsigned char* p = dst + static_cast<size_t>(i) * width;
       float y[V];
@@ -240,6 +252,8 @@ __global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant_
         const float2 f = from_e4m3x2(*reinterpret_cast<const uint16_t*>(p + k));
         y[k] = f.x * ratio;
         y[k + 1] = f.y * ratio;
+        y[k] = sticky(y[k], fmaf(f.x, ratio, -y[k]));
+        y[k + 1] = sticky(y[k + 1], fmaf(f.y, ratio, -y[k + 1]));
       }
       store8<V>(p, y);
     }
