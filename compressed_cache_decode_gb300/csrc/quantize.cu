@@ -14,15 +14,14 @@
 // its scale unless the new rows need a larger one; then its earlier rows are
 // rounded anew in place.
 //
-// Measured on GB300, back-to-back calls: 8 prompts of 4-8K rows, bf16, 32 heads
-// of rank 48, d_h 128: 81 us, 6.4 TB/s read and written (0.96 of a measured
-// copy's 6.7); 32 decode steps, rank 56, in pages: 3.6 us, a launch's latency
-// (a caller's own 10 us a call are the bound there).
+// Measured on GB300, back-to-back calls of a graph: 8 prompts of 4-8K rows, bf16,
+// 32 heads of rank 48, d_h 128: 80.3 us, 6.5 TB/s read and written (0.97 of a
+// measured copy's 6.7); 32 decode steps, rank 56, in pages: 3.0 us, a launch's
+// latency (a caller's own 10 us a call are the bound there).
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "cache8.h"
 #include "decode_plan.h"
@@ -219,29 +218,31 @@ __global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant_
   const float s = fmaxf(before, scale_for(s_amax[item]));
   if (owner) scale[at] = s;
   unsigned char* dst = A.cache[which] + row0 * width + col;
-  const float inv = 1.f / s;
-  const auto put = [&](auto divide) {
+  if ((__float_as_uint(s) & 0x7fffffu) == 0u) {  // a power of two, as all scales but a caller's own are: x / s is x (1 / s)
+    const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < kBlock8; ++i)
       if (i >= lo && i < hi) {
         float y[V];
-        if (decltype(divide)::value) {
-          // (in a range where what the quotient leaves is a number)
-          const float up = s < 0x1p-60f ? 0x1p64f : 1.f, d = s * up;
-#pragma unroll
-          for (int k = 0; k < V; ++k) {
-            const float f = x[i].get(k) * up, p = f / d;
-            y[k] = sticky(p, fmaf(-p, d, f));
-          }
-        } else {
-          x[i].scaled(inv, y);
-        }
+        x[i].scaled(inv, y);
         store8<V>(dst + static_cast<size_t>(i) * width, y);
       }
-  };
-  // x / s is x * (1 / s) where s is a power of two, as all scales but a caller's own are
-  if ((__float_as_uint(s) & 0x7fffffu) == 0u) put(std::false_type{});
-  else put(std::true_type{});
+  } else {  // (the rows once more, one at a time, so that this side takes no registers: 81.5 us with it on `x`, 80.3 so)
+    // (in a range where what the quotient leaves is a number)
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.f, d = s * up;
+#pragma unroll 1
+    for (int i = lo; i < hi; ++i) {
+      Vec<T, V> v;
+      float y[V];
+      v.load(src + static_cast<long long>(i) * width);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float f = v.get(k) * up, p = f / d;
+        y[k] = sticky(p, fmaf(-p, d, f));
+      }
+      store8<V>(dst + static_cast<size_t>(i) * width, y);
+    }
+  }
   if (lo > 0 && s > before) {  // the earlier rows, to the larger scale
     const float ratio = before / s;  // (exact: s is a power of two)
     for (int i = 0; i < lo; ++i) {
