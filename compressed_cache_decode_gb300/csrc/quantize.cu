@@ -157,8 +157,10 @@ __global__ void __maxnreg__(kQzRegs) lrkv_quantize_kernel(const __grid_constant_
   const int end = static_cast<int>(min(max(start + n, 0ll), static_cast<long long>(A.max_len)));
   bad = bad || (n > 0 && (start < 0 || start + n > A.max_len));
   if (bad && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) record_status(A.status, kDevBounds);
-  const int base = (first / kBlock8 + static_cast<int>(blockIdx.x)) * kBlock8;  // the block's first row
-  if (base >= end) return;
+  // (blocks are compared, not rows: a grid may go on past row 2^31)
+  const int block = first / kBlock8 + static_cast<int>(blockIdx.x);
+  if (end == 0 || block > (end - 1) / kBlock8) return;
+  const int base = block * kBlock8;  // the block's first row
   // where the block lies
   size_t row0 = static_cast<size_t>(b) * A.max_len + base;
   size_t blk = static_cast<size_t>(b) * ((A.max_len + kBlock8 - 1) / kBlock8) + base / kBlock8;
