@@ -1037,7 +1037,10 @@ class Cache8:
             if lead != batch:
                 raise ValueError(f"the cache holds {lead} sequences, the call {batch}")
             return rows, 0, 0
-        return block_table.shape[1] * rows, rows, lead
+        max_len = block_table.shape[1] * rows
+        if max_len > 0x7fffffff:   # (the library's int)
+            raise ValueError(f"the table's {max_len} rows a sequence are more than 2^31 - 1")
+        return max_len, rows, lead
 
 
 def empty_cache8(lead: int, rows: int, heads: int, head_dim: int, rank: int, device="cuda") -> Cache8:

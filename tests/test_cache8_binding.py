@@ -52,3 +52,22 @@ def test_memory_exchanged_under_a_tensor_is_kept_and_noticed(parts):
 def test_a_cache_without_latents(parts):
     cache = lrkv.Cache8(**dict(parts, z_k=None, z_v=None, z_k_scale=None, z_v_scale=None))
     assert len(cache.pools()) == 4 and held(cache)[2] is None and cache.shape == (B, L, 0, DH, 0)
+
+
+def test_a_table_of_more_rows_than_an_int_holds(monkeypatch):
+    """2^32 + 2^20 rows a sequence would reach the library as 2^20."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    rows = torch.zeros(1, 1 << 20, 16, dtype=E4M3)
+    scales = torch.ones(1, 1 << 16)
+    cache = lrkv.Cache8(rows, rows, None, None, scales, scales, None, None)
+    for blocks, fits in ((2047, True), (2048, False), (4097, False)):
+        table = torch.zeros(2, blocks, dtype=torch.int32)
+        if fits:
+            assert cache.rows(table, 2, 1, 16, 0, 0) == (blocks << 20, 1 << 20, 1)
+            continue
+        with pytest.raises(ValueError, match="more than"):
+            lrkv.decode8(torch.zeros(2, 1, 16).bfloat16(), cache, None, None, torch.ones(2, dtype=torch.int32),
+                         block_table=table)
+        with pytest.raises(ValueError, match="more than"):
+            new = torch.zeros(2, 1, 16).bfloat16()
+            lrkv.quantize(new, new, None, None, torch.ones(2, dtype=torch.int32), cache, block_table=table)
