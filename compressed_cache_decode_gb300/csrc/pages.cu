@@ -14,9 +14,9 @@
 // memory: a warp per 2 KB segment of a page of a pool.  It reads how many
 // there are from the workspace, so the host never waits.
 //
-// Measured on GB300, back-to-back calls of a graph: a fork of 64 x 64 blocks 4.6 us,
-// of 512 x 512 blocks 9 us; room for one more row of 256 sequences, four to a
-// prompt, whose begun pages are copied (39 MB of an 8-bit cache), 17 us, of which
+// Measured on GB300, back-to-back calls of a graph: a fork of 64 x 64 blocks 4.4 us,
+// of 512 x 512 blocks 9.2 us; room for one more row of 256 sequences, four to a
+// prompt, whose begun pages are copied (39 MB of an 8-bit cache), 16.7 us, of which
 // the copies' bytes are 6; a compaction that moves 1,067 pages of 426 KB (909 MB
 // read and written) 147 us, 0.93 of a measured copy's rate.  The plans are bound
 // by latency: each pass waits for the loads of the one before.
@@ -552,10 +552,10 @@ bool fork_cluster_fits() {
   return fits;
 }
 
-// One CTA for the smallest tables, where its barriers are the cheapest.  (One against eight CTAs: 6.1 and 4.6 us for a
-// fork of 64 x 64 blocks, 59 and 12.4 us for 512 x 512.)  Sixteen for a fork, whose passes share the table out (12.1
-// and 9.1 us for 512 x 512 with prompts in common, 7.1 and 6.7 for 128 x 128, 94 and 52 for 2048 x 512); not for the
-// others, whose passes over the sequences every CTA makes for itself (16.9 and 18.2 us for 256 more rows).
+// One CTA for the smallest tables, where its barriers are the cheapest.  (One against eight CTAs: 5.9 and 4.4 us for a
+// fork of 64 x 64 blocks, 59 and 12.3 us for 512 x 512 with prompts in common.)  Sixteen for a fork, whose passes share
+// the table out (12.3 and 9.2 us for 512 x 512); not for the others, whose passes over the sequences every CTA makes
+// for itself (an extension for 256 more rows took 1.3 us longer).
 template <typename K>
 lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cudaStream_t stream) {
   const long long work = static_cast<long long>(A.B) * A.nb + A.pages;
@@ -568,7 +568,9 @@ lrkv_status pages_launch(K kern, const PagesArgs& A, int most, size_t smem, cuda
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = n;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  // (launched ahead of the end of the launch before, for which it waits: 19.3 -> 17.4 us for 256 more rows)
+  // (launched ahead of the end of the launch before, for which it waits: 0.2 to 0.4 us less of every call in a graph,
+  // 17.1 -> 16.7 for 256 more rows; one by one from Python 20.5 -> 18.4 to 19.8 there, 149-152 -> 145-147 for 4,269
+  // pages, nothing where the host is the bound)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};

@@ -1092,7 +1092,8 @@ def decode8(q, cache: Cache8, b_k, b_v, seq_lens, block_table=None, scale: float
     max_len, page_size, num_pages = cache.rows(block_table, B, H, dh, r, dev)
     dims = make_dims(B, H, dh, r, max_len, dt, scale)
     _check(dev, ("q", q, dt, (B, H, dh)), ("b_k", b_k if r else None, dt, basis),
-           ("b_v", b_v if r else None, dt, basis), ("seq_lens", seq_lens, _I32, (B,)), ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
+           ("b_v", b_v if r else None, dt, basis), ("seq_lens", seq_lens, _I32, (B,)),
+           ("block_table", block_table, _I32, (B, max_len // (page_size or 1))),
            ("out", out, _F32, (B, H, dh)), ("lse", lse, _F32, (B, H)))
     with _On(q, stream) as on:
         if out is None:

@@ -58,8 +58,9 @@
  *    ends; so do all calls here that write a decode's input, but for
  *    lrkv_decode_step, whose new rows are sure to be seen by its own decode
  *    and by calls that wait (the next lrkv_decode_step, lrkv_append,
- *    lrkv_evict, lrkv_prefill_weights).  A kernel of the caller's that signals
- *    early must not write q, positions, lengths, tables or rows afterwards.
+ *    lrkv_evict, lrkv_prefill_weights, lrkv_quantize, lrkv_pages_*).  A kernel
+ *    of the caller's that signals early must not write q, positions, lengths,
+ *    tables or rows afterwards.
  *  * Planning.  Launch grids and workspace sizes follow the current device's
  *    SM count, or LRKV_SM_COUNT when that environment variable holds a
  *    positive number (read at each call: workspace sizes without a device;
@@ -535,8 +536,8 @@ lrkv_status lrkv_prefill_weights(const lrkv_dims* dims, int q_len, int window, c
  * after an eviction the row index no longer tells the age.
  * block_table as in lrkv_decode_paged (NULL: contiguous), here with any
  * power-of-two page_size; pages past a sequence's last kept row are free after
- * the call.  Pages that are written must belong to one sequence only.  A row
- * whose block names no page of the pool is not moved (its weight, age and
+ * the call.  Pages that are written must belong to one sequence only (not to
+ * several after lrkv_pages_fork).  A row whose block names no page of the pool is not moved (its weight, age and
  * kept entry are) and sets LRKV_ERR_DEVICE_BOUNDS, as a length outside
  * [0, max_len], which is clamped, does.
  * dtype BF16 or F32; rows of a multiple of 16 bytes; batch max_len at most
@@ -641,7 +642,10 @@ typedef struct {
  * whose status word the call ORs its bits into (the caller clears it).
  * dims->dtype (BF16 or F32) is that of the rows.  Supported: head_dim a
  * multiple of 16 up to 256, rank even up to 64, heads rank a multiple of 16,
- * heads <= 256; page_size a power of two >= 16; block_table NULL: contiguous.
+ * heads <= 256, batch <= 4096; batch max_len, batch n_new and num_pages
+ * page_size below 2^31 (batch max_len of a paged cache too, where max_len is
+ * the width of its table in rows); page_size a power of two >= 16; block_table
+ * NULL: contiguous.
  *
  * lrkv_decode8 is lrkv_decode over an 8-bit cache (block_table NULL:
  * contiguous).  The cache's numbers enter the products as they are; what
@@ -684,7 +688,8 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
  * lowest free pages, in the order of the sequences.  page_size: a power of two
  * >= 16.  Lengths outside [0, max_blocks page_size] are clamped; these, and an
  * entry in use that names no page of the pool, set LRKV_ERR_DEVICE_BOUNDS (such
- * an entry stays as it is).  ws: lrkv_pages_workspace_size() bytes, its status
+ * an entry stays as it is; lrkv_pages_extend looks only at those that its new
+ * rows begin inside of).  ws: lrkv_pages_workspace_size() bytes, its status
  * word set afresh.  num_pages and batch * max_blocks at most 2^30, batch <= 4096.
  *
  * lrkv_pages_fork: sequence b becomes the first keep[b] rows of sequence
@@ -694,7 +699,10 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
  * its own; -1: empty.  keep NULL: all rows; keep[b] past the parent's length
  * means all.  refs gains the entries in use after the call and loses those
  * before.  Entries not in use become -1.  Other values of parent, or a
- * negative keep, empty the sequence (LRKV_ERR_DEVICE_BOUNDS).
+ * negative keep, empty the sequence (LRKV_ERR_DEVICE_BOUNDS).  A sequence that
+ * shares pages after a fork cannot be evicted: lrkv_evict moves rows inside of
+ * pages that must be one sequence's own, and lrkv_pages_extend copies only the
+ * page that new rows begin inside of.
  *
  * lrkv_pages_extend: room for the rows [seq_lens[b], new_lens[b]) of every
  * sequence (new_lens[b] <= seq_lens[b]: none), before they are appended.
@@ -718,8 +726,8 @@ lrkv_status lrkv_decode8(const lrkv_dims* dims, const void* q, int page_size, in
  * entries: page p of a pool is page_size / rows pieces of `bytes` bytes from
  * data + p * (page_size / rows) * bytes on, one piece for every `rows` rows (1:
  * a row of a cache tensor; LRKV_BLOCK8: the scales of a block of an 8-bit
- * cache).  data and bytes are multiples of 4; rows divides page_size; all pools have num_pages
- * pages.  Pools do not overlap.
+ * cache).  data and bytes are multiples of 4; rows divides page_size; all pools
+ * have num_pages pages.  Pools do not overlap.
  */
 typedef struct {
   void* data;
