@@ -49,10 +49,12 @@ inline cudaError_t ensure_kernel_smem(const void* func, int bytes, bool max_shar
   auto it = set_bytes.find(key);
   if (it != set_bytes.end() && it->second >= bytes) return cudaSuccess;
   cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, func)) != cudaSuccess) return e;
-  if (bytes + attr.sharedSizeBytes > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
-    return e;
+  if (bytes > 0) {
+    if ((e = cudaFuncGetAttributes(&attr, func)) != cudaSuccess) return e;
+    if (bytes + attr.sharedSizeBytes > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
+      return e;
+  }
   if (max_shared_carveout &&
       (e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared)) != cudaSuccess)
