@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
   // [tile parity][half][warp]: maxima of 4 scores, largest and smallest value scale of the shared rows, of the latents;
   // [half][warp]: maxima of 4 + 4 products
   __shared__ __align__(16) float s_red[2][2][4][8], s_top[2][4][8];
-  __shared__ float s_fac[4][24];                      // [tile % 4]: alpha[8], the products' powers: latents[8], shared[8]
+  __shared__ float s_fac[4][24];                      // [tile % 4]: alpha[8], factors of the products: latents[8], shared[8]
   __shared__ float s_sum[2][4][4];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   volatile int* fail = &s_fail;
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
         smax = fmaxf(smax, e.x); smin = fminf(smin, e.y);
         zmax = fmaxf(zmax, e.z); zmin = fminf(zmin, e.w);
       }
-      // one online softmax per head: maxima and sums against those of the tiles before, probabilities against the tile's
+      // one online softmax per head: the sum over the tiles before's maximum, probabilities over the tile's own
       float xs[4], xz[4], ps[4], pz[4], alpha[4], beta[4], below = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(k8Threads, 1)
       // the power in the largest scale.
       if (smax <= 64.f * smin && zmax <= 64.f * zmin && fmaxf(smax, zmax) < 0x1p100f && fminf(smin, zmin) > 0x1p-100f &&
           below > -64.f) {
-        const float us = vs * (down_to_one(smax) * 128.f), uz = down_to_one(zmax) * 128.f;
+        const float us = vs * (down_to_one(smax) * 128.f), uz = zmax > 0.f ? down_to_one(zmax) * 128.f : 0.f;
         const float fs = power_in(smax) * (1.f / 128.f), fz = power_in(zmax) * (1.f / 128.f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -638,8 +638,8 @@ __global__ void __launch_bounds__(k8Threads, 1)
           pz[k] = fz * beta[k];
         }
       } else {
-        // Any scales, as m 2^e: over a power of two 2^E next to the largest 2^(x + e), x = log2 of the probability, found
-        // in a turn of its own.  The probability, which may be too small for a number, does not enter by itself.  (E
+        // Any scales, as m 2^e: over a power of two 2^E next to the largest 2^(x + e), x = log2 of the probability,
+        // found in a turn of its own.  The probability, which may be too small for a number, does not enter by itself.  (E
         // from -119 on: a 2^-30th of 2^-126 is no number any more.  All tiles this way: 19.5 us for 8 x 4096 rows, 16
         // heads, rank 28, d_h 64, for 17.2; with the turn taken along with that of the scores: 17.7.)
         float es, ez[4];
